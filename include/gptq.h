@@ -53,7 +53,10 @@ typedef enum {
                                 entry point (gptq_quantize_layer_noalloc)                  */
 } gptq_status;
 
-typedef enum { GPTQ_F32 = 0, GPTQ_BF16 = 1, GPTQ_F16 = 2 } gptq_dtype;
+/* GPTQ_E4M3 (4 exponent bits, 3 mantissa bits, largest value 448, no infinity) and
+ * GPTQ_E8M0 (a scale 2^(b - 127), b = 255: NaN) are the 8-bit types of the block-scaled
+ * calls at the end of this file; no other call takes them. */
+typedef enum { GPTQ_F32 = 0, GPTQ_BF16 = 1, GPTQ_F16 = 2, GPTQ_E4M3 = 3, GPTQ_E8M0 = 4 } gptq_dtype;
 
 /* Quantizer knobs ("GPTQ Architecture, in depth", "The algorithm in code" and
  * "Groups, act-order and other knobs"; damping: "Same Ruler, Smarter Placement:
@@ -94,7 +97,10 @@ typedef enum {
   GPTQ_WS_PREPARE = 1,
   GPTQ_WS_QUANTIZE = 2,
   GPTQ_WS_W4A16_REPACK = 3,
-  GPTQ_WS_W4A16 = 4
+  GPTQ_WS_W4A16 = 4,
+  GPTQ_WS_FP8_MATMUL = 5,
+  GPTQ_WS_FP8_GROUPED = 6,
+  GPTQ_WS_MOE_GROUP = 7
 } gptq_ws_call;
 
 /*
@@ -290,11 +296,147 @@ gptq_status gptq_w4a16_matmul(int m, int d_out, int d_in, int n_groups, gptq_dty
                               const uint16_t* scales_f16, float* Y, int64_t ldy, void* workspace,
                               size_t workspace_bytes, hipStream_t stream);
 
+/*
+ * Rounding to 8 bits with a scale per block: blocks of block_rows x 128 (block_rows = 1:
+ * activations, one scale per row and 128 inputs; block_rows = 128: weights).  For every
+ * problem e < batch and block b of X[e] [rows, cols] (the last ones may be cut short):
+ *   top_b   = max |x| over the block
+ *   scale_b = max(fp32(top_b / 448), 2^-126)             s_dtype GPTQ_F32
+ *             max(2^ceil(log2(top_b / 448)), 2^-126)     s_dtype GPTQ_E8M0
+ *   Q       = the e4m3 value nearest to x / scale_b (the true quotient), ties to even
+ * A block that holds an infinity or a NaN gets scale NaN and codes 0.  X is bf16, fp16 or
+ * fp32 with row stride ldx (>= cols) and batch stride batch_stride_x; Q is dense uint8
+ * [batch, rows, cols] and 16-byte aligned; the scale of block (i, j) of problem e is element
+ * e * batch_stride_s + i * ld_s_row + j * ld_s_block of `scales` (fp32 or E8M0 bytes).
+ * Requires cols % 16 == 0; rows may be 0 (no-op).
+ */
+gptq_status gptq_fp8_quantize(int batch, int64_t rows, int cols, gptq_dtype x_dtype, const void* X,
+                              int64_t ldx, int64_t batch_stride_x, int block_rows,
+                              gptq_dtype s_dtype, uint8_t* Q, void* scales, int64_t ld_s_row,
+                              int64_t ld_s_block, int64_t batch_stride_s, hipStream_t stream);
+
+/*
+ * Product of 8-bit activations and 8-bit weights with block scales:
+ *   Y[r, o] = sum over blocks b of 128 inputs of
+ *             xs[r, b] * ws[o / 128, b] * sum_{c in b} xq[r, c] * q[o, c]
+ * qweight: e4m3 [d_out, d_in], dense, 16-byte aligned; w_scales [ceil(d_out / 128),
+ * ceil(d_in / 128)] dense, fp32 or E8M0 by s_dtype (as written by gptq_fp8_quantize with
+ * block_rows = 128).  X [m, d_in], row stride ldx (>= d_in):
+ *   GPTQ_E4M3           xq, 16-byte aligned with ldx % 16 == 0; xs[r, b] is element
+ *                       r * ld_xs_row + b * ld_xs_block of x_scales (type s_dtype)
+ *   GPTQ_BF16, GPTQ_F16 rounded first as gptq_fp8_quantize does with block_rows = 1 and
+ *                       scales of s_dtype; x_scales and its strides are ignored
+ * Y [m, d_out] fp32, bf16 or fp16, row stride ldy (>= d_out).  Products are exact.  For fp32 Y
+ * sums are fp32; for 16-bit Y the chip's 8-bit matrix instructions cut products at 2^-13 of
+ * the largest among 8 consecutive inputs, and sums of blocks are fp32, rounded once.  The
+ * product xs * ws of any two scales has to be a normal fp32 number (or its block's products
+ * zero).  workspace: gptq_workspace_size(GPTQ_WS_FP8_MATMUL, batch = 1, d_out, d_in,
+ * n_tokens_hint = m, NULL) bytes, 16-byte aligned.  Requires d_in % 16 == 0, d_out >= 1; m may be 0 (no-op).
+ */
+gptq_status gptq_fp8_matmul(int64_t m, int d_out, int d_in, gptq_dtype x_dtype, const void* X,
+                            int64_t ldx, gptq_dtype s_dtype, const void* x_scales,
+                            int64_t ld_xs_row, int64_t ld_xs_block, const uint8_t* qweight,
+                            const void* w_scales, gptq_dtype y_dtype, void* Y, int64_t ldy,
+                            void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * The same product for the experts of a mixture-of-experts block: `batch` weights qweight
+ * [batch, d_out, d_in] with scales [batch, ceil(d_out / 128), ceil(d_in / 128)], and
+ * n_rows output rows grouped by expert, expert e owning rows p of token_offsets[e] ..
+ * token_offsets[e + 1] - 1 (DEVICE int64 [batch + 1], not decreasing; each range is clamped to
+ * [0, n_rows]):
+ *   Y[p, :] = X[row_index[p], :] times expert e's weights (row_index NULL: X[p, :])
+ * X has x_rows rows and is rounded once per row, not per output row, when it is bf16 or
+ * fp16.  row_index: DEVICE int32 [n_rows]; an entry outside [0, x_rows) gives a row of
+ * zeros.  Rows of Y outside every range are left as they were.  token_offsets and row_index as
+ * written by gptq_moe_group_tokens.  workspace: gptq_workspace_size(GPTQ_WS_FP8_GROUPED,
+ * batch, d_out, d_in, n_tokens_hint = x_rows, NULL) bytes, 16-byte aligned.
+ */
+gptq_status gptq_fp8_matmul_grouped(int batch, int64_t x_rows, int64_t n_rows, int d_out, int d_in,
+                                    gptq_dtype x_dtype, const void* X, int64_t ldx,
+                                    gptq_dtype s_dtype, const void* x_scales, int64_t ld_xs_row,
+                                    int64_t ld_xs_block, const uint8_t* qweight,
+                                    const void* w_scales, const int64_t* token_offsets,
+                                    const int32_t* row_index, gptq_dtype y_dtype, void* Y,
+                                    int64_t ldy, void* workspace, size_t workspace_bytes,
+                                    hipStream_t stream);
+
+/* How gptq_moe_route scores and picks.
+ *   scoring      0: s = softmax of the token's logits; 1: s = 1 / (1 + exp(-logit))
+ *   n_groups     groups of n_experts / n_groups consecutive experts (1: no groups)
+ *   top_groups   groups whose experts can be chosen, 1..n_groups
+ *   group_score  0: a group ranks by its best choice value; 1: by the sum of its two best
+ *   top_k        experts per token
+ *   renormalize  nonzero: the chosen scores are divided by their sum
+ *   scale        factor on the weights                                                  */
+typedef struct {
+  int scoring;
+  int n_groups;
+  int top_groups;
+  int group_score;
+  int top_k;
+  int renormalize;
+  float scale;
+} gptq_route_params;
+
+/*
+ * Routing of tokens to experts.  For every token t with logits [n_tokens, n_experts] (fp32,
+ * bf16 or fp16, row stride ldl):
+ *   c = s + bias                            choice values (bias fp32 [n_experts]), in fp64;
+ *                                           without a bias the logits themselves, except that
+ *                                           sums of two rank groups by s
+ *   the experts of the top_groups best groups, and of those the top_k largest c, in
+ *   descending order; equal values (of groups and of experts): the lower index first
+ *   ids[t, j]     int32 [n_tokens, top_k]   the chosen experts
+ *   weights[t, j] fp32  [n_tokens, top_k]   scale * s, or scale * s / sum of the chosen s
+ *                                           (0 where that sum is 0)
+ * An expert whose logit is -inf or NaN, or whose bias is -inf or NaN, is never chosen (a
+ * masked logit also adds nothing to the softmax); where fewer than top_k experts can be
+ * chosen the remaining ids are -1 with weight 0.  Softmax over logits of +inf shares the
+ * weight among them.  Requires 1 <= n_experts <= 1024, n_groups dividing n_experts, n_groups <= 64,
+ * 1 <= top_k <= 32 and top_k <= top_groups * n_experts / n_groups; n_tokens may be 0 (no-op).
+ */
+gptq_status gptq_moe_route(int64_t n_tokens, int n_experts, gptq_dtype l_dtype, const void* logits,
+                           int64_t ldl, const float* bias, const gptq_route_params* p, int32_t* ids,
+                           float* weights, hipStream_t stream);
+
+/*
+ * Tokens grouped by expert, from the chosen experts ids [n_tokens, top_k] (int32, dense; a
+ * value outside [0, n_experts) is no choice):
+ *   token_offsets int64 [n_experts + 1]     expert e owns positions token_offsets[e] ..
+ *                                           token_offsets[e + 1] - 1 (the ranges that
+ *                                           gptq_accumulate_hessian_grouped and
+ *                                           gptq_fp8_matmul_grouped take)
+ *   row_index     int32 [n_tokens * top_k]  the token at each position, in token order (then
+ *                                           choice order) inside an expert; -1 behind the
+ *                                           last range
+ *   place         int32 [n_tokens, top_k]   the position of each choice, -1 for no choice
+ * workspace: gptq_workspace_size(GPTQ_WS_MOE_GROUP, 1, n_experts, top_k, n_tokens, NULL) bytes,
+ * 16-byte aligned.  Requires 1 <= n_experts <= 1024, top_k >= 1, n_tokens * top_k < 2^31;
+ * n_tokens may be 0 (all offsets 0).
+ */
+gptq_status gptq_moe_group_tokens(int64_t n_tokens, int top_k, int n_experts, const int32_t* ids,
+                                  int64_t* token_offsets, int32_t* row_index, int32_t* place,
+                                  void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Sum of every token's expert outputs:
+ *   out[t, :] = sum over j (in order, fp32) of weights[t, j] * Y[place[t, j], :]
+ * Y [n_rows, d] fp32, bf16 or fp16, row stride ldy; place int32 [n_tokens, top_k] (an entry
+ * outside [0, n_rows) adds nothing) and weights fp32 [n_tokens, top_k], dense; out [n_tokens,
+ * d] of Y's type, row stride ldo, zeros for a token without choices.  Requires top_k >= 1.
+ */
+gptq_status gptq_moe_combine(int64_t n_tokens, int top_k, int64_t n_rows, int d, gptq_dtype y_dtype,
+                             const void* Y, int64_t ldy, const int32_t* place, const float* weights,
+                             void* out, int64_t ldo, hipStream_t stream);
+
 /* Bytes of workspace the given call needs (0 on invalid arguments).  For
  * GPTQ_WS_HESSIAN `d_out` is ignored and `n_tokens_hint` is the largest n_tokens per call
  * (it only sizes the split over tokens); for GPTQ_WS_W4A16 `n_tokens_hint` is the number
- * of activation rows m and p->group_size the group size (-1: one grid per row); for the
- * other calls it is ignored. */
+ * of activation rows m and p->group_size the group size (-1: one grid per row); for
+ * GPTQ_WS_FP8_MATMUL and GPTQ_WS_FP8_GROUPED `n_tokens_hint` is the number of rows of X; for
+ * GPTQ_WS_MOE_GROUP `d_out` is n_experts and `d_in` is top_k; for the other calls it is
+ * ignored. */
 size_t gptq_workspace_size(gptq_ws_call which, int batch, int d_out, int d_in,
                            int64_t n_tokens_hint, const gptq_params* p);
 

@@ -23,7 +23,7 @@ LIB = os.path.join(PKG, "libgptq.so")
 # the column sweep's instantiations (sweep_*.hip) are the slowest to compile: first, so
 # that they start at once
 SOURCES = ["sweep_g0.hip", "sweep_g128.hip", "sweep_misc.hip", "quantize.hip", "gptq_abi.hip", "hessian.hip",
-           "gemm.hip", "prepare.hip", "pack.hip", "serve.hip"]
+           "gemm.hip", "prepare.hip", "fp8.hip", "pack.hip", "serve.hip", "moe.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc" if os.path.exists("/opt/rocm/bin/hipcc") else "hipcc")
 

@@ -133,6 +133,40 @@ gptq_status pack_enqueue(int batch, int d_out, int d_in, int n_groups, const uin
                          const float* scales, const uint8_t* zeros, int32_t* qweight, int32_t* qzeros,
                          uint16_t* scales_f16, hipStream_t stream);
 
+// Block-scaled 8-bit calls (fp8.hip).
+gptq_status fp8_quantize_enqueue(int batch, int64_t rows, int cols, gptq_dtype x_dtype, const void* X, int64_t ldx,
+                                 int64_t bsx, int block_rows, bool e8, uint8_t* Q, void* S, int64_t lsr, int64_t lsb,
+                                 int64_t bss, hipStream_t stream);
+struct Fp8Problem {
+  int batch;                    // experts; 1 without offsets
+  int64_t x_rows, n_rows;
+  int n, k;
+  gptq_dtype x_dtype;
+  const void* X; int64_t ldx;
+  bool e8;                      // scales are E8M0
+  const void* xs; int64_t xsr, xsb;
+  const uint8_t* W;
+  const void* ws;
+  const int64_t* offsets;       // null: one dense product
+  const int32_t* row_index;
+  gptq_dtype y_dtype;
+  void* Y; int64_t ldy;
+  void* workspace; size_t workspace_bytes;
+};
+size_t fp8_workspace(int64_t x_rows, int k);
+gptq_status fp8_matmul_enqueue(const Fp8Problem& p, hipStream_t stream);
+
+// Routing, grouping and combination of experts (moe.hip).
+gptq_status route_enqueue(int64_t n_tokens, int n_experts, gptq_dtype l_dtype, const void* logits, int64_t ldl,
+                          const float* bias, const gptq_route_params& p, int32_t* ids, float* weights,
+                          hipStream_t stream);
+size_t group_workspace(int n_experts, int64_t slots);
+gptq_status group_enqueue(int64_t n_tokens, int top_k, int n_experts, const int32_t* ids, int64_t* token_offsets,
+                          int32_t* row_index, int32_t* place, void* ws, size_t ws_bytes, hipStream_t stream);
+gptq_status combine_enqueue(int64_t n_tokens, int top_k, int64_t n_rows, int d, gptq_dtype y_dtype, const void* Y,
+                            int64_t ldy, const int32_t* place, const float* weights, void* out, int64_t ldo,
+                            hipStream_t stream);
+
 // Launch timing (gptq_timing_enable / gptq_timing_read): returns the event pair to record
 // around the next launch of the given class, or nulls when timing is off.
 constexpr int kTimedKinds = 5;

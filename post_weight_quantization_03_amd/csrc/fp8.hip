@@ -1,0 +1,559 @@
+// Block-scaled 8-bit linear layers on gfx950: rounding to e4m3 with a scale per block of 128
+// inputs, and the product of such activations and weights, dense or grouped by expert.
+//
+//   scale_b = max |x| / 448 (or the power of two at or above it),  q = rne_e4m3(x / scale_b)
+//   Y[r, o] = sum_b xs[r, b] ws[o / 128, b] sum_{c in b} xq[r, c] q[o, c]
+//
+// For 16-bit Y the inner sums are v_mfma_f32_16x16x128_f8f6f4: one instruction's K is one block
+// of 128, so its 16x16 result takes one scale per row and 128 outputs.  Weights are the first
+// operand and activations the second: a lane then holds one activation row and 4 consecutive
+// outputs, its scale is one register, and its outputs are stored together.  fp32 scales
+// multiply each block's result in fp32; E8M0 scales are operands of the instruction itself.
+// The 8-bit matrix instructions of this chip (all shapes alike, by experiment) add 8
+// consecutive products at the scale of the largest and cut what lies 2^-13 below it: at most
+// 7 * 2^-13 of sum |x q|, 1.5e-5 of the result's norm on normal inputs.  That is below a 16-bit
+// Y's own half step (2^-9, 2^-12) but not fp32's.  For fp32 Y the codes are therefore turned into bf16, which holds them
+// exactly, and multiplied by v_mfma_f32_16x16x32_bf16 with fp32 sums, at half the rate.
+#include <algorithm>
+#include <cfloat>
+
+#include "common.h"
+
+namespace gptq {
+namespace {
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int FB = 128;   // inputs per scale
+
+template <typename T>
+__device__ __forceinline__ T from_f32(float v);
+template <>
+__device__ __forceinline__ float from_f32<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ BF16 from_f32<BF16>(float v) {
+  return BF16{__builtin_bit_cast(uint16_t, static_cast<__bf16>(v))};
+}
+template <>
+__device__ __forceinline__ F16 from_f32<F16>(float v) {
+  return F16{__builtin_bit_cast(uint16_t, static_cast<_Float16>(v))};
+}
+
+// ---------------------------------------------------------------------------- rounding
+
+template <typename T, int V>
+struct alignas(sizeof(T) * V) Vec {
+  T v[V];
+};
+
+// N consecutive elements as fp32; 16-byte loads where rows are aligned.
+template <typename T, int N, bool kVec>
+__device__ __forceinline__ void load_row(const T* p, float* x) {
+  constexpr int V = kVec ? 16 / sizeof(T) : 1;
+#pragma unroll
+  for (int i = 0; i < N; i += V) {
+    const Vec<T, V> w = *reinterpret_cast<const Vec<T, V>*>(p + i);
+#pragma unroll
+    for (int j = 0; j < V; ++j) x[i + j] = load_as_f32(&w.v[j]);
+  }
+}
+
+// The larger of |x| as bits: orders all finite values, infinity and NaN above them.
+template <int N>
+__device__ __forceinline__ uint32_t top_bits(const float* x) {
+  uint32_t t = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) t = max(t, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+  return t;
+}
+
+struct Scale {
+  float s;        // the scale
+  uint8_t code;   // its E8M0 code
+};
+template <bool E8>
+__device__ __forceinline__ Scale block_scale(uint32_t top) {
+  if (top >= 0x7F800000u) return {__uint_as_float(0x7FC00000u), 255};
+  if constexpr (E8) {
+    // 448 = 1.75 * 2^8
+    int e = static_cast<int>(top >> 23) - 127 - 8 + ((top & 0x7FFFFFu) > 0x600000u);
+    e = max(e, -126);
+    return {__uint_as_float(static_cast<uint32_t>(e + 127) << 23), static_cast<uint8_t>(e + 127)};
+  } else {
+    return {fmaxf(__uint_as_float(top) / 448.0f, __uint_as_float(0x00800000u)), 0};
+  }
+}
+
+// fp32 toward which the exact quotient lies, last bit set where it is inexact (rounding to odd):
+// rounding that to e4m3 is rounding the quotient itself, since e4m3's values and midpoints have
+// that bit clear.
+__device__ __forceinline__ float odd_quotient(float x, float s, float r) {
+  const float q0 = x * r;
+  const float q = fmaf(fmaf(-q0, s, x), r, q0);
+  const float e = fmaf(-q, s, x);   // exact sign of the true quotient less q
+  const uint32_t u = __float_as_uint(q);
+  const uint32_t down = (u ^ __float_as_uint(e)) >> 31;
+  return e == 0.0f ? q : __uint_as_float((u - down) | 1u);
+}
+
+// N values of a block as e4m3 bytes, 4 to a word.
+template <bool E8, int N>
+__device__ __forceinline__ void round_values(const float* x, Scale sc, uint32_t* w) {
+  float v[N];
+  if (!(sc.s == sc.s)) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = 0.0f;
+  } else if constexpr (E8) {
+    const float r = __uint_as_float((254u - sc.code) << 23);
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = x[i] * r;   // exact
+  } else {
+    // both sides by 2^64 where the residual of a tiny quotient would leave fp32's range
+    const float up = sc.s < 0x1p-60f ? 0x1p64f : 1.0f;
+    const float s = sc.s * up, r = 1.0f / s;
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = odd_quotient(x[i] * up, s, r);
+  }
+#pragma unroll
+  for (int i = 0; i < N; i += 4) {
+    int p = __builtin_amdgcn_cvt_pk_fp8_f32(v[i], v[i + 1], 0, false);
+    p = __builtin_amdgcn_cvt_pk_fp8_f32(v[i + 2], v[i + 3], p, true);
+    w[i / 4] = static_cast<uint32_t>(p);
+  }
+}
+
+struct QuantArgs {
+  int64_t rows;
+  int cols;
+  const void* X;
+  int64_t ldx, bsx;
+  uint8_t* Q;
+  void* S;
+  int64_t lsr, lsb, bss;
+};
+
+template <bool E8>
+__device__ __forceinline__ void store_scale(const QuantArgs& a, int64_t i, Scale sc) {
+  if constexpr (E8) static_cast<uint8_t*>(a.S)[i] = sc.code;
+  else static_cast<float*>(a.S)[i] = sc.s;
+}
+
+// 1 x 128 blocks: 8 lanes per block, 16 values each; a workgroup takes one block of 32 rows, so
+// that scales stored block by block (ld_s_row = 1) leave it as one run.
+template <typename T, bool E8, bool kVec>
+__global__ __launch_bounds__(256) void quant_rows_kernel(QuantArgs a) {
+  const int b = blockIdx.y;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * 32 + threadIdx.x / 8;
+  const int col = b * FB + (threadIdx.x & 7) * 16;
+  const bool live = row < a.rows && col < a.cols;
+  float x[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) x[i] = 0.0f;
+  if (live) load_row<T, 16, kVec>(static_cast<const T*>(a.X) + blockIdx.z * a.bsx + row * a.ldx + col, x);
+  uint32_t top = top_bits<16>(x);
+  for (int d = 1; d < 8; d <<= 1) top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), d)));
+  if (!live) return;
+  const Scale sc = block_scale<E8>(top);
+  uint32_t w[4];
+  round_values<E8, 16>(x, sc, w);
+  *reinterpret_cast<uint4*>(a.Q + (blockIdx.z * a.rows + row) * a.cols + col) = make_uint4(w[0], w[1], w[2], w[3]);
+  if ((threadIdx.x & 7) == 0) store_scale<E8>(a, blockIdx.z * a.bss + row * a.lsr + b * a.lsb, sc);
+}
+
+// 128 x 128 blocks: one workgroup per block, 64 values per thread (4 rows of 16) in registers.
+template <typename T, bool E8, bool kVec>
+__global__ __launch_bounds__(256) void quant_tile_kernel(QuantArgs a) {
+  __shared__ uint32_t tops[4];
+  const int b = blockIdx.y;
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * FB + threadIdx.x / 8;
+  const int col = b * FB + (threadIdx.x & 7) * 16;
+  float x[4][16];
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) x[i][j] = 0.0f;
+    if (row0 + 32 * i < a.rows && col < a.cols)
+      load_row<T, 16, kVec>(static_cast<const T*>(a.X) + blockIdx.z * a.bsx + (row0 + 32 * i) * a.ldx + col, x[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) top = max(top, top_bits<16>(x[i]));
+  for (int d = 1; d < 64; d <<= 1) top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), d)));
+  if ((threadIdx.x & 63) == 0) tops[threadIdx.x >> 6] = top;
+  __syncthreads();
+  top = max(max(tops[0], tops[1]), max(tops[2], tops[3]));
+  const Scale sc = block_scale<E8>(top);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (row0 + 32 * i >= a.rows || col >= a.cols) continue;
+    uint32_t w[4];
+    round_values<E8, 16>(x[i], sc, w);
+    *reinterpret_cast<uint4*>(a.Q + (blockIdx.z * a.rows + row0 + 32 * i) * a.cols + col) =
+        make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  if (threadIdx.x == 0) store_scale<E8>(a, blockIdx.z * a.bss + blockIdx.x * a.lsr + b * a.lsb, sc);
+}
+
+template <typename T, bool E8, bool kVec>
+gptq_status launch_quant(const QuantArgs& a, int batch, int block_rows, hipStream_t stream) {
+  const int per = block_rows == 1 ? 32 : FB;
+  const int64_t gx = (a.rows + per - 1) / per, gy = (a.cols + FB - 1) / FB;
+  if (gx > (1 << 24) - 1 || gy > 65535 || batch > 65535) return GPTQ_ERR_UNSUPPORTED;
+  const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(gy), batch);
+  if (block_rows == 1) GPTQ_LAUNCH((quant_rows_kernel<T, E8, kVec>), grid, dim3(256), 0, stream, a);
+  else GPTQ_LAUNCH((quant_tile_kernel<T, E8, kVec>), grid, dim3(256), 0, stream, a);
+  return GPTQ_OK;
+}
+
+template <typename T>
+gptq_status launch_quant_t(const QuantArgs& a, int batch, int block_rows, bool e8, hipStream_t stream) {
+  constexpr int V = 16 / sizeof(T);
+  const bool vec = reinterpret_cast<uintptr_t>(a.X) % 16 == 0 && a.ldx % V == 0 && (batch == 1 || a.bsx % V == 0);
+  if (vec)
+    return e8 ? launch_quant<T, true, true>(a, batch, block_rows, stream)
+              : launch_quant<T, false, true>(a, batch, block_rows, stream);
+  return e8 ? launch_quant<T, true, false>(a, batch, block_rows, stream)
+            : launch_quant<T, false, false>(a, batch, block_rows, stream);
+}
+
+// ---------------------------------------------------------------------------- product
+
+struct MmArgs {
+  int64_t m;             // output rows
+  int n, k, kb, nb;      // outputs, inputs and their blocks
+  const uint8_t* X;      // e4m3 rows
+  int64_t ldx, x_rows;
+  const void* xs;        // their scales
+  int64_t xsr, xsb;
+  const uint8_t* W;
+  const void* ws;
+  void* Y;
+  int64_t ldy;
+  int y_dtype;
+  bool e8;               // scales are E8M0
+  bool vec_y;            // rows of Y take 4 values in one store
+  const int64_t* off;    // grouped: the experts' ranges
+  const int32_t* rows;   // grouped: rows of X, or null
+  int experts;
+  int tiles_n;
+};
+
+__device__ const u32x4 zero16 = {0, 0, 0, 0};
+
+// One tile of output rows: rows p0 .. p0 + count - 1 of expert e (count <= 0: no tile).
+struct Tile {
+  int e;
+  int64_t p0;
+  int count;
+};
+// The mt-th tile of TM rows: of the one problem, or counting tiles expert by expert.  Every wave
+// finds it for itself, 64 experts at a time.
+template <int TM>
+__device__ __forceinline__ Tile find_tile(const MmArgs& a, int64_t mt) {
+  if (a.off == nullptr) {
+    const int64_t p0 = mt * TM;
+    return {0, p0, static_cast<int>(min(static_cast<int64_t>(TM), a.m - p0))};
+  }
+  const int lane = threadIdx.x & 63;
+  int64_t before = 0;
+  for (int e0 = 0; e0 < a.experts; e0 += 64) {
+    int64_t lo = 0, n = 0;
+    if (e0 + lane < a.experts) {
+      lo = min(max(a.off[e0 + lane], static_cast<int64_t>(0)), a.m);
+      n = min(max(a.off[e0 + lane + 1], lo), a.m) - lo;
+    }
+    int64_t inc = (n + TM - 1) / TM;
+    const int64_t own = inc;
+    for (int d = 1; d < 64; d <<= 1) {
+      const int64_t o = __shfl_up(inc, d);
+      if (lane >= d) inc += o;
+    }
+    const uint64_t past = __ballot(before + inc > mt);
+    if (past) {
+      const int l = __builtin_ctzll(past);
+      const int64_t first = before + __shfl(inc - own, l);
+      const int64_t r0 = (mt - first) * TM;
+      const int64_t lo_l = __shfl(lo, l), n_l = __shfl(n, l);
+      return {__builtin_amdgcn_readfirstlane(e0 + l), lo_l + r0, static_cast<int>(min(static_cast<int64_t>(TM), n_l - r0))};
+    }
+    before += __shfl(inc, 63);
+  }
+  return {0, 0, 0};
+}
+
+// The row of X behind output row p, -1 for none.
+__device__ __forceinline__ int64_t source_row(const MmArgs& a, int64_t p) {
+  if (a.rows == nullptr) return p < a.x_rows ? p : -1;
+  const int64_t r = a.rows[p];
+  return r >= 0 && r < a.x_rows ? r : -1;
+}
+
+// An E8M0 code as fp32 (2^-127 is subnormal there).
+__device__ __forceinline__ float e8m0_f32(int code) {
+  return code == 255 ? __uint_as_float(0x7FC00000u) : code == 0 ? __uint_as_float(0x00400000u)
+                                                                 : __uint_as_float(static_cast<uint32_t>(code) << 23);
+}
+
+// How a kernel multiplies: 8-bit instructions with fp32 or E8M0 scales, or bf16 ones.
+enum MmaKind { kMmaF32Scale = 0, kMmaE8M0 = 1, kMmaExact = 2 };
+
+// A lane's 32 codes of a block: as they are, or as bf16 (4 operands of 8).
+template <int KIND>
+struct Operand {
+  i32x8 v;
+  Operand() = default;
+  __device__ __forceinline__ explicit Operand(i32x8 x) : v(x) {}
+};
+template <>
+struct Operand<kMmaExact> {
+  bf16x8 v[4];
+  Operand() = default;
+  __device__ __forceinline__ explicit Operand(i32x8 x) {
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const bf16x2 lo = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[i], 1.0f, false);
+      const bf16x2 hi = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[i], 1.0f, true);
+      v[i / 2][4 * (i & 1) + 0] = lo[0];
+      v[i / 2][4 * (i & 1) + 1] = lo[1];
+      v[i / 2][4 * (i & 1) + 2] = hi[0];
+      v[i / 2][4 * (i & 1) + 3] = hi[1];
+    }
+  }
+};
+
+// acc += (w x) sx sw for one block of 128 inputs of 16 outputs and 16 rows.
+template <int KIND>
+__device__ __forceinline__ void block_mma(const Operand<KIND>& w, const Operand<KIND>& x, float sx, float sw,
+                                          f32x4& acc) {
+  const f32x4 z = {0.0f, 0.0f, 0.0f, 0.0f};
+  if constexpr (KIND == kMmaE8M0) {
+    acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w.v, x.v, acc, 0, 0, 0, __float_as_int(sw), 0,
+                                                           __float_as_int(sx));
+  } else {
+    f32x4 t;
+    if constexpr (KIND == kMmaExact) {
+      t = z;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w.v[i], x.v[i], t, 0, 0, 0);
+    } else {
+      t = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w.v, x.v, z, 0, 0, 0, 0, 0, 0);
+    }
+    const float s = sx * sw;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) acc[r] = fmaf(t[r], s, acc[r]);
+  }
+}
+
+// Scale i of an array: fp32, or for kMmaE8M0 the code itself in a register.
+template <int KIND>
+__device__ __forceinline__ float load_scale(const MmArgs& a, const void* p, int64_t i) {
+  if constexpr (KIND == kMmaE8M0) return __int_as_float(static_cast<const uint8_t*>(p)[i]);
+  if constexpr (KIND == kMmaExact)
+    if (a.e8) return e8m0_f32(static_cast<const uint8_t*>(p)[i]);
+  return static_cast<const float*>(p)[i];
+}
+template <int KIND>
+__device__ __forceinline__ float load_xs(const MmArgs& a, int64_t row, int b) {
+  return load_scale<KIND>(a, a.xs, row * a.xsr + b * a.xsb);
+}
+template <int KIND>
+__device__ __forceinline__ float load_ws(const MmArgs& a, int e, int ob, int b) {
+  return load_scale<KIND>(a, a.ws, (static_cast<int64_t>(e) * a.nb + ob) * a.kb + b);
+}
+
+template <typename T>
+__device__ __forceinline__ void store4(T* p, const float* v, int n, bool vec) {
+  if (vec && n >= 4) {
+    Vec<T, 4> o;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o.v[i] = from_f32<T>(v[i]);
+    *reinterpret_cast<Vec<T, 4>*>(p) = o;
+  } else {
+    for (int i = 0; i < min(n, 4); ++i) p[i] = from_f32<T>(v[i]);
+  }
+}
+// outputs o .. o + 3 of output row p
+__device__ __forceinline__ void store_y(const MmArgs& a, int64_t p, int o, const float* v) {
+  const int n = a.n - o;
+  if (n <= 0) return;
+  const int64_t i = p * a.ldy + o;
+  if (a.y_dtype == GPTQ_F32) store4(static_cast<float*>(a.Y) + i, v, n, a.vec_y);
+  else if (a.y_dtype == GPTQ_BF16) store4(static_cast<BF16*>(a.Y) + i, v, n, a.vec_y);
+  else store4(static_cast<F16*>(a.Y) + i, v, n, a.vec_y);
+}
+
+// One wave copies 64 16-byte pieces to LDS: lane l's bytes land at base + 16 l (base uniform).
+// Issued from inline assembly, which has no register result; the caller waits with wait_copies.
+__device__ __forceinline__ void copy16(const void* src, unsigned base) {
+  unsigned saved;
+  asm volatile(
+      "s_mov_b32 %0, m0\n\t"
+      "s_mov_b32 m0, %2\n\t"
+      "global_load_lds_dwordx4 %1, off\n\t"
+      "s_mov_b32 m0, %0"
+      : "=&s"(saved)
+      : "v"(src), "s"(base)
+      : "memory");
+}
+__device__ __forceinline__ void wait_copies() { __builtin_amdgcn_s_waitcnt(0xF70); }   // vmcnt(0)
+
+// Tiles of TM rows x TN outputs, WM x WN waves.  A stage is one block of 128 inputs: TM + TN
+// rows of 128 bytes in LDS, two buffers, the next stage's copies in flight during this one's
+// products.  The 16-byte piece c of row r lies at c ^ (r / 2 % 8), so that 16 lanes reading
+// the same piece of 16 rows cover all 64 banks.
+template <int TM, int TN, int WM, int WN, int KIND>
+__global__ __launch_bounds__(WM* WN * 64) void fp8_tile_kernel(MmArgs a) {
+  constexpr int NW = WM * WN, NT = NW * 64;
+  constexpr int FM = TM / WM / 16, FN = TN / WN / 16;
+  constexpr int STAGE = (TM + TN) * FB;
+  constexpr int LD = (TM + TN) / 8 / NW;
+  static_assert(NW % 2 == 0 && (TM + TN) % (8 * NW) == 0 && TM <= NT && FB % (TN / WN) == 0, "tile shape");
+  __shared__ __attribute__((aligned(128))) uint8_t lds[2 * STAGE];
+  __shared__ float sxs[2 * TM];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int64_t mt = blockIdx.x / a.tiles_n;
+  const int n0 = static_cast<int>(blockIdx.x - mt * a.tiles_n) * TN;
+  const Tile t = find_tile<TM>(a, mt);
+  if (t.count <= 0) return;
+  const uint8_t* We = a.W + static_cast<int64_t>(t.e) * a.n * a.k;
+  const uint8_t* zeros = reinterpret_cast<const uint8_t*>(&zero16);
+
+  const int c = (lane & 7) ^ ((4 * wave + lane / 16) & 7);   // this lane's piece: the same in every copy
+  const uint8_t* src[LD];
+#pragma unroll
+  for (int i = 0; i < LD; ++i) {
+    const int r = (wave + NW * i) * 8 + lane / 8;
+    if (r < TM) {
+      const int64_t row = source_row(a, t.p0 + min(r, t.count - 1));
+      src[i] = row >= 0 ? a.X + row * a.ldx + 16 * c : nullptr;
+    } else {
+      src[i] = We + static_cast<int64_t>(min(n0 + r - TM, a.n - 1)) * a.k + 16 * c;
+    }
+  }
+  const int64_t srow = tid < TM ? source_row(a, t.p0 + min(tid, t.count - 1)) : -1;
+  float sx_next = 0.0f;
+  const unsigned lds0 = static_cast<unsigned>(reinterpret_cast<uintptr_t>(
+      (__attribute__((address_space(3))) uint8_t*)lds));
+  auto issue = [&](int s) {
+    const int k0 = s * FB;
+    const bool in = k0 + 16 * c < a.k;
+    if (srow >= 0) sx_next = load_xs<KIND>(a, srow, s);
+#pragma unroll
+    for (int i = 0; i < LD; ++i)
+      copy16(in && src[i] != nullptr ? src[i] + k0 : zeros, lds0 + (s & 1) * STAGE + (wave + NW * i) * 1024);
+  };
+
+  const int wm = wave / WN, wn = wave % WN;
+  const int j = lane & 15, q = lane >> 4;
+  const int ob = min((n0 + wn * (TN / WN)) / FB, a.nb - 1);
+  const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+  f32x4 y[FM][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int h = 0; h < FN; ++h) y[i][h] = zero;
+  auto frag = [&](const uint8_t* base, int r) {
+    const int sw = (r >> 1) & 7;
+    const i32x4 lo = *reinterpret_cast<const i32x4*>(base + r * FB + 16 * ((2 * q) ^ sw));
+    const i32x4 hi = *reinterpret_cast<const i32x4*>(base + r * FB + 16 * ((2 * q + 1) ^ sw));
+    return Operand<KIND>(i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]});
+  };
+  issue(0);
+  for (int s = 0; s < a.kb; ++s) {
+    wait_copies();
+    if (tid < TM) sxs[(s & 1) * TM + tid] = sx_next;
+    __syncthreads();
+    if (s + 1 < a.kb) issue(s + 1);
+    const float sw = load_ws<KIND>(a, t.e, ob, s);
+    const uint8_t* xb = lds + (s & 1) * STAGE;
+    const uint8_t* wb = xb + TM * FB;
+    Operand<KIND> xf[FM];
+#pragma unroll
+    for (int i = 0; i < FM; ++i) xf[i] = frag(xb, wm * (TM / WM) + 16 * i + j);
+#pragma unroll
+    for (int h = 0; h < FN; ++h) {
+      const Operand<KIND> wf = frag(wb, wn * (TN / WN) + 16 * h + j);
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+        block_mma<KIND>(wf, xf[i], sxs[(s & 1) * TM + wm * (TM / WM) + 16 * i + j], sw, y[i][h]);
+    }
+  }
+  // lane: row j of each 16, outputs 4 q .. 4 q + 3
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+    const int r = wm * (TM / WM) + 16 * i + j;
+    if (r >= t.count) continue;
+#pragma unroll
+    for (int h = 0; h < FN; ++h) {
+      const float v[4] = {y[i][h][0], y[i][h][1], y[i][h][2], y[i][h][3]};
+      store_y(a, t.p0 + r, n0 + wn * (TN / WN) + 16 * h + 4 * q, v);
+    }
+  }
+}
+
+template <int TM, int TN, int WM, int WN>
+gptq_status launch_tile(MmArgs a, int64_t tiles_m, hipStream_t stream) {
+  a.tiles_n = (a.n + TN - 1) / TN;
+  const int64_t grid = tiles_m * a.tiles_n;
+  if (grid > (1 << 22)) return GPTQ_ERR_UNSUPPORTED;
+  const dim3 g(static_cast<unsigned>(grid)), b(WM * WN * 64);
+  if (a.y_dtype == GPTQ_F32) GPTQ_LAUNCH((fp8_tile_kernel<TM, TN, WM, WN, kMmaExact>), g, b, 0, stream, a);
+  else if (a.e8) GPTQ_LAUNCH((fp8_tile_kernel<TM, TN, WM, WN, kMmaE8M0>), g, b, 0, stream, a);
+  else GPTQ_LAUNCH((fp8_tile_kernel<TM, TN, WM, WN, kMmaF32Scale>), g, b, 0, stream, a);
+  return GPTQ_OK;
+}
+
+struct Fp8Layout {
+  size_t q, s, total;
+};
+Fp8Layout fp8_layout(int64_t rows, int k) {
+  const size_t kb = (static_cast<size_t>(k) + FB - 1) / FB;
+  Fp8Layout l{};
+  l.s = align_up(static_cast<size_t>(rows) * k, 256);
+  l.total = std::max<size_t>(256, l.s + align_up(static_cast<size_t>(rows) * kb * 4, 256));
+  return l;
+}
+
+}  // namespace
+
+size_t fp8_workspace(int64_t x_rows, int k) { return fp8_layout(x_rows, k).total; }
+
+gptq_status fp8_quantize_enqueue(int batch, int64_t rows, int cols, gptq_dtype x_dtype, const void* X, int64_t ldx,
+                                 int64_t bsx, int block_rows, bool e8, uint8_t* Q, void* S, int64_t lsr, int64_t lsb,
+                                 int64_t bss, hipStream_t stream) {
+  const QuantArgs a{rows, cols, X, ldx, bsx, Q, S, lsr, lsb, bss};
+  if (x_dtype == GPTQ_F32) return launch_quant_t<float>(a, batch, block_rows, e8, stream);
+  if (x_dtype == GPTQ_BF16) return launch_quant_t<BF16>(a, batch, block_rows, e8, stream);
+  return launch_quant_t<F16>(a, batch, block_rows, e8, stream);
+}
+
+gptq_status fp8_matmul_enqueue(const Fp8Problem& p, hipStream_t stream) {
+  MmArgs a{};
+  a.m = p.n_rows; a.n = p.n; a.k = p.k; a.kb = (p.k + FB - 1) / FB; a.nb = (p.n + FB - 1) / FB;
+  a.x_rows = p.x_rows; a.W = p.W; a.ws = p.ws; a.Y = p.Y; a.ldy = p.ldy; a.y_dtype = p.y_dtype; a.e8 = p.e8;
+  const size_t yb = p.y_dtype == GPTQ_F32 ? 16 : 8;
+  a.vec_y = p.ldy % 4 == 0 && reinterpret_cast<uintptr_t>(p.Y) % yb == 0;
+  a.off = p.offsets; a.rows = p.row_index; a.experts = p.batch;
+  if (p.x_dtype == GPTQ_E4M3) {
+    a.X = static_cast<const uint8_t*>(p.X); a.ldx = p.ldx; a.xs = p.xs; a.xsr = p.xsr; a.xsb = p.xsb;
+  } else {
+    const Fp8Layout l = fp8_layout(p.x_rows, p.k);
+    if (p.workspace == nullptr || p.workspace_bytes < l.total) return GPTQ_ERR_WORKSPACE;
+    uint8_t* ws = static_cast<uint8_t*>(p.workspace);
+    if (p.x_rows > 0) {
+      const gptq_status st = fp8_quantize_enqueue(1, p.x_rows, p.k, p.x_dtype, p.X, p.ldx, 0, 1, p.e8, ws, ws + l.s, 1,
+                                                  p.x_rows, 0, stream);
+      if (st != GPTQ_OK) return st;
+    }
+    a.X = ws; a.ldx = p.k; a.xs = ws + l.s; a.xsr = 1; a.xsb = p.x_rows;
+  }
+  constexpr int TM = 128;
+  const int64_t tiles = a.off == nullptr ? (a.m + TM - 1) / TM
+                                         : a.m / TM + std::min<int64_t>(a.experts, a.m);
+  return launch_tile<TM, 128, 2, 2>(a, tiles, stream);
+}
+
+}  // namespace gptq

@@ -275,6 +275,116 @@ gptq_status gptq_w4a16_matmul(int m, int d_out, int d_in, int n_groups, gptq_dty
                              workspace, workspace_bytes, stream);
 }
 
+namespace {
+bool real_dtype(int t) { return t == GPTQ_F32 || t == GPTQ_BF16 || t == GPTQ_F16; }
+
+// Arguments shared by the dense and the grouped 8-bit product.
+gptq_status check_fp8(const gptq::Fp8Problem& p, gptq_dtype s_dtype) {
+  if (p.batch < 1 || p.n < 1 || p.k < 16 || p.k % 16 != 0 || p.x_rows < 0 || p.n_rows < 0) return GPTQ_ERR_INVALID_ARG;
+  if (p.x_dtype != GPTQ_E4M3 && p.x_dtype != GPTQ_BF16 && p.x_dtype != GPTQ_F16) return GPTQ_ERR_INVALID_ARG;
+  if ((s_dtype != GPTQ_F32 && s_dtype != GPTQ_E8M0) || !real_dtype(p.y_dtype)) return GPTQ_ERR_INVALID_ARG;
+  if (p.n_rows == 0) return GPTQ_OK;
+  if (p.W == nullptr || p.ws == nullptr || p.Y == nullptr || (p.X == nullptr && p.x_rows > 0)) return GPTQ_ERR_INVALID_ARG;
+  if (p.ldx < p.k || p.ldy < p.n || !aligned(p.W, 16)) return GPTQ_ERR_INVALID_ARG;
+  const size_t yb = dtype_bytes(p.y_dtype), sb = s_dtype == GPTQ_F32 ? 4 : 1;
+  if (!aligned(p.Y, yb) || !aligned(p.ws, sb)) return GPTQ_ERR_INVALID_ARG;
+  if (p.x_dtype == GPTQ_E4M3) {
+    if ((p.xs == nullptr && p.x_rows > 0) || !aligned(p.xs, sb) || p.xsr < 1 || p.xsb < 1 || !aligned(p.X, 16) ||
+        p.ldx % 16 != 0)
+      return GPTQ_ERR_INVALID_ARG;
+  } else if (!aligned(p.X, 2) || !aligned(p.workspace, 16)) {
+    return GPTQ_ERR_INVALID_ARG;
+  }
+  return GPTQ_OK;
+}
+}  // namespace
+
+gptq_status gptq_fp8_quantize(int batch, int64_t rows, int cols, gptq_dtype x_dtype, const void* X, int64_t ldx,
+                              int64_t batch_stride_x, int block_rows, gptq_dtype s_dtype, uint8_t* Q, void* scales,
+                              int64_t ld_s_row, int64_t ld_s_block, int64_t batch_stride_s, hipStream_t stream) {
+  if (batch < 1 || rows < 0 || cols < 16 || cols % 16 != 0 || !real_dtype(x_dtype)) return GPTQ_ERR_INVALID_ARG;
+  if ((block_rows != 1 && block_rows != 128) || (s_dtype != GPTQ_F32 && s_dtype != GPTQ_E8M0))
+    return GPTQ_ERR_INVALID_ARG;
+  if (rows == 0) return GPTQ_OK;
+  if (X == nullptr || Q == nullptr || scales == nullptr) return GPTQ_ERR_INVALID_ARG;
+  if (ldx < cols || ld_s_row < 1 || ld_s_block < 1 || !aligned(Q, 16) || !aligned(X, dtype_bytes(x_dtype)) ||
+      (s_dtype == GPTQ_F32 && !aligned(scales, 4)))
+    return GPTQ_ERR_INVALID_ARG;
+  if (batch > 1 && (batch_stride_x < ldx * (rows - 1) + cols || batch_stride_s < 1)) return GPTQ_ERR_INVALID_ARG;
+  return gptq::fp8_quantize_enqueue(batch, rows, cols, x_dtype, X, ldx, batch > 1 ? batch_stride_x : 0, block_rows,
+                                    s_dtype == GPTQ_E8M0, Q, scales, ld_s_row, ld_s_block,
+                                    batch > 1 ? batch_stride_s : 0, stream);
+}
+
+gptq_status gptq_fp8_matmul(int64_t m, int d_out, int d_in, gptq_dtype x_dtype, const void* X, int64_t ldx,
+                            gptq_dtype s_dtype, const void* x_scales, int64_t ld_xs_row, int64_t ld_xs_block,
+                            const uint8_t* qweight, const void* w_scales, gptq_dtype y_dtype, void* Y, int64_t ldy,
+                            void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  const gptq::Fp8Problem p{1, m, m, d_out, d_in, x_dtype, X, ldx, s_dtype == GPTQ_E8M0, x_scales, ld_xs_row,
+                           ld_xs_block, qweight, w_scales, nullptr, nullptr, y_dtype, Y, ldy, workspace,
+                           workspace_bytes};
+  const gptq_status st = check_fp8(p, s_dtype);
+  if (st != GPTQ_OK || m == 0) return st;
+  return gptq::fp8_matmul_enqueue(p, stream);
+}
+
+gptq_status gptq_fp8_matmul_grouped(int batch, int64_t x_rows, int64_t n_rows, int d_out, int d_in, gptq_dtype x_dtype,
+                                    const void* X, int64_t ldx, gptq_dtype s_dtype, const void* x_scales,
+                                    int64_t ld_xs_row, int64_t ld_xs_block, const uint8_t* qweight,
+                                    const void* w_scales, const int64_t* token_offsets, const int32_t* row_index,
+                                    gptq_dtype y_dtype, void* Y, int64_t ldy, void* workspace, size_t workspace_bytes,
+                                    hipStream_t stream) {
+  const gptq::Fp8Problem p{batch, x_rows, n_rows, d_out, d_in, x_dtype, X, ldx, s_dtype == GPTQ_E8M0, x_scales,
+                           ld_xs_row, ld_xs_block, qweight, w_scales, token_offsets, row_index, y_dtype, Y, ldy,
+                           workspace, workspace_bytes};
+  const gptq_status st = check_fp8(p, s_dtype);
+  if (st != GPTQ_OK || n_rows == 0) return st;
+  if (token_offsets == nullptr || !aligned(token_offsets, 8) || !aligned(row_index, 4)) return GPTQ_ERR_INVALID_ARG;
+  return gptq::fp8_matmul_enqueue(p, stream);
+}
+
+gptq_status gptq_moe_route(int64_t n_tokens, int n_experts, gptq_dtype l_dtype, const void* logits, int64_t ldl,
+                           const float* bias, const gptq_route_params* p, int32_t* ids, float* weights,
+                           hipStream_t stream) {
+  if (n_tokens < 0 || n_experts < 1 || n_experts > 1024 || !real_dtype(l_dtype) || p == nullptr)
+    return GPTQ_ERR_INVALID_ARG;
+  if (p->scoring < 0 || p->scoring > 1 || p->group_score < 0 || p->group_score > 1 || p->n_groups < 1 ||
+      p->n_groups > 64 || n_experts % p->n_groups != 0 || p->top_groups < 1 || p->top_groups > p->n_groups ||
+      !std::isfinite(p->scale))
+    return GPTQ_ERR_INVALID_ARG;
+  if (p->top_k < 1 || p->top_k > 32 || p->top_k > p->top_groups * (n_experts / p->n_groups)) return GPTQ_ERR_INVALID_ARG;
+  if (n_tokens == 0) return GPTQ_OK;
+  if (logits == nullptr || ids == nullptr || weights == nullptr || ldl < n_experts) return GPTQ_ERR_INVALID_ARG;
+  if (!aligned(logits, dtype_bytes(l_dtype)) || !aligned(bias, 4) || !aligned(ids, 4) || !aligned(weights, 4))
+    return GPTQ_ERR_INVALID_ARG;
+  return gptq::route_enqueue(n_tokens, n_experts, l_dtype, logits, ldl, bias, *p, ids, weights, stream);
+}
+
+gptq_status gptq_moe_group_tokens(int64_t n_tokens, int top_k, int n_experts, const int32_t* ids,
+                                  int64_t* token_offsets, int32_t* row_index, int32_t* place, void* workspace,
+                                  size_t workspace_bytes, hipStream_t stream) {
+  if (n_tokens < 0 || top_k < 1 || n_experts < 1 || n_experts > 1024 || n_tokens > INT32_MAX / top_k)
+    return GPTQ_ERR_INVALID_ARG;
+  if (token_offsets == nullptr || !aligned(token_offsets, 8)) return GPTQ_ERR_INVALID_ARG;
+  if (n_tokens > 0 && (ids == nullptr || row_index == nullptr || place == nullptr || !aligned(ids, 4) ||
+                       !aligned(row_index, 4) || !aligned(place, 4) || !aligned(workspace, 16)))
+    return GPTQ_ERR_INVALID_ARG;
+  return gptq::group_enqueue(n_tokens, top_k, n_experts, ids, token_offsets, row_index, place, workspace,
+                             workspace_bytes, stream);
+}
+
+gptq_status gptq_moe_combine(int64_t n_tokens, int top_k, int64_t n_rows, int d, gptq_dtype y_dtype, const void* Y,
+                             int64_t ldy, const int32_t* place, const float* weights, void* out, int64_t ldo,
+                             hipStream_t stream) {
+  if (n_tokens < 0 || top_k < 1 || n_rows < 0 || d < 1 || !real_dtype(y_dtype)) return GPTQ_ERR_INVALID_ARG;
+  if (n_tokens == 0) return GPTQ_OK;
+  if ((Y == nullptr && n_rows > 0) || place == nullptr || weights == nullptr || out == nullptr || ldy < d || ldo < d)
+    return GPTQ_ERR_INVALID_ARG;
+  const size_t b = dtype_bytes(y_dtype);
+  if (!aligned(Y, b) || !aligned(out, b) || !aligned(place, 4) || !aligned(weights, 4)) return GPTQ_ERR_INVALID_ARG;
+  return gptq::combine_enqueue(n_tokens, top_k, n_rows, d, y_dtype, Y, ldy, place, weights, out, ldo, stream);
+}
+
 size_t gptq_workspace_size(gptq_ws_call which, int batch, int d_out, int d_in, int64_t n_tokens_hint,
                            const gptq_params* p) {
   switch (which) {
@@ -295,6 +405,13 @@ size_t gptq_workspace_size(gptq_ws_call which, int batch, int d_out, int d_in, i
       if (ng == 0) return 0;
       return gptq::serve_workspace(static_cast<int>(n_tokens_hint), d_out, d_in, ng);
     }
+    case GPTQ_WS_FP8_MATMUL:
+    case GPTQ_WS_FP8_GROUPED:
+      if (batch < 1 || d_out < 1 || d_in < 16 || d_in % 16 != 0 || n_tokens_hint < 0) return 0;
+      return gptq::fp8_workspace(n_tokens_hint, d_in);
+    case GPTQ_WS_MOE_GROUP:
+      if (d_out < 1 || d_out > 1024 || d_in < 1 || n_tokens_hint < 0 || n_tokens_hint > INT32_MAX / d_in) return 0;
+      return gptq::group_workspace(d_out, n_tokens_hint * d_in);
   }
   return 0;
 }
@@ -312,6 +429,6 @@ const char* gptq_status_string(gptq_status s) {
   return "unknown status";
 }
 
-const char* gptq_version(void) { return "0.2.0"; }
+const char* gptq_version(void) { return "0.3.0"; }
 
 }  // extern "C"

@@ -7,7 +7,8 @@ library has not been built: there is no fallback path.
 
 Names follow the C ABI: ``accumulate_hessian``, ``prepare_hinv``, ``quantize_layer``,
 ``pack_int4``.  Tensors may carry a leading batch dimension (independent problems, e.g.
-mixture-of-experts layers).
+mixture-of-experts layers).  ``moe_*`` route tokens to experts and ``fp8_*`` serve layers in
+8 bits; no call records a gradient.
 """
 
 from __future__ import annotations
@@ -25,9 +26,12 @@ GPTQ_OK, GPTQ_ERR_INVALID_ARG, GPTQ_ERR_NOT_SPD, GPTQ_ERR_HIP, GPTQ_ERR_WORKSPAC
 GPTQ_ERR_TOO_LARGE = -6
 NOALLOC_SCRATCH_BYTES = 64 << 20
 WS_HESSIAN, WS_PREPARE, WS_QUANTIZE, WS_W4A16_REPACK, WS_W4A16 = 0, 1, 2, 3, 4
+WS_FP8_MATMUL, WS_FP8_GROUPED, WS_MOE_GROUP = 5, 6, 7
 
 EXPORTED = ("gptq_accumulate_hessian", "gptq_prepare_hinv", "gptq_quantize_layer", "gptq_quantize_layer_noalloc",
             "gptq_accumulate_hessian_grouped", "gptq_pack_int4", "gptq_w4a16_repack", "gptq_w4a16_matmul",
+            "gptq_fp8_quantize", "gptq_fp8_matmul", "gptq_fp8_matmul_grouped", "gptq_moe_route",
+            "gptq_moe_group_tokens", "gptq_moe_combine",
             "gptq_workspace_size", "gptq_status_string", "gptq_version", "gptq_timing_enable", "gptq_timing_read")
 
 
@@ -45,6 +49,12 @@ class _Params(ctypes.Structure):
     _fields_ = [("bits", ctypes.c_int), ("group_size", ctypes.c_int), ("block_size", ctypes.c_int),
                 ("damp", ctypes.c_float), ("act_order", ctypes.c_int), ("sym", ctypes.c_int),
                 ("static_groups", ctypes.c_int)]
+
+
+class _RouteParams(ctypes.Structure):
+    _fields_ = [("scoring", ctypes.c_int), ("n_groups", ctypes.c_int), ("top_groups", ctypes.c_int),
+                ("group_score", ctypes.c_int), ("top_k", ctypes.c_int), ("renormalize", ctypes.c_int),
+                ("scale", ctypes.c_float)]
 
 
 @dataclasses.dataclass(frozen=True)
@@ -91,6 +101,13 @@ def lib() -> ctypes.CDLL:
     L.gptq_pack_int4.argtypes = [i32, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp]
     L.gptq_w4a16_repack.argtypes = [i32, i32, i32, i32, vp, vp, vp, vp, vp, sz, vp]
     L.gptq_w4a16_matmul.argtypes = [i32, i32, i32, i32, i32, vp, i64, vp, vp, vp, vp, vp, i64, vp, sz, vp]
+    L.gptq_fp8_quantize.argtypes = [i32, i64, i32, i32, vp, i64, i64, i32, i32, vp, vp, i64, i64, i64, vp]
+    L.gptq_fp8_matmul.argtypes = [i64, i32, i32, i32, vp, i64, i32, vp, i64, i64, vp, vp, i32, vp, i64, vp, sz, vp]
+    L.gptq_fp8_matmul_grouped.argtypes = [i32, i64, i64, i32, i32, i32, vp, i64, i32, vp, i64, i64, vp, vp, vp, vp,
+                                          i32, vp, i64, vp, sz, vp]
+    L.gptq_moe_route.argtypes = [i64, i32, i32, vp, i64, vp, ctypes.POINTER(_RouteParams), vp, vp, vp]
+    L.gptq_moe_group_tokens.argtypes = [i64, i32, i32, vp, vp, vp, vp, vp, sz, vp]
+    L.gptq_moe_combine.argtypes = [i64, i32, i64, i32, i32, vp, i64, vp, vp, vp, i64, vp]
     L.gptq_workspace_size.argtypes = [i32, i32, i32, i32, i64, ctypes.POINTER(_Params)]
     L.gptq_workspace_size.restype = sz
     L.gptq_status_string.argtypes = [i32]
@@ -101,7 +118,8 @@ def lib() -> ctypes.CDLL:
     L.gptq_timing_read.argtypes = [i32, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_int64)]
     for name in ("gptq_accumulate_hessian", "gptq_accumulate_hessian_grouped", "gptq_prepare_hinv", "gptq_quantize_layer", "gptq_quantize_layer_noalloc",
                  "gptq_pack_int4", "gptq_w4a16_repack", "gptq_w4a16_matmul", "gptq_timing_enable",
-                 "gptq_timing_read"):
+                 "gptq_timing_read", "gptq_fp8_quantize", "gptq_fp8_matmul", "gptq_fp8_matmul_grouped",
+                 "gptq_moe_route", "gptq_moe_group_tokens", "gptq_moe_combine"):
         getattr(L, name).restype = i32
     _lib = L
     return L
@@ -381,6 +399,263 @@ def w4a16_matmul(X: torch.Tensor, qweight_s: torch.Tensor, qzeros: torch.Tensor,
                                    scales_f16.data_ptr(), Y.data_ptr(), Y.stride(0), ws.data_ptr(), ws.numel(),
                                    _stream(stream)), "gptq_w4a16_matmul")
     return Y
+
+
+E4M3, E8M0 = 3, 4
+_SDT = {torch.float32: 0, torch.float8_e8m0fnu: E8M0}
+_FP8_BLOCK = 128
+
+
+def _launch(tensors, stream, call) -> None:
+    """call(stream handle) for tensors of one GPU, with that GPU as the current device: on
+    ``stream``, or on the GPU's current stream."""
+    device = None
+    for t in tensors:
+        if t is None:
+            continue
+        if t.device.type != "cuda":
+            raise ValueError("tensors must be on a GPU")
+        if device is None:
+            device = t.device
+        elif t.device != device:
+            raise ValueError("tensors must be on one GPU")
+    if stream is not None and stream.device != device:
+        raise ValueError("stream and tensors must be on one GPU")
+    if device.index == torch.cuda.current_device():
+        call(_stream(stream))
+    else:
+        with torch.cuda.device(device):
+            call(_stream(stream))
+
+
+def _keep_inputs(stream, *tensors) -> None:
+    """Like _keep_for, for the caller's tensors: they may be freed on the current stream
+    before a call on another stream is done with them."""
+    if stream is not None:
+        for t in tensors:
+            if t is not None and stream != torch.cuda.current_stream(t.device):
+                t.record_stream(stream)
+
+
+def _out(out, shape, dtype, device, name="out"):
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if tuple(out.shape) != tuple(shape) or out.dtype != dtype or out.stride(-1) != 1 or (
+            len(shape) > 1 and shape[0] > 1 and out.stride(0) < shape[-1]):
+        raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)} with contiguous rows")
+    return out
+
+
+def _row_stride(t: torch.Tensor) -> int:
+    """Elements between rows; the row length where there is one row (its stride says nothing)."""
+    return t.stride(-2) if t.shape[-2] > 1 else t.shape[-1]
+
+
+def fp8_quantize(X: torch.Tensor, block_rows: int = 1, scale_dtype: torch.dtype = torch.float32, stream=None):
+    """-> (q float8_e4m3fn of X's shape, scales [(b,) ceil(rows / block_rows), ceil(cols / 128)]):
+    X [(b,) rows, cols] fp32/bf16/fp16 in blocks of block_rows x 128, q = X / scale rounded to
+    nearest even, scale = max|X| / 448 (fp32) or the power of two at or above it
+    (``scale_dtype`` float8_e8m0fnu).  block_rows 1 for activations, 128 for weights.  The
+    scales of activations are stored block by block (stride 1 along the rows), as the products
+    read them."""
+    if X.dtype not in _DT or scale_dtype not in _SDT:
+        raise TypeError("X must be fp32/bf16/fp16, scale_dtype float32 or float8_e8m0fnu")
+    if block_rows not in (1, _FP8_BLOCK) or X.dim() not in (2, 3):
+        raise ValueError("X must be [(batch,) rows, cols], block_rows 1 or 128")
+    Xb = _batched(X, 2)
+    batch, rows, cols = Xb.shape
+    if cols < 16 or cols % 16 or batch < 1:
+        raise ValueError("cols must be a positive multiple of 16")
+    if Xb.stride(2) != 1:
+        raise ValueError("X rows must be contiguous")
+    rb, cb = -(-rows // block_rows), -(-cols // _FP8_BLOCK)
+    q = torch.empty(X.shape, dtype=torch.float8_e4m3fn, device=X.device)
+    if block_rows == 1:
+        S = torch.empty(batch, cb, rb, dtype=scale_dtype, device=X.device).transpose(1, 2)
+        strides = (1, max(rb, 1))
+    else:
+        S = torch.empty(batch, rb, cb, dtype=scale_dtype, device=X.device)
+        strides = (cb, 1)
+    _launch((X,), stream, lambda st: _check(lib().gptq_fp8_quantize(
+        batch, rows, cols, _DT[X.dtype], Xb.data_ptr(), _row_stride(Xb), Xb.stride(0), block_rows, _SDT[scale_dtype],
+        q.data_ptr(), S.data_ptr(), *strides, rb * cb, st), "gptq_fp8_quantize"))
+    _keep_for(stream, q, S)
+    _keep_inputs(stream, X)
+    return q, S if X.dim() == 3 else S[0]
+
+
+def _fp8_operands(X, x_scales, qweight, w_scales, out_dtype):
+    """Checks shared by the dense and the grouped product; -> the scales' type code."""
+    if qweight.dtype != torch.float8_e4m3fn or w_scales.dtype not in _SDT or out_dtype not in _DT:
+        raise TypeError("qweight must be float8_e4m3fn, scales fp32 or float8_e8m0fnu, out_dtype fp32/bf16/fp16")
+    d_out, d_in = qweight.shape[-2:]
+    blocks = -(-d_in // _FP8_BLOCK)
+    if d_in < 16 or d_in % 16 or d_out < 1:
+        raise ValueError("d_in must be a positive multiple of 16")
+    if X.dim() != 2 or X.shape[1] != d_in or X.stride(1) != 1:
+        raise ValueError("X must be [rows, d_in] with contiguous rows")
+    if w_scales.shape != (*qweight.shape[:-2], -(-d_out // _FP8_BLOCK), blocks):
+        raise ValueError("w_scales must be [(batch,) ceil(d_out / 128), ceil(d_in / 128)]")
+    if not (qweight.is_contiguous() and w_scales.is_contiguous()):
+        raise ValueError("qweight and w_scales must be contiguous")
+    if X.dtype == torch.float8_e4m3fn:
+        if x_scales is None or x_scales.dtype != w_scales.dtype:
+            raise TypeError("x_scales must come with float8_e4m3fn X, of the type of w_scales")
+        if x_scales.shape != (X.shape[0], blocks):
+            raise ValueError("x_scales must be [rows, ceil(d_in / 128)]")
+        if x_scales.numel() and (x_scales.stride(0) < 1 or x_scales.stride(1) < 1):
+            raise ValueError("x_scales must not be an expanded tensor")
+    elif X.dtype in (torch.bfloat16, torch.float16):
+        if x_scales is not None:
+            raise TypeError("x_scales belong to float8_e4m3fn X")
+    else:
+        raise TypeError("X must be float8_e4m3fn, bf16 or fp16")
+    return _SDT[w_scales.dtype]
+
+
+def _fp8_workspace(which, batch, X, qweight, workspace, stream):
+    d_out, d_in = qweight.shape[-2:]
+    if X.dtype == torch.float8_e4m3fn:
+        return workspace
+    return _workspace(workspace_size(which, batch, d_out, d_in, X.shape[0]), X.device, workspace, stream)
+
+
+def fp8_matmul(X: torch.Tensor, qweight: torch.Tensor, w_scales: torch.Tensor, x_scales: torch.Tensor | None = None,
+               out_dtype: torch.dtype = torch.bfloat16, out: torch.Tensor | None = None,
+               workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Y [m, d_out] = X What^T with e4m3 weights [d_out, d_in] and the scales of their 128 x 128
+    blocks (:func:`fp8_quantize` with block_rows 128).  X [m, d_in] is float8_e4m3fn with
+    ``x_scales`` [m, ceil(d_in / 128)], or bf16 / fp16, then rounded first as
+    :func:`fp8_quantize` does."""
+    if qweight.dim() != 2:
+        raise ValueError("qweight must be [d_out, d_in]")
+    sdt = _fp8_operands(X, x_scales, qweight, w_scales, out_dtype)
+    (m, d_in), d_out = X.shape, qweight.shape[0]
+    Y = _out(out, (m, d_out), out_dtype, X.device)
+    ws = _fp8_workspace(WS_FP8_MATMUL, 1, X, qweight, workspace, stream)
+    xs, sr, sb = (None, 0, 0) if x_scales is None else (x_scales.data_ptr(), max(x_scales.stride(0), 1),
+                                                        max(x_scales.stride(1), 1))
+    _launch((X, qweight, w_scales, x_scales, Y, ws), stream, lambda st: _check(lib().gptq_fp8_matmul(
+        m, d_out, d_in, _DT.get(X.dtype, E4M3), X.data_ptr(), _row_stride(X), sdt, xs, sr, sb, qweight.data_ptr(),
+        w_scales.data_ptr(), _DT[out_dtype], Y.data_ptr(), _row_stride(Y), None if ws is None else ws.data_ptr(),
+        0 if ws is None else ws.numel(), st), "gptq_fp8_matmul"))
+    _keep_for(stream, Y)
+    _keep_inputs(stream, X, qweight, w_scales, x_scales)
+    return Y
+
+
+def fp8_matmul_grouped(X: torch.Tensor, qweight: torch.Tensor, w_scales: torch.Tensor, token_offsets: torch.Tensor,
+                       row_index: torch.Tensor | None = None, x_scales: torch.Tensor | None = None,
+                       out_dtype: torch.dtype = torch.bfloat16, out: torch.Tensor | None = None,
+                       workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The experts' products: row p of Y [n_rows, d_out], token_offsets[e] <= p <
+    token_offsets[e + 1], is row row_index[p] of X (row p without ``row_index``) times
+    expert e's weights qweight [experts, d_out, d_in]; operands otherwise as in
+    :func:`fp8_matmul`.  ``token_offsets`` int64 [experts + 1] and ``row_index`` int32 [n_rows]
+    come from :func:`moe_group_tokens`.  Rows outside every range are not written."""
+    if qweight.dim() != 3 or qweight.shape[0] < 1:
+        raise ValueError("qweight must be [experts, d_out, d_in]")
+    sdt = _fp8_operands(X, x_scales, qweight, w_scales, out_dtype)
+    (x_rows, d_in), (experts, d_out) = X.shape, qweight.shape[:2]
+    if token_offsets.dtype != torch.int64 or not token_offsets.is_contiguous() or token_offsets.shape != (experts + 1,):
+        raise ValueError("token_offsets must be contiguous int64 [experts + 1]")
+    if row_index is not None and (row_index.dtype != torch.int32 or row_index.dim() != 1 or
+                                  not row_index.is_contiguous()):
+        raise ValueError("row_index must be contiguous int32 [n_rows]")
+    n_rows = x_rows if row_index is None else row_index.numel()
+    Y = _out(out, (n_rows, d_out), out_dtype, X.device)
+    ws = _fp8_workspace(WS_FP8_GROUPED, experts, X, qweight, workspace, stream)
+    xs, sr, sb = (None, 0, 0) if x_scales is None else (x_scales.data_ptr(), max(x_scales.stride(0), 1),
+                                                        max(x_scales.stride(1), 1))
+    _launch((X, qweight, w_scales, token_offsets, row_index, x_scales, Y, ws), stream, lambda st: _check(
+        lib().gptq_fp8_matmul_grouped(
+            experts, x_rows, n_rows, d_out, d_in, _DT.get(X.dtype, E4M3), X.data_ptr(), _row_stride(X), sdt, xs, sr,
+            sb, qweight.data_ptr(), w_scales.data_ptr(), token_offsets.data_ptr(),
+            None if row_index is None else row_index.data_ptr(), _DT[out_dtype], Y.data_ptr(), _row_stride(Y),
+            None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(), st), "gptq_fp8_matmul_grouped"))
+    _keep_for(stream, Y)
+    _keep_inputs(stream, X, qweight, w_scales, token_offsets, row_index, x_scales)
+    return Y
+
+
+_SCORING, _GROUP_SCORE = {"softmax": 0, "sigmoid": 1}, {"max": 0, "top2": 1}
+
+
+def moe_route(logits: torch.Tensor, top_k: int, bias: torch.Tensor | None = None, scoring: str = "softmax",
+              n_groups: int = 1, top_groups: int | None = None, group_score: str = "max", renormalize: bool = True,
+              scale: float = 1.0, stream=None):
+    """-> (ids int32 [tokens, top_k], weights fp32 [tokens, top_k]) from router logits [tokens,
+    experts] (fp32/bf16/fp16): the ``top_k`` largest of softmax or sigmoid scores + ``bias``
+    (fp32 [experts]) among the experts of the ``top_groups`` best of ``n_groups`` groups
+    (ranked by their best choice value or the sum of their two best), in descending order,
+    equal values by index; weights are ``scale`` times the scores without bias, divided by
+    their sum with ``renormalize``.  Logits or biases of -inf or NaN take an expert out; ids
+    are -1 (weight 0) where none is left."""
+    if logits.dtype not in _DT or (bias is not None and bias.dtype != torch.float32):
+        raise TypeError("logits must be fp32/bf16/fp16, bias fp32")
+    if logits.dim() != 2 or logits.shape[1] < 1 or (logits.stride(1) != 1 and logits.shape[1] > 1):
+        raise ValueError("logits must be [tokens, experts] with contiguous rows")
+    tokens, experts = logits.shape
+    if bias is not None and (bias.shape != (experts,) or not bias.is_contiguous()):
+        raise ValueError("bias must be contiguous [experts]")
+    if scoring not in _SCORING or group_score not in _GROUP_SCORE:
+        raise ValueError("scoring must be 'softmax' or 'sigmoid', group_score 'max' or 'top2'")
+    p = _RouteParams(_SCORING[scoring], n_groups, n_groups if top_groups is None else top_groups,
+                     _GROUP_SCORE[group_score], top_k, int(renormalize), scale)
+    ids = torch.empty(tokens, max(top_k, 0), dtype=torch.int32, device=logits.device)
+    weights = torch.empty(tokens, max(top_k, 0), dtype=torch.float32, device=logits.device)
+    _launch((logits, bias), stream, lambda st: _check(lib().gptq_moe_route(
+        tokens, experts, _DT[logits.dtype], logits.data_ptr(), _row_stride(logits),
+        None if bias is None else bias.data_ptr(), ctypes.byref(p), ids.data_ptr(), weights.data_ptr(), st),
+        "gptq_moe_route"))
+    _keep_for(stream, ids, weights)
+    _keep_inputs(stream, logits, bias)
+    return ids, weights
+
+
+def moe_group_tokens(ids: torch.Tensor, n_experts: int, workspace: torch.Tensor | None = None, stream=None):
+    """-> (token_offsets int64 [n_experts + 1], row_index int32 [tokens * top_k], place int32
+    [tokens, top_k]): the choices ids [tokens, top_k] sorted by expert, in token order inside an
+    expert.  ``token_offsets`` are the experts' ranges that accumulate_hessian_grouped and
+    fp8_matmul_grouped take, ``row_index`` the token at each position (-1 behind the last
+    range), ``place`` the position of each choice (-1 for an id outside [0, n_experts))."""
+    if ids.dtype != torch.int32:
+        raise TypeError("ids must be int32")
+    if ids.dim() != 2 or not ids.is_contiguous() or ids.shape[1] < 1 or not 1 <= n_experts <= 1024:
+        raise ValueError("ids must be contiguous [tokens, top_k], n_experts 1..1024")
+    tokens, k = ids.shape
+    offsets = torch.empty(n_experts + 1, dtype=torch.int64, device=ids.device)
+    rows = torch.empty(tokens * k, dtype=torch.int32, device=ids.device)
+    place = torch.empty_like(ids)
+    ws = _workspace(workspace_size(WS_MOE_GROUP, 1, n_experts, k, tokens), ids.device, workspace, stream)
+    _launch((ids, ws), stream, lambda st: _check(lib().gptq_moe_group_tokens(
+        tokens, k, n_experts, ids.data_ptr(), offsets.data_ptr(), rows.data_ptr(), place.data_ptr(), ws.data_ptr(),
+        ws.numel(), st), "gptq_moe_group_tokens"))
+    _keep_for(stream, offsets, rows, place)
+    _keep_inputs(stream, ids)
+    return offsets, rows, place
+
+
+def moe_combine(Y: torch.Tensor, place: torch.Tensor, weights: torch.Tensor, out: torch.Tensor | None = None,
+                stream=None) -> torch.Tensor:
+    """out [tokens, d] (Y's type) = sum over j of weights[:, j] * Y[place[:, j]]: every token's
+    expert outputs, summed in fp32 in the order of its choices; a place outside Y adds
+    nothing."""
+    if Y.dtype not in _DT or place.dtype != torch.int32 or weights.dtype != torch.float32:
+        raise TypeError("Y must be fp32/bf16/fp16, place int32, weights fp32")
+    if Y.dim() != 2 or Y.shape[1] < 1 or Y.stride(1) != 1:
+        raise ValueError("Y must be [rows, d] with contiguous rows")
+    if place.dim() != 2 or place.shape[1] < 1 or weights.shape != place.shape or not (
+            place.is_contiguous() and weights.is_contiguous()):
+        raise ValueError("place and weights must be contiguous [tokens, top_k]")
+    (tokens, k), (rows, d) = place.shape, Y.shape
+    res = _out(out, (tokens, d), Y.dtype, Y.device)
+    _launch((Y, place, weights, res), stream, lambda st: _check(lib().gptq_moe_combine(
+        tokens, k, rows, d, _DT[Y.dtype], Y.data_ptr(), _row_stride(Y), place.data_ptr(), weights.data_ptr(),
+        res.data_ptr(), _row_stride(res), st), "gptq_moe_combine"))
+    _keep_for(stream, res)
+    _keep_inputs(stream, Y, place, weights)
+    return res
 
 
 def timing_enable(on: bool = True, kinds=None) -> None:
