@@ -248,6 +248,13 @@ struct Tile {
   int64_t p0;
   int count;
 };
+// A value that is the same in every lane, in a scalar register.
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ int64_t uniform(int64_t v) {
+  const uint32_t lo = uniform(static_cast<int>(v)), hi = uniform(static_cast<int>(v >> 32));
+  return static_cast<int64_t>((static_cast<uint64_t>(hi) << 32) | lo);
+}
+
 // The mt-th tile of TM rows: of the one problem, or counting tiles expert by expert.  Every wave
 // finds it for itself, 64 experts at a time.
 template <int TM>
@@ -276,7 +283,8 @@ __device__ __forceinline__ Tile find_tile(const MmArgs& a, int64_t mt) {
       const int64_t first = before + __shfl(inc - own, l);
       const int64_t r0 = (mt - first) * TM;
       const int64_t lo_l = __shfl(lo, l), n_l = __shfl(n, l);
-      return {__builtin_amdgcn_readfirstlane(e0 + l), lo_l + r0, static_cast<int>(min(static_cast<int64_t>(TM), n_l - r0))};
+      return {uniform(e0 + l), uniform(lo_l + r0),
+              uniform(static_cast<int>(min(static_cast<int64_t>(TM), n_l - r0)))};
     }
     before += __shfl(inc, 63);
   }
@@ -324,23 +332,28 @@ struct Operand<kMmaExact> {
   }
 };
 
+// w x of one block of 128 inputs of 16 outputs and 16 rows, without scales.
+template <int KIND>
+__device__ __forceinline__ f32x4 block_dot(const Operand<KIND>& w, const Operand<KIND>& x) {
+  f32x4 t = {0.0f, 0.0f, 0.0f, 0.0f};
+  if constexpr (KIND == kMmaExact) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w.v[i], x.v[i], t, 0, 0, 0);
+    return t;
+  } else {
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w.v, x.v, t, 0, 0, 0, 0, 0, 0);
+  }
+}
+
 // acc += (w x) sx sw for one block of 128 inputs of 16 outputs and 16 rows.
 template <int KIND>
 __device__ __forceinline__ void block_mma(const Operand<KIND>& w, const Operand<KIND>& x, float sx, float sw,
                                           f32x4& acc) {
-  const f32x4 z = {0.0f, 0.0f, 0.0f, 0.0f};
   if constexpr (KIND == kMmaE8M0) {
     acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w.v, x.v, acc, 0, 0, 0, __float_as_int(sw), 0,
                                                            __float_as_int(sx));
   } else {
-    f32x4 t;
-    if constexpr (KIND == kMmaExact) {
-      t = z;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w.v[i], x.v[i], t, 0, 0, 0);
-    } else {
-      t = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w.v, x.v, z, 0, 0, 0, 0, 0, 0);
-    }
+    const f32x4 t = block_dot<KIND>(w, x);
     const float s = sx * sw;
 #pragma unroll
     for (int r = 0; r < 4; ++r) acc[r] = fmaf(t[r], s, acc[r]);
@@ -375,6 +388,13 @@ __device__ __forceinline__ void store4(T* p, const float* v, int n, bool vec) {
     for (int i = 0; i < min(n, 4); ++i) p[i] = from_f32<T>(v[i]);
   }
 }
+// four values as bf16 or fp16
+__device__ __forceinline__ uint2 pack16(f32x4 v, bool bf16) {
+  uint16_t u[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) u[i] = bf16 ? from_f32<BF16>(v[i]).bits : from_f32<F16>(v[i]).bits;
+  return make_uint2(u[0] | static_cast<uint32_t>(u[1]) << 16, u[2] | static_cast<uint32_t>(u[3]) << 16);
+}
 // outputs o .. o + 3 of output row p
 __device__ __forceinline__ void store_y(const MmArgs& a, int64_t p, int o, const float* v) {
   const int n = a.n - o;
@@ -396,6 +416,18 @@ __device__ __forceinline__ void copy16(const void* src, unsigned base) {
       "s_mov_b32 m0, %0"
       : "=&s"(saved)
       : "v"(src), "s"(base)
+      : "memory");
+}
+// The same from a scalar base and 32-bit offsets.
+__device__ __forceinline__ void copy16_at(const void* from, uint32_t off, unsigned base) {
+  unsigned saved;
+  asm volatile(
+      "s_mov_b32 %0, m0\n\t"
+      "s_mov_b32 m0, %3\n\t"
+      "global_load_lds_dwordx4 %1, %2\n\t"
+      "s_mov_b32 m0, %0"
+      : "=&s"(saved)
+      : "v"(off), "s"(from), "s"(base)
       : "memory");
 }
 __device__ __forceinline__ void wait_copies() { __builtin_amdgcn_s_waitcnt(0xF70); }   // vmcnt(0)
@@ -470,15 +502,15 @@ __global__ __launch_bounds__(WM* WN * 64) void fp8_tile_kernel(MmArgs a) {
     const float sw = load_ws<KIND>(a, t.e, ob, s);
     const uint8_t* xb = lds + (s & 1) * STAGE;
     const uint8_t* wb = xb + TM * FB;
-    Operand<KIND> xf[FM];
+    Operand<KIND> wf[FN];
 #pragma unroll
-    for (int i = 0; i < FM; ++i) xf[i] = frag(xb, wm * (TM / WM) + 16 * i + j);
+    for (int h = 0; h < FN; ++h) wf[h] = frag(wb, wn * (TN / WN) + 16 * h + j);
 #pragma unroll
-    for (int h = 0; h < FN; ++h) {
-      const Operand<KIND> wf = frag(wb, wn * (TN / WN) + 16 * h + j);
+    for (int i = 0; i < FM; ++i) {
+      const Operand<KIND> xf = frag(xb, wm * (TM / WM) + 16 * i + j);
+      const float sx = sxs[(s & 1) * TM + wm * (TM / WM) + 16 * i + j];
 #pragma unroll
-      for (int i = 0; i < FM; ++i)
-        block_mma<KIND>(wf, xf[i], sxs[(s & 1) * TM + wm * (TM / WM) + 16 * i + j], sw, y[i][h]);
+      for (int h = 0; h < FN; ++h) block_mma<KIND>(wf[h], xf, sx, sw, y[i][h]);
     }
   }
   // lane: row j of each 16, outputs 4 q .. 4 q + 3
@@ -495,14 +527,323 @@ __global__ __launch_bounds__(WM* WN * 64) void fp8_tile_kernel(MmArgs a) {
 }
 
 template <int TM, int TN, int WM, int WN>
-gptq_status launch_tile(MmArgs a, int64_t tiles_m, hipStream_t stream) {
+gptq_status launch_tile(MmArgs a, hipStream_t stream) {
   a.tiles_n = (a.n + TN - 1) / TN;
-  const int64_t grid = tiles_m * a.tiles_n;
+  const int64_t tiles = a.off == nullptr ? (a.m + TM - 1) / TM : a.m / TM + std::min<int64_t>(a.experts, a.m);
+  const int64_t grid = tiles * a.tiles_n;
   if (grid > (1 << 22)) return GPTQ_ERR_UNSUPPORTED;
   const dim3 g(static_cast<unsigned>(grid)), b(WM * WN * 64);
   if (a.y_dtype == GPTQ_F32) GPTQ_LAUNCH((fp8_tile_kernel<TM, TN, WM, WN, kMmaExact>), g, b, 0, stream, a);
   else if (a.e8) GPTQ_LAUNCH((fp8_tile_kernel<TM, TN, WM, WN, kMmaE8M0>), g, b, 0, stream, a);
   else GPTQ_LAUNCH((fp8_tile_kernel<TM, TN, WM, WN, kMmaF32Scale>), g, b, 0, stream, a);
+  return GPTQ_OK;
+}
+
+// The same product for large problems: 256 x 256 tiles, 8 waves of 128 x 64 (8 x 4 blocks of
+// 16 x 16), one workgroup per CU.  Two buffers of 64 KB; operands go global -> LDS with a
+// scalar base that moves by 128 bytes a stage and one 32-bit offset per lane and copy, so that
+// a stage's copies cost little vector arithmetic.  Before a wave's last two rows of blocks it
+// has read all it needs of the stage: there the workgroup waits for the next stage's copies,
+// starts those of the one after it, and the last 8 products cover the first reads of the next
+// stage.  The fold of a row of blocks (y += t * scale) runs under the next row's products.
+template <int KIND>
+__global__ __launch_bounds__(512) void fp8_big_kernel(MmArgs a) {
+  constexpr int TM = 256, TN = 256, WN = 4, NW = 8, FM = 8, FN = 4;
+  constexpr int STAGE = (TM + TN) * FB;
+  constexpr int LD = (TM + TN) / 8 / NW;   // copies per wave and stage: 4 of X, 4 of W
+  constexpr bool E8 = KIND == kMmaE8M0;
+  __shared__ __attribute__((aligned(128))) uint8_t lds[2 * STAGE];
+  __shared__ float scs[2][2][TM];   // the rows' scales; with fp32 scales times those of each 128 outputs
+  __shared__ float scw[2][2];       // E8M0: the outputs' scales
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int64_t mt = blockIdx.x / a.tiles_n;
+  const int n0 = static_cast<int>(blockIdx.x - mt * a.tiles_n) * TN;
+  const Tile t = find_tile<TM>(a, mt);
+  if (t.count <= 0) return;
+
+  const int c = (lane & 7) ^ ((4 * wave + lane / 16) & 7);   // this lane's piece: the same in every copy
+  const uint8_t* xbase = a.X + (a.rows == nullptr ? t.p0 * a.ldx : 0);
+  const uint8_t* wbase = a.W + (static_cast<int64_t>(t.e) * a.n + n0) * a.k;
+  uint32_t off[LD];
+#pragma unroll
+  for (int i = 0; i < LD; ++i) {
+    const int r = (wave + NW * i) * 8 + lane / 8;
+    if (i < LD / 2) {
+      const int64_t row = source_row(a, t.p0 + min(r, t.count - 1));   // none: row 0, and zeros at the end
+      off[i] = static_cast<uint32_t>(max(a.rows == nullptr ? row - t.p0 : row, static_cast<int64_t>(0)) * a.ldx) + 16 * c;
+    } else {
+      off[i] = static_cast<uint32_t>(min(r - TM, a.n - 1 - n0)) * static_cast<uint32_t>(a.k) + 16 * c;
+    }
+  }
+  const int srow_r = tid & (TM - 1), half = tid >> 8;
+  const int64_t srow = max(source_row(a, t.p0 + min(srow_r, t.count - 1)), static_cast<int64_t>(0));
+  const int sob = min(n0 / FB + half, a.nb - 1);
+  float sx_next = 0.0f, sw_next = 0.0f;
+  const unsigned lds0 = static_cast<unsigned>(reinterpret_cast<uintptr_t>(
+      (__attribute__((address_space(3))) uint8_t*)lds));
+  const bool cut = 16 * c >= a.k - (a.kb - 1) * FB;   // this lane's piece of the last stage lies past K
+  auto issue = [&](int s) {
+    sx_next = load_xs<KIND>(a, srow, s);
+    sw_next = load_ws<KIND>(a, t.e, sob, s);
+    const uint8_t* xb = xbase + static_cast<int64_t>(s) * FB;
+    const uint8_t* wb = wbase + static_cast<int64_t>(s) * FB;
+    const unsigned dst = lds0 + (s & 1) * STAGE + wave * 1024;
+    const uint32_t back = s == a.kb - 1 && cut ? 16 * c : 0;   // the row's first piece instead; zeroed below
+#pragma unroll
+    for (int i = 0; i < LD; ++i) copy16_at(i < LD / 2 ? xb : wb, off[i] - back, dst + NW * i * 1024);
+  };
+  // the copies and scales of stage s have landed; the next barrier makes them visible
+  auto land = [&](int s, bool last) {
+    wait_copies();
+    if (last && cut) {
+#pragma unroll
+      for (int i = 0; i < LD; ++i)
+        *reinterpret_cast<uint4*>(lds + (s & 1) * STAGE + (wave + NW * i) * 1024 + 16 * lane) = make_uint4(0, 0, 0, 0);
+    }
+    scs[s & 1][half][srow_r] = E8 ? sx_next : sx_next * sw_next;
+    if (E8 && srow_r == 0) scw[s & 1][half] = sw_next;
+  };
+  auto barrier = [&] {
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  };
+
+  const int wm = wave / WN, wn = wave % WN;
+  const int j = lane & 15, q = lane >> 4;
+  const int xr = wm * 16 * FM, wr = TM + wn * 16 * FN;
+  // pieces q and q + 4 of a row are this lane's 32 inputs (any order that both operands share):
+  // the lanes that one LDS access serves together then meet no bank twice
+  const int swz = (j >> 1) & 7;
+  const int at0 = j * FB + 16 * (q ^ swz), at1 = j * FB + 16 * ((q + 4) ^ swz);
+  auto frag = [&](int s, int r) {
+    const uint8_t* p = lds + (s & 1) * STAGE + r * FB;
+    const i32x4 lo = *reinterpret_cast<const i32x4*>(p + at0);
+    const i32x4 hi = *reinterpret_cast<const i32x4*>(p + at1);
+    return Operand<KIND>(i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]});
+  };
+  auto scale_of = [&](int s, int i) { return scs[s & 1][E8 ? 0 : wn / 2][xr + 16 * i + j]; };
+
+  const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+  f32x4 y[FM][FN], td[2][FN];
+#pragma unroll
+  for (int h = 0; h < FN; ++h) {
+#pragma unroll
+    for (int i = 0; i < FM; ++i) y[i][h] = zero;
+    td[0][h] = td[1][h] = zero;
+  }
+  Operand<KIND> xf[3], wf[FN];
+  float sc[3], sd = 0.0f, sw = 0.0f;   // sd: the scale of the products that wait in td
+  // products of row of blocks i, output block h; with E8M0 scales straight into y
+  auto dot = [&](int i, int h) {
+    if constexpr (E8) block_mma<KIND>(wf[h], xf[i % 3], sc[i % 3], sw, y[i][h]);
+    else td[i & 1][h] = block_dot<KIND>(wf[h], xf[i % 3]);
+  };
+  // the empty constraint keeps the multiply-adds here (the compiler moves them all behind the
+  // last product and spills the products)
+  auto fold = [&](int i, int h, float s) {
+    if constexpr (!E8) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) y[i][h][r] = fmaf(td[i & 1][h][r], s, y[i][h][r]);
+      asm volatile("" : "+v"(y[i][h]));
+    }
+  };
+
+  // the order of one row of blocks: reads for two rows ahead, then each product under the last
+  // row's fold; left to itself the compiler hoists reads until registers spill
+  auto interleave = [] {
+    __builtin_amdgcn_sched_group_barrier(0x100, 3, 0);   // LDS reads
+#pragma unroll
+    for (int h = 0; h < FN; ++h) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);   // a product
+      __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);   // four multiply-adds
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+
+  // one stage; kMore: another follows, kIssue: and one after that (constants, so that the
+  // loop's body has no branch for the compiler to move products across)
+  auto stage = [&](int s, auto kMore, auto kIssue) {
+#pragma unroll
+    for (int i = 0; i < FM - 2; ++i) {
+      xf[(i + 2) % 3] = frag(s, xr + 16 * (i + 2));
+      sc[(i + 2) % 3] = scale_of(s, i + 2);
+#pragma unroll
+      for (int h = 0; h < FN; ++h) {
+        dot(i, h);
+        fold((i + FM - 1) % FM, h, sd);
+      }
+      sd = sc[i % 3];
+      interleave();
+    }
+    if constexpr (kMore) {
+      land(s + 1, !kIssue);
+      barrier();
+      if constexpr (kIssue) issue(s + 2);
+    }
+    // the last two rows of blocks (operands 0 and 1), output block by output block: a weight
+    // operand makes room for the next stage's after its second product
+    float sw1 = 0.0f;
+    if constexpr (E8 && kMore) sw1 = scw[(s + 1) & 1][wn / 2];
+#pragma unroll
+    for (int h = 0; h < FN; ++h) {
+      dot(FM - 2, h);
+      fold(FM - 3, h, sd);
+      dot(FM - 1, h);
+      if constexpr (kMore) wf[h] = frag(s + 1, wr + 16 * h);
+      if (h > 0) fold(FM - 2, h - 1, sc[0]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    fold(FM - 2, FN - 1, sc[0]);
+    sd = sc[1];
+    if constexpr (kMore) {
+      xf[0] = frag(s + 1, xr);
+      sc[0] = scale_of(s + 1, 0);
+      xf[1] = frag(s + 1, xr + 16);
+      sc[1] = scale_of(s + 1, 1);
+      sw = sw1;
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+
+  issue(0);
+  land(0, a.kb == 1);
+  barrier();
+  if (a.kb > 1) issue(1);
+  xf[0] = frag(0, xr);
+  sc[0] = scale_of(0, 0);
+#pragma unroll
+  for (int h = 0; h < FN; ++h) wf[h] = frag(0, wr + 16 * h);
+  xf[1] = frag(0, xr + 16);
+  sc[1] = scale_of(0, 1);
+  if constexpr (E8) sw = scw[0][wn / 2];
+  const std::true_type yes;
+  const std::false_type no;
+  for (int s = 0; s + 2 < a.kb; ++s) stage(s, yes, yes);
+  if (a.kb > 1) stage(a.kb - 2, yes, no);
+  stage(a.kb - 1, no, no);
+#pragma unroll
+  for (int h = 0; h < FN; ++h) fold(FM - 1, h, sd);
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+    const int r = xr + 16 * i + j;
+    if (r >= t.count) continue;
+    const bool none = a.rows != nullptr && source_row(a, t.p0 + r) < 0;
+    uint16_t* out = static_cast<uint16_t*>(a.Y) + (t.p0 + r) * a.ldy;
+#pragma unroll
+    for (int h = 0; h < FN; ++h) {
+      const int o = n0 + wn * 16 * FN + 16 * h + 4 * q;
+      const uint2 v = none ? make_uint2(0, 0) : pack16(y[i][h], a.y_dtype == GPTQ_BF16);
+      if (a.vec_y && o + 4 <= a.n) {
+        *reinterpret_cast<uint2*>(out + o) = v;
+      } else {
+        if (o < a.n) out[o] = static_cast<uint16_t>(v.x);
+        if (o + 1 < a.n) out[o + 1] = static_cast<uint16_t>(v.x >> 16);
+        if (o + 2 < a.n) out[o + 2] = static_cast<uint16_t>(v.y);
+        if (o + 3 < a.n) out[o + 3] = static_cast<uint16_t>(v.y >> 16);
+      }
+    }
+  }
+}
+
+gptq_status launch_big(MmArgs a, hipStream_t stream) {
+  a.tiles_n = (a.n + 255) / 256;
+  const int64_t tiles = a.off == nullptr ? (a.m + 255) / 256 : a.m / 256 + std::min<int64_t>(a.experts, a.m);
+  const int64_t grid = tiles * a.tiles_n;
+  if (grid > (1 << 22)) return GPTQ_ERR_UNSUPPORTED;
+  const dim3 g(static_cast<unsigned>(grid)), b(512);
+  if (a.e8) GPTQ_LAUNCH((fp8_big_kernel<kMmaE8M0>), g, b, 0, stream, a);
+  else GPTQ_LAUNCH((fp8_big_kernel<kMmaF32Scale>), g, b, 0, stream, a);
+  return GPTQ_OK;
+}
+
+// Few rows: 16 outputs x 16 FM rows per workgroup, its NW waves taking every NW-th block of
+// inputs straight from memory to registers, U blocks in flight per wave; the waves' sums meet
+// in LDS and are added in wave order.
+template <int FM, int NW, int KIND>
+__global__ __launch_bounds__(NW * 64) void fp8_rows_kernel(MmArgs a) {
+  constexpr int U = FM <= 2 ? 4 : 2, TM = 16 * FM;
+  __shared__ __attribute__((aligned(16))) float part[NW][TM][16];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int64_t mt = blockIdx.x / a.tiles_n;
+  const int n0 = static_cast<int>(blockIdx.x - mt * a.tiles_n) * 16;
+  const Tile t = find_tile<TM>(a, mt);
+  if (t.count <= 0) return;
+  const int j = lane & 15, q = lane >> 4;
+  const uint8_t* zeros = reinterpret_cast<const uint8_t*>(&zero16);
+  const uint8_t* w = a.W + (static_cast<int64_t>(t.e) * a.n + min(n0 + j, a.n - 1)) * a.k + 32 * q;
+  const uint8_t* x[FM];
+  int64_t row[FM];
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+    row[i] = source_row(a, t.p0 + min(16 * i + j, t.count - 1));
+    x[i] = a.X + row[i] * a.ldx + 32 * q;
+  }
+  i32x4 wl[U], wh[U], xl[U][FM], xh[U][FM];
+  float sw[U], sx[U][FM];
+  auto load = [&](int u, int b) {
+    const int c = FB * b + 32 * q;
+    const bool lo = c < a.k, hi = c + 16 < a.k;
+    wl[u] = *reinterpret_cast<const i32x4*>(lo ? w + FB * b : zeros);
+    wh[u] = *reinterpret_cast<const i32x4*>(hi ? w + FB * b + 16 : zeros);
+    sw[u] = load_ws<KIND>(a, t.e, n0 / FB, b);
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      xl[u][i] = *reinterpret_cast<const i32x4*>(lo && row[i] >= 0 ? x[i] + FB * b : zeros);
+      xh[u][i] = *reinterpret_cast<const i32x4*>(hi && row[i] >= 0 ? x[i] + FB * b + 16 : zeros);
+      sx[u][i] = row[i] >= 0 ? load_xs<KIND>(a, row[i], b) : 0.0f;
+    }
+  };
+  const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+  f32x4 y[FM];
+#pragma unroll
+  for (int i = 0; i < FM; ++i) y[i] = zero;
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (wave + NW * u < a.kb) load(u, wave + NW * u);
+  for (int b0 = wave; b0 < a.kb; b0 += NW * U) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int b = b0 + NW * u;
+      if (b < a.kb) {
+        const Operand<KIND> wf(i32x8{wl[u][0], wl[u][1], wl[u][2], wl[u][3], wh[u][0], wh[u][1], wh[u][2], wh[u][3]});
+#pragma unroll
+        for (int i = 0; i < FM; ++i) {
+          const Operand<KIND> xf(i32x8{xl[u][i][0], xl[u][i][1], xl[u][i][2], xl[u][i][3], xh[u][i][0], xh[u][i][1],
+                                       xh[u][i][2], xh[u][i][3]});
+          block_mma<KIND>(wf, xf, sx[u][i], sw[u], y[i]);
+        }
+        if (b + NW * U < a.kb) load(u, b + NW * U);
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < FM; ++i) *reinterpret_cast<f32x4*>(&part[wave][16 * i + j][4 * q]) = y[i];
+  __syncthreads();
+  for (int r = tid / 4; r < min(TM, t.count); r += NW * 16) {
+    f32x4 v = zero;
+#pragma unroll
+    for (int h = 0; h < NW; ++h) {
+      const f32x4 o = *reinterpret_cast<const f32x4*>(&part[h][r][4 * (tid & 3)]);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) v[c] += o[c];
+    }
+    const float f[4] = {v[0], v[1], v[2], v[3]};
+    store_y(a, t.p0 + r, n0 + 4 * (tid & 3), f);
+  }
+}
+
+template <int FM, int NW>
+gptq_status launch_rows(MmArgs a, hipStream_t stream) {
+  constexpr int TM = 16 * FM;
+  a.tiles_n = (a.n + 15) / 16;
+  const int64_t tiles = a.off == nullptr ? (a.m + TM - 1) / TM : a.m / TM + std::min<int64_t>(a.experts, a.m);
+  const int64_t grid = tiles * a.tiles_n;
+  if (grid > (1 << 22)) return GPTQ_ERR_UNSUPPORTED;
+  const dim3 g(static_cast<unsigned>(grid)), b(NW * 64);
+  if (a.y_dtype == GPTQ_F32) GPTQ_LAUNCH((fp8_rows_kernel<FM, NW, kMmaExact>), g, b, 0, stream, a);
+  else if (a.e8) GPTQ_LAUNCH((fp8_rows_kernel<FM, NW, kMmaE8M0>), g, b, 0, stream, a);
+  else GPTQ_LAUNCH((fp8_rows_kernel<FM, NW, kMmaF32Scale>), g, b, 0, stream, a);
   return GPTQ_OK;
 }
 
@@ -550,10 +891,11 @@ gptq_status fp8_matmul_enqueue(const Fp8Problem& p, hipStream_t stream) {
     }
     a.X = ws; a.ldx = p.k; a.xs = ws + l.s; a.xsr = 1; a.xsb = p.x_rows;
   }
-  constexpr int TM = 128;
-  const int64_t tiles = a.off == nullptr ? (a.m + TM - 1) / TM
-                                         : a.m / TM + std::min<int64_t>(a.experts, a.m);
-  return launch_tile<TM, 128, 2, 2>(a, tiles, stream);
+  const int64_t per = a.off == nullptr ? a.m : a.m / a.experts;   // rows that share weights
+  if (per <= 16) return launch_rows<1, 8>(a, stream);
+  if (per <= 64) return launch_rows<4, 8>(a, stream);
+  if (getenv("T256") && a.y_dtype != GPTQ_F32) return launch_big(a, stream);
+  return launch_tile<128, 128, 2, 2>(a, stream);
 }
 
 }  // namespace gptq

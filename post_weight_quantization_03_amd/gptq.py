@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import functools
 import os
 
 import torch
@@ -406,35 +407,45 @@ _SDT = {torch.float32: 0, torch.float8_e8m0fnu: E8M0}
 _FP8_BLOCK = 128
 
 
-def _launch(tensors, stream, call) -> None:
-    """call(stream handle) for tensors of one GPU, with that GPU as the current device: on
-    ``stream``, or on the GPU's current stream."""
-    device = None
+def _run(what: str, stream, tensors, *args) -> None:
+    """The library's call ``what`` with ``args`` and a stream handle, for tensors (or None) of
+    one GPU, with that GPU as the current device: on ``stream``, or on its current stream.
+    The first of ``tensors`` is not None.  Small calls last a few microseconds, so this path
+    creates no Stream object (2.8 us of a 12.9 us call)."""
+    device = tensors[0].get_device()
     for t in tensors:
-        if t is None:
-            continue
-        if t.device.type != "cuda":
-            raise ValueError("tensors must be on a GPU")
-        if device is None:
-            device = t.device
-        elif t.device != device:
+        if t is not None and t.get_device() != device:
             raise ValueError("tensors must be on one GPU")
-    if stream is not None and stream.device != device:
-        raise ValueError("stream and tensors must be on one GPU")
-    if device.index == torch.cuda.current_device():
-        call(_stream(stream))
+    if device < 0:
+        raise ValueError("tensors must be on a GPU")
+    fn = getattr(lib(), what)
+    if stream is None and device == torch.cuda.current_device():
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(device))
     else:
+        if stream is not None and stream.device.index != device:
+            raise ValueError("stream and tensors must be on one GPU")
         with torch.cuda.device(device):
-            call(_stream(stream))
+            status = fn(*args, _stream(stream))
+        if stream is not None and stream != torch.cuda.current_stream(stream.device):
+            # also the caller's tensors: they may be freed on the current stream before a call
+            # on another one is done with them
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(stream)
+    if status != GPTQ_OK:
+        _check(status, what)
 
 
-def _keep_inputs(stream, *tensors) -> None:
-    """Like _keep_for, for the caller's tensors: they may be freed on the current stream
-    before a call on another stream is done with them."""
-    if stream is not None:
-        for t in tensors:
-            if t is not None and stream != torch.cuda.current_stream(t.device):
-                t.record_stream(stream)
+@functools.lru_cache(maxsize=4096)
+def _workspace_bytes(which: int, batch: int, d_out: int, d_in: int, hint: int) -> int:
+    return workspace_size(which, batch, d_out, d_in, hint)
+
+
+def _scratch(which, batch, d_out, d_in, hint, device, workspace) -> torch.Tensor:
+    nbytes = _workspace_bytes(which, batch, d_out, d_in, hint)
+    if workspace is not None and workspace.numel() * workspace.element_size() >= nbytes:
+        return workspace
+    return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
 
 
 def _out(out, shape, dtype, device, name="out"):
@@ -448,7 +459,8 @@ def _out(out, shape, dtype, device, name="out"):
 
 def _row_stride(t: torch.Tensor) -> int:
     """Elements between rows; the row length where there is one row (its stride says nothing)."""
-    return t.stride(-2) if t.shape[-2] > 1 else t.shape[-1]
+    rows, cols = t.shape[-2:]
+    return t.stride()[-2] if rows > 1 else cols
 
 
 def fp8_quantize(X: torch.Tensor, block_rows: int = 1, scale_dtype: torch.dtype = torch.float32, stream=None):
@@ -469,19 +481,15 @@ def fp8_quantize(X: torch.Tensor, block_rows: int = 1, scale_dtype: torch.dtype 
     if Xb.stride(2) != 1:
         raise ValueError("X rows must be contiguous")
     rb, cb = -(-rows // block_rows), -(-cols // _FP8_BLOCK)
+    ld_row, ld_block = (1, max(rb, 1)) if block_rows == 1 else (cb, 1)
     q = torch.empty(X.shape, dtype=torch.float8_e4m3fn, device=X.device)
-    if block_rows == 1:
-        S = torch.empty(batch, cb, rb, dtype=scale_dtype, device=X.device).transpose(1, 2)
-        strides = (1, max(rb, 1))
+    if X.dim() == 2:
+        S = torch.empty_strided((rb, cb), (ld_row, ld_block), dtype=scale_dtype, device=X.device)
     else:
-        S = torch.empty(batch, rb, cb, dtype=scale_dtype, device=X.device)
-        strides = (cb, 1)
-    _launch((X,), stream, lambda st: _check(lib().gptq_fp8_quantize(
-        batch, rows, cols, _DT[X.dtype], Xb.data_ptr(), _row_stride(Xb), Xb.stride(0), block_rows, _SDT[scale_dtype],
-        q.data_ptr(), S.data_ptr(), *strides, rb * cb, st), "gptq_fp8_quantize"))
-    _keep_for(stream, q, S)
-    _keep_inputs(stream, X)
-    return q, S if X.dim() == 3 else S[0]
+        S = torch.empty_strided((batch, rb, cb), (rb * cb, ld_row, ld_block), dtype=scale_dtype, device=X.device)
+    _run("gptq_fp8_quantize", stream, (X, q, S), batch, rows, cols, _DT[X.dtype], X.data_ptr(), _row_stride(Xb),
+         Xb.stride(0), block_rows, _SDT[scale_dtype], q.data_ptr(), S.data_ptr(), ld_row, ld_block, rb * cb)
+    return q, S
 
 
 def _fp8_operands(X, x_scales, qweight, w_scales, out_dtype):
@@ -513,11 +521,12 @@ def _fp8_operands(X, x_scales, qweight, w_scales, out_dtype):
     return _SDT[w_scales.dtype]
 
 
-def _fp8_workspace(which, batch, X, qweight, workspace, stream):
-    d_out, d_in = qweight.shape[-2:]
-    if X.dtype == torch.float8_e4m3fn:
-        return workspace
-    return _workspace(workspace_size(which, batch, d_out, d_in, X.shape[0]), X.device, workspace, stream)
+def _fp8_scales(x_scales):
+    """Pointer and strides of the scales of 8-bit activations."""
+    if x_scales is None:
+        return None, 0, 0
+    sr, sb = x_scales.stride()
+    return x_scales.data_ptr(), max(sr, 1), max(sb, 1)
 
 
 def fp8_matmul(X: torch.Tensor, qweight: torch.Tensor, w_scales: torch.Tensor, x_scales: torch.Tensor | None = None,
@@ -532,15 +541,11 @@ def fp8_matmul(X: torch.Tensor, qweight: torch.Tensor, w_scales: torch.Tensor, x
     sdt = _fp8_operands(X, x_scales, qweight, w_scales, out_dtype)
     (m, d_in), d_out = X.shape, qweight.shape[0]
     Y = _out(out, (m, d_out), out_dtype, X.device)
-    ws = _fp8_workspace(WS_FP8_MATMUL, 1, X, qweight, workspace, stream)
-    xs, sr, sb = (None, 0, 0) if x_scales is None else (x_scales.data_ptr(), max(x_scales.stride(0), 1),
-                                                        max(x_scales.stride(1), 1))
-    _launch((X, qweight, w_scales, x_scales, Y, ws), stream, lambda st: _check(lib().gptq_fp8_matmul(
-        m, d_out, d_in, _DT.get(X.dtype, E4M3), X.data_ptr(), _row_stride(X), sdt, xs, sr, sb, qweight.data_ptr(),
-        w_scales.data_ptr(), _DT[out_dtype], Y.data_ptr(), _row_stride(Y), None if ws is None else ws.data_ptr(),
-        0 if ws is None else ws.numel(), st), "gptq_fp8_matmul"))
-    _keep_for(stream, Y)
-    _keep_inputs(stream, X, qweight, w_scales, x_scales)
+    ws = None if X.dtype == torch.float8_e4m3fn else _scratch(WS_FP8_MATMUL, 1, d_out, d_in, m, X.device, workspace)
+    _run("gptq_fp8_matmul", stream, (X, qweight, w_scales, x_scales, Y, ws), m, d_out, d_in, _DT.get(X.dtype, E4M3),
+         X.data_ptr(), _row_stride(X), sdt, *_fp8_scales(x_scales), qweight.data_ptr(), w_scales.data_ptr(),
+         _DT[out_dtype], Y.data_ptr(), _row_stride(Y), None if ws is None else ws.data_ptr(),
+         0 if ws is None else ws.numel() * ws.element_size())
     return Y
 
 
@@ -564,17 +569,13 @@ def fp8_matmul_grouped(X: torch.Tensor, qweight: torch.Tensor, w_scales: torch.T
         raise ValueError("row_index must be contiguous int32 [n_rows]")
     n_rows = x_rows if row_index is None else row_index.numel()
     Y = _out(out, (n_rows, d_out), out_dtype, X.device)
-    ws = _fp8_workspace(WS_FP8_GROUPED, experts, X, qweight, workspace, stream)
-    xs, sr, sb = (None, 0, 0) if x_scales is None else (x_scales.data_ptr(), max(x_scales.stride(0), 1),
-                                                        max(x_scales.stride(1), 1))
-    _launch((X, qweight, w_scales, token_offsets, row_index, x_scales, Y, ws), stream, lambda st: _check(
-        lib().gptq_fp8_matmul_grouped(
-            experts, x_rows, n_rows, d_out, d_in, _DT.get(X.dtype, E4M3), X.data_ptr(), _row_stride(X), sdt, xs, sr,
-            sb, qweight.data_ptr(), w_scales.data_ptr(), token_offsets.data_ptr(),
-            None if row_index is None else row_index.data_ptr(), _DT[out_dtype], Y.data_ptr(), _row_stride(Y),
-            None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(), st), "gptq_fp8_matmul_grouped"))
-    _keep_for(stream, Y)
-    _keep_inputs(stream, X, qweight, w_scales, token_offsets, row_index, x_scales)
+    ws = None if X.dtype == torch.float8_e4m3fn else _scratch(WS_FP8_GROUPED, experts, d_out, d_in, x_rows, X.device,
+                                                              workspace)
+    _run("gptq_fp8_matmul_grouped", stream, (X, qweight, w_scales, token_offsets, row_index, x_scales, Y, ws), experts,
+         x_rows, n_rows, d_out, d_in, _DT.get(X.dtype, E4M3), X.data_ptr(), _row_stride(X), sdt,
+         *_fp8_scales(x_scales), qweight.data_ptr(), w_scales.data_ptr(), token_offsets.data_ptr(),
+         None if row_index is None else row_index.data_ptr(), _DT[out_dtype], Y.data_ptr(), _row_stride(Y),
+         None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel() * ws.element_size())
     return Y
 
 
@@ -604,12 +605,9 @@ def moe_route(logits: torch.Tensor, top_k: int, bias: torch.Tensor | None = None
                      _GROUP_SCORE[group_score], top_k, int(renormalize), scale)
     ids = torch.empty(tokens, max(top_k, 0), dtype=torch.int32, device=logits.device)
     weights = torch.empty(tokens, max(top_k, 0), dtype=torch.float32, device=logits.device)
-    _launch((logits, bias), stream, lambda st: _check(lib().gptq_moe_route(
-        tokens, experts, _DT[logits.dtype], logits.data_ptr(), _row_stride(logits),
-        None if bias is None else bias.data_ptr(), ctypes.byref(p), ids.data_ptr(), weights.data_ptr(), st),
-        "gptq_moe_route"))
-    _keep_for(stream, ids, weights)
-    _keep_inputs(stream, logits, bias)
+    _run("gptq_moe_route", stream, (logits, bias, ids, weights), tokens, experts, _DT[logits.dtype], logits.data_ptr(),
+         _row_stride(logits), None if bias is None else bias.data_ptr(), ctypes.byref(p), ids.data_ptr(),
+         weights.data_ptr())
     return ids, weights
 
 
@@ -627,12 +625,9 @@ def moe_group_tokens(ids: torch.Tensor, n_experts: int, workspace: torch.Tensor 
     offsets = torch.empty(n_experts + 1, dtype=torch.int64, device=ids.device)
     rows = torch.empty(tokens * k, dtype=torch.int32, device=ids.device)
     place = torch.empty_like(ids)
-    ws = _workspace(workspace_size(WS_MOE_GROUP, 1, n_experts, k, tokens), ids.device, workspace, stream)
-    _launch((ids, ws), stream, lambda st: _check(lib().gptq_moe_group_tokens(
-        tokens, k, n_experts, ids.data_ptr(), offsets.data_ptr(), rows.data_ptr(), place.data_ptr(), ws.data_ptr(),
-        ws.numel(), st), "gptq_moe_group_tokens"))
-    _keep_for(stream, offsets, rows, place)
-    _keep_inputs(stream, ids)
+    ws = _scratch(WS_MOE_GROUP, 1, n_experts, k, tokens, ids.device, workspace)
+    _run("gptq_moe_group_tokens", stream, (ids, offsets, rows, place, ws), tokens, k, n_experts, ids.data_ptr(),
+         offsets.data_ptr(), rows.data_ptr(), place.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size())
     return offsets, rows, place
 
 
@@ -650,11 +645,8 @@ def moe_combine(Y: torch.Tensor, place: torch.Tensor, weights: torch.Tensor, out
         raise ValueError("place and weights must be contiguous [tokens, top_k]")
     (tokens, k), (rows, d) = place.shape, Y.shape
     res = _out(out, (tokens, d), Y.dtype, Y.device)
-    _launch((Y, place, weights, res), stream, lambda st: _check(lib().gptq_moe_combine(
-        tokens, k, rows, d, _DT[Y.dtype], Y.data_ptr(), _row_stride(Y), place.data_ptr(), weights.data_ptr(),
-        res.data_ptr(), _row_stride(res), st), "gptq_moe_combine"))
-    _keep_for(stream, res)
-    _keep_inputs(stream, Y, place, weights)
+    _run("gptq_moe_combine", stream, (Y, place, weights, res), tokens, k, rows, d, _DT[Y.dtype], Y.data_ptr(),
+         _row_stride(Y), place.data_ptr(), weights.data_ptr(), res.data_ptr(), _row_stride(res))
     return res
 
 
