@@ -350,7 +350,8 @@ gptq_status gptq_fp8_matmul(int64_t m, int d_out, int d_in, gptq_dtype x_dtype, 
  * fp16.  row_index: DEVICE int32 [n_rows]; an entry outside [0, x_rows) gives a row of
  * zeros.  Rows of Y outside every range are left as they were.  token_offsets and row_index as
  * written by gptq_moe_group_tokens.  workspace: gptq_workspace_size(GPTQ_WS_FP8_GROUPED,
- * batch, d_out, d_in, n_tokens_hint = x_rows, NULL) bytes, 16-byte aligned.
+ * batch, d_out, d_in, n_tokens_hint = x_rows, NULL) bytes, 16-byte aligned.  Requires
+ * (n_rows / 16 + 1) * batch < 2^31 (GPTQ_ERR_UNSUPPORTED).
  */
 gptq_status gptq_fp8_matmul_grouped(int batch, int64_t x_rows, int64_t n_rows, int d_out, int d_in,
                                     gptq_dtype x_dtype, const void* X, int64_t ldx,

@@ -220,6 +220,32 @@ gptq_status launch_quant_t(const QuantArgs& a, int batch, int block_rows, bool e
 
 // ---------------------------------------------------------------------------- product
 
+// Which tile a workgroup takes.  Workgroups go to the 8 XCDs in turn, 32 CUs each; tiles are
+// numbered in bands of 4 tile rows, column by column, and an XCD takes runs of consecutive ones
+// (32, or an eighth of a small grid): the 32 tiles it works on at once are then 4 x 8 and read 12
+// operand panels through its L2 instead of the 18 of a row-by-row grid.
+struct TileOrder {
+  int tiles_n;
+  int64_t tiles_m, total, run;
+};
+inline TileOrder tile_order(int64_t tiles_m, int tiles_n) {
+  const int64_t total = tiles_m * tiles_n;
+  return {tiles_n, tiles_m, total, std::min<int64_t>(32, (total + 7) / 8)};
+}
+inline int64_t order_grid(const TileOrder& o) { return (o.total + 8 * o.run - 1) / (8 * o.run) * 8 * o.run; }
+// (tile row, tile column) of workgroup b; false for none
+__device__ __forceinline__ bool ordered_tile(const TileOrder& o, uint32_t b, int64_t* mt, int* nt) {
+  const uint32_t slot = b / 8, run = static_cast<uint32_t>(o.run);
+  const int64_t p = (static_cast<int64_t>(slot / run) * 8 + b % 8) * run + slot % run;
+  if (p >= o.total) return false;
+  const uint32_t per = 4u * static_cast<uint32_t>(o.tiles_n);
+  const uint32_t band = static_cast<uint32_t>(p) / per, r = static_cast<uint32_t>(p) % per;
+  const uint32_t rows = static_cast<uint32_t>(min(static_cast<int64_t>(4), o.tiles_m - 4 * static_cast<int64_t>(band)));
+  *mt = 4 * static_cast<int64_t>(band) + r % rows;
+  *nt = static_cast<int>(r / rows);
+  return true;
+}
+
 struct MmArgs {
   int64_t m;             // output rows
   int n, k, kb, nb;      // outputs, inputs and their blocks
@@ -238,6 +264,7 @@ struct MmArgs {
   const int32_t* rows;   // grouped: rows of X, or null
   int experts;
   int tiles_n;
+  TileOrder order;
 };
 
 __device__ const u32x4 zero16 = {0, 0, 0, 0};
@@ -264,24 +291,23 @@ __device__ __forceinline__ Tile find_tile(const MmArgs& a, int64_t mt) {
     return {0, p0, static_cast<int>(min(static_cast<int64_t>(TM), a.m - p0))};
   }
   const int lane = threadIdx.x & 63;
-  int64_t before = 0;
+  int before = 0;   // tiles of earlier experts; the launch bounds their number
   for (int e0 = 0; e0 < a.experts; e0 += 64) {
     int64_t lo = 0, n = 0;
     if (e0 + lane < a.experts) {
       lo = min(max(a.off[e0 + lane], static_cast<int64_t>(0)), a.m);
       n = min(max(a.off[e0 + lane + 1], lo), a.m) - lo;
     }
-    int64_t inc = (n + TM - 1) / TM;
-    const int64_t own = inc;
+    const int own = static_cast<int>((n + TM - 1) / TM);
+    int inc = own;
     for (int d = 1; d < 64; d <<= 1) {
-      const int64_t o = __shfl_up(inc, d);
+      const int o = __shfl_up(inc, d);
       if (lane >= d) inc += o;
     }
     const uint64_t past = __ballot(before + inc > mt);
     if (past) {
       const int l = __builtin_ctzll(past);
-      const int64_t first = before + __shfl(inc - own, l);
-      const int64_t r0 = (mt - first) * TM;
+      const int64_t r0 = (mt - (before + __shfl(inc - own, l))) * TM;
       const int64_t lo_l = __shfl(lo, l), n_l = __shfl(n, l);
       return {uniform(e0 + l), uniform(lo_l + r0),
               uniform(static_cast<int>(min(static_cast<int64_t>(TM), n_l - r0)))};
@@ -430,6 +456,12 @@ __device__ __forceinline__ void copy16_at(const void* from, uint32_t off, unsign
       : "v"(off), "s"(from), "s"(base)
       : "memory");
 }
+// s_waitcnt vmcnt(N): all but the last N copies and loads are done.
+template <int N>
+__device__ __forceinline__ void wait_vmcnt() {
+  static_assert(N >= 0 && N < 64, "vmcnt field");
+  __builtin_amdgcn_s_waitcnt(0xF70 | (N & 15) | ((N >> 4) << 14));
+}
 __device__ __forceinline__ void wait_copies() { __builtin_amdgcn_s_waitcnt(0xF70); }   // vmcnt(0)
 
 // Tiles of TM rows x TN outputs, WM x WN waves.  A stage is one block of 128 inputs: TM + TN
@@ -556,8 +588,10 @@ __global__ __launch_bounds__(512) void fp8_big_kernel(MmArgs a) {
   __shared__ float scs[2][2][TM];   // the rows' scales; with fp32 scales times those of each 128 outputs
   __shared__ float scw[2][2];       // E8M0: the outputs' scales
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int64_t mt = blockIdx.x / a.tiles_n;
-  const int n0 = static_cast<int>(blockIdx.x - mt * a.tiles_n) * TN;
+  int64_t mt;
+  int nt;
+  if (!ordered_tile(a.order, blockIdx.x, &mt, &nt)) return;
+  const int n0 = nt * TN;
   const Tile t = find_tile<TM>(a, mt);
   if (t.count <= 0) return;
 
@@ -747,9 +781,9 @@ __global__ __launch_bounds__(512) void fp8_big_kernel(MmArgs a) {
 }
 
 gptq_status launch_big(MmArgs a, hipStream_t stream) {
-  a.tiles_n = (a.n + 255) / 256;
-  const int64_t tiles = a.off == nullptr ? (a.m + 255) / 256 : a.m / 256 + std::min<int64_t>(a.experts, a.m);
-  const int64_t grid = tiles * a.tiles_n;
+  a.order = tile_order(a.off == nullptr ? (a.m + 255) / 256 : a.m / 256 + std::min<int64_t>(a.experts, a.m),
+                       (a.n + 255) / 256);
+  const int64_t grid = order_grid(a.order);
   if (grid > (1 << 22)) return GPTQ_ERR_UNSUPPORTED;
   const dim3 g(static_cast<unsigned>(grid)), b(512);
   if (a.e8) GPTQ_LAUNCH((fp8_big_kernel<kMmaE8M0>), g, b, 0, stream, a);
@@ -757,14 +791,121 @@ gptq_status launch_big(MmArgs a, hipStream_t stream) {
   return GPTQ_OK;
 }
 
-// Few rows: 16 outputs x 16 FM rows per workgroup, its NW waves taking every NW-th block of
-// inputs straight from memory to registers, U blocks in flight per wave; the waves' sums meet
-// in LDS and are added in wave order.
-template <int FM, int NW, int KIND>
-__global__ __launch_bounds__(NW * 64) void fp8_rows_kernel(MmArgs a) {
+// The same product for grids of few tiles, where a stage lasts no longer than a copy takes:
+// 64 x 64 tiles, 4 waves of 32 x 32, four buffers of 16 KB and three stages of copies in
+// flight.  All scales of the tile are in LDS before the first stage, so that the loop has no
+// other loads and can wait for copies by their number.
+constexpr int MID_KB = 224;   // most blocks of inputs (their scales are 256 bytes each)
+template <int KIND>
+__global__ __launch_bounds__(256) void fp8_mid_kernel(MmArgs a) {
+  constexpr int TM = 64, TN = 64, NW = 4, NB = 4;
+  constexpr int STAGE = (TM + TN) * FB;
+  constexpr int LD = (TM + TN) / 8 / NW;
+  __shared__ __attribute__((aligned(128))) uint8_t lds[NB * STAGE];
+  extern __shared__ float scales[];   // [kb][TM] of the rows, then [kb] of the outputs
+  const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+  int64_t mt;
+  int nt;
+  if (!ordered_tile(a.order, blockIdx.x, &mt, &nt)) return;
+  const int n0 = nt * TN;
+  const Tile t = find_tile<TM>(a, mt);
+  if (t.count <= 0) return;
+  const uint8_t* We = a.W + static_cast<int64_t>(t.e) * a.n * a.k;
+  const uint8_t* zeros = reinterpret_cast<const uint8_t*>(&zero16);
+  const int c = (lane & 7) ^ ((4 * wave + lane / 16) & 7);
+  const uint8_t* src[LD];
+#pragma unroll
+  for (int i = 0; i < LD; ++i) {
+    const int r = (wave + NW * i) * 8 + lane / 8;
+    if (r < TM) {
+      const int64_t row = source_row(a, t.p0 + min(r, t.count - 1));
+      src[i] = row >= 0 ? a.X + row * a.ldx + 16 * c : nullptr;
+    } else {
+      src[i] = We + static_cast<int64_t>(min(n0 + r - TM, a.n - 1)) * a.k + 16 * c;
+    }
+  }
+  const unsigned lds0 = static_cast<unsigned>(reinterpret_cast<uintptr_t>(
+      (__attribute__((address_space(3))) uint8_t*)lds));
+  auto issue = [&](int s) {
+    const int k0 = s * FB;
+    const bool in = k0 + 16 * c < a.k;
+#pragma unroll
+    for (int i = 0; i < LD; ++i)
+      copy16(in && src[i] != nullptr ? src[i] + k0 : zeros, lds0 + (s % NB) * STAGE + (wave + NW * i) * 1024);
+  };
+  {
+    const int64_t row = source_row(a, t.p0 + min(lane, t.count - 1));
+    for (int b = wave; b < a.kb; b += NW) scales[b * TM + lane] = row >= 0 ? load_xs<KIND>(a, row, b) : 0.0f;
+    for (int b = tid; b < a.kb; b += 256) scales[a.kb * TM + b] = load_ws<KIND>(a, t.e, n0 / FB, b);
+  }
+  const int wm = wave / 2, wn = wave % 2;
+  const int j = lane & 15, q = lane >> 4;
+  const int swz = (j >> 1) & 7;
+  const int at0 = j * FB + 16 * (q ^ swz), at1 = j * FB + 16 * ((q + 4) ^ swz);
+  const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+  f32x4 y[2][2] = {{zero, zero}, {zero, zero}};
+  // the loads above are done with before the first copy: the loop counts copies alone
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+#pragma unroll
+  for (int s = 0; s < NB - 1; ++s)
+    if (s < a.kb) issue(s);
+  for (int s = 0; s < a.kb; ++s) {
+    // this stage's copies are the oldest of those of up to three stages
+    if (s + 2 < a.kb) wait_vmcnt<2 * LD>();
+    else if (s + 1 < a.kb) wait_vmcnt<LD>();
+    else wait_vmcnt<0>();
+    __syncthreads();   // everyone's copies have landed, and everyone is done with the stage before
+    if (s + NB - 1 < a.kb) issue(s + NB - 1);
+    const uint8_t* xb = lds + (s % NB) * STAGE + wm * 32 * FB;
+    const uint8_t* wb = lds + (s % NB) * STAGE + (TM + wn * 32) * FB;
+    auto frag = [&](const uint8_t* p) {
+      const i32x4 lo = *reinterpret_cast<const i32x4*>(p + at0);
+      const i32x4 hi = *reinterpret_cast<const i32x4*>(p + at1);
+      return Operand<KIND>(i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]});
+    };
+    const Operand<KIND> xf[2] = {frag(xb), frag(xb + 16 * FB)}, wf[2] = {frag(wb), frag(wb + 16 * FB)};
+    const float sw = scales[a.kb * TM + s];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float sx = scales[s * TM + wm * 32 + 16 * i + j];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) block_mma<KIND>(wf[h], xf[i], sx, sw, y[i][h]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int r = wm * 32 + 16 * i + j;
+    if (r >= t.count) continue;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float v[4] = {y[i][h][0], y[i][h][1], y[i][h][2], y[i][h][3]};
+      store_y(a, t.p0 + r, n0 + wn * 32 + 16 * h + 4 * q, v);
+    }
+  }
+}
+
+gptq_status launch_mid(MmArgs a, hipStream_t stream) {
+  a.order = tile_order(a.off == nullptr ? (a.m + 63) / 64 : a.m / 64 + std::min<int64_t>(a.experts, a.m),
+                       (a.n + 63) / 64);
+  const int64_t grid = order_grid(a.order);
+  if (grid > (1 << 22)) return GPTQ_ERR_UNSUPPORTED;
+  const dim3 g(static_cast<unsigned>(grid)), b(256);
+  const size_t lds = static_cast<size_t>(a.kb) * 65 * sizeof(float);
+  if (a.y_dtype == GPTQ_F32) GPTQ_LAUNCH((fp8_mid_kernel<kMmaExact>), g, b, lds, stream, a);
+  else if (a.e8) GPTQ_LAUNCH((fp8_mid_kernel<kMmaE8M0>), g, b, lds, stream, a);
+  else GPTQ_LAUNCH((fp8_mid_kernel<kMmaF32Scale>), g, b, lds, stream, a);
+  return GPTQ_OK;
+}
+
+// Few rows: 16 outputs x 16 FM rows per workgroup, whose WK waves take every WK-th block of
+// inputs straight from memory to registers, U blocks in flight per wave; their sums meet in LDS
+// and are added in wave order.  (Several groups of 16 outputs per workgroup, with fewer waves
+// along the inputs, measured the same or slower.)
+template <int FM, int WK, int KIND>
+__global__ __launch_bounds__(WK * 64) void fp8_rows_kernel(MmArgs a) {
   constexpr int U = FM <= 2 ? 4 : 2, TM = 16 * FM;
-  __shared__ __attribute__((aligned(16))) float part[NW][TM][16];
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  __shared__ __attribute__((aligned(16))) float part[WK][TM][16];
+  const int tid = threadIdx.x, lane = tid & 63, wk = uniform(tid >> 6);
   const int64_t mt = blockIdx.x / a.tiles_n;
   const int n0 = static_cast<int>(blockIdx.x - mt * a.tiles_n) * 16;
   const Tile t = find_tile<TM>(a, mt);
@@ -800,11 +941,11 @@ __global__ __launch_bounds__(NW * 64) void fp8_rows_kernel(MmArgs a) {
   for (int i = 0; i < FM; ++i) y[i] = zero;
 #pragma unroll
   for (int u = 0; u < U; ++u)
-    if (wave + NW * u < a.kb) load(u, wave + NW * u);
-  for (int b0 = wave; b0 < a.kb; b0 += NW * U) {
+    if (wk + WK * u < a.kb) load(u, wk + WK * u);
+  for (int b0 = wk; b0 < a.kb; b0 += WK * U) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int b = b0 + NW * u;
+      const int b = b0 + WK * u;
       if (b < a.kb) {
         const Operand<KIND> wf(i32x8{wl[u][0], wl[u][1], wl[u][2], wl[u][3], wh[u][0], wh[u][1], wh[u][2], wh[u][3]});
 #pragma unroll
@@ -813,38 +954,89 @@ __global__ __launch_bounds__(NW * 64) void fp8_rows_kernel(MmArgs a) {
                                        xh[u][i][2], xh[u][i][3]});
           block_mma<KIND>(wf, xf, sx[u][i], sw[u], y[i]);
         }
-        if (b + NW * U < a.kb) load(u, b + NW * U);
+        if (b + WK * U < a.kb) load(u, b + WK * U);
       }
     }
   }
 #pragma unroll
-  for (int i = 0; i < FM; ++i) *reinterpret_cast<f32x4*>(&part[wave][16 * i + j][4 * q]) = y[i];
+  for (int i = 0; i < FM; ++i) *reinterpret_cast<f32x4*>(&part[wk][16 * i + j][4 * q]) = y[i];
   __syncthreads();
-  for (int r = tid / 4; r < min(TM, t.count); r += NW * 16) {
+  for (int g = tid; g < min(TM, t.count) * 4; g += WK * 64) {
+    const int c = g & 3, r = g >> 2;
     f32x4 v = zero;
 #pragma unroll
-    for (int h = 0; h < NW; ++h) {
-      const f32x4 o = *reinterpret_cast<const f32x4*>(&part[h][r][4 * (tid & 3)]);
+    for (int h = 0; h < WK; ++h) {
+      const f32x4 o = *reinterpret_cast<const f32x4*>(&part[h][r][4 * c]);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) v[c] += o[c];
+      for (int e = 0; e < 4; ++e) v[e] += o[e];
     }
     const float f[4] = {v[0], v[1], v[2], v[3]};
-    store_y(a, t.p0 + r, n0 + 4 * (tid & 3), f);
+    store_y(a, t.p0 + r, n0 + 4 * c, f);
   }
 }
 
-template <int FM, int NW>
+template <int FM, int WK>
 gptq_status launch_rows(MmArgs a, hipStream_t stream) {
   constexpr int TM = 16 * FM;
   a.tiles_n = (a.n + 15) / 16;
   const int64_t tiles = a.off == nullptr ? (a.m + TM - 1) / TM : a.m / TM + std::min<int64_t>(a.experts, a.m);
   const int64_t grid = tiles * a.tiles_n;
   if (grid > (1 << 22)) return GPTQ_ERR_UNSUPPORTED;
-  const dim3 g(static_cast<unsigned>(grid)), b(NW * 64);
-  if (a.y_dtype == GPTQ_F32) GPTQ_LAUNCH((fp8_rows_kernel<FM, NW, kMmaExact>), g, b, 0, stream, a);
-  else if (a.e8) GPTQ_LAUNCH((fp8_rows_kernel<FM, NW, kMmaE8M0>), g, b, 0, stream, a);
-  else GPTQ_LAUNCH((fp8_rows_kernel<FM, NW, kMmaF32Scale>), g, b, 0, stream, a);
+  const dim3 g(static_cast<unsigned>(grid)), b(WK * 64);
+  if (a.y_dtype == GPTQ_F32) GPTQ_LAUNCH((fp8_rows_kernel<FM, WK, kMmaExact>), g, b, 0, stream, a);
+  else if (a.e8) GPTQ_LAUNCH((fp8_rows_kernel<FM, WK, kMmaE8M0>), g, b, 0, stream, a);
+  else GPTQ_LAUNCH((fp8_rows_kernel<FM, WK, kMmaF32Scale>), g, b, 0, stream, a);
   return GPTQ_OK;
+}
+
+// Which kernel: the least of four estimates in microseconds.  Their constants are device times
+// of the kernels on one MI355X, per stage of 128 inputs and round of workgroups:
+//   rows  2.5 + bytes through the L2s at 7 TB/s, every 16 outputs reading all of X again
+//         (4096 x 14336: 11.9 us at 1 row, 18.3 at 16, 27.7 at 32, 45.8 at 64)
+//   mid   64 x 64, one workgroup per CU 0.46 us, two 0.57 (both fit up to 60 blocks of inputs)
+//         (4096 x 14336: 52 us at 64 rows, 55 at 256, 103 at 512; 14336 x 4096 at 64: 19, rows 56)
+//   tile  128 x 128, one workgroup per CU 1.17 us, two 1.5
+//         (4096 x 14336: 135 us at 1024 rows, mid 204; 171 at 2048, big 189)
+//   big   256 x 256, a round 1.65 us on up to half of the CUs, else 2.0
+//         (4096 x 4096 at 4096 rows: 70 us, tile 97; 49152 rows of 64 experts: 237, tile 298)
+// Grouped problems have about half a tile more per expert, and every kernel needs the time to
+// read the weights once (5 TB/s).  The large tiles are not built for fp32 Y (their operands would
+// not fit the registers) and address a tile's rows by 32-bit offsets.
+gptq_status launch_product(const MmArgs& a, hipStream_t stream) {
+  const bool grouped = a.off != nullptr;
+  if (grouped && (a.m / 16 + 1) * a.experts > INT32_MAX) return GPTQ_ERR_UNSUPPORTED;
+  const double used = grouped ? static_cast<double>(std::min<int64_t>(a.experts, a.m)) : 1.0;
+  const double weights = static_cast<double>(a.n) * a.k;
+  auto tiles = [&](int tm, int tn) {
+    const double rows = grouped ? static_cast<double>(a.m) / tm + 0.5 * used : static_cast<double>((a.m + tm - 1) / tm);
+    return rows * ((a.n + tn - 1) / tn);
+  };
+  auto rounds = [](double t, double slots, double half, double full) {   // time of t workgroups
+    const double r = static_cast<double>(static_cast<int64_t>(t / slots)), rest = t - r * slots;
+    return r * full + (rest <= 0.0 ? 0.0 : rest <= slots / 2 ? half : full);
+  };
+  const double read = 0.7 * used * weights / 5e6;
+  const double row_tiles = grouped ? static_cast<double>(a.m) / 16 + 0.5 * used : 1.0;
+  const double t_rows = a.m > 64 && !grouped ? 1e30
+                        : 2.5 + std::max(read, (row_tiles * weights + static_cast<double>(a.m) * a.k * a.n / 16) / 7e6);
+  const double t_mid = a.kb > MID_KB ? 1e30
+                       : 3 + std::max(read, a.kb * (a.kb <= 60 ? rounds(tiles(64, 64), 512, 0.46, 0.57)
+                                                               : rounds(tiles(64, 64), 256, 0.46, 0.46)));
+  const double t_tile = 3 + std::max(read, a.kb * rounds(tiles(128, 128), 512, 1.17, 1.5));
+  const int64_t span = a.rows == nullptr ? 256 * a.ldx : a.x_rows * a.ldx;
+  const bool narrow = span <= INT32_MAX && 256 * static_cast<int64_t>(a.k) <= INT32_MAX;
+  const double t_big = a.y_dtype == GPTQ_F32 || !narrow || a.x_rows == 0
+                           ? 1e30
+                           : 6 + std::max(read, a.kb * rounds(tiles(256, 256), 256, 1.65, 2.0));
+  const double best = std::min(std::min(t_rows, t_mid), std::min(t_tile, t_big));
+  if (best == t_big) return launch_big(a, stream);
+  if (best == t_tile) return launch_tile<128, 128, 2, 2>(a, stream);
+  if (best == t_mid) return launch_mid(a, stream);
+  // 16-row tiles for grouped rows; 8 waves along the inputs while each has 3 blocks or more
+  // (4096 x 4096 at 1 row: 5.5 us with 8, 6.5 with 4; 64 experts of 1408 x 2048, 96 rows: 35 and 24)
+  if (!grouped && a.m > 32) return launch_rows<4, 8>(a, stream);
+  if (!grouped && a.m > 16) return launch_rows<2, 8>(a, stream);
+  return a.kb >= 24 ? launch_rows<1, 8>(a, stream) : launch_rows<1, 4>(a, stream);
 }
 
 struct Fp8Layout {
@@ -891,11 +1083,7 @@ gptq_status fp8_matmul_enqueue(const Fp8Problem& p, hipStream_t stream) {
     }
     a.X = ws; a.ldx = p.k; a.xs = ws + l.s; a.xsr = 1; a.xsb = p.x_rows;
   }
-  const int64_t per = a.off == nullptr ? a.m : a.m / a.experts;   // rows that share weights
-  if (per <= 16) return launch_rows<1, 8>(a, stream);
-  if (per <= 64) return launch_rows<4, 8>(a, stream);
-  if (getenv("T256") && a.y_dtype != GPTQ_F32) return launch_big(a, stream);
-  return launch_tile<128, 128, 2, 2>(a, stream);
+  return launch_product(a, stream);
 }
 
 }  // namespace gptq
