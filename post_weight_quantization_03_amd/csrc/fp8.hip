@@ -444,6 +444,18 @@ __device__ __forceinline__ void copy16(const void* src, unsigned base) {
       : "v"(src), "s"(base)
       : "memory");
 }
+// 64 4-byte pieces, lane l's to base + 4 l.
+__device__ __forceinline__ void copy4(const void* src, unsigned base) {
+  unsigned saved;
+  asm volatile(
+      "s_mov_b32 %0, m0\n\t"
+      "s_mov_b32 m0, %2\n\t"
+      "global_load_lds_dword %1, off\n\t"
+      "s_mov_b32 m0, %0"
+      : "=&s"(saved)
+      : "v"(src), "s"(base)
+      : "memory");
+}
 // The same from a scalar base and 32-bit offsets.
 __device__ __forceinline__ void copy16_at(const void* from, uint32_t off, unsigned base) {
   unsigned saved;
@@ -574,19 +586,21 @@ gptq_status launch_tile(MmArgs a, hipStream_t stream) {
 // The same product for large problems: 256 x 256 tiles, 8 waves of 128 x 64 (8 x 4 blocks of
 // 16 x 16), one workgroup per CU.  Two buffers of 64 KB; operands go global -> LDS with a
 // scalar base that moves by 128 bytes a stage and one 32-bit offset per lane and copy, so that
-// a stage's copies cost little vector arithmetic.  Before a wave's last two rows of blocks it
-// has read all it needs of the stage: there the workgroup waits for the next stage's copies,
-// starts those of the one after it, and the last 8 products cover the first reads of the next
-// stage.  The fold of a row of blocks (y += t * scale) runs under the next row's products.
-template <int KIND>
-__global__ __launch_bounds__(512) void fp8_big_kernel(MmArgs a) {
-  constexpr int TM = 256, TN = 256, WN = 4, NW = 8, FM = 8, FN = 4;
+// a stage's copies cost little vector arithmetic.  Before a wave's last three rows of blocks it
+// has read all it needs of the stage: there the workgroup waits for the next stage's copies, and
+// the last 12 products cover the first reads of the next stage and half of the copies of the one
+// after it; the other half goes out with the next stage's first products.  The fold of a
+// product (y += t * scale) runs under the third product after it.
+constexpr int BIG_KB = 2048;   // most blocks of inputs (LDS for the outputs' scales)
+template <int KIND, int NW>
+__global__ __launch_bounds__(NW * 64) void fp8_big_kernel(MmArgs a) {
+  constexpr int TM = 256, TN = 256, WN = NW / 2, FM = 8, FN = TN / WN / 16;
   constexpr int STAGE = (TM + TN) * FB;
   constexpr int LD = (TM + TN) / 8 / NW;   // copies per wave and stage: 4 of X, 4 of W
   constexpr bool E8 = KIND == kMmaE8M0;
   __shared__ __attribute__((aligned(128))) uint8_t lds[2 * STAGE];
-  __shared__ float scs[2][2][TM];   // the rows' scales; with fp32 scales times those of each 128 outputs
-  __shared__ float scw[2][2];       // E8M0: the outputs' scales
+  __shared__ float scs[2][2][TM];   // the rows' scales (fp32: twice, so that every wave copies 64)
+  extern __shared__ float scw[];    // the outputs' scales: [2][kb]
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   int64_t mt;
   int nt;
@@ -609,22 +623,33 @@ __global__ __launch_bounds__(512) void fp8_big_kernel(MmArgs a) {
       off[i] = static_cast<uint32_t>(min(r - TM, a.n - 1 - n0)) * static_cast<uint32_t>(a.k) + 16 * c;
     }
   }
-  const int srow_r = tid & (TM - 1), half = tid >> 8;
+  constexpr int SB = E8 ? 1 : 4;   // bytes of a scale
+  const int srow_r = tid & (TM - 1);
   const int64_t srow = max(source_row(a, t.p0 + min(srow_r, t.count - 1)), static_cast<int64_t>(0));
-  const int sob = min(n0 / FB + half, a.nb - 1);
-  float sx_next = 0.0f, sw_next = 0.0f;
+  const uint8_t* xsp = static_cast<const uint8_t*>(a.xs) + srow * a.xsr * SB;   // moves by a block of inputs a stage
+  const int64_t xstep = a.xsb * SB;
+  float sx_next = 0.0f;
+  for (int b = tid; b < 2 * a.kb; b += NW * 64)
+    scw[b] = load_ws<KIND>(a, t.e, min(n0 / FB + (b >= a.kb), a.nb - 1), b >= a.kb ? b - a.kb : b);
   const unsigned lds0 = static_cast<unsigned>(reinterpret_cast<uintptr_t>(
       (__attribute__((address_space(3))) uint8_t*)lds));
   const bool cut = 16 * c >= a.k - (a.kb - 1) * FB;   // this lane's piece of the last stage lies past K
-  auto issue = [&](int s) {
-    sx_next = load_xs<KIND>(a, srow, s);
-    sw_next = load_ws<KIND>(a, t.e, sob, s);
+  const unsigned scs0 = static_cast<unsigned>(reinterpret_cast<uintptr_t>(
+      (__attribute__((address_space(3))) float*)&scs[0][0][0]));
+  // the scales of the stage after the last call's.  fp32 ones go to LDS like the operands: loads
+  // to registers between those copies cost 30 us of 400 at 8192 x 4096 x 14336
+  auto issue_scales = [&](int s) {
+    if constexpr (E8) sx_next = __int_as_float(*xsp);
+    else copy4(xsp, scs0 + ((s & 1) * 2 * TM + wave * 64) * 4);
+    xsp += xstep;
+  };
+  auto issue_copies = [&](int s, int from, int to) {
     const uint8_t* xb = xbase + static_cast<int64_t>(s) * FB;
     const uint8_t* wb = wbase + static_cast<int64_t>(s) * FB;
     const unsigned dst = lds0 + (s & 1) * STAGE + wave * 1024;
     const uint32_t back = s == a.kb - 1 && cut ? 16 * c : 0;   // the row's first piece instead; zeroed below
 #pragma unroll
-    for (int i = 0; i < LD; ++i) copy16_at(i < LD / 2 ? xb : wb, off[i] - back, dst + NW * i * 1024);
+    for (int i = from; i < to; ++i) copy16_at(i < LD / 2 ? xb : wb, off[i] - back, dst + NW * i * 1024);
   };
   // the copies and scales of stage s have landed; the next barrier makes them visible
   auto land = [&](int s, bool last) {
@@ -634,8 +659,7 @@ __global__ __launch_bounds__(512) void fp8_big_kernel(MmArgs a) {
       for (int i = 0; i < LD; ++i)
         *reinterpret_cast<uint4*>(lds + (s & 1) * STAGE + (wave + NW * i) * 1024 + 16 * lane) = make_uint4(0, 0, 0, 0);
     }
-    scs[s & 1][half][srow_r] = E8 ? sx_next : sx_next * sw_next;
-    if (E8 && srow_r == 0) scw[s & 1][half] = sw_next;
+    if constexpr (E8) scs[s & 1][0][srow_r] = sx_next;
   };
   auto barrier = [&] {
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
@@ -650,114 +674,135 @@ __global__ __launch_bounds__(512) void fp8_big_kernel(MmArgs a) {
   // the lanes that one LDS access serves together then meet no bank twice
   const int swz = (j >> 1) & 7;
   const int at0 = j * FB + 16 * (q ^ swz), at1 = j * FB + 16 * ((q + 4) ^ swz);
-  auto frag = [&](int s, int r) {
-    const uint8_t* p = lds + (s & 1) * STAGE + r * FB;
-    const i32x4 lo = *reinterpret_cast<const i32x4*>(p + at0);
-    const i32x4 hi = *reinterpret_cast<const i32x4*>(p + at1);
-    return Operand<KIND>(i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]});
+  auto half_frag = [&](int s, int r, int half, Operand<KIND>& o) {
+    const i32x4 v = *reinterpret_cast<const i32x4*>(lds + (s & 1) * STAGE + r * FB + (half ? at1 : at0));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o.v[4 * half + i] = v[i];
   };
-  auto scale_of = [&](int s, int i) { return scs[s & 1][E8 ? 0 : wn / 2][xr + 16 * i + j]; };
+  auto scale_of = [&](int s, int i) { return scs[s & 1][E8 ? 0 : wn & 1][xr + 16 * i + j]; };
+  const float* const swp = scw + wn * FN / 8 * a.kb;   // this wave's 128 outputs
 
   const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
-  f32x4 y[FM][FN], td[2][FN];
+  f32x4 y[FM][FN], td[4];   // td: the last products, not folded yet
+  float ts[4];              // and their scales
 #pragma unroll
-  for (int h = 0; h < FN; ++h) {
+  for (int i = 0; i < FM; ++i)
 #pragma unroll
-    for (int i = 0; i < FM; ++i) y[i][h] = zero;
-    td[0][h] = td[1][h] = zero;
+    for (int h = 0; h < FN; ++h) y[i][h] = zero;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    td[i] = zero;
+    ts[i] = 0.0f;
   }
-  Operand<KIND> xf[3], wf[FN];
-  float sc[3], sd = 0.0f, sw = 0.0f;   // sd: the scale of the products that wait in td
-  // products of row of blocks i, output block h; with E8M0 scales straight into y
-  auto dot = [&](int i, int h) {
-    if constexpr (E8) block_mma<KIND>(wf[h], xf[i % 3], sc[i % 3], sw, y[i][h]);
-    else td[i & 1][h] = block_dot<KIND>(wf[h], xf[i % 3]);
-  };
-  // the empty constraint keeps the multiply-adds here (the compiler moves them all behind the
-  // last product and spills the products)
-  auto fold = [&](int i, int h, float s) {
-    if constexpr (!E8) {
+  Operand<KIND> xf[4], wf[FN];   // row of blocks i in xf[i % 4]
+  float sc[4], sw = 0.0f;
+  // Product p of a stage, p = 0 .. 31: rows of blocks 0 .. 4 one after another, then rows 5, 6
+  // and 7 together, output block by output block.
+  constexpr int LAST = 3, SPLIT = (FM - LAST) * FN;   // rows taken together, products before them
+  constexpr int EARLY = LAST * FN / 2;                // copies issued with them, one after every second product
+  auto row_at = [](int p) constexpr { return p < SPLIT ? p / FN : FM - LAST + (p - SPLIT) % LAST; };
+  auto col_at = [](int p) constexpr { return p < SPLIT ? p % FN : (p - SPLIT) / LAST; };
+  // issue product p and fold the one three before it; with E8M0 scales it goes straight into
+  // y.  The empty constraint keeps the multiply-adds here and the barrier keeps everything in the
+  // order written (left to itself the compiler puts all folds behind the last product, or all
+  // reads before the first, and spills).
+  auto product = [&](auto P) {
+    constexpr int p = P, i = row_at(p), h = col_at(p);
+    if constexpr (E8) {
+      block_mma<KIND>(wf[h], xf[i % 4], sc[i % 4], sw, y[i][h]);
+    } else {
+      constexpr int o = (p + FM * FN - 3) % (FM * FN), oi = row_at(o), oh = col_at(o);
+      td[p % 4] = block_dot<KIND>(wf[h], xf[i % 4]);
+      if constexpr (h == 0) sc[i % 4] *= sw;
+      ts[p % 4] = sc[i % 4];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) y[i][h][r] = fmaf(td[i & 1][h][r], s, y[i][h][r]);
-      asm volatile("" : "+v"(y[i][h]));
-    }
-  };
-
-  // the order of one row of blocks: reads for two rows ahead, then each product under the last
-  // row's fold; left to itself the compiler hoists reads until registers spill
-  auto interleave = [] {
-    __builtin_amdgcn_sched_group_barrier(0x100, 3, 0);   // LDS reads
-#pragma unroll
-    for (int h = 0; h < FN; ++h) {
-      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);   // a product
-      __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);   // four multiply-adds
+      for (int r = 0; r < 4; ++r) y[oi][oh][r] = fmaf(td[o % 4][r], ts[o % 4], y[oi][oh][r]);
+      asm volatile("" : "+v"(y[oi][oh]));
     }
     __builtin_amdgcn_sched_barrier(0);
   };
-
   // one stage; kMore: another follows, kIssue: and one after that (constants, so that the
-  // loop's body has no branch for the compiler to move products across)
+  // loop's body has no branch)
   auto stage = [&](int s, auto kMore, auto kIssue) {
-#pragma unroll
-    for (int i = 0; i < FM - 2; ++i) {
-      xf[(i + 2) % 3] = frag(s, xr + 16 * (i + 2));
-      sc[(i + 2) % 3] = scale_of(s, i + 2);
-#pragma unroll
-      for (int h = 0; h < FN; ++h) {
-        dot(i, h);
-        fold((i + FM - 1) % FM, h, sd);
-      }
-      sd = sc[i % 3];
-      interleave();
-    }
+    // rows 0 .. 4; row i + 3 is read meanwhile, one access after each product
+    static_for(std::make_integer_sequence<int, SPLIT>{}, [&](auto P) {
+      constexpr int p = P, i = p / FN, h = p % FN;
+      product(P);
+      if constexpr (h == 0) half_frag(s, xr + 16 * (i + 3), 0, xf[(i + 3) % 4]);
+      if constexpr (h == 1) half_frag(s, xr + 16 * (i + 3), 1, xf[(i + 3) % 4]);
+      if constexpr (h == 2) sc[(i + 3) % 4] = scale_of(s, i + 3);
+      // the rest of the next stage's copies
+      if constexpr (kMore && p % 2 == 1 && EARLY + p / 2 < LD) issue_copies(s + 1, EARLY + p / 2, EARLY + p / 2 + 1);
+      __builtin_amdgcn_sched_barrier(0);
+    });
+    float sw1 = 0.0f;
     if constexpr (kMore) {
       land(s + 1, !kIssue);
       barrier();
-      if constexpr (kIssue) issue(s + 2);
-    }
-    // the last two rows of blocks (operands 0 and 1), output block by output block: a weight
-    // operand makes room for the next stage's after its second product
-    float sw1 = 0.0f;
-    if constexpr (E8 && kMore) sw1 = scw[(s + 1) & 1][wn / 2];
-#pragma unroll
-    for (int h = 0; h < FN; ++h) {
-      dot(FM - 2, h);
-      fold(FM - 3, h, sd);
-      dot(FM - 1, h);
-      if constexpr (kMore) wf[h] = frag(s + 1, wr + 16 * h);
-      if (h > 0) fold(FM - 2, h - 1, sc[0]);
+      if constexpr (kIssue) issue_scales(s + 2);
+      // operand 0 is free: the next stage's first
+      half_frag(s + 1, xr, 0, xf[0]);
+      half_frag(s + 1, xr, 1, xf[0]);
+      sc[0] = scale_of(s + 1, 0);
+      sw1 = swp[s + 1];
       __builtin_amdgcn_sched_barrier(0);
     }
-    fold(FM - 2, FN - 1, sc[0]);
-    sd = sc[1];
+    // rows 5, 6 and 7: a weight operand makes room for the next stage's after its third product
+    static_for(std::make_integer_sequence<int, LAST * FN>{}, [&](auto Q) {
+      constexpr int n = Q, h = n / LAST;
+      product(std::integral_constant<int, SPLIT + n>{});
+      if constexpr (kMore && n % LAST == LAST - 1) {
+        half_frag(s + 1, wr + 16 * h, 0, wf[h]);
+        half_frag(s + 1, wr + 16 * h, 1, wf[h]);
+      }
+      // a copy takes the CU's address unit 16 cycles: issued together, the waves' copies hold up
+      // their next products
+      if constexpr (kIssue && n % 2 == 1) issue_copies(s + 2, n / 2, n / 2 + 1);
+      __builtin_amdgcn_sched_barrier(0);
+    });
     if constexpr (kMore) {
-      xf[0] = frag(s + 1, xr);
-      sc[0] = scale_of(s + 1, 0);
-      xf[1] = frag(s + 1, xr + 16);
-      sc[1] = scale_of(s + 1, 1);
+#pragma unroll
+      for (int i = 1; i < 3; ++i) {
+        half_frag(s + 1, xr + 16 * i, 0, xf[i]);
+        half_frag(s + 1, xr + 16 * i, 1, xf[i]);
+        sc[i] = scale_of(s + 1, i);
+      }
       sw = sw1;
+      __builtin_amdgcn_sched_barrier(0);
     }
-    __builtin_amdgcn_sched_barrier(0);
   };
 
-  issue(0);
+  issue_scales(0);
+  issue_copies(0, 0, LD);
   land(0, a.kb == 1);
   barrier();
-  if (a.kb > 1) issue(1);
-  xf[0] = frag(0, xr);
-  sc[0] = scale_of(0, 0);
+  if (a.kb > 1) {
+    issue_scales(1);
+    issue_copies(1, 0, EARLY);
+  }
 #pragma unroll
-  for (int h = 0; h < FN; ++h) wf[h] = frag(0, wr + 16 * h);
-  xf[1] = frag(0, xr + 16);
-  sc[1] = scale_of(0, 1);
-  if constexpr (E8) sw = scw[0][wn / 2];
+  for (int i = 0; i < 3; ++i) {
+    half_frag(0, xr + 16 * i, 0, xf[i]);
+    half_frag(0, xr + 16 * i, 1, xf[i]);
+    sc[i] = scale_of(0, i);
+  }
+#pragma unroll
+  for (int h = 0; h < FN; ++h) {
+    half_frag(0, wr + 16 * h, 0, wf[h]);
+    half_frag(0, wr + 16 * h, 1, wf[h]);
+  }
+  sw = swp[0];
   const std::true_type yes;
   const std::false_type no;
   for (int s = 0; s + 2 < a.kb; ++s) stage(s, yes, yes);
   if (a.kb > 1) stage(a.kb - 2, yes, no);
   stage(a.kb - 1, no, no);
+  if constexpr (!E8)
+    static_for(std::make_integer_sequence<int, 3>{}, [&](auto P) {
+      constexpr int p = FM * FN - 3 + P, i = row_at(p), h = col_at(p);
 #pragma unroll
-  for (int h = 0; h < FN; ++h) fold(FM - 1, h, sd);
+      for (int r = 0; r < 4; ++r) y[i][h][r] = fmaf(td[p % 4][r], ts[p % 4], y[i][h][r]);
+    });
 #pragma unroll
   for (int i = 0; i < FM; ++i) {
     const int r = xr + 16 * i + j;
@@ -785,9 +830,10 @@ gptq_status launch_big(MmArgs a, hipStream_t stream) {
                        (a.n + 255) / 256);
   const int64_t grid = order_grid(a.order);
   if (grid > (1 << 22)) return GPTQ_ERR_UNSUPPORTED;
-  const dim3 g(static_cast<unsigned>(grid)), b(512);
-  if (a.e8) GPTQ_LAUNCH((fp8_big_kernel<kMmaE8M0>), g, b, 0, stream, a);
-  else GPTQ_LAUNCH((fp8_big_kernel<kMmaF32Scale>), g, b, 0, stream, a);
+  const dim3 g(static_cast<unsigned>(grid));
+  const size_t lds = 2 * static_cast<size_t>(a.kb) * sizeof(float);
+  if (a.e8) GPTQ_LAUNCH((fp8_big_kernel<kMmaE8M0, 4>), g, dim3(256), lds, stream, a);
+  else GPTQ_LAUNCH((fp8_big_kernel<kMmaF32Scale, 8>), g, dim3(512), lds, stream, a);
   return GPTQ_OK;
 }
 
@@ -996,9 +1042,10 @@ gptq_status launch_rows(MmArgs a, hipStream_t stream) {
 //   mid   64 x 64, one workgroup per CU 0.46 us, two 0.57 (both fit up to 60 blocks of inputs)
 //         (4096 x 14336: 52 us at 64 rows, 55 at 256, 103 at 512; 14336 x 4096 at 64: 19, rows 56)
 //   tile  128 x 128, one workgroup per CU 1.17 us, two 1.5
-//         (4096 x 14336: 135 us at 1024 rows, mid 204; 171 at 2048, big 189)
-//   big   256 x 256, a round 1.65 us on up to half of the CUs, else 2.0
-//         (4096 x 4096 at 4096 rows: 70 us, tile 97; 49152 rows of 64 experts: 237, tile 298)
+//         (4096 x 4096: 42 us at 1024 rows, mid 44, big 48)
+//   big   256 x 256, a round 1.4 us on up to half of the CUs, else 1.85
+//         (4096 x 4096: 51 us at 2048 rows, tile 54; 67 at 4096, tile 104; 49152 rows of 64
+//         experts: 228, tile 299)
 // Grouped problems have about half a tile more per expert, and every kernel needs the time to
 // read the weights once (5 TB/s).  The large tiles are not built for fp32 Y (their operands would
 // not fit the registers) and address a tile's rows by 32-bit offsets.
@@ -1025,13 +1072,13 @@ gptq_status launch_product(const MmArgs& a, hipStream_t stream) {
   const double t_tile = 3 + std::max(read, a.kb * rounds(tiles(128, 128), 512, 1.17, 1.5));
   const int64_t span = a.rows == nullptr ? 256 * a.ldx : a.x_rows * a.ldx;
   const bool narrow = span <= INT32_MAX && 256 * static_cast<int64_t>(a.k) <= INT32_MAX;
-  const double t_big = a.y_dtype == GPTQ_F32 || !narrow || a.x_rows == 0
+  const double t_big = a.y_dtype == GPTQ_F32 || !narrow || a.x_rows == 0 || a.kb > BIG_KB
                            ? 1e30
-                           : 6 + std::max(read, a.kb * rounds(tiles(256, 256), 256, 1.65, 2.0));
+                           : 6 + std::max(read, a.kb * rounds(tiles(256, 256), 256, 1.4, 1.85));
   const double best = std::min(std::min(t_rows, t_mid), std::min(t_tile, t_big));
-  if (best == t_big) return launch_big(a, stream);
+  if (best == t_mid) return launch_mid(a, stream);   // the smallest tile of those that wait for the weights
   if (best == t_tile) return launch_tile<128, 128, 2, 2>(a, stream);
-  if (best == t_mid) return launch_mid(a, stream);
+  if (best == t_big) return launch_big(a, stream);
   // 16-row tiles for grouped rows; 8 waves along the inputs while each has 3 blocks or more
   // (4096 x 4096 at 1 row: 5.5 us with 8, 6.5 with 4; 64 experts of 1408 x 2048, 96 rows: 35 and 24)
   if (!grouped && a.m > 32) return launch_rows<4, 8>(a, stream);
@@ -1074,7 +1121,7 @@ gptq_status fp8_matmul_enqueue(const Fp8Problem& p, hipStream_t stream) {
     a.X = static_cast<const uint8_t*>(p.X); a.ldx = p.ldx; a.xs = p.xs; a.xsr = p.xsr; a.xsb = p.xsb;
   } else {
     const Fp8Layout l = fp8_layout(p.x_rows, p.k);
-    if (p.workspace == nullptr || p.workspace_bytes < l.total) return GPTQ_ERR_WORKSPACE;
+    if (p.x_rows > 0 && (p.workspace == nullptr || p.workspace_bytes < l.total)) return GPTQ_ERR_WORKSPACE;
     uint8_t* ws = static_cast<uint8_t*>(p.workspace);
     if (p.x_rows > 0) {
       const gptq_status st = fp8_quantize_enqueue(1, p.x_rows, p.k, p.x_dtype, p.X, p.ldx, 0, 1, p.e8, ws, ws + l.s, 1,

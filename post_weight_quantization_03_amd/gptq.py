@@ -413,13 +413,13 @@ def _run(what: str, stream, tensors, *args) -> None:
     The first of ``tensors`` is not None.  Small calls last a few microseconds, so this path
     creates no Stream object (2.8 us of a 12.9 us call)."""
     device = tensors[0].get_device()
+    if device < 0:
+        raise ValueError("tensors must be on a GPU")
     for t in tensors:
         if t is not None and t.get_device() != device:
             raise ValueError("tensors must be on one GPU")
-    if device < 0:
-        raise ValueError("tensors must be on a GPU")
-    fn = getattr(lib(), what)
-    if stream is None and device == torch.cuda.current_device():
+    fn = getattr(_lib or lib(), what)
+    if stream is None and device == torch._C._cuda_getDevice():
         status = fn(*args, torch._C._cuda_getCurrentRawStream(device))
     else:
         if stream is not None and stream.device.index != device:
@@ -441,11 +441,27 @@ def _workspace_bytes(which: int, batch: int, d_out: int, d_in: int, hint: int) -
     return workspace_size(which, batch, d_out, d_in, hint)
 
 
-def _scratch(which, batch, d_out, d_in, hint, device, workspace) -> torch.Tensor:
+def _scratch(which, batch, d_out, d_in, hint, device, workspace) -> torch.Tensor | None:
+    """The caller's workspace if it is large enough, else a new one; None where the call needs none."""
     nbytes = _workspace_bytes(which, batch, d_out, d_in, hint)
+    if nbytes <= 256:   # the least size: nothing is kept in it
+        return None
     if workspace is not None and workspace.numel() * workspace.element_size() >= nbytes:
         return workspace
-    return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
+    return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _bytes(t):
+    return 0 if t is None else t.numel() * t.element_size()
+
+
+@functools.lru_cache(maxsize=256)
+def _route_params(*values) -> _RouteParams:
+    return _RouteParams(*values)
 
 
 def _out(out, shape, dtype, device, name="out"):
@@ -544,8 +560,8 @@ def fp8_matmul(X: torch.Tensor, qweight: torch.Tensor, w_scales: torch.Tensor, x
     ws = None if X.dtype == torch.float8_e4m3fn else _scratch(WS_FP8_MATMUL, 1, d_out, d_in, m, X.device, workspace)
     _run("gptq_fp8_matmul", stream, (X, qweight, w_scales, x_scales, Y, ws), m, d_out, d_in, _DT.get(X.dtype, E4M3),
          X.data_ptr(), _row_stride(X), sdt, *_fp8_scales(x_scales), qweight.data_ptr(), w_scales.data_ptr(),
-         _DT[out_dtype], Y.data_ptr(), _row_stride(Y), None if ws is None else ws.data_ptr(),
-         0 if ws is None else ws.numel() * ws.element_size())
+         _DT[out_dtype], Y.data_ptr(), _row_stride(Y), _ptr(ws),
+         _bytes(ws))
     return Y
 
 
@@ -574,8 +590,8 @@ def fp8_matmul_grouped(X: torch.Tensor, qweight: torch.Tensor, w_scales: torch.T
     _run("gptq_fp8_matmul_grouped", stream, (X, qweight, w_scales, token_offsets, row_index, x_scales, Y, ws), experts,
          x_rows, n_rows, d_out, d_in, _DT.get(X.dtype, E4M3), X.data_ptr(), _row_stride(X), sdt,
          *_fp8_scales(x_scales), qweight.data_ptr(), w_scales.data_ptr(), token_offsets.data_ptr(),
-         None if row_index is None else row_index.data_ptr(), _DT[out_dtype], Y.data_ptr(), _row_stride(Y),
-         None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel() * ws.element_size())
+         _ptr(row_index), _DT[out_dtype], Y.data_ptr(), _row_stride(Y),
+         _ptr(ws), _bytes(ws))
     return Y
 
 
@@ -601,12 +617,12 @@ def moe_route(logits: torch.Tensor, top_k: int, bias: torch.Tensor | None = None
         raise ValueError("bias must be contiguous [experts]")
     if scoring not in _SCORING or group_score not in _GROUP_SCORE:
         raise ValueError("scoring must be 'softmax' or 'sigmoid', group_score 'max' or 'top2'")
-    p = _RouteParams(_SCORING[scoring], n_groups, n_groups if top_groups is None else top_groups,
-                     _GROUP_SCORE[group_score], top_k, int(renormalize), scale)
-    ids = torch.empty(tokens, max(top_k, 0), dtype=torch.int32, device=logits.device)
-    weights = torch.empty(tokens, max(top_k, 0), dtype=torch.float32, device=logits.device)
+    p = _route_params(_SCORING[scoring], n_groups, n_groups if top_groups is None else top_groups,
+                      _GROUP_SCORE[group_score], top_k, int(renormalize), scale)
+    ids = torch.empty((tokens, max(top_k, 0)), dtype=torch.int32, device=logits.device)
+    weights = torch.empty_like(ids, dtype=torch.float32)
     _run("gptq_moe_route", stream, (logits, bias, ids, weights), tokens, experts, _DT[logits.dtype], logits.data_ptr(),
-         _row_stride(logits), None if bias is None else bias.data_ptr(), ctypes.byref(p), ids.data_ptr(),
+         _row_stride(logits), _ptr(bias), ctypes.byref(p), ids.data_ptr(),
          weights.data_ptr())
     return ids, weights
 
@@ -627,7 +643,7 @@ def moe_group_tokens(ids: torch.Tensor, n_experts: int, workspace: torch.Tensor 
     place = torch.empty_like(ids)
     ws = _scratch(WS_MOE_GROUP, 1, n_experts, k, tokens, ids.device, workspace)
     _run("gptq_moe_group_tokens", stream, (ids, offsets, rows, place, ws), tokens, k, n_experts, ids.data_ptr(),
-         offsets.data_ptr(), rows.data_ptr(), place.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size())
+         offsets.data_ptr(), rows.data_ptr(), place.data_ptr(), _ptr(ws), _bytes(ws))
     return offsets, rows, place
 
 

@@ -377,3 +377,108 @@ def test_captured_and_replayed(m):
         want = call()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want)), i
+
+
+def random_operands(seed, rows, cols, block_rows, e8m0, batch=()):
+    """Codes and scales made on the GPU: any code but NaN, scales within a factor of 16."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    q = torch.randint(0, 253, (*batch, rows, cols), generator=g, device="cuda", dtype=torch.uint8)
+    q = torch.where(q >= 127, q + 1, q).contiguous().view(torch.float8_e4m3fn)
+    shape = (*batch, -(-rows // block_rows), -(-cols // 128))
+    s = torch.exp2(4 * torch.rand(shape, generator=g, device="cuda") - 10)
+    return q, (torch.exp2(torch.round(torch.log2(s))).to(torch.float8_e8m0fnu) if e8m0 else s)
+
+
+def wide(q, s, block_rows):
+    """Operands in 64 bits."""
+    s = s.double().repeat_interleave(block_rows, -2)[..., :q.shape[-2], :]
+    return q.double() * s.repeat_interleave(128, -1)[..., :q.shape[-1]]
+
+
+def check_large(Y, x, w, k, out):
+    ref, B = x @ w.t(), x.abs() @ w.abs().t()
+    check_y(Y, ref.cpu().numpy(), B.cpu().numpy(), k, out)
+
+
+@pytest.mark.parametrize("m,n,k,e8m0,out", [
+    (4090, 4095, 1040, False, "bf16"), (4090, 4095, 1040, True, "f16"),      # ragged tiles, 16 inputs in the last block
+    (3900, 4000, 400, True, "bf16"), (3900, 4000, 400, False, "f16"),
+    (8192, 8192, 256, False, "bf16"), (8192, 8192, 128, True, "bf16"), (8192, 8100, 112, False, "bf16"),
+    (2050, 2050, 656, False, "bf16"), (2050, 2050, 656, True, "bf16"), (2050, 2050, 656, False, "f32"),
+    (4096, 4096, 272, True, "f32"), (1027, 4096, 2064, False, "bf16"), (513, 2304, 1056, True, "f32")])
+def test_large_products(m, n, k, e8m0, out):
+    # sizes at which the larger tiles are taken
+    q, s = random_operands(m + k, m, k, 1, e8m0)
+    w, ws = random_operands(n, n, k, 128, e8m0)
+    Y = lib().fp8_matmul(q, w, ws, s, out_dtype=DT[out])
+    check_large(Y, wide(q, s, 1), wide(w, ws, 128), k, out)
+    assert torch.equal(lib().fp8_matmul(q, w, ws, s, out_dtype=DT[out]), Y)
+
+
+@pytest.mark.parametrize("n,k,e8m0,out", [(2050, 912, False, "bf16"), (2050, 912, True, "f16"), (1030, 912, True, "bf16"),
+                                          (2050, 912, False, "f32"), (2100, 400, True, "bf16")])
+def test_large_grouped(n, k, e8m0, out):
+    counts = [4000, 0, 17, 2500, 2483] if k > 400 else [5000, 6999, 1]
+    tokens, lead, tail = 3000, 5, 300
+    rng = np.random.default_rng(n)
+    offsets = lead + np.concatenate([[0], np.cumsum(counts)])
+    rows = rng.integers(0, tokens, int(offsets[-1]) + tail).astype(np.int32)
+    rows[[7, 300, 4100]] = -1, tokens, -2 ** 31
+    q, s = random_operands(k, tokens, k, 1, e8m0)
+    w, ws = random_operands(n, n, k, 128, e8m0, (len(counts),))
+    Y = torch.full((len(rows), n), 2.5, dtype=DT[out], device="cuda")
+    lib().fp8_matmul_grouped(q, w, ws, torch.from_numpy(offsets).cuda(), torch.from_numpy(rows).cuda(), s,
+                             out_dtype=DT[out], out=Y)
+    assert bool((Y[:lead] == 2.5).all()) and bool((Y[int(offsets[-1]):] == 2.5).all())
+    assert bool((Y[[7, 300, 4100]] == 0).all())
+    x = wide(q, s, 1)
+    for e, c in enumerate(counts):
+        lo = int(offsets[e])
+        idx = torch.from_numpy(rows[lo:lo + c].astype(np.int64)).cuda()
+        ok = (idx >= 0) & (idx < tokens)
+        if c:
+            check_large(Y[lo:lo + c][ok], x[idx[ok]], wide(w[e], ws[e], 128), k, out)
+
+
+def test_large_product_nan_and_16bit_rows():
+    m, n, k = 4090, 4096, 1040
+    w, ws = random_operands(1, n, k, 128, False)
+    X = torch.randn(m, k, device="cuda").to(torch.bfloat16)
+    X[5, 200], X[4000, 1039] = float("nan"), float("inf")
+    q, s = lib().fp8_quantize(X)
+    Y = lib().fp8_matmul(X, w, ws)
+    assert torch.equal(torch.nan_to_num(Y, nan=1e4), torch.nan_to_num(lib().fp8_matmul(q, w, ws, s), nan=1e4))
+    assert torch.equal(Y.isnan().any(1).nonzero().view(-1).cpu(), torch.tensor([5, 4000]))
+    keep = torch.ones(m, dtype=torch.bool, device="cuda")
+    keep[[5, 4000]] = False
+    check_large(Y[keep], wide(q, s, 1)[keep], wide(w, ws, 128), k, "bf16")
+
+
+@pytest.mark.parametrize("e8m0", [False, True])
+def test_elements_past_32_bit_offsets(e8m0):
+    # 5 GB of activations: rows at the start, around 2 GB and 4 GB, and at the end
+    m, n, k = 300000, 256, 16384
+    w, ws = random_operands(1, n, k, 128, e8m0)
+    q = torch.full((m, k), 0x38, dtype=torch.uint8, device="cuda")
+    s = torch.ones(-(-k // 128), m, device="cuda").to(sdt(e8m0)).t()
+    at = torch.cat([torch.arange(3), torch.arange(131070, 131075), torch.arange(262142, 262146),
+                    torch.arange(m - 3, m)]).cuda()
+    some, _ = random_operands(2, len(at), k, 1, e8m0)
+    q[at] = some.view(torch.uint8)
+    Y = lib().fp8_matmul(q.view(torch.float8_e4m3fn), w, ws, s)
+    W = wide(w, ws, 128)
+    check_large(Y[at], some.double(), W, k, "bf16")
+    check_large(Y[m // 2:m // 2 + 1], torch.ones(1, k, dtype=torch.float64, device="cuda"), W, k, "bf16")
+
+
+def test_quantize_past_32_bit_offsets():
+    X = torch.zeros(70000, 32768, dtype=torch.bfloat16, device="cuda")
+    at = [0, 65535, 65536, 69999]
+    X[at] = torch.randn(4, 32768, device="cuda").to(torch.bfloat16)
+    q, s = lib().fp8_quantize(X)
+    for i, r in enumerate(at):
+        codes, scales = F.ref_quantize(X[r:r + 1].double().cpu().numpy(), 1, False)
+        assert np.array_equal(q[r:r + 1].double().cpu().numpy(), F.E4M3[codes])
+        assert np.array_equal(s[r:r + 1].double().cpu().numpy(), scales)
+    assert int(q.view(torch.uint8).ne(0).any(1).sum()) == 4
