@@ -69,6 +69,11 @@ __device__ __forceinline__ uint32_t top_bits(const float* x) {
   return t;
 }
 
+__device__ __forceinline__ uint32_t eight_lanes_max(uint32_t t) {
+  for (int d = 1; d < 8; d <<= 1) t = max(t, static_cast<uint32_t>(__shfl_xor(static_cast<int>(t), d)));
+  return t;
+}
+
 struct Scale {
   float s;        // the scale
   uint8_t code;   // its E8M0 code
@@ -140,20 +145,21 @@ __device__ __forceinline__ void store_scale(const QuantArgs& a, int64_t i, Scale
   else static_cast<float*>(a.S)[i] = sc.s;
 }
 
-// 1 x 128 blocks: 8 lanes per block, 16 values each; a workgroup takes one block of 32 rows, so
-// that scales stored block by block (ld_s_row = 1) leave it as one run.
-template <typename T, bool E8, bool kVec>
+// 1 x 128 blocks: 8 lanes per block, 16 values each; a workgroup takes QB blocks of 32 / QB rows.
+// Bound by memory.  32 blocks of one row are 8 KB in one piece (8192 x 4096 in bf16: 20.2 us, 5.0
+// TB/s, a copy's rate here; one block of 32 rows 25.9 us although its scales leave in one
+// piece); rows of fewer than 16 blocks take 4.
+template <typename T, bool E8, bool kVec, int QB>
 __global__ __launch_bounds__(256) void quant_rows_kernel(QuantArgs a) {
-  const int b = blockIdx.y;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * 32 + threadIdx.x / 8;
+  const int u = threadIdx.x / 8, b = blockIdx.y * QB + u % QB;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * (32 / QB) + u / QB;
   const int col = b * FB + (threadIdx.x & 7) * 16;
   const bool live = row < a.rows && col < a.cols;
   float x[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i) x[i] = 0.0f;
   if (live) load_row<T, 16, kVec>(static_cast<const T*>(a.X) + blockIdx.z * a.bsx + row * a.ldx + col, x);
-  uint32_t top = top_bits<16>(x);
-  for (int d = 1; d < 8; d <<= 1) top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), d)));
+  const uint32_t top = eight_lanes_max(top_bits<16>(x));
   if (!live) return;
   const Scale sc = block_scale<E8>(top);
   uint32_t w[4];
@@ -198,12 +204,14 @@ __global__ __launch_bounds__(256) void quant_tile_kernel(QuantArgs a) {
 
 template <typename T, bool E8, bool kVec>
 gptq_status launch_quant(const QuantArgs& a, int batch, int block_rows, hipStream_t stream) {
-  const int per = block_rows == 1 ? 32 : FB;
-  const int64_t gx = (a.rows + per - 1) / per, gy = (a.cols + FB - 1) / FB;
+  const int64_t kb = (a.cols + FB - 1) / FB;
+  const int qb = block_rows == FB ? 1 : kb >= 16 ? 32 : 4, qr = block_rows == FB ? FB : 32 / qb;
+  const int64_t gx = (a.rows + qr - 1) / qr, gy = (kb + qb - 1) / qb;
   if (gx > (1 << 24) - 1 || gy > 65535 || batch > 65535) return GPTQ_ERR_UNSUPPORTED;
-  const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(gy), batch);
-  if (block_rows == 1) GPTQ_LAUNCH((quant_rows_kernel<T, E8, kVec>), grid, dim3(256), 0, stream, a);
-  else GPTQ_LAUNCH((quant_tile_kernel<T, E8, kVec>), grid, dim3(256), 0, stream, a);
+  const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(gy), batch), block(256);
+  if (block_rows == FB) GPTQ_LAUNCH((quant_tile_kernel<T, E8, kVec>), grid, block, 0, stream, a);
+  else if (qb == 32) GPTQ_LAUNCH((quant_rows_kernel<T, E8, kVec, 32>), grid, block, 0, stream, a);
+  else GPTQ_LAUNCH((quant_rows_kernel<T, E8, kVec, 4>), grid, block, 0, stream, a);
   return GPTQ_OK;
 }
 
@@ -947,9 +955,14 @@ gptq_status launch_mid(MmArgs a, hipStream_t stream) {
 // inputs straight from memory to registers, U blocks in flight per wave; their sums meet in LDS
 // and are added in wave order.  (Several groups of 16 outputs per workgroup, with fewer waves
 // along the inputs, measured the same or slower.)
-template <int FM, int WK, int KIND>
+// T: 16-bit activations, rounded by every workgroup for itself while its first weights are
+// on the way, into LDS (void: 8-bit ones from memory).  That saves a launch: one row of 4096 x
+// 14336 takes 12.7 us after a 3.5 us launch that rounds it, and 14.2 us together.
+template <int FM, int WK, int KIND, typename T>
 __global__ __launch_bounds__(WK * 64) void fp8_rows_kernel(MmArgs a) {
   constexpr int U = FM <= 2 ? 4 : 2, TM = 16 * FM;
+  constexpr bool kRaw = !std::is_void_v<T>;
+  extern __shared__ __attribute__((aligned(16))) uint8_t raw[];   // kRaw: rows of codes, then [row][block] scales
   __shared__ __attribute__((aligned(16))) float part[WK][TM][16];
   const int tid = threadIdx.x, lane = tid & 63, wk = uniform(tid >> 6);
   const int64_t mt = blockIdx.x / a.tiles_n;
@@ -974,6 +987,7 @@ __global__ __launch_bounds__(WK * 64) void fp8_rows_kernel(MmArgs a) {
     wl[u] = *reinterpret_cast<const i32x4*>(lo ? w + FB * b : zeros);
     wh[u] = *reinterpret_cast<const i32x4*>(hi ? w + FB * b + 16 : zeros);
     sw[u] = load_ws<KIND>(a, t.e, n0 / FB, b);
+    if constexpr (!kRaw)
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
       xl[u][i] = *reinterpret_cast<const i32x4*>(lo && row[i] >= 0 ? x[i] + FB * b : zeros);
@@ -988,6 +1002,28 @@ __global__ __launch_bounds__(WK * 64) void fp8_rows_kernel(MmArgs a) {
 #pragma unroll
   for (int u = 0; u < U; ++u)
     if (wk + WK * u < a.kb) load(u, wk + WK * u);
+  const int pitch = a.kb * FB + 16;   // rows start 16 bytes apart mod 128
+  float* const rs = reinterpret_cast<float*>(raw + (a.off == nullptr ? min(static_cast<int64_t>(TM), a.m) : TM) * pitch);
+  if constexpr (kRaw) {
+    for (int g = tid / 8; g < min(TM, t.count) * a.kb; g += WK * 8) {
+      const int r = g / a.kb, b = g - r * a.kb, col = b * FB + (tid & 7) * 16;
+      const int64_t p = source_row(a, t.p0 + r);
+      float v[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = 0.0f;
+      if (p >= 0 && col < a.k)
+        load_row<T, 16, true>(reinterpret_cast<const T*>(a.X) + p * a.ldx + col, v);
+      const uint32_t top = eight_lanes_max(top_bits<16>(v));
+      const bool e8 = KIND == kMmaE8M0 || (KIND == kMmaExact && a.e8);
+      const Scale sc = e8 ? block_scale<true>(top) : block_scale<false>(top);
+      uint32_t o[4];
+      if (e8) round_values<true, 16>(v, sc, o);
+      else round_values<false, 16>(v, sc, o);
+      *reinterpret_cast<uint4*>(raw + r * pitch + col) = make_uint4(o[0], o[1], o[2], o[3]);
+      if ((tid & 7) == 0) rs[r * a.kb + b] = KIND == kMmaE8M0 ? __int_as_float(sc.code) : sc.s;
+    }
+    __syncthreads();
+  }
   for (int b0 = wk; b0 < a.kb; b0 += WK * U) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -996,9 +1032,15 @@ __global__ __launch_bounds__(WK * 64) void fp8_rows_kernel(MmArgs a) {
         const Operand<KIND> wf(i32x8{wl[u][0], wl[u][1], wl[u][2], wl[u][3], wh[u][0], wh[u][1], wh[u][2], wh[u][3]});
 #pragma unroll
         for (int i = 0; i < FM; ++i) {
-          const Operand<KIND> xf(i32x8{xl[u][i][0], xl[u][i][1], xl[u][i][2], xl[u][i][3], xh[u][i][0], xh[u][i][1],
-                                       xh[u][i][2], xh[u][i][3]});
-          block_mma<KIND>(wf, xf, sx[u][i], sw[u], y[i]);
+          if constexpr (kRaw) {
+            const int r = min(16 * i + j, t.count - 1);
+            const i32x8 v = *reinterpret_cast<const i32x8*>(raw + r * pitch + FB * b + 32 * q);
+            block_mma<KIND>(wf, Operand<KIND>(v), rs[r * a.kb + b], sw[u], y[i]);
+          } else {
+            const Operand<KIND> xf(i32x8{xl[u][i][0], xl[u][i][1], xl[u][i][2], xl[u][i][3], xh[u][i][0], xh[u][i][1],
+                                         xh[u][i][2], xh[u][i][3]});
+            block_mma<KIND>(wf, xf, sx[u][i], sw[u], y[i]);
+          }
         }
         if (b + WK * U < a.kb) load(u, b + WK * U);
       }
@@ -1021,7 +1063,13 @@ __global__ __launch_bounds__(WK * 64) void fp8_rows_kernel(MmArgs a) {
   }
 }
 
-template <int FM, int WK>
+// LDS of a tile's 16-bit rows, rounded: of the rows that it can hold.
+size_t raw_lds(const MmArgs& a, int tm) {
+  const size_t rows = a.off == nullptr ? std::min<int64_t>(tm, a.m) : tm;
+  return rows * (static_cast<size_t>(a.kb) * FB + 16 + a.kb * sizeof(float));
+}
+
+template <int FM, int WK, typename T>
 gptq_status launch_rows(MmArgs a, hipStream_t stream) {
   constexpr int TM = 16 * FM;
   a.tiles_n = (a.n + 15) / 16;
@@ -1029,9 +1077,10 @@ gptq_status launch_rows(MmArgs a, hipStream_t stream) {
   const int64_t grid = tiles * a.tiles_n;
   if (grid > (1 << 22)) return GPTQ_ERR_UNSUPPORTED;
   const dim3 g(static_cast<unsigned>(grid)), b(WK * 64);
-  if (a.y_dtype == GPTQ_F32) GPTQ_LAUNCH((fp8_rows_kernel<FM, WK, kMmaExact>), g, b, 0, stream, a);
-  else if (a.e8) GPTQ_LAUNCH((fp8_rows_kernel<FM, WK, kMmaE8M0>), g, b, 0, stream, a);
-  else GPTQ_LAUNCH((fp8_rows_kernel<FM, WK, kMmaF32Scale>), g, b, 0, stream, a);
+  const size_t lds = std::is_void_v<T> ? 0 : raw_lds(a, TM);
+  if (a.y_dtype == GPTQ_F32) GPTQ_LAUNCH((fp8_rows_kernel<FM, WK, kMmaExact, T>), g, b, lds, stream, a);
+  else if (a.e8) GPTQ_LAUNCH((fp8_rows_kernel<FM, WK, kMmaE8M0, T>), g, b, lds, stream, a);
+  else GPTQ_LAUNCH((fp8_rows_kernel<FM, WK, kMmaF32Scale, T>), g, b, lds, stream, a);
   return GPTQ_OK;
 }
 
@@ -1049,9 +1098,9 @@ gptq_status launch_rows(MmArgs a, hipStream_t stream) {
 // Grouped problems have about half a tile more per expert, and every kernel needs the time to
 // read the weights once (5 TB/s).  The large tiles are not built for fp32 Y (their operands would
 // not fit the registers) and address a tile's rows by 32-bit offsets.
-gptq_status launch_product(const MmArgs& a, hipStream_t stream) {
+enum Product { kRows, kMid, kTile, kBig };
+Product choose_product(const MmArgs& a) {
   const bool grouped = a.off != nullptr;
-  if (grouped && (a.m / 16 + 1) * a.experts > INT32_MAX) return GPTQ_ERR_UNSUPPORTED;
   const double used = grouped ? static_cast<double>(std::min<int64_t>(a.experts, a.m)) : 1.0;
   const double weights = static_cast<double>(a.n) * a.k;
   auto tiles = [&](int tm, int tn) {
@@ -1076,14 +1125,36 @@ gptq_status launch_product(const MmArgs& a, hipStream_t stream) {
                            ? 1e30
                            : 6 + std::max(read, a.kb * rounds(tiles(256, 256), 256, 1.4, 1.85));
   const double best = std::min(std::min(t_rows, t_mid), std::min(t_tile, t_big));
-  if (best == t_mid) return launch_mid(a, stream);   // the smallest tile of those that wait for the weights
-  if (best == t_tile) return launch_tile<128, 128, 2, 2>(a, stream);
-  if (best == t_big) return launch_big(a, stream);
+  if (best == t_mid) return kMid;   // the smallest tile of those that wait for the weights
+  return best == t_tile ? kTile : best == t_big ? kBig : kRows;
+}
+
+gptq_status launch_product(const MmArgs& a, Product kind, hipStream_t stream) {
+  if (kind == kMid) return launch_mid(a, stream);
+  if (kind == kTile) return launch_tile<128, 128, 2, 2>(a, stream);
+  if (kind == kBig) return launch_big(a, stream);
+  const bool grouped = a.off != nullptr;
   // 16-row tiles for grouped rows; 8 waves along the inputs while each has 3 blocks or more
   // (4096 x 4096 at 1 row: 5.5 us with 8, 6.5 with 4; 64 experts of 1408 x 2048, 96 rows: 35 and 24)
-  if (!grouped && a.m > 32) return launch_rows<4, 8>(a, stream);
-  if (!grouped && a.m > 16) return launch_rows<2, 8>(a, stream);
-  return a.kb >= 24 ? launch_rows<1, 8>(a, stream) : launch_rows<1, 4>(a, stream);
+  if (!grouped && a.m > 32) return launch_rows<4, 8, void>(a, stream);
+  if (!grouped && a.m > 16) return launch_rows<2, 8, void>(a, stream);
+  return a.kb >= 24 ? launch_rows<1, 8, void>(a, stream) : launch_rows<1, 4, void>(a, stream);
+}
+
+// 16-bit rows straight into the kernel for few rows, where rows can be read in 16-byte pieces and
+// the workgroups' repeated rounding stays small: at most 32 values a thread, 4 M over the launch
+// (4096 x 14336 at 1 row: 14.2 us, against 3.5 + 12.7 in two launches; 4096 x 4096 at 8 rows: 11.5
+// against 3.6 + 6.6; 96 rows of 64 experts of 1408 x 2048: 29.4 against 3.9 + 23.8), and 16 rows
+// of a group fit 48 KB, which leaves three workgroups on a CU.
+bool rounds_itself(const MmArgs& a, const void* X, int64_t ldx) {
+  if (reinterpret_cast<uintptr_t>(X) % 16 != 0 || ldx % 8 != 0 || a.m * a.k > (1 << 22)) return false;
+  if (a.m * a.k * ((a.n + 15) / 16) > (1 << 22)) return false;
+  if (a.off != nullptr) return a.m <= 2 * static_cast<int64_t>(a.experts) && raw_lds(a, 16) <= 48 * 1024;
+  return a.m <= 16 && a.m * a.k <= 16384;
+}
+template <typename T>
+gptq_status launch_raw(const MmArgs& a, hipStream_t stream) {
+  return a.kb >= 24 ? launch_rows<1, 8, T>(a, stream) : launch_rows<1, 4, T>(a, stream);
 }
 
 struct Fp8Layout {
@@ -1117,20 +1188,26 @@ gptq_status fp8_matmul_enqueue(const Fp8Problem& p, hipStream_t stream) {
   const size_t yb = p.y_dtype == GPTQ_F32 ? 16 : 8;
   a.vec_y = p.ldy % 4 == 0 && reinterpret_cast<uintptr_t>(p.Y) % yb == 0;
   a.off = p.offsets; a.rows = p.row_index; a.experts = p.batch;
-  if (p.x_dtype == GPTQ_E4M3) {
-    a.X = static_cast<const uint8_t*>(p.X); a.ldx = p.ldx; a.xs = p.xs; a.xsr = p.xsr; a.xsb = p.xsb;
-  } else {
-    const Fp8Layout l = fp8_layout(p.x_rows, p.k);
-    if (p.x_rows > 0 && (p.workspace == nullptr || p.workspace_bytes < l.total)) return GPTQ_ERR_WORKSPACE;
-    uint8_t* ws = static_cast<uint8_t*>(p.workspace);
-    if (p.x_rows > 0) {
-      const gptq_status st = fp8_quantize_enqueue(1, p.x_rows, p.k, p.x_dtype, p.X, p.ldx, 0, 1, p.e8, ws, ws + l.s, 1,
-                                                  p.x_rows, 0, stream);
-      if (st != GPTQ_OK) return st;
-    }
-    a.X = ws; a.ldx = p.k; a.xs = ws + l.s; a.xsr = 1; a.xsb = p.x_rows;
+  if (a.off != nullptr && (a.m / 16 + 1) * a.experts > INT32_MAX) return GPTQ_ERR_UNSUPPORTED;
+  a.X = static_cast<const uint8_t*>(p.X);
+  a.ldx = p.ldx; a.xs = p.xs; a.xsr = p.xsr; a.xsb = p.xsb;
+  if (p.x_dtype == GPTQ_E4M3) return launch_product(a, choose_product(a), stream);
+  const Fp8Layout l = fp8_layout(p.x_rows, p.k);
+  if (p.x_rows > 0 && (p.workspace == nullptr || p.workspace_bytes < l.total)) return GPTQ_ERR_WORKSPACE;
+  a.ldx = p.k;   // as the product will read them
+  const Product kind = choose_product(a);
+  if (kind == kRows && rounds_itself(a, p.X, p.ldx)) {
+    a.ldx = p.ldx;
+    return p.x_dtype == GPTQ_BF16 ? launch_raw<BF16>(a, stream) : launch_raw<F16>(a, stream);
   }
-  return launch_product(a, stream);
+  uint8_t* ws = static_cast<uint8_t*>(p.workspace);
+  if (p.x_rows > 0) {
+    const gptq_status st = fp8_quantize_enqueue(1, p.x_rows, p.k, p.x_dtype, p.X, p.ldx, 0, 1, p.e8, ws, ws + l.s, 1,
+                                                p.x_rows, 0, stream);
+    if (st != GPTQ_OK) return st;
+  }
+  a.X = ws; a.xs = ws + l.s; a.xsr = 1; a.xsb = p.x_rows;
+  return launch_product(a, kind, stream);
 }
 
 }  // namespace gptq

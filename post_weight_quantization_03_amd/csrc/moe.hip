@@ -106,26 +106,30 @@ __device__ __forceinline__ void route_exact(const RouteArgs& a, int64_t t, doubl
   const T* row = static_cast<const T*>(a.logits) + t * a.ldl;
   const double ninf = -INFINITY;
   double l[PER], s[PER], c[PER];
-  double m = ninf;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int e = lane * PER + i;
     const double v = e < a.E ? static_cast<double>(load_as_f32(row + e)) : ninf;
     l[i] = v == v ? v : ninf;
-    m = fmax(m, l[i]);
-  }
-  for (int d = 32; d; d >>= 1) m = fmax(m, __shfl_xor(m, d));
-  double sum = 0.0;
-#pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    if (a.scoring == 0) s[i] = l[i] == ninf ? 0.0 : l[i] == m ? 1.0 : exp(l[i] - m);
-    else s[i] = l[i] == ninf ? 0.0 : 1.0 / (1.0 + exp(-l[i]));
-    sum += s[i];
   }
   if (a.scoring == 0) {
-    sum = lanes_sum(sum, 64);
+    uint32_t k = key_of(static_cast<float>(l[0]));   // logits are fp32 values
+#pragma unroll
+    for (int i = 1; i < PER; ++i) k = max(k, key_of(static_cast<float>(l[i])));
+    const double m = static_cast<double>(of_key(wave_max(k)));
+    double sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      s[i] = exp(l[i] == ninf ? -800.0 : l[i] == m ? 0.0 : fmax(l[i] - m, -800.0));   // exp(-800) is 0
+      sum += s[i];
+    }
+    sum = row_sum(sum);
+    sum = lane_value(sum, 0) + lane_value(sum, 16) + (lane_value(sum, 32) + lane_value(sum, 48));
 #pragma unroll
     for (int i = 0; i < PER; ++i) s[i] = sum > 0.0 ? s[i] / sum : 0.0;
+  } else {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) s[i] = 1.0 / (1.0 + exp(l[i] == ninf ? 800.0 : -l[i]));
   }
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
@@ -271,7 +275,8 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
         for (int d = PER / 2; d; d /= 2)
 #pragma unroll
           for (int i = 0; i < d; ++i) part[i] += part[i + d];
-        total = lanes_sum(static_cast<double>(part[0]), 64);
+        total = row_sum(static_cast<double>(part[0]));
+        total = lane_value(total, 0) + lane_value(total, 16) + (lane_value(total, 32) + lane_value(total, 48));
       }
       if (biased || by_s) {
         const float r = softmax && total > 0.0 ? __builtin_amdgcn_rcpf(static_cast<float>(total)) : 0.0f;
@@ -437,7 +442,26 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
 // row of 16 lanes, four at a time per wave, PER experts per lane.  A group is 16 / G lanes, each
 // with `each` of its experts; everything between the lanes of a row is data-parallel moves, so
 // that the four tokens' chains run side by side where the kernel above waits for each step
-// (16384 tokens of 256 experts in 8 groups: 34 us there).  Values, checks and results are the same.
+// (16384 tokens of 256 experts in 8 groups: 34 us there).  Values and results are the same; the
+// check of two choice values takes 2^-18, since keys give 4 bits to their number.
+// Batcher's merging network, largest first.
+template <int N>
+__device__ __forceinline__ void sort_descending(uint32_t (&v)[N]) {
+#pragma unroll
+  for (int p = 1; p < N; p *= 2)
+#pragma unroll
+    for (int k = p; k >= 1; k /= 2)
+#pragma unroll
+      for (int j = k % p; j < N - k; j += 2 * k)
+#pragma unroll
+        for (int i = 0; i < k; ++i)
+          if (i + j + k < N && (i + j) / (2 * p) == (i + j + k) / (2 * p)) {
+            const uint32_t hi = max(v[i + j], v[i + j + k]), lo = min(v[i + j], v[i + j + k]);
+            v[i + j] = hi;
+            v[i + j + k] = lo;
+          }
+}
+
 template <typename T, int PER>
 __global__ __launch_bounds__(256) void route_rows_kernel(RouteArgs a) {
   __shared__ double scratch[4][256];   // route_exact's
@@ -551,35 +575,42 @@ __global__ __launch_bounds__(256) void route_rows_kernel(RouteArgs a) {
 #pragma unroll
     for (int i = 0; i < PER; ++i) key[i] = !in ? kKeyNone : by_s ? key_of(l[i]) : key[i];
   }
-  // one choice after another, and with biases the best that is left behind; lane j keeps choice j
+  // Keys carry their number in the lane in the low 4 bits (28 bits of value: all that 16-bit
+  // logits have), so that sorting them is maxima and minima alone.
+#pragma unroll
+  for (int i = 0; i < PER; ++i) key[i] = (key[i] & ~15u) | static_cast<uint32_t>(15 - i);
+  sort_descending<PER>(key);
+  // one choice after another, and the best that is left behind where near values matter; lane j
+  // keeps choice j
+  const bool exact = !biased && sizeof(T) == 2;   // keys are logits in full
   uint32_t got = 0;
-  int pos = -1;   // lane * 32 + number in the lane
-  for (int j = 0; j < a.k + (biased ? 1 : 0); ++j) {
-    uint32_t best = key[0];
+  int owner = -1;
+  for (int j = 0; j < a.k + (exact ? 0 : 1); ++j) {
+    const uint32_t value = row_max(key[0] & ~15u);
+    // the lowest lane that holds it, and its number there
+    const uint32_t at = row_max((key[0] & ~15u) == value ? (15u - l16) << 4 | (key[0] & 15u) : 0u);
+    const uint32_t top = value | (at & 15u), first = 15u - (at >> 4);
+    // that lane moves up its keys, by a bit mask (as selections the compiler turns this into
+    // indexing, 400 instructions)
+    uint32_t out = l16 == static_cast<int>(first) ? ~0u : 0u;
+    asm("" : "+v"(out));
 #pragma unroll
-    for (int i = 1; i < PER; ++i) best = max(best, key[i]);
-    const uint32_t top = row_max(best);
-    uint32_t where = 0xFFFFu;
-#pragma unroll
-    for (int i = PER - 1; i >= 0; --i) where = key[i] == top ? static_cast<uint32_t>(i) : where;
-    where += l16 * 32;
-    where = ~row_max(~where);   // the lowest place that holds it
-    const int num = static_cast<int>(where) - l16 * 32;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) key[i] = num == i ? kKeyNone : key[i];
+    for (int i = 0; i < PER; ++i) key[i] = ((i + 1 < PER ? key[i + 1 < PER ? i + 1 : 0] : kKeyNone) & out) | (key[i] & ~out);
     const bool here = l16 == j && top > kKeyNone;
     got = here ? top : got;
-    pos = here ? static_cast<int>(where) : pos;
+    owner = here ? static_cast<int>(first) : owner;
   }
-  const int pl = pos >> 5;
-  const int id = pos < 0 ? -1 : (pl >> a.log_lanes) * per + (pl & (lanes - 1)) * each + (pos & 31);
-  if (biased) {
+  const int id = owner < 0 ? -1
+                           : (owner >> a.log_lanes) * per + (owner & (lanes - 1)) * each + 15 - static_cast<int>(got & 15u);
+  if (!exact) {
     const uint32_t next = moved<0x101>(got);                               // the lane after (row_shl 1)
     const int next_id = static_cast<int>(moved<0x101>(static_cast<uint32_t>(id + 1))) - 1;
     if (l16 < a.k && next_id >= 0) {
-      const float u = of_key(got), v = of_key(next);
-      if (!(u - v > 0x1p-19f * fmaxf(1.0f, fmaxf(fabsf(u), fabsf(v)))))
-        near = near || !(load_as_f32(row + id) == load_as_f32(row + next_id) && a.bias[id] == a.bias[next_id]);
+      const float u = of_key(got & ~15u), v = of_key(next & ~15u);
+      const float tol = biased ? 0x1p-18f * fmaxf(1.0f, fmaxf(fabsf(u), fabsf(v))) : 0.0f;
+      if (!(u - v > tol))
+        near = near || !(load_as_f32(row + id) == load_as_f32(row + next_id) &&
+                         (!biased || a.bias[id] == a.bias[next_id]));
     }
   }
   uint64_t again = __ballot(near && live);

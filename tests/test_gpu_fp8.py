@@ -482,3 +482,28 @@ def test_quantize_past_32_bit_offsets():
         assert np.array_equal(q[r:r + 1].double().cpu().numpy(), F.E4M3[codes])
         assert np.array_equal(s[r:r + 1].double().cpu().numpy(), scales)
     assert int(q.view(torch.uint8).ne(0).any(1).sum()) == 4
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("e8m0", [False, True])
+@pytest.mark.parametrize("n,k", [(40, 400), (130, 2064), (16, 112)])
+def test_few_16bit_rows_of_experts(n, k, e8m0, dtype):
+    # one or two rows an expert, rounded where they are multiplied
+    rng = np.random.default_rng(n + k)
+    counts = [1, 0, 3, 1, 0, 2, 1]
+    _, _, wq, ws, offsets, rows = grouped_case(rng, counts, 9, e8m0, n, k)
+    rows[2] = -1
+    X = torch.from_numpy(values(rng, 9, k).clip(-3e4, 3e4)).to(DT[dtype]).cuda()
+    W, WS, off, idx = code_tensor(wq), scale_tensor(ws, e8m0), torch.from_numpy(offsets).cuda(), torch.from_numpy(rows).cuda()
+    xq, xs = F.ref_quantize(X.double().cpu().numpy(), 1, e8m0)
+    ref, B, _ = F.ref_grouped(xq, xs, wq, ws, offsets, rows)
+    for out in ("bf16", "f32"):
+        Y = lib().fp8_matmul_grouped(X, W, WS, off, idx, out_dtype=DT[out])
+        check_y(Y, ref, B, k, out)
+        assert bool((Y[2] == 0).all())
+        q, s = lib().fp8_quantize(X, 1, sdt(e8m0))
+        assert torch.equal(lib().fp8_matmul_grouped(q, W, WS, off, idx, s, out_dtype=DT[out]), Y)
+    # rows that cannot be read in 16-byte pieces take the other way to the same result
+    odd = torch.zeros(9, k + 3, dtype=DT[dtype], device="cuda")[:, 1:k + 1]
+    odd.copy_(X)
+    assert torch.equal(lib().fp8_matmul_grouped(odd, W, WS, off, idx, out_dtype=torch.float32), Y)
