@@ -845,19 +845,28 @@ gptq_status launch_big(MmArgs a, hipStream_t stream) {
   return GPTQ_OK;
 }
 
-// The same product for grids of few tiles, where a stage lasts no longer than a copy takes:
-// 64 x 64 tiles, 4 waves of 32 x 32, four buffers of 16 KB and three stages of copies in
-// flight.  All scales of the tile are in LDS before the first stage, so that the loop has no
-// other loads and can wait for copies by their number.
-constexpr int MID_KB = 224;   // most blocks of inputs (their scales are 256 bytes each)
-template <int KIND>
-__global__ __launch_bounds__(256) void fp8_mid_kernel(MmArgs a) {
+// The same product for grids of few tiles: 64 x 64 tiles by 4 waves of 32 x 32, four buffers of
+// 16 KB and three stages of copies in flight.  One such group of waves issues its stage's
+// instructions in about 0.47 us however early the copies come (eight buffers, or operands read
+// a stage ahead, gained nothing); a second group with every other stage and buffers of its own
+// (KG = 2) fills the gaps where the CU has room for it.  All scales of the tile are in LDS before
+// the first stage, so that the loop has no other loads and can wait for copies by their number.
+constexpr int MID_KB[3] = {0, 224, 112};   // most blocks of inputs (260 bytes of scales each) by groups
+constexpr int MID_PAIR = 60;               // most blocks with which two workgroups of one group fit a CU
+// Two groups where a CU has one workgroup of one group at a time, by the number of workgroups or by
+// their LDS (4096 x 14336 at 256 rows: 34.8 us with two, 55 with one; 1416 x 2000 at 333 rows, fp32
+// Y: 10.8 and 13.8), and there are stages enough to share.
+__host__ inline int mid_groups(int kb, double grid) {
+  return kb >= 8 && kb <= MID_KB[2] && (grid <= 256 || kb > MID_PAIR) ? 2 : 1;
+}
+template <int KIND, int KG>
+__global__ __launch_bounds__(KG * 256) void fp8_mid_kernel(MmArgs a) {
   constexpr int TM = 64, TN = 64, NW = 4, NB = 4;
   constexpr int STAGE = (TM + TN) * FB;
   constexpr int LD = (TM + TN) / 8 / NW;
-  __shared__ __attribute__((aligned(128))) uint8_t lds[NB * STAGE];
+  __shared__ __attribute__((aligned(128))) uint8_t lds[KG * NB * STAGE];
   extern __shared__ float scales[];   // [kb][TM] of the rows, then [kb] of the outputs
-  const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+  const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6) % NW, group = uniform(tid >> 6) / NW;
   int64_t mt;
   int nt;
   if (!ordered_tile(a.order, blockIdx.x, &mt, &nt)) return;
@@ -879,18 +888,19 @@ __global__ __launch_bounds__(256) void fp8_mid_kernel(MmArgs a) {
     }
   }
   const unsigned lds0 = static_cast<unsigned>(reinterpret_cast<uintptr_t>(
-      (__attribute__((address_space(3))) uint8_t*)lds));
+      (__attribute__((address_space(3))) uint8_t*)lds)) + group * NB * STAGE + wave * 1024;
+  const int own = (a.kb - group + KG - 1) / KG;   // this group's stages: blocks group, group + KG, ..
   auto issue = [&](int s) {
-    const int k0 = s * FB;
+    const int k0 = (s * KG + group) * FB;
     const bool in = k0 + 16 * c < a.k;
 #pragma unroll
     for (int i = 0; i < LD; ++i)
-      copy16(in && src[i] != nullptr ? src[i] + k0 : zeros, lds0 + (s % NB) * STAGE + (wave + NW * i) * 1024);
+      copy16(in && src[i] != nullptr ? src[i] + k0 : zeros, lds0 + (s % NB) * STAGE + NW * i * 1024);
   };
   {
     const int64_t row = source_row(a, t.p0 + min(lane, t.count - 1));
-    for (int b = wave; b < a.kb; b += NW) scales[b * TM + lane] = row >= 0 ? load_xs<KIND>(a, row, b) : 0.0f;
-    for (int b = tid; b < a.kb; b += 256) scales[a.kb * TM + b] = load_ws<KIND>(a, t.e, n0 / FB, b);
+    for (int b = tid / 64; b < a.kb; b += KG * NW) scales[b * TM + lane] = row >= 0 ? load_xs<KIND>(a, row, b) : 0.0f;
+    for (int b = tid; b < a.kb; b += KG * 256) scales[a.kb * TM + b] = load_ws<KIND>(a, t.e, n0 / FB, b);
   }
   const int wm = wave / 2, wn = wave % 2;
   const int j = lane & 15, q = lane >> 4;
@@ -902,29 +912,51 @@ __global__ __launch_bounds__(256) void fp8_mid_kernel(MmArgs a) {
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 #pragma unroll
   for (int s = 0; s < NB - 1; ++s)
-    if (s < a.kb) issue(s);
-  for (int s = 0; s < a.kb; ++s) {
+    if (s < own) issue(s);
+  for (int s = 0; s < (a.kb + KG - 1) / KG; ++s) {   // the first group's number of stages: the longest
     // this stage's copies are the oldest of those of up to three stages
-    if (s + 2 < a.kb) wait_vmcnt<2 * LD>();
-    else if (s + 1 < a.kb) wait_vmcnt<LD>();
+    if (s + 2 < own) wait_vmcnt<2 * LD>();
+    else if (s + 1 < own) wait_vmcnt<LD>();
     else wait_vmcnt<0>();
     __syncthreads();   // everyone's copies have landed, and everyone is done with the stage before
-    if (s + NB - 1 < a.kb) issue(s + NB - 1);
-    const uint8_t* xb = lds + (s % NB) * STAGE + wm * 32 * FB;
-    const uint8_t* wb = lds + (s % NB) * STAGE + (TM + wn * 32) * FB;
+    if (s + NB - 1 < own) issue(s + NB - 1);
+    if (s >= own) break;   // behind the last barrier of the loop
+    const int b = s * KG + group;
+    const uint8_t* xb = lds + (group * NB + s % NB) * STAGE + wm * 32 * FB;
+    const uint8_t* wb = lds + (group * NB + s % NB) * STAGE + (TM + wn * 32) * FB;
     auto frag = [&](const uint8_t* p) {
       const i32x4 lo = *reinterpret_cast<const i32x4*>(p + at0);
       const i32x4 hi = *reinterpret_cast<const i32x4*>(p + at1);
       return Operand<KIND>(i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]});
     };
     const Operand<KIND> xf[2] = {frag(xb), frag(xb + 16 * FB)}, wf[2] = {frag(wb), frag(wb + 16 * FB)};
-    const float sw = scales[a.kb * TM + s];
+    const float sw = scales[a.kb * TM + b];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const float sx = scales[s * TM + wm * 32 + 16 * i + j];
+      const float sx = scales[b * TM + wm * 32 + 16 * i + j];
 #pragma unroll
       for (int h = 0; h < 2; ++h) block_mma<KIND>(wf[h], xf[i], sx, sw, y[i][h]);
     }
+  }
+  if constexpr (KG == 2) {
+    // the second group's sums through LDS, in one order: first + second
+    f32x4* const part = reinterpret_cast<f32x4*>(lds);
+    __syncthreads();
+    if (group == 1)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) part[((wave * 2 + i) * 2 + h) * 64 + lane] = y[i][h];
+    __syncthreads();
+    if (group == 1) return;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const f32x4 o = part[((wave * 2 + i) * 2 + h) * 64 + lane];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[i][h][e] += o[e];
+      }
   }
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -938,17 +970,23 @@ __global__ __launch_bounds__(256) void fp8_mid_kernel(MmArgs a) {
   }
 }
 
+template <int KG>
+gptq_status launch_mid_groups(const MmArgs& a, unsigned grid, hipStream_t stream) {
+  const dim3 g(grid), b(KG * 256);
+  const size_t lds = static_cast<size_t>(a.kb) * 65 * sizeof(float);
+  if (a.y_dtype == GPTQ_F32) GPTQ_LAUNCH((fp8_mid_kernel<kMmaExact, KG>), g, b, lds, stream, a);
+  else if (a.e8) GPTQ_LAUNCH((fp8_mid_kernel<kMmaE8M0, KG>), g, b, lds, stream, a);
+  else GPTQ_LAUNCH((fp8_mid_kernel<kMmaF32Scale, KG>), g, b, lds, stream, a);
+  return GPTQ_OK;
+}
+
 gptq_status launch_mid(MmArgs a, hipStream_t stream) {
   a.order = tile_order(a.off == nullptr ? (a.m + 63) / 64 : a.m / 64 + std::min<int64_t>(a.experts, a.m),
                        (a.n + 63) / 64);
   const int64_t grid = order_grid(a.order);
   if (grid > (1 << 22)) return GPTQ_ERR_UNSUPPORTED;
-  const dim3 g(static_cast<unsigned>(grid)), b(256);
-  const size_t lds = static_cast<size_t>(a.kb) * 65 * sizeof(float);
-  if (a.y_dtype == GPTQ_F32) GPTQ_LAUNCH((fp8_mid_kernel<kMmaExact>), g, b, lds, stream, a);
-  else if (a.e8) GPTQ_LAUNCH((fp8_mid_kernel<kMmaE8M0>), g, b, lds, stream, a);
-  else GPTQ_LAUNCH((fp8_mid_kernel<kMmaF32Scale>), g, b, lds, stream, a);
-  return GPTQ_OK;
+  if (mid_groups(a.kb, static_cast<double>(grid)) == 2) return launch_mid_groups<2>(a, static_cast<unsigned>(grid), stream);
+  return launch_mid_groups<1>(a, static_cast<unsigned>(grid), stream);
 }
 
 // Few rows: 16 outputs x 16 FM rows per workgroup, whose WK waves take every WK-th block of
@@ -1088,8 +1126,8 @@ gptq_status launch_rows(MmArgs a, hipStream_t stream) {
 // of the kernels on one MI355X, per stage of 128 inputs and round of workgroups:
 //   rows  2.5 + bytes through the L2s at 7 TB/s, every 16 outputs reading all of X again
 //         (4096 x 14336: 11.9 us at 1 row, 18.3 at 16, 27.7 at 32, 45.8 at 64)
-//   mid   64 x 64, one workgroup per CU 0.46 us, two 0.57 (both fit up to 60 blocks of inputs)
-//         (4096 x 14336: 52 us at 64 rows, 55 at 256, 103 at 512; 14336 x 4096 at 64: 19, rows 56)
+//   mid   64 x 64, 0.29 us with two groups of waves; with one 0.46 us, two workgroups per CU 0.57
+//         (4096 x 14336: 32 us at 64 rows, rows 46; 35 at 256, tile 131; 14336 x 4096 at 64: 14)
 //   tile  128 x 128, one workgroup per CU 1.17 us, two 1.5
 //         (4096 x 4096: 42 us at 1024 rows, mid 44, big 48)
 //   big   256 x 256, a round 1.4 us on up to half of the CUs, else 1.85
@@ -1115,9 +1153,11 @@ Product choose_product(const MmArgs& a) {
   const double row_tiles = grouped ? static_cast<double>(a.m) / 16 + 0.5 * used : 1.0;
   const double t_rows = a.m > 64 && !grouped ? 1e30
                         : 2.5 + std::max(read, (row_tiles * weights + static_cast<double>(a.m) * a.k * a.n / 16) / 7e6);
-  const double t_mid = a.kb > MID_KB ? 1e30
-                       : 3 + std::max(read, a.kb * (a.kb <= 60 ? rounds(tiles(64, 64), 512, 0.46, 0.57)
-                                                               : rounds(tiles(64, 64), 256, 0.46, 0.46)));
+  const double mid = tiles(64, 64);
+  const double t_mid = a.kb > MID_KB[1] ? 1e30
+                       : 3 + std::max(read, a.kb * (mid_groups(a.kb, mid) == 2 ? rounds(mid, 256, 0.29, 0.29)
+                                                    : a.kb <= MID_PAIR         ? rounds(mid, 512, 0.46, 0.57)
+                                                                               : rounds(mid, 256, 0.47, 0.47)));
   const double t_tile = 3 + std::max(read, a.kb * rounds(tiles(128, 128), 512, 1.17, 1.5));
   const int64_t span = a.rows == nullptr ? 256 * a.ldx : a.x_rows * a.ldx;
   const bool narrow = span <= INT32_MAX && 256 * static_cast<int64_t>(a.k) <= INT32_MAX;

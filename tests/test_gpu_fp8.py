@@ -507,3 +507,34 @@ def test_few_16bit_rows_of_experts(n, k, e8m0, dtype):
     odd = torch.zeros(9, k + 3, dtype=DT[dtype], device="cuda")[:, 1:k + 1]
     odd.copy_(X)
     assert torch.equal(lib().fp8_matmul_grouped(odd, W, WS, off, idx, out_dtype=torch.float32), Y)
+
+
+@pytest.mark.parametrize("out", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("e8m0", [False, True])
+@pytest.mark.parametrize("m,n,k", [(65, 200, 1040), (300, 640, 896), (70, 260, 14336), (70, 130, 14352), (300, 4096, 7808)])
+def test_long_products_of_few_tiles(m, n, k, e8m0, out):
+    # inputs shared by two groups of waves: an odd number of blocks, the shortest, the longest, one past it
+    q, s = random_operands(m + k, m, k, 1, e8m0)
+    w, ws = random_operands(n, n, k, 128, e8m0)
+    Y = lib().fp8_matmul(q, w, ws, s, out_dtype=DT[out])
+    check_large(Y, wide(q, s, 1), wide(w, ws, 128), k, out)
+    assert torch.equal(lib().fp8_matmul(q, w, ws, s, out_dtype=DT[out]), Y)
+
+
+@pytest.mark.parametrize("e8m0", [False, True])
+def test_long_products_of_few_grouped_tiles(e8m0):
+    counts, n, k = [100, 0, 260, 1, 170], 520, 1168
+    offsets = 2 + np.concatenate([[0], np.cumsum(counts)])
+    rows = np.random.default_rng(8).integers(0, 90, int(offsets[-1]) + 3).astype(np.int32)
+    rows[[5, 300]] = -1, 90
+    q, s = random_operands(k, 90, k, 1, e8m0)
+    w, ws = random_operands(n, n, k, 128, e8m0, (len(counts),))
+    Y = torch.full((len(rows), n), 2.5, dtype=torch.bfloat16, device="cuda")
+    lib().fp8_matmul_grouped(q, w, ws, torch.from_numpy(offsets).cuda(), torch.from_numpy(rows).cuda(), s, out=Y)
+    assert bool((Y[:2] == 2.5).all()) and bool((Y[int(offsets[-1]):] == 2.5).all()) and bool((Y[[5, 300]] == 0).all())
+    for e, c in enumerate(counts):
+        lo = int(offsets[e])
+        idx = torch.from_numpy(rows[lo:lo + c].astype(np.int64)).cuda()
+        ok = (idx >= 0) & (idx < 90)
+        if c:
+            check_large(Y[lo:lo + c][ok], wide(q, s, 1)[idx[ok]], wide(w[e], ws[e], 128), k, "bf16")
