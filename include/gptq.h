@@ -345,7 +345,7 @@ gptq_status gptq_fp8_matmul(int64_t m, int d_out, int d_in, gptq_dtype x_dtype, 
  * n_rows output rows grouped by expert, expert e owning rows p of token_offsets[e] ..
  * token_offsets[e + 1] - 1 (DEVICE int64 [batch + 1], not decreasing; each range is clamped to
  * [0, n_rows]):
- *   Y[p, :] = X[row_index[p], :] times expert e's weights (row_index NULL: X[p, :])
+ *   Y[p, :] = X[row_index[p], :] times expert e's weights (row_index NULL: X[p, :], n_rows <= x_rows)
  * X has x_rows rows and is rounded once per row, not per output row, when it is bf16 or
  * fp16.  row_index: DEVICE int32 [n_rows]; an entry outside [0, x_rows) gives a row of
  * zeros.  Rows of Y outside every range are left as they were.  token_offsets and row_index as

@@ -340,6 +340,7 @@ gptq_status gptq_fp8_matmul_grouped(int batch, int64_t x_rows, int64_t n_rows, i
   const gptq_status st = check_fp8(p, s_dtype);
   if (st != GPTQ_OK || n_rows == 0) return st;
   if (token_offsets == nullptr || !aligned(token_offsets, 8) || !aligned(row_index, 4)) return GPTQ_ERR_INVALID_ARG;
+  if (row_index == nullptr && n_rows > x_rows) return GPTQ_ERR_INVALID_ARG;   // row p of X for every p
   return gptq::fp8_matmul_enqueue(p, stream);
 }
 

@@ -161,3 +161,11 @@ def test_binding_refuses_bad_routing_arguments():
     refused(ValueError, gptq.moe_combine, y, ids, w[:3])
     refused(ValueError, gptq.moe_combine, y.t(), ids, w)
     refused(ValueError, gptq.moe_combine, y, ids, w, out=torch.zeros(4, 15))
+
+
+def test_grouped_rows_past_the_activations():
+    # without an index output row p reads row p of X
+    a = dict(batch=2, xr=4, rows=5, n=64, k=128, xt=E4M3, X=16, ldx=128, st=F32, xs=16, xsr=1, xsb=4, W=16, ws=16,
+             off=16, idx=None, yt=BF16, Y=16, ldy=64, wsp=None, wsb=0, stream=None)
+    assert gptq.lib().gptq_fp8_matmul_grouped(*a.values()) == BAD
+    assert gptq.lib().gptq_fp8_matmul_grouped(*{**a, "xr": 2 ** 31, "rows": 2 ** 31 + 1}.values()) == BAD
