@@ -332,6 +332,9 @@ __device__ __forceinline__ int64_t source_row(const MmArgs& a, int64_t p) {
   return r >= 0 && r < a.x_rows ? r : -1;
 }
 
+// Output rows without a row of X are zeros, also where a weight or its scale is NaN.
+__device__ __forceinline__ bool lost_row(const MmArgs& a, int64_t p) { return a.rows != nullptr && source_row(a, p) < 0; }
+
 // An E8M0 code as fp32 (2^-127 is subnormal there).
 __device__ __forceinline__ float e8m0_f32(int code) {
   return code == 255 ? __uint_as_float(0x7FC00000u) : code == 0 ? __uint_as_float(0x00400000u)
@@ -570,9 +573,11 @@ __global__ __launch_bounds__(WM* WN * 64) void fp8_tile_kernel(MmArgs a) {
   for (int i = 0; i < FM; ++i) {
     const int r = wm * (TM / WM) + 16 * i + j;
     if (r >= t.count) continue;
+    const bool none = lost_row(a, t.p0 + r);
 #pragma unroll
     for (int h = 0; h < FN; ++h) {
-      const float v[4] = {y[i][h][0], y[i][h][1], y[i][h][2], y[i][h][3]};
+      const f32x4 s = none ? zero : y[i][h];
+      const float v[4] = {s[0], s[1], s[2], s[3]};
       store_y(a, t.p0 + r, n0 + wn * (TN / WN) + 16 * h + 4 * q, v);
     }
   }
@@ -815,7 +820,7 @@ __global__ __launch_bounds__(NW * 64) void fp8_big_kernel(MmArgs a) {
   for (int i = 0; i < FM; ++i) {
     const int r = xr + 16 * i + j;
     if (r >= t.count) continue;
-    const bool none = a.rows != nullptr && source_row(a, t.p0 + r) < 0;
+    const bool none = lost_row(a, t.p0 + r);
     uint16_t* out = static_cast<uint16_t*>(a.Y) + (t.p0 + r) * a.ldy;
 #pragma unroll
     for (int h = 0; h < FN; ++h) {
@@ -962,9 +967,11 @@ __global__ __launch_bounds__(KG * 256) void fp8_mid_kernel(MmArgs a) {
   for (int i = 0; i < 2; ++i) {
     const int r = wm * 32 + 16 * i + j;
     if (r >= t.count) continue;
+    const bool none = lost_row(a, t.p0 + r);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const float v[4] = {y[i][h][0], y[i][h][1], y[i][h][2], y[i][h][3]};
+      const f32x4 s = none ? zero : y[i][h];
+      const float v[4] = {s[0], s[1], s[2], s[3]};
       store_y(a, t.p0 + r, n0 + wn * 32 + 16 * h + 4 * q, v);
     }
   }
@@ -1072,8 +1079,10 @@ __global__ __launch_bounds__(WK * 64) void fp8_rows_kernel(MmArgs a) {
         for (int i = 0; i < FM; ++i) {
           if constexpr (kRaw) {
             const int r = min(16 * i + j, t.count - 1);
-            const i32x8 v = *reinterpret_cast<const i32x8*>(raw + r * pitch + FB * b + 32 * q);
-            block_mma<KIND>(wf, Operand<KIND>(v), rs[r * a.kb + b], sw[u], y[i]);
+            const i32x4* p = reinterpret_cast<const i32x4*>(raw + r * pitch + FB * b + 32 * q);
+            const i32x4 lo = p[0], hi = p[1];
+            const Operand<KIND> xf(i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]});
+            block_mma<KIND>(wf, xf, rs[r * a.kb + b], sw[u], y[i]);
           } else {
             const Operand<KIND> xf(i32x8{xl[u][i][0], xl[u][i][1], xl[u][i][2], xl[u][i][3], xh[u][i][0], xh[u][i][1],
                                          xh[u][i][2], xh[u][i][3]});
@@ -1096,6 +1105,7 @@ __global__ __launch_bounds__(WK * 64) void fp8_rows_kernel(MmArgs a) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[e] += o[e];
     }
+    if (lost_row(a, t.p0 + r)) v = zero;
     const float f[4] = {v[0], v[1], v[2], v[3]};
     store_y(a, t.p0 + r, n0 + 4 * c, f);
   }

@@ -538,3 +538,30 @@ def test_long_products_of_few_grouped_tiles(e8m0):
         ok = (idx >= 0) & (idx < 90)
         if c:
             check_large(Y[lo:lo + c][ok], wide(q, s, 1)[idx[ok]], wide(w[e], ws[e], 128), k, "bf16")
+
+
+@pytest.mark.parametrize("e8m0", [False, True])
+@pytest.mark.parametrize("n_rows,n,k,out", [(20, 48, 272, "bf16"), (400, 200, 272, "f32"), (400, 200, 1040, "f16"),
+                                            (6000, 1030, 912, "f32"), (9000, 2050, 912, "bf16")])
+def test_rows_without_a_source_are_zeros(n_rows, n, k, out, e8m0):
+    # whatever the weights hold: one expert has a block without a scale
+    q, s = random_operands(k, 64, k, 1, e8m0)
+    w, ws = random_operands(n, n, k, 128, e8m0, (3,))
+    ws[1, 0, 1] = float("nan")
+    off = torch.tensor([0, n_rows // 4, n_rows - 5, n_rows], device="cuda")
+    g = torch.Generator(device="cuda")
+    g.manual_seed(2)
+    rows = torch.randint(-3, 67, (n_rows,), generator=g, device="cuda", dtype=torch.int32)
+    lost = (rows < 0) | (rows >= 64)
+    Y = lib().fp8_matmul_grouped(q, w, ws, off, rows, s, out_dtype=DT[out])
+    assert bool((Y[lost] == 0).all()) and int(lost.sum()) > 0
+    mid = ~lost
+    mid[:n_rows // 4] = False
+    mid[n_rows - 5:] = False
+    assert bool(Y[mid][:, :128].isnan().all())
+    assert bool(Y[:n_rows // 4].isfinite().all())
+    # 16-bit rows, rounded where they are multiplied when they are few
+    X = torch.randn(64, k, device="cuda").to(torch.bfloat16)
+    few = lib().fp8_matmul_grouped(X, w, ws, torch.tensor([0, 1, 4, 5], device="cuda"), rows[:5].clamp(max=70).index_fill(
+        0, torch.tensor([2], device="cuda"), -1), out_dtype=DT[out])
+    assert bool((few[2] == 0).all())
