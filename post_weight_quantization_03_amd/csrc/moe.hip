@@ -837,7 +837,7 @@ __global__ __launch_bounds__(256) void combine_kernel(int64_t n_tokens, int k, i
                                                       int64_t ldy, const int32_t* place, const float* weights, T* out,
                                                       int64_t ldo) {
   const int per = (d + V - 1) / V;
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  const int64_t i = (static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x) * 256 + threadIdx.x;
   const int64_t t = i / per;
   if (t >= n_tokens) return;
   const int64_t col = (i - t * per) * V;
@@ -865,8 +865,10 @@ gptq_status launch_combine(int64_t n_tokens, int k, int64_t n_rows, int d, const
   const bool wide = d % V == 0 && ldy % V == 0 && ldo % V == 0 && reinterpret_cast<uintptr_t>(Y) % 16 == 0 &&
                     reinterpret_cast<uintptr_t>(out) % 16 == 0;
   const int64_t n = n_tokens * (wide ? d / V : d);
-  if ((n + 255) / 256 > INT32_MAX) return GPTQ_ERR_UNSUPPORTED;
-  const dim3 grid(static_cast<unsigned>((n + 255) / 256)), block(256);
+  // a launch's threads along x stay below 2^32
+  const int64_t blocks = (n + 255) / 256, gx = std::min<int64_t>(blocks, 1 << 22), gy = (blocks + gx - 1) / gx;
+  if (gy > 65535) return GPTQ_ERR_UNSUPPORTED;
+  const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(gy)), block(256);
   if (wide)
     GPTQ_LAUNCH((combine_kernel<T, V>), grid, block, 0, stream, n_tokens, k, n_rows, d, static_cast<const T*>(Y), ldy,
                 place, weights, static_cast<T*>(out), ldo);

@@ -298,3 +298,17 @@ def test_ranges_feed_the_grouped_hessian():
         want = 2 * mine.T @ mine
         assert int(n[i]) == len(mine)
         assert np.linalg.norm(H[i].cpu().numpy() - want) <= 1e-5 * np.linalg.norm(want)
+
+
+def test_combine_past_32_bit_elements():
+    # rows of an odd length: one thread per output
+    tokens, d = 65600, 65537
+    y = torch.arange(1, 5, device="cuda").to(torch.bfloat16)[:, None].repeat(1, d)
+    place = torch.full((tokens, 1), -1, dtype=torch.int32, device="cuda")
+    at = [0, 40000, 65535, 65536, tokens - 1]
+    place[at, 0] = torch.tensor([0, 1, 2, 3, 2], dtype=torch.int32, device="cuda")
+    out = lib().moe_combine(y, place, torch.ones(tokens, 1, device="cuda"), out=torch.full(
+        (tokens, d), 7.0, dtype=torch.bfloat16, device="cuda"))
+    for i, v in zip(at, (1, 2, 3, 4, 3)):
+        assert bool((out[i] == v).all())
+    assert int(out.any(1).sum()) == len(at)
