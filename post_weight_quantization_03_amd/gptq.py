@@ -446,8 +446,11 @@ def _scratch(which, batch, d_out, d_in, hint, device, workspace) -> torch.Tensor
     nbytes = _workspace_bytes(which, batch, d_out, d_in, hint)
     if nbytes <= 256:   # the least size: nothing is kept in it
         return None
-    if workspace is not None and workspace.numel() * workspace.element_size() >= nbytes:
-        return workspace
+    if workspace is not None:
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+        if _bytes(workspace) >= nbytes:
+            return workspace
     return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 

@@ -169,3 +169,12 @@ def test_grouped_rows_past_the_activations():
              off=16, idx=None, yt=BF16, Y=16, ldy=64, wsp=None, wsb=0, stream=None)
     assert gptq.lib().gptq_fp8_matmul_grouped(*a.values()) == BAD
     assert gptq.lib().gptq_fp8_matmul_grouped(*{**a, "xr": 2 ** 31, "rows": 2 ** 31 + 1}.values()) == BAD
+
+
+def test_binding_refuses_a_workspace_with_less_memory_than_elements():
+    ws = torch.empty(1, dtype=torch.uint8).expand(1 << 24)
+    q, s = torch.empty(64, 128, dtype=torch.float8_e4m3fn), torch.empty(1, 1)
+    with pytest.raises(ValueError, match="workspace"):
+        gptq.fp8_matmul(torch.empty(4, 128, dtype=torch.bfloat16), q, s, workspace=ws)
+    with pytest.raises(ValueError, match="workspace"):
+        gptq.moe_group_tokens(torch.zeros(20000, 2, dtype=torch.int32), 8, workspace=ws)
