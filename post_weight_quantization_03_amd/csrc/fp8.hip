@@ -267,7 +267,7 @@ struct MmArgs {
   int64_t ldy;
   int y_dtype;
   bool e8;               // scales are E8M0
-  bool vec_y;            // rows of Y take 4 values in one store
+  bool vec_y;            // rows of Y are 16-byte aligned
   const int64_t* off;    // grouped: the experts' ranges
   const int32_t* rows;   // grouped: rows of X, or null
   int experts;
@@ -332,8 +332,9 @@ __device__ __forceinline__ int64_t source_row(const MmArgs& a, int64_t p) {
   return r >= 0 && r < a.x_rows ? r : -1;
 }
 
-// Output rows without a row of X are zeros, also where a weight or its scale is NaN.
-__device__ __forceinline__ bool lost_row(const MmArgs& a, int64_t p) { return a.rows != nullptr && source_row(a, p) < 0; }
+// Output rows without a row of X are zeros, also where a weight or its scale is NaN: the kernels
+// mark them in LDS before their first stage (a load of row_index between the stores of Y would
+// wait for the stores before it: 49152 rows of 64 experts of 1408 x 2048 238 us, 229 so).
 
 // An E8M0 code as fp32 (2^-127 is subnormal there).
 __device__ __forceinline__ float e8m0_f32(int code) {
@@ -500,6 +501,7 @@ __global__ __launch_bounds__(WM* WN * 64) void fp8_tile_kernel(MmArgs a) {
   static_assert(NW % 2 == 0 && (TM + TN) % (8 * NW) == 0 && TM <= NT && FB % (TN / WN) == 0, "tile shape");
   __shared__ __attribute__((aligned(128))) uint8_t lds[2 * STAGE];
   __shared__ float sxs[2 * TM];
+  __shared__ bool lost[TM];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int64_t mt = blockIdx.x / a.tiles_n;
   const int n0 = static_cast<int>(blockIdx.x - mt * a.tiles_n) * TN;
@@ -521,6 +523,7 @@ __global__ __launch_bounds__(WM* WN * 64) void fp8_tile_kernel(MmArgs a) {
     }
   }
   const int64_t srow = tid < TM ? source_row(a, t.p0 + min(tid, t.count - 1)) : -1;
+  if (tid < TM) lost[tid] = srow < 0;
   float sx_next = 0.0f;
   const unsigned lds0 = static_cast<unsigned>(reinterpret_cast<uintptr_t>(
       (__attribute__((address_space(3))) uint8_t*)lds));
@@ -573,7 +576,7 @@ __global__ __launch_bounds__(WM* WN * 64) void fp8_tile_kernel(MmArgs a) {
   for (int i = 0; i < FM; ++i) {
     const int r = wm * (TM / WM) + 16 * i + j;
     if (r >= t.count) continue;
-    const bool none = lost_row(a, t.p0 + r);
+    const bool none = lost[r];
 #pragma unroll
     for (int h = 0; h < FN; ++h) {
       const f32x4 s = none ? zero : y[i][h];
@@ -612,6 +615,7 @@ __global__ __launch_bounds__(NW * 64) void fp8_big_kernel(MmArgs a) {
   constexpr int LD = (TM + TN) / 8 / NW;   // copies per wave and stage: 4 of X, 4 of W
   constexpr bool E8 = KIND == kMmaE8M0;
   __shared__ __attribute__((aligned(128))) uint8_t lds[2 * STAGE];
+  __shared__ bool lost[TM];
   __shared__ float scs[2][2][TM];   // the rows' scales (fp32: twice, so that every wave copies 64)
   extern __shared__ float scw[];    // the outputs' scales: [2][kb]
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -638,7 +642,8 @@ __global__ __launch_bounds__(NW * 64) void fp8_big_kernel(MmArgs a) {
   }
   constexpr int SB = E8 ? 1 : 4;   // bytes of a scale
   const int srow_r = tid & (TM - 1);
-  const int64_t srow = max(source_row(a, t.p0 + min(srow_r, t.count - 1)), static_cast<int64_t>(0));
+  const int64_t own = source_row(a, t.p0 + min(srow_r, t.count - 1)), srow = max(own, static_cast<int64_t>(0));
+  lost[srow_r] = own < 0;
   const uint8_t* xsp = static_cast<const uint8_t*>(a.xs) + srow * a.xsr * SB;   // moves by a block of inputs a stage
   const int64_t xstep = a.xsb * SB;
   float sx_next = 0.0f;
@@ -816,23 +821,28 @@ __global__ __launch_bounds__(NW * 64) void fp8_big_kernel(MmArgs a) {
 #pragma unroll
       for (int r = 0; r < 4; ++r) y[i][h][r] = fmaf(td[p % 4][r], ts[p % 4], y[i][h][r]);
     });
+  // Of outputs 16 h + 4 q .. of two neighbouring h, lanes of odd and even q exchange one each: a
+  // lane then stores 8 in 16 bytes, and four lanes 64 bytes of a row in one piece
 #pragma unroll
   for (int i = 0; i < FM; ++i) {
     const int r = xr + 16 * i + j;
-    if (r >= t.count) continue;
-    const bool none = lost_row(a, t.p0 + r);
+    const bool none = lost[r];
     uint16_t* out = static_cast<uint16_t*>(a.Y) + (t.p0 + r) * a.ldy;
 #pragma unroll
-    for (int h = 0; h < FN; ++h) {
-      const int o = n0 + wn * 16 * FN + 16 * h + 4 * q;
-      const uint2 v = none ? make_uint2(0, 0) : pack16(y[i][h], a.y_dtype == GPTQ_BF16);
-      if (a.vec_y && o + 4 <= a.n) {
-        *reinterpret_cast<uint2*>(out + o) = v;
+    for (int h = 0; h < FN; h += 2) {
+      const uint2 u = pack16(y[i][h], a.y_dtype == GPTQ_BF16), v = pack16(y[i][h + 1], a.y_dtype == GPTQ_BF16);
+      const auto lo = __builtin_amdgcn_permlane16_swap(u.x, v.x, false, false);
+      const auto hi = __builtin_amdgcn_permlane16_swap(u.y, v.y, false, false);
+      if (r >= t.count) continue;
+      const uint4 w = none ? make_uint4(0, 0, 0, 0) : make_uint4(lo[0], hi[0], lo[1], hi[1]);
+      const int o = n0 + wn * 16 * FN + 16 * (h + (q & 1)) + 8 * (q >> 1);
+      if (a.vec_y && o + 8 <= a.n) {
+        *reinterpret_cast<uint4*>(out + o) = w;
       } else {
-        if (o < a.n) out[o] = static_cast<uint16_t>(v.x);
-        if (o + 1 < a.n) out[o + 1] = static_cast<uint16_t>(v.x >> 16);
-        if (o + 2 < a.n) out[o + 2] = static_cast<uint16_t>(v.y);
-        if (o + 3 < a.n) out[o + 3] = static_cast<uint16_t>(v.y >> 16);
+        const uint32_t e[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int x = 0; x < 8; ++x)
+          if (o + x < a.n) out[o + x] = static_cast<uint16_t>(e[x / 2] >> (16 * (x & 1)));
       }
     }
   }
@@ -871,6 +881,7 @@ __global__ __launch_bounds__(KG * 256) void fp8_mid_kernel(MmArgs a) {
   constexpr int LD = (TM + TN) / 8 / NW;
   __shared__ __attribute__((aligned(128))) uint8_t lds[KG * NB * STAGE];
   extern __shared__ float scales[];   // [kb][TM] of the rows, then [kb] of the outputs
+  __shared__ bool lost[TM];
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6) % NW, group = uniform(tid >> 6) / NW;
   int64_t mt;
   int nt;
@@ -904,6 +915,7 @@ __global__ __launch_bounds__(KG * 256) void fp8_mid_kernel(MmArgs a) {
   };
   {
     const int64_t row = source_row(a, t.p0 + min(lane, t.count - 1));
+    if (tid < TM) lost[tid] = row < 0;
     for (int b = tid / 64; b < a.kb; b += KG * NW) scales[b * TM + lane] = row >= 0 ? load_xs<KIND>(a, row, b) : 0.0f;
     for (int b = tid; b < a.kb; b += KG * 256) scales[a.kb * TM + b] = load_ws<KIND>(a, t.e, n0 / FB, b);
   }
@@ -967,7 +979,7 @@ __global__ __launch_bounds__(KG * 256) void fp8_mid_kernel(MmArgs a) {
   for (int i = 0; i < 2; ++i) {
     const int r = wm * 32 + 16 * i + j;
     if (r >= t.count) continue;
-    const bool none = lost_row(a, t.p0 + r);
+    const bool none = lost[r];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const f32x4 s = none ? zero : y[i][h];
@@ -1009,6 +1021,7 @@ __global__ __launch_bounds__(WK * 64) void fp8_rows_kernel(MmArgs a) {
   constexpr bool kRaw = !std::is_void_v<T>;
   extern __shared__ __attribute__((aligned(16))) uint8_t raw[];   // kRaw: rows of codes, then [row][block] scales
   __shared__ __attribute__((aligned(16))) float part[WK][TM][16];
+  __shared__ bool lost[TM];
   const int tid = threadIdx.x, lane = tid & 63, wk = uniform(tid >> 6);
   const int64_t mt = blockIdx.x / a.tiles_n;
   const int n0 = static_cast<int>(blockIdx.x - mt * a.tiles_n) * 16;
@@ -1023,6 +1036,7 @@ __global__ __launch_bounds__(WK * 64) void fp8_rows_kernel(MmArgs a) {
   for (int i = 0; i < FM; ++i) {
     row[i] = source_row(a, t.p0 + min(16 * i + j, t.count - 1));
     x[i] = a.X + row[i] * a.ldx + 32 * q;
+    if (tid < 16) lost[16 * i + j] = row[i] < 0;
   }
   i32x4 wl[U], wh[U], xl[U][FM], xh[U][FM];
   float sw[U], sx[U][FM];
@@ -1105,7 +1119,7 @@ __global__ __launch_bounds__(WK * 64) void fp8_rows_kernel(MmArgs a) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[e] += o[e];
     }
-    if (lost_row(a, t.p0 + r)) v = zero;
+    if (lost[r]) v = zero;
     const float f[4] = {v[0], v[1], v[2], v[3]};
     store_y(a, t.p0 + r, n0 + 4 * c, f);
   }
@@ -1235,8 +1249,7 @@ gptq_status fp8_matmul_enqueue(const Fp8Problem& p, hipStream_t stream) {
   MmArgs a{};
   a.m = p.n_rows; a.n = p.n; a.k = p.k; a.kb = (p.k + FB - 1) / FB; a.nb = (p.n + FB - 1) / FB;
   a.x_rows = p.x_rows; a.W = p.W; a.ws = p.ws; a.Y = p.Y; a.ldy = p.ldy; a.y_dtype = p.y_dtype; a.e8 = p.e8;
-  const size_t yb = p.y_dtype == GPTQ_F32 ? 16 : 8;
-  a.vec_y = p.ldy % 4 == 0 && reinterpret_cast<uintptr_t>(p.Y) % yb == 0;
+  a.vec_y = p.ldy % (p.y_dtype == GPTQ_F32 ? 4 : 8) == 0 && reinterpret_cast<uintptr_t>(p.Y) % 16 == 0;
   a.off = p.offsets; a.rows = p.row_index; a.experts = p.batch;
   if (a.off != nullptr && (a.m / 16 + 1) * a.experts > INT32_MAX) return GPTQ_ERR_UNSUPPORTED;
   a.X = static_cast<const uint8_t*>(p.X);
