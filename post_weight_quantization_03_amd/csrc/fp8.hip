@@ -267,7 +267,8 @@ struct MmArgs {
   int64_t ldy;
   int y_dtype;
   bool e8;               // scales are E8M0
-  bool vec_y;            // rows of Y are 16-byte aligned
+  bool vec_y;            // rows of Y take 4 values in one store
+  bool wide_y;           // and 8 of 16 bits
   const int64_t* off;    // grouped: the experts' ranges
   const int32_t* rows;   // grouped: rows of X, or null
   int experts;
@@ -607,24 +608,28 @@ gptq_status launch_tile(MmArgs a, hipStream_t stream) {
 // the last 12 products cover the first reads of the next stage and half of the copies of the one
 // after it; the other half goes out with the next stage's first products.  The fold of a
 // product (y += t * scale) runs under the third product after it.
+// A tile of up to 128 rows or outputs (the last of a ragged problem or expert) goes the same way
+// with half the work per wave: 384 rows of operands a stage and waves of 128 x 64 or 64 x 64.
 constexpr int BIG_KB = 2048;   // most blocks of inputs (LDS for the outputs' scales)
-template <int KIND, int NW>
-__global__ __launch_bounds__(NW * 64) void fp8_big_kernel(MmArgs a) {
-  constexpr int TM = 256, TN = 256, WN = NW / 2, FM = 8, FN = TN / WN / 16;
-  constexpr int STAGE = (TM + TN) * FB;
-  constexpr int LD = (TM + TN) / 8 / NW;   // copies per wave and stage: 4 of X, 4 of W
+constexpr int BIG = 256, BIG_STAGE = 2 * BIG * FB;
+struct BigLds {
+  uint8_t* lds;     // two stages
+  bool* lost;       // [BIG]
+  float* scs;       // [2][2][BIG]: the rows' scales (fp32: twice, so that every wave copies 64)
+  float* scw;       // [2][kb]: the outputs' scales
+};
+// Outputs n0 .. of the rows of t: xrows rows of X and ROWS - xrows of W, waves_n waves beside each
+// other.
+template <int KIND, int NW, int FM, int FN, int ROWS>
+__device__ __forceinline__ void big_tile(const MmArgs& a, const Tile& t, int n0, int xrows, int waves_n, const BigLds& m) {
+  constexpr int TM = BIG, STAGE = BIG_STAGE;
+  constexpr int LD = ROWS / 8 / NW;   // copies per wave and stage
   constexpr bool E8 = KIND == kMmaE8M0;
-  __shared__ __attribute__((aligned(128))) uint8_t lds[2 * STAGE];
-  __shared__ bool lost[TM];
-  __shared__ float scs[2][2][TM];   // the rows' scales (fp32: twice, so that every wave copies 64)
-  extern __shared__ float scw[];    // the outputs' scales: [2][kb]
+  uint8_t* const lds = m.lds;
+  bool* const lost = m.lost;
+  float* const scw = m.scw;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  int64_t mt;
-  int nt;
-  if (!ordered_tile(a.order, blockIdx.x, &mt, &nt)) return;
-  const int n0 = nt * TN;
-  const Tile t = find_tile<TM>(a, mt);
-  if (t.count <= 0) return;
+  const int ldx = xrows / 8 / NW;     // of them of X
 
   const int c = (lane & 7) ^ ((4 * wave + lane / 16) & 7);   // this lane's piece: the same in every copy
   const uint8_t* xbase = a.X + (a.rows == nullptr ? t.p0 * a.ldx : 0);
@@ -633,11 +638,11 @@ __global__ __launch_bounds__(NW * 64) void fp8_big_kernel(MmArgs a) {
 #pragma unroll
   for (int i = 0; i < LD; ++i) {
     const int r = (wave + NW * i) * 8 + lane / 8;
-    if (i < LD / 2) {
+    if (i < ldx) {
       const int64_t row = source_row(a, t.p0 + min(r, t.count - 1));   // none: row 0, and zeros at the end
       off[i] = static_cast<uint32_t>(max(a.rows == nullptr ? row - t.p0 : row, static_cast<int64_t>(0)) * a.ldx) + 16 * c;
     } else {
-      off[i] = static_cast<uint32_t>(min(r - TM, a.n - 1 - n0)) * static_cast<uint32_t>(a.k) + 16 * c;
+      off[i] = static_cast<uint32_t>(min(r - xrows, a.n - 1 - n0)) * static_cast<uint32_t>(a.k) + 16 * c;
     }
   }
   constexpr int SB = E8 ? 1 : 4;   // bytes of a scale
@@ -652,8 +657,9 @@ __global__ __launch_bounds__(NW * 64) void fp8_big_kernel(MmArgs a) {
   const unsigned lds0 = static_cast<unsigned>(reinterpret_cast<uintptr_t>(
       (__attribute__((address_space(3))) uint8_t*)lds));
   const bool cut = 16 * c >= a.k - (a.kb - 1) * FB;   // this lane's piece of the last stage lies past K
+  float(*const scs)[2][TM] = reinterpret_cast<float(*)[2][TM]>(m.scs);
   const unsigned scs0 = static_cast<unsigned>(reinterpret_cast<uintptr_t>(
-      (__attribute__((address_space(3))) float*)&scs[0][0][0]));
+      (__attribute__((address_space(3))) float*)m.scs));
   // the scales of the stage after the last call's.  fp32 ones go to LDS like the operands: loads
   // to registers between those copies cost 30 us of 400 at 8192 x 4096 x 14336
   auto issue_scales = [&](int s) {
@@ -667,7 +673,7 @@ __global__ __launch_bounds__(NW * 64) void fp8_big_kernel(MmArgs a) {
     const unsigned dst = lds0 + (s & 1) * STAGE + wave * 1024;
     const uint32_t back = s == a.kb - 1 && cut ? 16 * c : 0;   // the row's first piece instead; zeroed below
 #pragma unroll
-    for (int i = from; i < to; ++i) copy16_at(i < LD / 2 ? xb : wb, off[i] - back, dst + NW * i * 1024);
+    for (int i = from; i < to; ++i) copy16_at(i < ldx ? xb : wb, off[i] - back, dst + NW * i * 1024);
   };
   // the copies and scales of stage s have landed; the next barrier makes them visible
   auto land = [&](int s, bool last) {
@@ -685,9 +691,9 @@ __global__ __launch_bounds__(NW * 64) void fp8_big_kernel(MmArgs a) {
     asm volatile("" ::: "memory");
   };
 
-  const int wm = wave / WN, wn = wave % WN;
+  const int wm = wave / waves_n, wn = wave % waves_n;
   const int j = lane & 15, q = lane >> 4;
-  const int xr = wm * 16 * FM, wr = TM + wn * 16 * FN;
+  const int xr = wm * 16 * FM, wr = xrows + wn * 16 * FN;
   // pieces q and q + 4 of a row are this lane's 32 inputs (any order that both operands share):
   // the lanes that one LDS access serves together then meet no bank twice
   const int swz = (j >> 1) & 7;
@@ -714,8 +720,8 @@ __global__ __launch_bounds__(NW * 64) void fp8_big_kernel(MmArgs a) {
   }
   Operand<KIND> xf[4], wf[FN];   // row of blocks i in xf[i % 4]
   float sc[4], sw = 0.0f;
-  // Product p of a stage, p = 0 .. 31: rows of blocks 0 .. 4 one after another, then rows 5, 6
-  // and 7 together, output block by output block.
+  // Products of a stage: rows of blocks one after another, then the last three together, output
+  // block by output block.
   constexpr int LAST = 3, SPLIT = (FM - LAST) * FN;   // rows taken together, products before them
   constexpr int EARLY = LAST * FN / 2;                // copies issued with them, one after every second product
   auto row_at = [](int p) constexpr { return p < SPLIT ? p / FN : FM - LAST + (p - SPLIT) % LAST; };
@@ -742,7 +748,7 @@ __global__ __launch_bounds__(NW * 64) void fp8_big_kernel(MmArgs a) {
   // one stage; kMore: another follows, kIssue: and one after that (constants, so that the
   // loop's body has no branch)
   auto stage = [&](int s, auto kMore, auto kIssue) {
-    // rows 0 .. 4; row i + 3 is read meanwhile, one access after each product
+    // all rows but the last three; row i + 3 is read meanwhile, one access after each product
     static_for(std::make_integer_sequence<int, SPLIT>{}, [&](auto P) {
       constexpr int p = P, i = p / FN, h = p % FN;
       product(P);
@@ -765,7 +771,7 @@ __global__ __launch_bounds__(NW * 64) void fp8_big_kernel(MmArgs a) {
       sw1 = swp[s + 1];
       __builtin_amdgcn_sched_barrier(0);
     }
-    // rows 5, 6 and 7: a weight operand makes room for the next stage's after its third product
+    // the last three rows: a weight operand makes room for the next stage's after its third product
     static_for(std::make_integer_sequence<int, LAST * FN>{}, [&](auto Q) {
       constexpr int n = Q, h = n / LAST;
       product(std::integral_constant<int, SPLIT + n>{});
@@ -836,8 +842,11 @@ __global__ __launch_bounds__(NW * 64) void fp8_big_kernel(MmArgs a) {
       if (r >= t.count) continue;
       const uint4 w = none ? make_uint4(0, 0, 0, 0) : make_uint4(lo[0], hi[0], lo[1], hi[1]);
       const int o = n0 + wn * 16 * FN + 16 * (h + (q & 1)) + 8 * (q >> 1);
-      if (a.vec_y && o + 8 <= a.n) {
+      if (a.wide_y && o + 8 <= a.n) {
         *reinterpret_cast<uint4*>(out + o) = w;
+      } else if (a.vec_y && o + 8 <= a.n) {
+        *reinterpret_cast<uint2*>(out + o) = make_uint2(w.x, w.y);
+        *reinterpret_cast<uint2*>(out + o + 4) = make_uint2(w.z, w.w);
       } else {
         const uint32_t e[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
@@ -846,6 +855,26 @@ __global__ __launch_bounds__(NW * 64) void fp8_big_kernel(MmArgs a) {
       }
     }
   }
+}
+
+template <int KIND, int NW>
+__global__ __launch_bounds__(NW * 64) void fp8_big_kernel(MmArgs a) {
+  __shared__ __attribute__((aligned(128))) uint8_t lds[2 * BIG_STAGE];
+  __shared__ bool lost[BIG];
+  __shared__ float scs[2 * 2 * BIG];
+  extern __shared__ float scw[];
+  int64_t mt;
+  int nt;
+  if (!ordered_tile(a.order, blockIdx.x, &mt, &nt)) return;
+  const int n0 = nt * BIG;
+  const Tile t = find_tile<BIG>(a, mt);
+  if (t.count <= 0) return;
+  const BigLds m{lds, lost, scs, scw};
+  const bool few_rows = t.count <= BIG / 2;
+  if (few_rows || a.n - n0 <= BIG / 2)
+    big_tile<KIND, NW, 32 / NW, 4, BIG + BIG / 2>(a, t, n0, few_rows ? BIG / 2 : BIG, few_rows ? 4 : 2, m);
+  else
+    big_tile<KIND, NW, 8, 32 / NW, 2 * BIG>(a, t, n0, BIG, NW / 2, m);
 }
 
 gptq_status launch_big(MmArgs a, hipStream_t stream) {
@@ -1249,7 +1278,9 @@ gptq_status fp8_matmul_enqueue(const Fp8Problem& p, hipStream_t stream) {
   MmArgs a{};
   a.m = p.n_rows; a.n = p.n; a.k = p.k; a.kb = (p.k + FB - 1) / FB; a.nb = (p.n + FB - 1) / FB;
   a.x_rows = p.x_rows; a.W = p.W; a.ws = p.ws; a.Y = p.Y; a.ldy = p.ldy; a.y_dtype = p.y_dtype; a.e8 = p.e8;
-  a.vec_y = p.ldy % (p.y_dtype == GPTQ_F32 ? 4 : 8) == 0 && reinterpret_cast<uintptr_t>(p.Y) % 16 == 0;
+  const size_t yb = p.y_dtype == GPTQ_F32 ? 16 : 8;
+  a.vec_y = p.ldy % 4 == 0 && reinterpret_cast<uintptr_t>(p.Y) % yb == 0;
+  a.wide_y = p.ldy % 8 == 0 && reinterpret_cast<uintptr_t>(p.Y) % 16 == 0;
   a.off = p.offsets; a.rows = p.row_index; a.experts = p.batch;
   if (a.off != nullptr && (a.m / 16 + 1) * a.experts > INT32_MAX) return GPTQ_ERR_UNSUPPORTED;
   a.X = static_cast<const uint8_t*>(p.X);

@@ -565,3 +565,17 @@ def test_rows_without_a_source_are_zeros(n_rows, n, k, out, e8m0):
     few = lib().fp8_matmul_grouped(X, w, ws, torch.tensor([0, 1, 4, 5], device="cuda"), rows[:5].clamp(max=70).index_fill(
         0, torch.tensor([2], device="cuda"), -1), out_dtype=DT[out])
     assert bool((few[2] == 0).all())
+
+
+@pytest.mark.parametrize("e8m0", [False, True])
+@pytest.mark.parametrize("m,n,k", [(8200, 8256, 112), (4200, 4256, 384), (4353, 4225, 656)])
+def test_large_products_with_short_last_tiles(m, n, k, e8m0):
+    # the last tiles have few rows, few outputs, or both
+    q, s = random_operands(m, m, k, 1, e8m0)
+    w, ws = random_operands(n, n, k, 128, e8m0)
+    Y = lib().fp8_matmul(q, w, ws, s)
+    check_large(Y, wide(q, s, 1), wide(w, ws, 128), k, "bf16")
+    out = torch.full((m, n + 3), 2.5, dtype=torch.float16, device="cuda")
+    lib().fp8_matmul(q, w, ws, s, out_dtype=torch.float16, out=out[:, :n])
+    check_large(out[:, :n], wide(q, s, 1), wide(w, ws, 128), k, "f16")
+    assert bool((out[:, n:] == 2.5).all())
