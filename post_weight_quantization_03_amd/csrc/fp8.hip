@@ -428,11 +428,27 @@ __device__ __forceinline__ void store4(T* p, const float* v, int n, bool vec) {
   }
 }
 // four values as bf16 or fp16
-__device__ __forceinline__ uint2 pack16(f32x4 v, bool bf16) {
+template <bool kBf16>
+__device__ __forceinline__ uint2 pack16(f32x4 v) {
   uint16_t u[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) u[i] = bf16 ? from_f32<BF16>(v[i]).bits : from_f32<F16>(v[i]).bits;
+  for (int i = 0; i < 4; ++i) u[i] = kBf16 ? from_f32<BF16>(v[i]).bits : from_f32<F16>(v[i]).bits;
   return make_uint2(u[0] | static_cast<uint32_t>(u[1]) << 16, u[2] | static_cast<uint32_t>(u[3]) << 16);
+}
+// eight 16-bit outputs o .. o + 7, those below n
+__device__ __forceinline__ void store_narrow(const MmArgs& a, uint16_t* p, int o, uint4 v) {
+  if (a.vec_y && o + 8 <= a.n) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(v.x, v.y);
+    *reinterpret_cast<uint2*>(p + 4) = make_uint2(v.z, v.w);
+    return;
+  }
+  uint64_t lo = static_cast<uint64_t>(v.y) << 32 | v.x, hi = static_cast<uint64_t>(v.w) << 32 | v.z;
+#pragma unroll 1
+  for (int i = 0; i < 8 && o + i < a.n; ++i) {
+    p[i] = static_cast<uint16_t>(lo);
+    lo = lo >> 16 | hi << 48;
+    hi >>= 16;
+  }
 }
 // outputs o .. o + 3 of output row p
 __device__ __forceinline__ void store_y(const MmArgs& a, int64_t p, int o, const float* v) {
@@ -827,33 +843,36 @@ __device__ __forceinline__ void big_tile(const MmArgs& a, const Tile& t, int n0,
 #pragma unroll
       for (int r = 0; r < 4; ++r) y[i][h][r] = fmaf(td[p % 4][r], ts[p % 4], y[i][h][r]);
     });
-  // Of outputs 16 h + 4 q .. of two neighbouring h, lanes of odd and even q exchange one each: a
-  // lane then stores 8 in 16 bytes, and four lanes 64 bytes of a row in one piece
+  // Of outputs 16 h + 4 q .. of two neighbouring h, lanes of odd and even q exchange one each (they
+  // are of one row): a lane then stores 8 in 16 bytes, and four lanes 64 bytes of a row in one
+  // piece.  The code is short because it runs once a tile, from outside the instruction cache.
+  const int o0 = n0 + wn * 16 * FN + 16 * (q & 1) + 8 * (q >> 1);
+  const bool wide = a.wide_y && n0 + (wn + 1) * 16 * FN <= a.n;
+  auto store = [&](auto kBf16, auto kWide) {
+    uint16_t* out = static_cast<uint16_t*>(a.Y) + (t.p0 + xr + j) * a.ldy + o0;
 #pragma unroll
-  for (int i = 0; i < FM; ++i) {
-    const int r = xr + 16 * i + j;
-    const bool none = lost[r];
-    uint16_t* out = static_cast<uint16_t*>(a.Y) + (t.p0 + r) * a.ldy;
+    for (int i = 0; i < FM; ++i) {
+      if (xr + 16 * i + j < t.count) {
+        const bool none = lost[xr + 16 * i + j];
 #pragma unroll
-    for (int h = 0; h < FN; h += 2) {
-      const uint2 u = pack16(y[i][h], a.y_dtype == GPTQ_BF16), v = pack16(y[i][h + 1], a.y_dtype == GPTQ_BF16);
-      const auto lo = __builtin_amdgcn_permlane16_swap(u.x, v.x, false, false);
-      const auto hi = __builtin_amdgcn_permlane16_swap(u.y, v.y, false, false);
-      if (r >= t.count) continue;
-      const uint4 w = none ? make_uint4(0, 0, 0, 0) : make_uint4(lo[0], hi[0], lo[1], hi[1]);
-      const int o = n0 + wn * 16 * FN + 16 * (h + (q & 1)) + 8 * (q >> 1);
-      if (a.wide_y && o + 8 <= a.n) {
-        *reinterpret_cast<uint4*>(out + o) = w;
-      } else if (a.vec_y && o + 8 <= a.n) {
-        *reinterpret_cast<uint2*>(out + o) = make_uint2(w.x, w.y);
-        *reinterpret_cast<uint2*>(out + o + 4) = make_uint2(w.z, w.w);
-      } else {
-        const uint32_t e[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int x = 0; x < 8; ++x)
-          if (o + x < a.n) out[o + x] = static_cast<uint16_t>(e[x / 2] >> (16 * (x & 1)));
+        for (int h = 0; h < FN; h += 2) {
+          const uint2 u = pack16<kBf16>(y[i][h]), v = pack16<kBf16>(y[i][h + 1]);
+          const auto lo = __builtin_amdgcn_permlane16_swap(u.x, v.x, false, false);
+          const auto hi = __builtin_amdgcn_permlane16_swap(u.y, v.y, false, false);
+          const uint4 w = none ? make_uint4(0, 0, 0, 0) : make_uint4(lo[0], hi[0], lo[1], hi[1]);
+          if constexpr (kWide) *reinterpret_cast<uint4*>(out + 16 * h) = w;
+          else store_narrow(a, out + 16 * h, o0 + 16 * h, w);
+        }
       }
+      out += 16 * a.ldy;
     }
+  };
+  if (a.y_dtype == GPTQ_BF16) {
+    if (wide) store(yes, yes);
+    else store(yes, no);
+  } else {
+    if (wide) store(no, yes);
+    else store(no, no);
   }
 }
 
