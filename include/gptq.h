@@ -308,7 +308,9 @@ gptq_status gptq_w4a16_matmul(int m, int d_out, int d_in, int n_groups, gptq_dty
  * fp32 with row stride ldx (>= cols) and batch stride batch_stride_x; Q is dense uint8
  * [batch, rows, cols] and 16-byte aligned; the scale of block (i, j) of problem e is element
  * e * batch_stride_s + i * ld_s_row + j * ld_s_block of `scales` (fp32 or E8M0 bytes).
- * Requires cols % 16 == 0; rows may be 0 (no-op).
+ * Requires cols % 16 == 0; rows may be 0 (no-op); more than 2^24 - 1 rows of 2048 or more
+ * columns (8 times as many shorter ones), or more than 65535 problems, are refused
+ * (GPTQ_ERR_UNSUPPORTED).
  */
 gptq_status gptq_fp8_quantize(int batch, int64_t rows, int cols, gptq_dtype x_dtype, const void* X,
                               int64_t ldx, int64_t batch_stride_x, int block_rows,
@@ -331,7 +333,9 @@ gptq_status gptq_fp8_quantize(int batch, int64_t rows, int cols, gptq_dtype x_dt
  * the largest among 8 consecutive inputs, and sums of blocks are fp32, rounded once.  The
  * product xs * ws of any two scales has to be a normal fp32 number (or its block's products
  * zero).  workspace: gptq_workspace_size(GPTQ_WS_FP8_MATMUL, batch = 1, d_out, d_in,
- * n_tokens_hint = m, NULL) bytes, 16-byte aligned.  Requires d_in % 16 == 0, d_out >= 1; m may be 0 (no-op).
+ * n_tokens_hint = m, NULL) bytes, 16-byte aligned; it serves one call at a time.  Requires
+ * d_in % 16 == 0, d_out >= 1; m may be 0 (no-op); more than 2^22 tiles of the kernel that fits the
+ * sizes (64 x 64 to 256 x 256 outputs) are refused (GPTQ_ERR_UNSUPPORTED).
  */
 gptq_status gptq_fp8_matmul(int64_t m, int d_out, int d_in, gptq_dtype x_dtype, const void* X,
                             int64_t ldx, gptq_dtype s_dtype, const void* x_scales,

@@ -169,6 +169,7 @@ __global__ __launch_bounds__(256) void quant_rows_kernel(QuantArgs a) {
 }
 
 // 128 x 128 blocks: one workgroup per block, 64 values per thread (4 rows of 16) in registers.
+// Bound by memory (64 x 1408 x 2048 in bf16: 108 us, 5.1 TB/s).
 template <typename T, bool E8, bool kVec>
 __global__ __launch_bounds__(256) void quant_tile_kernel(QuantArgs a) {
   __shared__ uint32_t tops[4];
@@ -508,7 +509,8 @@ __device__ __forceinline__ void wait_copies() { __builtin_amdgcn_s_waitcnt(0xF70
 // Tiles of TM rows x TN outputs, WM x WN waves.  A stage is one block of 128 inputs: TM + TN
 // rows of 128 bytes in LDS, two buffers, the next stage's copies in flight during this one's
 // products.  The 16-byte piece c of row r lies at c ^ (r / 2 % 8), so that 16 lanes reading
-// the same piece of 16 rows cover all 64 banks.
+// the same piece of 16 rows cover all 64 banks.  Bound by LDS reads and copies; two workgroups
+// per CU cover each other's waits (4096 x 4096 at 1024 rows: 42 us, 0.82 PFLOP/s).
 template <int TM, int TN, int WM, int WN, int KIND>
 __global__ __launch_bounds__(WM* WN * 64) void fp8_tile_kernel(MmArgs a) {
   constexpr int NW = WM * WN, NT = NW * 64;
@@ -617,11 +619,13 @@ gptq_status launch_tile(MmArgs a, hipStream_t stream) {
 }
 
 // The same product for large problems: 256 x 256 tiles, 8 waves of 128 x 64 (8 x 4 blocks of
-// 16 x 16), one workgroup per CU.  Two buffers of 64 KB; operands go global -> LDS with a
+// 16 x 16) or, with E8M0 scales, which leave no folds to do meanwhile, 4 of 128 x 128 (8192 x 4096 x
+// 14336: 402 us = 2.39 PFLOP/s, and 358 = 2.69, which 8 waves take 382 for); one workgroup per CU.
+// Bound by the matrix cores (67% busy).  Two buffers of 64 KB; operands go global -> LDS with a
 // scalar base that moves by 128 bytes a stage and one 32-bit offset per lane and copy, so that
 // a stage's copies cost little vector arithmetic.  Before a wave's last three rows of blocks it
 // has read all it needs of the stage: there the workgroup waits for the next stage's copies, and
-// the last 12 products cover the first reads of the next stage and half of the copies of the one
+// the products of these rows cover the first reads of the next stage and half of the copies of the one
 // after it; the other half goes out with the next stage's first products.  The fold of a
 // product (y += t * scale) runs under the third product after it.
 // A tile of up to 128 rows or outputs (the last of a ragged problem or expert) goes the same way
@@ -1203,8 +1207,8 @@ gptq_status launch_rows(MmArgs a, hipStream_t stream) {
 //   tile  128 x 128, one workgroup per CU 1.17 us, two 1.5
 //         (4096 x 4096: 42 us at 1024 rows, mid 44, big 48)
 //   big   256 x 256, a round 1.4 us on up to half of the CUs, else 1.85
-//         (4096 x 4096: 51 us at 2048 rows, tile 54; 67 at 4096, tile 104; 49152 rows of 64
-//         experts: 228, tile 299)
+//         (4096 x 4096: 48 us at 2048 rows, tile 54; 67 at 4096, tile 100; 49152 rows of 64
+//         experts: 195 to 200, tile 280 to 298)
 // Grouped problems have about half a tile more per expert, and every kernel needs the time to
 // read the weights once (5 TB/s).  The large tiles are not built for fp32 Y (their operands would
 // not fit the registers) and address a tile's rows by 32-bit offsets.

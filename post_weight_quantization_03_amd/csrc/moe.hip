@@ -442,7 +442,7 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
 // row of 16 lanes, four at a time per wave, PER experts per lane.  A group is 16 / G lanes, each
 // with `each` of its experts; everything between the lanes of a row is data-parallel moves, so
 // that the four tokens' chains run side by side where the kernel above waits for each step
-// (16384 tokens of 256 experts in 8 groups: 34 us there).  Values and results are the same; the
+// (16384 tokens of 256 experts in 8 groups: 17 us, and 34 there).  Values and results are the same; the
 // check of two choice values takes 2^-18, since keys give 4 bits to their number.
 // Batcher's merging network, largest first.
 template <int N>
@@ -694,7 +694,8 @@ __global__ __launch_bounds__(GR_NT) void group_count_kernel(const int32_t* __res
 // the start of its expert + the expert's slots in earlier chunks + in earlier waves of this
 // chunk + earlier in its wave (64 slots at a time: equal ids found by one ballot per bit).  Every
 // workgroup adds up the counts of all chunks for itself (up to 64 numbers per expert), which
-// saves a launch; no order of atomics reaches the result.
+// saves a launch; no order of atomics reaches the result.  Bound by latency (131072 slots of 256
+// experts: 2.9 us to count and 7.7 to place; 24 slots: 3.1).
 __global__ __launch_bounds__(GR_NT) void group_place_kernel(const int32_t* __restrict__ ids, int64_t slots, int chunk,
                                                             int E, int k, const int32_t* __restrict__ counts,
                                                             int64_t* __restrict__ offsets,
@@ -832,6 +833,7 @@ __device__ __forceinline__ F16 from_f32<F16>(float v) {
 }
 
 // One thread per V consecutive outputs of a token: V = 16 bytes where rows are aligned, else 1.
+// Bound by memory (16384 tokens of 6 x 2048 in bf16: 95 us, 4.95 TB/s).
 template <typename T, int V>
 __global__ __launch_bounds__(256) void combine_kernel(int64_t n_tokens, int k, int64_t n_rows, int d, const T* Y,
                                                       int64_t ldy, const int32_t* place, const float* weights, T* out,
