@@ -335,7 +335,7 @@ gptq_status gptq_fp8_quantize(int batch, int64_t rows, int cols, gptq_dtype x_dt
  * zero).  workspace: gptq_workspace_size(GPTQ_WS_FP8_MATMUL, batch = 1, d_out, d_in,
  * n_tokens_hint = m, NULL) bytes, 16-byte aligned; it serves one call at a time.  Requires
  * d_in % 16 == 0, d_out >= 1; m may be 0 (no-op); more than 2^22 tiles of the kernel that fits the
- * sizes (64 x 64 to 256 x 256 outputs) are refused (GPTQ_ERR_UNSUPPORTED).
+ * sizes (16 x 16 to 256 x 256 outputs) are refused (GPTQ_ERR_UNSUPPORTED).
  */
 gptq_status gptq_fp8_matmul(int64_t m, int d_out, int d_in, gptq_dtype x_dtype, const void* X,
                             int64_t ldx, gptq_dtype s_dtype, const void* x_scales,

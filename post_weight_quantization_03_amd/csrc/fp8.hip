@@ -230,27 +230,27 @@ gptq_status launch_quant_t(const QuantArgs& a, int batch, int block_rows, bool e
 // ---------------------------------------------------------------------------- product
 
 // Which tile a workgroup takes.  Workgroups go to the 8 XCDs in turn, 32 CUs each; tiles are
-// numbered in bands of 4 tile rows, column by column, and an XCD takes runs of consecutive ones
-// (32, or an eighth of a small grid): the 32 tiles it works on at once are then 4 x 8 and read 12
-// operand panels through its L2 instead of the 18 of a row-by-row grid.
+// numbered in bands of 4 tile rows, column by column, and an XCD takes runs of 32 consecutive ones:
+// the 32 tiles it works on at once are then 4 x 8 and read 12 operand panels through its L2 instead
+// of the 18 of a row-by-row grid.  What is left of whole rounds of 256 is shared out evenly (in
+// runs of 32 some XCDs had 32 tiles more than others: 5000 x 5000 x 4096 116 us, 108 so; runs of 8
+// throughout: 111 there, but 8192 x 4096 x 14336 413 instead of 405).
 struct TileOrder {
   int tiles_n;
-  int64_t tiles_m, total, run;
+  int64_t tiles_m;
 };
-inline TileOrder tile_order(int64_t tiles_m, int tiles_n) {
-  const int64_t total = tiles_m * tiles_n;
-  return {tiles_n, tiles_m, total, std::min<int64_t>(32, (total + 7) / 8)};
-}
-inline int64_t order_grid(const TileOrder& o) { return (o.total + 8 * o.run - 1) / (8 * o.run) * 8 * o.run; }
+inline int64_t order_grid(const TileOrder& o) { return (o.tiles_m * o.tiles_n + 7) / 8 * 8; }
 // (tile row, tile column) of workgroup b; false for none
 __device__ __forceinline__ bool ordered_tile(const TileOrder& o, uint32_t b, int64_t* mt, int* nt) {
-  const uint32_t slot = b / 8, run = static_cast<uint32_t>(o.run);
-  const int64_t p = (static_cast<int64_t>(slot / run) * 8 + b % 8) * run + slot % run;
-  if (p >= o.total) return false;
+  const uint32_t total = static_cast<uint32_t>(o.tiles_m) * static_cast<uint32_t>(o.tiles_n);   // at most 2^22
+  const uint32_t whole = total & ~255u, run = b < whole ? 32 : (total - whole + 7) / 8;
+  const uint32_t first = b < whole ? b & ~255u : whole, slot = b - first;
+  const uint32_t p = first + slot % 8 * run + slot / 8;
+  if (slot / 8 >= run || p >= total) return false;
   const uint32_t per = 4u * static_cast<uint32_t>(o.tiles_n);
-  const uint32_t band = static_cast<uint32_t>(p) / per, r = static_cast<uint32_t>(p) % per;
-  const uint32_t rows = static_cast<uint32_t>(min(static_cast<int64_t>(4), o.tiles_m - 4 * static_cast<int64_t>(band)));
-  *mt = 4 * static_cast<int64_t>(band) + r % rows;
+  const uint32_t band = p / per, r = p % per;
+  const uint32_t rows = min(4u, static_cast<uint32_t>(o.tiles_m) - 4 * band);
+  *mt = 4 * band + r % rows;
   *nt = static_cast<int>(r / rows);
   return true;
 }
@@ -901,8 +901,7 @@ __global__ __launch_bounds__(NW * 64) void fp8_big_kernel(MmArgs a) {
 }
 
 gptq_status launch_big(MmArgs a, hipStream_t stream) {
-  a.order = tile_order(a.off == nullptr ? (a.m + 255) / 256 : a.m / 256 + std::min<int64_t>(a.experts, a.m),
-                       (a.n + 255) / 256);
+  a.order = {(a.n + 255) / 256, a.off == nullptr ? (a.m + 255) / 256 : a.m / 256 + std::min<int64_t>(a.experts, a.m)};
   const int64_t grid = order_grid(a.order);
   if (grid > (1 << 22)) return GPTQ_ERR_UNSUPPORTED;
   const dim3 g(static_cast<unsigned>(grid));
@@ -1052,8 +1051,7 @@ gptq_status launch_mid_groups(const MmArgs& a, unsigned grid, hipStream_t stream
 }
 
 gptq_status launch_mid(MmArgs a, hipStream_t stream) {
-  a.order = tile_order(a.off == nullptr ? (a.m + 63) / 64 : a.m / 64 + std::min<int64_t>(a.experts, a.m),
-                       (a.n + 63) / 64);
+  a.order = {(a.n + 63) / 64, a.off == nullptr ? (a.m + 63) / 64 : a.m / 64 + std::min<int64_t>(a.experts, a.m)};
   const int64_t grid = order_grid(a.order);
   if (grid > (1 << 22)) return GPTQ_ERR_UNSUPPORTED;
   if (mid_groups(a.kb, static_cast<double>(grid)) == 2) return launch_mid_groups<2>(a, static_cast<unsigned>(grid), stream);

@@ -579,3 +579,13 @@ def test_large_products_with_short_last_tiles(m, n, k, e8m0):
     lib().fp8_matmul(q, w, ws, s, out_dtype=torch.float16, out=out[:, :n])
     check_large(out[:, :n], wide(q, s, 1), wide(w, ws, 128), k, "f16")
     assert bool((out[:, n:] == 2.5).all())
+
+
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("e8m0", [False, True])
+@pytest.mark.parametrize("m", [5, 100])
+def test_inputs_past_the_scales_that_fit_lds(m, e8m0, out):
+    n, k = 130, 28816
+    q, s = random_operands(m, m, k, 1, e8m0)
+    w, ws = random_operands(n, n, k, 128, e8m0)
+    check_large(lib().fp8_matmul(q, w, ws, s, out_dtype=DT[out]), wide(q, s, 1), wide(w, ws, 128), k, out)
