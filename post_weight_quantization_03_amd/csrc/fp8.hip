@@ -268,8 +268,6 @@ struct MmArgs {
   int64_t ldy;
   int y_dtype;
   bool e8;               // scales are E8M0
-  bool vec_y;            // rows of Y take 4 values in one store
-  bool wide_y;           // and 8 of 16 bits
   const int64_t* off;    // grouped: the experts' ranges
   const int32_t* rows;   // grouped: rows of X, or null
   int experts;
@@ -417,15 +415,17 @@ __device__ __forceinline__ float load_ws(const MmArgs& a, int e, int ob, int b) 
   return load_scale<KIND>(a, a.ws, (static_cast<int64_t>(e) * a.nb + ob) * a.kb + b);
 }
 
+// Rows of Y may start at any element: the chip takes 16-byte stores at any address (2443 x 6075 x
+// 5664, whose rows are of odd length: 98 us, 119 by single values).
 template <typename T>
-__device__ __forceinline__ void store4(T* p, const float* v, int n, bool vec) {
-  if (vec && n >= 4) {
+__device__ __forceinline__ void store4(T* p, const float* v, int n) {
+  if (n >= 4) {
     Vec<T, 4> o;
 #pragma unroll
     for (int i = 0; i < 4; ++i) o.v[i] = from_f32<T>(v[i]);
-    *reinterpret_cast<Vec<T, 4>*>(p) = o;
+    __builtin_memcpy(p, &o, sizeof(o));
   } else {
-    for (int i = 0; i < min(n, 4); ++i) p[i] = from_f32<T>(v[i]);
+    for (int i = 0; i < n; ++i) p[i] = from_f32<T>(v[i]);
   }
 }
 // four values as bf16 or fp16
@@ -438,9 +438,8 @@ __device__ __forceinline__ uint2 pack16(f32x4 v) {
 }
 // eight 16-bit outputs o .. o + 7, those below n
 __device__ __forceinline__ void store_narrow(const MmArgs& a, uint16_t* p, int o, uint4 v) {
-  if (a.vec_y && o + 8 <= a.n) {
-    *reinterpret_cast<uint2*>(p) = make_uint2(v.x, v.y);
-    *reinterpret_cast<uint2*>(p + 4) = make_uint2(v.z, v.w);
+  if (o + 8 <= a.n) {
+    __builtin_memcpy(p, &v, sizeof(v));
     return;
   }
   uint64_t lo = static_cast<uint64_t>(v.y) << 32 | v.x, hi = static_cast<uint64_t>(v.w) << 32 | v.z;
@@ -456,9 +455,9 @@ __device__ __forceinline__ void store_y(const MmArgs& a, int64_t p, int o, const
   const int n = a.n - o;
   if (n <= 0) return;
   const int64_t i = p * a.ldy + o;
-  if (a.y_dtype == GPTQ_F32) store4(static_cast<float*>(a.Y) + i, v, n, a.vec_y);
-  else if (a.y_dtype == GPTQ_BF16) store4(static_cast<BF16*>(a.Y) + i, v, n, a.vec_y);
-  else store4(static_cast<F16*>(a.Y) + i, v, n, a.vec_y);
+  if (a.y_dtype == GPTQ_F32) store4(static_cast<float*>(a.Y) + i, v, n);
+  else if (a.y_dtype == GPTQ_BF16) store4(static_cast<BF16*>(a.Y) + i, v, n);
+  else store4(static_cast<F16*>(a.Y) + i, v, n);
 }
 
 // One wave copies 64 16-byte pieces to LDS: lane l's bytes land at base + 16 l (base uniform).
@@ -851,7 +850,7 @@ __device__ __forceinline__ void big_tile(const MmArgs& a, const Tile& t, int n0,
   // are of one row): a lane then stores 8 in 16 bytes, and four lanes 64 bytes of a row in one
   // piece.  The code is short because it runs once a tile, from outside the instruction cache.
   const int o0 = n0 + wn * 16 * FN + 16 * (q & 1) + 8 * (q >> 1);
-  const bool wide = a.wide_y && n0 + (wn + 1) * 16 * FN <= a.n;
+  const bool wide = n0 + (wn + 1) * 16 * FN <= a.n;
   auto store = [&](auto kBf16, auto kWide) {
     uint16_t* out = static_cast<uint16_t*>(a.Y) + (t.p0 + xr + j) * a.ldy + o0;
 #pragma unroll
@@ -864,7 +863,7 @@ __device__ __forceinline__ void big_tile(const MmArgs& a, const Tile& t, int n0,
           const auto lo = __builtin_amdgcn_permlane16_swap(u.x, v.x, false, false);
           const auto hi = __builtin_amdgcn_permlane16_swap(u.y, v.y, false, false);
           const uint4 w = none ? make_uint4(0, 0, 0, 0) : make_uint4(lo[0], hi[0], lo[1], hi[1]);
-          if constexpr (kWide) *reinterpret_cast<uint4*>(out + 16 * h) = w;
+          if constexpr (kWide) __builtin_memcpy(out + 16 * h, &w, sizeof(w));
           else store_narrow(a, out + 16 * h, o0 + 16 * h, w);
         }
       }
@@ -1299,9 +1298,6 @@ gptq_status fp8_matmul_enqueue(const Fp8Problem& p, hipStream_t stream) {
   MmArgs a{};
   a.m = p.n_rows; a.n = p.n; a.k = p.k; a.kb = (p.k + FB - 1) / FB; a.nb = (p.n + FB - 1) / FB;
   a.x_rows = p.x_rows; a.W = p.W; a.ws = p.ws; a.Y = p.Y; a.ldy = p.ldy; a.y_dtype = p.y_dtype; a.e8 = p.e8;
-  const size_t yb = p.y_dtype == GPTQ_F32 ? 16 : 8;
-  a.vec_y = p.ldy % 4 == 0 && reinterpret_cast<uintptr_t>(p.Y) % yb == 0;
-  a.wide_y = p.ldy % 8 == 0 && reinterpret_cast<uintptr_t>(p.Y) % 16 == 0;
   a.off = p.offsets; a.rows = p.row_index; a.experts = p.batch;
   if (a.off != nullptr && (a.m / 16 + 1) * a.experts > INT32_MAX) return GPTQ_ERR_UNSUPPORTED;
   a.X = static_cast<const uint8_t*>(p.X);
