@@ -856,51 +856,59 @@ __device__ __forceinline__ F16 from_f32<F16>(float v) {
   return F16{__builtin_bit_cast(uint16_t, static_cast<_Float16>(v))};
 }
 
-// One thread per V consecutive outputs of a token: V = 16 bytes where rows are aligned, else 1.
-// Bound by memory (16384 tokens of 6 x 2048 in bf16: 95 us, 4.95 TB/s).
+// V neighbouring outputs of one token.
 template <typename T, int V>
-__global__ __launch_bounds__(256) void combine_kernel(int64_t n_tokens, int k, int64_t n_rows, int d, const T* Y,
-                                                      int64_t ldy, const int32_t* place, const float* weights, T* out,
-                                                      int64_t ldo) {
-  const int per = (d + V - 1) / V;
-  const int64_t i = (static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x) * 256 + threadIdx.x;
-  const int64_t t = i / per;
-  if (t >= n_tokens) return;
-  const int64_t col = (i - t * per) * V;
+__device__ __forceinline__ void combine_piece(int k, int64_t n_rows, const T* Y, int64_t ldy, const int32_t* place,
+                                              const float* weights, T* out) {
   float acc[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) acc[v] = 0.0f;
   for (int j = 0; j < k; ++j) {
-    const int p = place[t * k + j];
+    const int p = place[j];
     if (p < 0 || p >= n_rows) continue;
-    const float w = weights[t * k + j];
-    const Vec<T, V> y = *reinterpret_cast<const Vec<T, V>*>(Y + p * ldy + col);
+    const float w = weights[j];
+    T y[V];
+    __builtin_memcpy(y, Y + p * ldy, sizeof(y));
 #pragma unroll
-    for (int v = 0; v < V; ++v) acc[v] = fmaf(w, load_as_f32(&y.v[v]), acc[v]);
+    for (int v = 0; v < V; ++v) acc[v] = fmaf(w, load_as_f32(&y[v]), acc[v]);
   }
-  Vec<T, V> o;
+  T o[V];
 #pragma unroll
-  for (int v = 0; v < V; ++v) o.v[v] = from_f32<T>(acc[v]);
-  *reinterpret_cast<Vec<T, V>*>(out + t * ldo + col) = o;
+  for (int v = 0; v < V; ++v) o[v] = from_f32<T>(acc[v]);
+  __builtin_memcpy(out, o, sizeof(o));
+}
+
+// One thread per 16 bytes of a token's outputs; the chip loads and stores 16 bytes at any address,
+// so rows may start at any element.  Bound by memory (16384 tokens of 6 x 2048 in bf16: 95 us, 4.95
+// TB/s; of 6 x 2047: 101 us, 352 by single values).
+template <typename T>
+__global__ __launch_bounds__(256) void combine_kernel(int64_t n_tokens, int k, int64_t n_rows, int d, const T* Y,
+                                                      int64_t ldy, const int32_t* place, const float* weights, T* out,
+                                                      int64_t ldo) {
+  constexpr int V = 16 / sizeof(T);
+  const int per = (d + V - 1) / V;
+  const int64_t i = (static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x) * 256 + threadIdx.x;
+  const int64_t t = i / per;
+  if (t >= n_tokens) return;
+  // a row's last piece ends with the row: outputs that it shares with the one before get equal values
+  const int64_t col = max(min((i - t * per) * V, static_cast<int64_t>(d) - V), static_cast<int64_t>(0));
+  if (d >= V) combine_piece<T, V>(k, n_rows, Y + col, ldy, place + t * k, weights + t * k, out + t * ldo + col);
+  else
+    for (int v = 0; v < d; ++v)
+      combine_piece<T, 1>(k, n_rows, Y + v, ldy, place + t * k, weights + t * k, out + t * ldo + v);
 }
 
 template <typename T>
 gptq_status launch_combine(int64_t n_tokens, int k, int64_t n_rows, int d, const void* Y, int64_t ldy,
                            const int32_t* place, const float* weights, void* out, int64_t ldo, hipStream_t stream) {
   constexpr int V = 16 / sizeof(T);
-  const bool wide = d % V == 0 && ldy % V == 0 && ldo % V == 0 && reinterpret_cast<uintptr_t>(Y) % 16 == 0 &&
-                    reinterpret_cast<uintptr_t>(out) % 16 == 0;
-  const int64_t n = n_tokens * (wide ? d / V : d);
   // a launch's threads along x stay below 2^32
-  const int64_t blocks = (n + 255) / 256, gx = std::min<int64_t>(blocks, 1 << 22), gy = (blocks + gx - 1) / gx;
+  const int64_t blocks = (n_tokens * ((d + V - 1) / V) + 255) / 256;
+  const int64_t gx = std::min<int64_t>(blocks, 1 << 22), gy = (blocks + gx - 1) / gx;
   if (gy > 65535) return GPTQ_ERR_UNSUPPORTED;
   const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(gy)), block(256);
-  if (wide)
-    GPTQ_LAUNCH((combine_kernel<T, V>), grid, block, 0, stream, n_tokens, k, n_rows, d, static_cast<const T*>(Y), ldy,
-                place, weights, static_cast<T*>(out), ldo);
-  else
-    GPTQ_LAUNCH((combine_kernel<T, 1>), grid, block, 0, stream, n_tokens, k, n_rows, d, static_cast<const T*>(Y), ldy,
-                place, weights, static_cast<T*>(out), ldo);
+  GPTQ_LAUNCH((combine_kernel<T>), grid, block, 0, stream, n_tokens, k, n_rows, d, static_cast<const T*>(Y), ldy, place,
+              weights, static_cast<T*>(out), ldo);
   return GPTQ_OK;
 }
 

@@ -312,3 +312,21 @@ def test_combine_past_32_bit_elements():
     for i, v in zip(at, (1, 2, 3, 4, 3)):
         assert bool((out[i] == v).all())
     assert int(out.any(1).sum()) == len(at)
+
+
+@pytest.mark.parametrize("d", [1, 3, 4, 5, 7, 8, 9, 15, 17])
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_combine_short_rows(d, dtype):
+    # rows shorter and little longer than 16 bytes, of any alignment
+    rng = np.random.default_rng(d)
+    y = torch.from_numpy(rng.standard_normal((40, d + 1))).to(DT[dtype]).cuda()
+    place = rng.integers(-1, 41, (21, 3)).astype(np.int32)
+    w = torch.from_numpy(rng.standard_normal((21, 3))).float().cuda()
+    out = torch.full((21, d + 2), 7.0, dtype=DT[dtype], device="cuda")
+    lib().moe_combine(y[:, 1:], torch.from_numpy(place).cuda(), w, out=out[:, 1:d + 1])
+    ref, size = M.ref_combine(y[:, 1:].double().cpu().numpy(), place, w.cpu().numpy())
+    err = np.abs(out[:, 1:d + 1].double().cpu().numpy() - ref)
+    # the bound of test_combine
+    assert (err <= torch.finfo(DT[dtype]).eps / 2 * np.abs(ref) * (1 + 3 * 2.0 ** -24) + 3 * 2.0 ** -24 * size
+            + (2.0 ** -25 if dtype == "f16" else 0)).all()
+    assert bool((out[:, 0] == 7).all()) and bool((out[:, d + 1] == 7).all())
