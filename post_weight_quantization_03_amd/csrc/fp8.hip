@@ -48,16 +48,13 @@ struct alignas(sizeof(T) * V) Vec {
   T v[V];
 };
 
-// N consecutive elements as fp32; 16-byte loads where rows are aligned.
-template <typename T, int N, bool kVec>
+// N consecutive elements as fp32, in 16-byte loads, which the chip takes at any address.
+template <typename T, int N>
 __device__ __forceinline__ void load_row(const T* p, float* x) {
-  constexpr int V = kVec ? 16 / sizeof(T) : 1;
+  T w[N];
+  __builtin_memcpy(w, p, sizeof(w));
 #pragma unroll
-  for (int i = 0; i < N; i += V) {
-    const Vec<T, V> w = *reinterpret_cast<const Vec<T, V>*>(p + i);
-#pragma unroll
-    for (int j = 0; j < V; ++j) x[i + j] = load_as_f32(&w.v[j]);
-  }
+  for (int i = 0; i < N; ++i) x[i] = load_as_f32(&w[i]);
 }
 
 // The larger of |x| as bits: orders all finite values, infinity and NaN above them.
@@ -149,7 +146,7 @@ __device__ __forceinline__ void store_scale(const QuantArgs& a, int64_t i, Scale
 // Bound by memory.  32 blocks of one row are 8 KB in one piece (8192 x 4096 in bf16: 20.2 us, 5.0
 // TB/s, a copy's rate here; one block of 32 rows 25.9 us although its scales leave in one
 // piece); rows of fewer than 16 blocks take 4.
-template <typename T, bool E8, bool kVec, int QB>
+template <typename T, bool E8, int QB>
 __global__ __launch_bounds__(256) void quant_rows_kernel(QuantArgs a) {
   const int u = threadIdx.x / 8, b = blockIdx.y * QB + u % QB;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * (32 / QB) + u / QB;
@@ -158,7 +155,7 @@ __global__ __launch_bounds__(256) void quant_rows_kernel(QuantArgs a) {
   float x[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i) x[i] = 0.0f;
-  if (live) load_row<T, 16, kVec>(static_cast<const T*>(a.X) + blockIdx.z * a.bsx + row * a.ldx + col, x);
+  if (live) load_row<T, 16>(static_cast<const T*>(a.X) + blockIdx.z * a.bsx + row * a.ldx + col, x);
   const uint32_t top = eight_lanes_max(top_bits<16>(x));
   if (!live) return;
   const Scale sc = block_scale<E8>(top);
@@ -170,7 +167,7 @@ __global__ __launch_bounds__(256) void quant_rows_kernel(QuantArgs a) {
 
 // 128 x 128 blocks: one workgroup per block, 64 values per thread (4 rows of 16) in registers.
 // Bound by memory (64 x 1408 x 2048 in bf16: 108 us, 5.1 TB/s).
-template <typename T, bool E8, bool kVec>
+template <typename T, bool E8>
 __global__ __launch_bounds__(256) void quant_tile_kernel(QuantArgs a) {
   __shared__ uint32_t tops[4];
   const int b = blockIdx.y;
@@ -183,7 +180,7 @@ __global__ __launch_bounds__(256) void quant_tile_kernel(QuantArgs a) {
 #pragma unroll
     for (int j = 0; j < 16; ++j) x[i][j] = 0.0f;
     if (row0 + 32 * i < a.rows && col < a.cols)
-      load_row<T, 16, kVec>(static_cast<const T*>(a.X) + blockIdx.z * a.bsx + (row0 + 32 * i) * a.ldx + col, x[i]);
+      load_row<T, 16>(static_cast<const T*>(a.X) + blockIdx.z * a.bsx + (row0 + 32 * i) * a.ldx + col, x[i]);
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) top = max(top, top_bits<16>(x[i]));
@@ -203,28 +200,22 @@ __global__ __launch_bounds__(256) void quant_tile_kernel(QuantArgs a) {
   if (threadIdx.x == 0) store_scale<E8>(a, blockIdx.z * a.bss + blockIdx.x * a.lsr + b * a.lsb, sc);
 }
 
-template <typename T, bool E8, bool kVec>
+template <typename T, bool E8>
 gptq_status launch_quant(const QuantArgs& a, int batch, int block_rows, hipStream_t stream) {
   const int64_t kb = (a.cols + FB - 1) / FB;
   const int qb = block_rows == FB ? 1 : kb >= 16 ? 32 : 4, qr = block_rows == FB ? FB : 32 / qb;
   const int64_t gx = (a.rows + qr - 1) / qr, gy = (kb + qb - 1) / qb;
   if (gx > (1 << 24) - 1 || gy > 65535 || batch > 65535) return GPTQ_ERR_UNSUPPORTED;
   const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(gy), batch), block(256);
-  if (block_rows == FB) GPTQ_LAUNCH((quant_tile_kernel<T, E8, kVec>), grid, block, 0, stream, a);
-  else if (qb == 32) GPTQ_LAUNCH((quant_rows_kernel<T, E8, kVec, 32>), grid, block, 0, stream, a);
-  else GPTQ_LAUNCH((quant_rows_kernel<T, E8, kVec, 4>), grid, block, 0, stream, a);
+  if (block_rows == FB) GPTQ_LAUNCH((quant_tile_kernel<T, E8>), grid, block, 0, stream, a);
+  else if (qb == 32) GPTQ_LAUNCH((quant_rows_kernel<T, E8, 32>), grid, block, 0, stream, a);
+  else GPTQ_LAUNCH((quant_rows_kernel<T, E8, 4>), grid, block, 0, stream, a);
   return GPTQ_OK;
 }
 
 template <typename T>
 gptq_status launch_quant_t(const QuantArgs& a, int batch, int block_rows, bool e8, hipStream_t stream) {
-  constexpr int V = 16 / sizeof(T);
-  const bool vec = reinterpret_cast<uintptr_t>(a.X) % 16 == 0 && a.ldx % V == 0 && (batch == 1 || a.bsx % V == 0);
-  if (vec)
-    return e8 ? launch_quant<T, true, true>(a, batch, block_rows, stream)
-              : launch_quant<T, false, true>(a, batch, block_rows, stream);
-  return e8 ? launch_quant<T, true, false>(a, batch, block_rows, stream)
-            : launch_quant<T, false, false>(a, batch, block_rows, stream);
+  return e8 ? launch_quant<T, true>(a, batch, block_rows, stream) : launch_quant<T, false>(a, batch, block_rows, stream);
 }
 
 // ---------------------------------------------------------------------------- product
@@ -1120,7 +1111,7 @@ __global__ __launch_bounds__(WK * 64) void fp8_rows_kernel(MmArgs a) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) v[i] = 0.0f;
       if (p >= 0 && col < a.k)
-        load_row<T, 16, true>(reinterpret_cast<const T*>(a.X) + p * a.ldx + col, v);
+        load_row<T, 16>(reinterpret_cast<const T*>(a.X) + p * a.ldx + col, v);
       const uint32_t top = eight_lanes_max(top_bits<16>(v));
       const bool e8 = KIND == kMmaE8M0 || (KIND == kMmaExact && a.e8);
       const Scale sc = e8 ? block_scale<true>(top) : block_scale<false>(top);
@@ -1254,13 +1245,13 @@ gptq_status launch_product(const MmArgs& a, Product kind, hipStream_t stream) {
   return a.kb >= 24 ? launch_rows<1, 8, void>(a, stream) : launch_rows<1, 4, void>(a, stream);
 }
 
-// 16-bit rows straight into the kernel for few rows, where rows can be read in 16-byte pieces and
-// the workgroups' repeated rounding stays small: at most 32 values a thread, 4 M over the launch
+// 16-bit rows straight into the kernel for few rows, where the workgroups' repeated rounding stays
+// small: at most 32 values a thread, 4 M over the launch
 // (4096 x 14336 at 1 row: 14.2 us, against 3.5 + 12.7 in two launches; 4096 x 4096 at 8 rows: 11.5
 // against 3.6 + 6.6; 96 rows of 64 experts of 1408 x 2048: 29.4 against 3.9 + 23.8), and 16 rows
 // of a group fit 48 KB, which leaves three workgroups on a CU.
-bool rounds_itself(const MmArgs& a, const void* X, int64_t ldx) {
-  if (reinterpret_cast<uintptr_t>(X) % 16 != 0 || ldx % 8 != 0 || a.m * a.k > (1 << 22)) return false;
+bool rounds_itself(const MmArgs& a) {
+  if (a.m * a.k > (1 << 22)) return false;
   if (a.m * a.k * ((a.n + 15) / 16) > (1 << 22)) return false;
   if (a.off != nullptr) return a.m <= 2 * static_cast<int64_t>(a.experts) && raw_lds(a, 16) <= 48 * 1024;
   return a.m <= 16 && a.m * a.k <= 16384;
@@ -1307,7 +1298,7 @@ gptq_status fp8_matmul_enqueue(const Fp8Problem& p, hipStream_t stream) {
   if (p.x_rows > 0 && (p.workspace == nullptr || p.workspace_bytes < l.total)) return GPTQ_ERR_WORKSPACE;
   a.ldx = p.k;   // as the product will read them
   const Product kind = choose_product(a);
-  if (kind == kRows && rounds_itself(a, p.X, p.ldx)) {
+  if (kind == kRows && rounds_itself(a)) {
     a.ldx = p.ldx;
     return p.x_dtype == GPTQ_BF16 ? launch_raw<BF16>(a, stream) : launch_raw<F16>(a, stream);
   }
