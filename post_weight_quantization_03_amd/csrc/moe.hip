@@ -649,7 +649,7 @@ gptq_status launch_route(RouteArgs a, hipStream_t stream) {
     const int per = a.E / a.G, lanes = 16 / a.G, each = (per + lanes - 1) / lanes;
     const int slots = each <= 4 ? 4 : each <= 8 ? 8 : 16;
     const int piece = std::min<int>(16, slots * static_cast<int>(sizeof(T)));
-    a.vec = each == slots && per % each == 0 && reinterpret_cast<uintptr_t>(a.logits) % piece == 0 &&
+    a.vec = each == slots && per == lanes * each && reinterpret_cast<uintptr_t>(a.logits) % piece == 0 &&
             a.ldl * static_cast<int64_t>(sizeof(T)) % piece == 0 && reinterpret_cast<uintptr_t>(a.bias) % 16 == 0;
     a.per = per;
     a.each = each;

@@ -330,3 +330,24 @@ def test_combine_short_rows(d, dtype):
     assert (err <= torch.finfo(DT[dtype]).eps / 2 * np.abs(ref) * (1 + 3 * 2.0 ** -24) + 3 * 2.0 ** -24 * size
             + (2.0 ** -25 if dtype == "f16" else 0)).all()
     assert bool((out[:, 0] == 7).all()) and bool((out[:, d + 1] == 7).all())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("tokens", [1, 4, 5, 300])
+@pytest.mark.parametrize("experts,groups", [(4, 1), (12, 1), (52, 1), (60, 1), (120, 1), (56, 2), (233, 1), (48, 16),
+                                            (144, 16), (36, 2), (31, 1), (33, 1)])
+def test_route_experts_that_leave_lanes_over(experts, groups, tokens, dtype):
+    # tightly packed logits and rows of a wider tensor whose other columns would win
+    rng = np.random.default_rng(experts + tokens)
+    k = min(4, experts // groups)
+    logits = torch.from_numpy(1.5 * rng.standard_normal((tokens, experts))).to(DT[dtype]).cuda()
+    wide = torch.full((tokens, experts + 3), 60.0, dtype=DT[dtype], device="cuda")
+    wide[:, 1:experts + 1] = logits
+    bias = torch.from_numpy(0.001 * rng.integers(-60, 61, experts)).float().cuda()
+    biases = torch.full((experts + 5,), 50.0, device="cuda")
+    biases[1:experts + 1] = bias
+    for b, c, scoring in ((None, None, "softmax"), (bias, biases[1:experts + 1], "sigmoid")):
+        kw = dict(scoring=scoring, n_groups=groups, top_groups=max(1, groups // 2), group_score="top2")
+        ids, w = check_route(logits, k, bias=b, **kw)
+        same = lib().moe_route(wide[:, 1:experts + 1], k, bias=c, **kw)
+        assert np.array_equal(same[0].cpu().numpy(), ids) and np.array_equal(same[1].double().cpu().numpy(), w)
