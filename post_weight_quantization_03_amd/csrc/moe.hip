@@ -14,11 +14,6 @@ namespace {
 
 // ---------------------------------------------------------------------------- routing
 
-template <typename T, int V>
-struct alignas(sizeof(T) * V) Vec {
-  T v[V];
-};
-
 struct RouteArgs {
   int64_t n_tokens;
   int E;
@@ -31,7 +26,7 @@ struct RouteArgs {
   float* weights;
   int batch;   // route_kernel: tokens per wave and turn, 1, 2 or 4
   int per, each, log_lanes;   // route_rows_kernel: experts per group and per lane, log2 of lanes per group
-  bool vec;                   // and whether rows and biases take wide loads
+  bool exact;                 // and whether that is all experts, each once
 };
 
 // fp32 as integers in the same order (-0 as +0), which maxima over lanes take in one
@@ -480,27 +475,21 @@ __global__ __launch_bounds__(256) void route_rows_kernel(RouteArgs a) {
   const T* row = static_cast<const T*>(a.logits) + t * a.ldl;
 
   float l[PER], bias[PER], m = ninf;
-  if (a.vec) {   // whole 16-byte pieces
-    constexpr int V = 16 / sizeof(T) < PER ? 16 / sizeof(T) : PER;
+  // Wide loads, which the chip takes at any address, where the lanes' experts end with the row or
+  // run on into another row of these logits (what they hold of it is not used).
+  if (a.exact || (a.E >= 64 && t0 + 4 < a.n_tokens)) {
+    T w[PER];
+    __builtin_memcpy(w, row + e0, sizeof(w));
 #pragma unroll
-    for (int i = 0; i < PER; i += V) {
-      const Vec<T, V> v = *reinterpret_cast<const Vec<T, V>*>(row + e0 + i);
-#pragma unroll
-      for (int j = 0; j < V; ++j) l[i + j] = load_as_f32(&v.v[j]);
-    }
+    for (int i = 0; i < PER; ++i) l[i] = load_as_f32(&w[i]);
   } else {
 #pragma unroll
     for (int i = 0; i < PER; ++i) l[i] = load_as_f32(row + min(max(e0 + min(i, mine - 1), 0), a.E - 1));
   }
 #pragma unroll
   for (int i = 0; i < PER; ++i) bias[i] = 0.0f;
-  if (biased && a.vec) {
-#pragma unroll
-    for (int i = 0; i < PER; i += 4) {
-      const Vec<float, 4> v = *reinterpret_cast<const Vec<float, 4>*>(a.bias + e0 + i);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) bias[i + j] = v.v[j];
-    }
+  if (biased && a.exact) {
+    __builtin_memcpy(bias, a.bias + e0, sizeof(bias));
   } else if (biased) {
 #pragma unroll
     for (int i = 0; i < PER; ++i) bias[i] = a.bias[min(max(e0 + min(i, mine - 1), 0), a.E - 1)];
@@ -648,9 +637,7 @@ gptq_status launch_route(RouteArgs a, hipStream_t stream) {
   if (a.E <= 256 && a.k <= 15 && a.G <= 16 && 16 % a.G == 0) {
     const int per = a.E / a.G, lanes = 16 / a.G, each = (per + lanes - 1) / lanes;
     const int slots = each <= 4 ? 4 : each <= 8 ? 8 : 16;
-    const int piece = std::min<int>(16, slots * static_cast<int>(sizeof(T)));
-    a.vec = each == slots && per == lanes * each && reinterpret_cast<uintptr_t>(a.logits) % piece == 0 &&
-            a.ldl * static_cast<int64_t>(sizeof(T)) % piece == 0 && reinterpret_cast<uintptr_t>(a.bias) % 16 == 0;
+    a.exact = each == slots && per == lanes * each;
     a.per = per;
     a.each = each;
     a.log_lanes = __builtin_ctz(lanes);
