@@ -394,13 +394,25 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
         if (biased) {
           const uint32_t next = static_cast<uint32_t>(__shfl_down(static_cast<int>(got), 1));
           const int next_id = __shfl_down(id, 1);
-          bool close = false;
-          if (lane < a.k && next_id >= 0) {
-            const float u = of_key(got), v = of_key(next);
-            close = !(u - v > 0x1p-19f * fmaxf(1.0f, fmaxf(fabsf(u), fabsf(v))));
-            if (close) close = !(load_as_f32(row + id) == load_as_f32(row + next_id) && a.bias[id] == a.bias[next_id]);
+          auto close = [](float u, float v) { return !(u - v > 0x1p-19f * fmaxf(1.0f, fmaxf(fabsf(u), fabsf(v)))); };
+          bool differ = false, twins = false;
+          if (lane < a.k && next_id >= 0 && close(of_key(got), of_key(next))) {
+            const bool same = load_as_f32(row + id) == load_as_f32(row + next_id) && a.bias[id] == a.bias[next_id];
+            differ = !same;
+            twins = same && lane == a.k - 1;
           }
-          near = __ballot(close) != 0;
+          near = __ballot(differ) != 0;
+          if (!near && __ballot(twins)) {
+            const int last = __builtin_amdgcn_readlane(id, a.k - 1);
+            const float u = of_key(__builtin_amdgcn_readlane(static_cast<int>(got), a.k - 1));
+            const float l_last = load_as_f32(row + last), b_last = a.bias[last];
+            bool other = false;
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+              if (key[i] > kKeyNone && close(u, of_key(key[i])))
+                other = other || !(load_as_f32(row + at[i]) == l_last && a.bias[at[i]] == b_last);
+            near = __ballot(other) != 0;
+          }
         }
       }
       if (near) {
@@ -598,12 +610,30 @@ __global__ __launch_bounds__(256) void route_rows_kernel(RouteArgs a) {
   if (!exact) {
     const uint32_t next = moved<0x101>(got);                               // the lane after (row_shl 1)
     const int next_id = static_cast<int>(moved<0x101>(static_cast<uint32_t>(id + 1))) - 1;
-    if (l16 < a.k && next_id >= 0) {
-      const float u = of_key(got & ~15u), v = of_key(next & ~15u);
+    auto close = [&](uint32_t p, uint32_t q) {
+      const float u = of_key(p & ~15u), v = of_key(q & ~15u);
       const float tol = biased ? 0x1p-18f * fmaxf(1.0f, fmaxf(fabsf(u), fabsf(v))) : 0.0f;
-      if (!(u - v > tol))
-        near = near || !(load_as_f32(row + id) == load_as_f32(row + next_id) &&
-                         (!biased || a.bias[id] == a.bias[next_id]));
+      return !(u - v > tol);
+    };
+    auto alike = [&](int p, int q) {
+      return load_as_f32(row + p) == load_as_f32(row + q) && (!biased || a.bias[p] == a.bias[q]);
+    };
+    bool twins = false;
+    if (l16 < a.k && next_id >= 0 && close(got, next)) {
+      const bool same = alike(id, next_id);
+      near = near || !same;
+      twins = same && l16 == a.k - 1;
+    }
+    if (__ballot(twins)) {
+      const int src = (lane & 48) | (a.k - 1);
+      const uint32_t u = static_cast<uint32_t>(__shfl(static_cast<int>(got), src));
+      const int last = __shfl(id, src);
+      if (__shfl(static_cast<int>(twins), src)) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+          if (key[i] > kKeyNone && close(u, key[i]))
+            near = near || !alike(last, e0 + 15 - static_cast<int>(key[i] & 15u));
+      }
     }
   }
   uint64_t again = __ballot(near && live);

@@ -351,3 +351,56 @@ def test_route_experts_that_leave_lanes_over(experts, groups, tokens, dtype):
         ids, w = check_route(logits, k, bias=b, **kw)
         same = lib().moe_route(wide[:, 1:experts + 1], k, bias=c, **kw)
         assert np.array_equal(same[0].cpu().numpy(), ids) and np.array_equal(same[1].double().cpu().numpy(), w)
+
+
+# experts, groups, most choices: up to 256 experts in a power of two of groups take one kernel, the others another
+CUT_SHAPES = [(60, 1, 8), (64, 1, 15), (128, 1, 8), (256, 1, 8), (160, 8, 6), (256, 2, 15), (96, 3, 8), (128, 1, 16),
+              (384, 1, 8), (1024, 1, 32)]
+
+
+@pytest.mark.parametrize("experts,groups,most", CUT_SHAPES)
+def test_route_twins_at_the_cut_hide_no_larger_expert(experts, groups, most):
+    # two experts alike where the choice ends, and a third behind them in the kernel's rounded
+    # values that is larger in truth: the last step of an fp32 logit, a bias under a step of the
+    # score, scores of 1 in fp32
+    rng = np.random.default_rng(experts + most)
+    up = np.nextafter(np.float32(1), np.float32(2))
+    kw = dict(n_groups=groups, top_groups=groups)
+    for k in (1, 2, most - 1, most):
+        l = np.full((40, experts), -5, np.float32)
+        sat, b = l.copy(), np.zeros(experts, np.float32)
+        for row, t in enumerate(l):
+            at = rng.permutation(experts)
+            if row < 20:   # neighbours: often of one lane
+                at = (rng.integers(experts) + np.arange(experts)) % experts
+            t[at[:k - 1]] = 4 + np.arange(k - 1)
+            t[at[k - 1:k + 2]] = 1
+            t[at[k + 1]] = up
+            sat[row, at[:k - 1]], sat[row, at[k - 1:k + 2]], sat[row, at[k + 1]] = 36, 20, 30
+        check_route(torch.from_numpy(l).cuda(), k, **kw)
+        check_route(torch.from_numpy(l).cuda(), k, scoring="sigmoid", **kw)
+        check_route(torch.from_numpy(sat).cuda(), k, bias=torch.from_numpy(b).cuda(), scoring="sigmoid", **kw)
+        # one row of equal logits, told apart by the biases alone
+        at = rng.permutation(experts)
+        b[at[:k - 1]], b[at[k - 1:]] = 1, 0
+        b[at[k + 1]], b[at[k + 2:]] = 2.0 ** -27, -1
+        check_route(torch.zeros(1, experts, device="cuda"), k, bias=torch.from_numpy(b).cuda(), scoring="sigmoid", **kw)
+
+
+@pytest.mark.parametrize("experts,groups,most", CUT_SHAPES)
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_route_clusters_at_the_cut(experts, groups, most, scoring):
+    # clusters of equal and nearly equal experts, most cuts inside one
+    rng = np.random.default_rng(experts + most)
+    vals = np.float32(rng.standard_normal(16))
+    l = torch.from_numpy(vals[rng.integers(0, 16, (60, experts))]).cuda()
+    steps = torch.from_numpy(np.float32(1) + np.float32(2.0 ** -23) * rng.integers(0, 24, (60, experts)).astype(np.float32)).cuda()
+    few = torch.where(torch.from_numpy(rng.random((60, experts)) < 8 / experts).cuda(), steps, -steps)
+    for k in (1, 2, 4, most):
+        for tg in {groups, max(1, groups // 2)}:
+            kw = dict(scoring=scoring, n_groups=groups, top_groups=tg)
+            for step in (0.0, 1e-9):
+                bias = torch.from_numpy(step * rng.integers(-2, 3, experts)).float().cuda()
+                check_route(l, k, bias=bias, **kw)
+            check_route(steps, k, **kw)
+            check_route(few, k, group_score="top2", **kw)
