@@ -417,7 +417,8 @@ gptq_status gptq_moe_route(int64_t n_tokens, int n_experts, gptq_dtype l_dtype, 
  *                                           last range
  *   place         int32 [n_tokens, top_k]   the position of each choice, -1 for no choice
  * workspace: gptq_workspace_size(GPTQ_WS_MOE_GROUP, 1, n_experts, top_k, n_tokens, NULL) bytes,
- * 16-byte aligned.  Requires 1 <= n_experts <= 1024, top_k >= 1, n_tokens * top_k < 2^31;
+ * 16-byte aligned; where that is 256 (up to 8192 slots) the call keeps nothing there and takes
+ * NULL.  Requires 1 <= n_experts <= 1024, top_k >= 1, n_tokens * top_k < 2^31;
  * n_tokens may be 0 (all offsets 0).
  */
 gptq_status gptq_moe_group_tokens(int64_t n_tokens, int top_k, int n_experts, const int32_t* ids,

@@ -943,10 +943,12 @@ gptq_status route_enqueue(int64_t n_tokens, int n_experts, gptq_dtype l_dtype, c
   return launch_route<F16>(a, stream);
 }
 
+// 256 where nothing is kept in it, more where the counts are, however few experts there are: callers
+// pass none for 256.
 size_t group_workspace(int n_experts, int64_t slots) {
   const int chunk = group_chunk(slots);
   const int64_t chunks = (slots + chunk - 1) / chunk;
-  return chunks > 1 ? static_cast<size_t>(chunks) * n_experts * sizeof(int32_t) : 256;
+  return 256 + (chunks > 1 ? align_up(static_cast<size_t>(chunks) * n_experts * sizeof(int32_t), 256) : 0);
 }
 
 gptq_status group_enqueue(int64_t n_tokens, int top_k, int n_experts, const int32_t* ids, int64_t* token_offsets,

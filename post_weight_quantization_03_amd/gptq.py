@@ -444,7 +444,7 @@ def _workspace_bytes(which: int, batch: int, d_out: int, d_in: int, hint: int) -
 def _scratch(which, batch, d_out, d_in, hint, device, workspace) -> torch.Tensor | None:
     """The caller's workspace if it is large enough, else a new one; None where the call needs none."""
     nbytes = _workspace_bytes(which, batch, d_out, d_in, hint)
-    if nbytes <= 256:   # the least size: nothing is kept in it
+    if nbytes <= 256:   # the size of a workspace that nothing is kept in
         return None
     if workspace is not None:
         if not workspace.is_contiguous():

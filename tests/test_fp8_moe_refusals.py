@@ -178,3 +178,15 @@ def test_binding_refuses_a_workspace_with_less_memory_than_elements():
         gptq.fp8_matmul(torch.empty(4, 128, dtype=torch.bfloat16), q, s, workspace=ws)
     with pytest.raises(ValueError, match="workspace"):
         gptq.moe_group_tokens(torch.zeros(20000, 2, dtype=torch.int32), 8, workspace=ws)
+
+
+def test_group_workspace_tells_whether_it_is_used():
+    # 256 bytes mean that the call keeps nothing there: the binding then passes none
+    for experts in (1, 2, 3, 4, 7, 8, 63, 64, 1024):
+        for slots in (0, 1, 8192):
+            assert gptq.workspace_size(gptq.WS_MOE_GROUP, 1, experts, 1, slots) == 256
+        for slots in (8193, 9216, 16384, 32768, 2 ** 31 - 1):
+            need = gptq.workspace_size(gptq.WS_MOE_GROUP, 1, experts, 1, slots)
+            assert need > 256
+            assert gptq.lib().gptq_moe_group_tokens(slots, 1, experts, 16, 16, 16, 16, None, 0, None) == WS
+            assert gptq.lib().gptq_moe_group_tokens(slots, 1, experts, 16, 16, 16, 16, 16, need - 1, None) == WS

@@ -404,3 +404,23 @@ def test_route_clusters_at_the_cut(experts, groups, most, scoring):
                 check_route(l, k, bias=bias, **kw)
             check_route(steps, k, **kw)
             check_route(few, k, group_score="top2", **kw)
+
+
+@pytest.mark.parametrize("experts", [1, 2, 3, 4, 7, 8])
+@pytest.mark.parametrize("slots", [8192, 8193, 16384, 32768, 524289])
+def test_group_few_experts_many_slots(experts, slots):
+    rng = np.random.default_rng(slots + experts)
+    ids = rng.integers(-1, experts + 1, (slots, 1)).astype(np.int32)
+    keep = np.flatnonzero((ids[:, 0] >= 0) & (ids[:, 0] < experts))
+    order = keep[np.argsort(ids[keep, 0], kind="stable")]
+    want_off = np.concatenate([[0], np.cumsum(np.bincount(ids[keep, 0], minlength=experts))])
+    want_rows, want_place = np.full(slots, -1), np.full(slots, -1)
+    want_rows[:len(order)], want_place[order] = order, np.arange(len(order))
+    g = lib()
+    size = g.workspace_size(g.WS_MOE_GROUP, 1, experts, 1, slots)
+    for ws in (None, torch.empty(size, dtype=torch.uint8, device="cuda"),
+               torch.empty(16, dtype=torch.uint8, device="cuda")):
+        off, rows, place = g.moe_group_tokens(torch.from_numpy(ids).cuda(), experts, workspace=ws)
+        assert np.array_equal(off.cpu().numpy(), want_off)
+        assert np.array_equal(rows.cpu().numpy(), want_rows)
+        assert np.array_equal(place.cpu().numpy()[:, 0], want_place)
