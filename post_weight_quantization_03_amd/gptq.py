@@ -9,6 +9,9 @@ Names follow the C ABI: ``accumulate_hessian``, ``prepare_hinv``, ``quantize_lay
 ``pack_int4``.  Tensors may carry a leading batch dimension (independent problems, e.g.
 mixture-of-experts layers).  ``moe_*`` route tokens to experts and ``fp8_*`` serve layers in
 8 bits; no call records a gradient.
+
+``stream`` is the torch stream a call runs on (None: the current one).  Its inputs have to be
+ready there; what the call allocates comes from that stream's memory.
 """
 
 from __future__ import annotations
@@ -145,14 +148,21 @@ def _stream(stream) -> int:
     return s.cuda_stream
 
 
-def _keep_for(stream, *tensors) -> None:
-    """Tensors this module allocated (on torch's current stream) and hands to kernels on
-    another stream: tell the caching allocator about that stream, so that their memory
-    is not given to new work before the kernels queued there are done with it."""
-    if stream is None or stream == torch.cuda.current_stream(stream.device):
-        return
-    for t in tensors:
-        t.record_stream(stream)
+def _empty(shape, dtype: torch.dtype, device, stream=None, strides=None) -> torch.Tensor:
+    """A new tensor that kernels on ``stream`` (None: the current one) write.  On another stream
+    than the current one its memory comes from that stream's blocks: one freed on the current
+    stream may still have work queued there, which that stream would not wait for.  The current
+    stream is told to the caching allocator, since the caller goes on to use the tensor there."""
+    if stream is not None:
+        current = torch.cuda.current_stream(stream.device)
+        if stream != current:
+            with torch.cuda.stream(stream):
+                t = _empty(shape, dtype, device, None, strides)
+            t.record_stream(current)
+            return t
+    if strides is not None:
+        return torch.empty_strided(shape, strides, dtype=dtype, device=device)
+    return torch.empty(shape, dtype=dtype, device=device)
 
 
 def _batched(t: torch.Tensor, nd: int) -> torch.Tensor:
@@ -168,9 +178,7 @@ def workspace_size(which: int, batch: int, d_out: int, d_in: int, n_tokens_hint:
 def _workspace(nbytes: int, device, workspace: torch.Tensor | None, stream=None) -> torch.Tensor:
     if workspace is not None and workspace.numel() >= nbytes:
         return workspace
-    ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
-    _keep_for(stream, ws)
-    return ws
+    return _empty(max(nbytes, 1), torch.uint8, device, stream)
 
 
 def new_hessian(d_in: int, batch: int | None = None, device="cuda"):
@@ -257,10 +265,9 @@ def prepare_hinv(H: torch.Tensor, diag_key: torch.Tensor, params: Params, worksp
     if not Hb.is_contiguous() or not diag_key.is_contiguous():
         raise ValueError("H and diag_key must be contiguous")
     shp = H.shape[:-1]
-    U = torch.empty(*H.shape, dtype=torch.float32, device=H.device)
-    perm = torch.empty(*shp, dtype=torch.int32, device=H.device)
-    dead = torch.empty(*shp, dtype=torch.uint8, device=H.device)
-    _keep_for(stream, U, perm, dead)
+    U = _empty(H.shape, torch.float32, H.device, stream)
+    perm = _empty(shp, torch.int32, H.device, stream)
+    dead = _empty(shp, torch.uint8, H.device, stream)
     ws = _workspace(workspace_size(WS_PREPARE, batch, 0, d_in, 0, params), H.device, workspace, stream)
     p = params.c()
     _check(lib().gptq_prepare_hinv(batch, d_in, Hb.data_ptr(), d_in * d_in, diag_key.data_ptr(), ctypes.byref(p),
@@ -281,11 +288,10 @@ def quantize_layer(W: torch.Tensor, U: torch.Tensor, perm: torch.Tensor, dead: t
         raise ValueError("W rows, U, perm and dead must be contiguous")
     ng = params.n_groups(d_in)
     lead = W.shape[:-2]
-    codes = torch.empty(*lead, d_out, d_in, dtype=torch.uint8, device=W.device)
-    scales = torch.empty(*lead, ng, d_out, dtype=torch.float32, device=W.device)
-    zeros = torch.empty(*lead, ng, d_out, dtype=torch.uint8, device=W.device)
-    g_idx = torch.empty(*lead, d_in, dtype=torch.int32, device=W.device)
-    _keep_for(stream, codes, scales, zeros, g_idx)
+    codes = _empty((*lead, d_out, d_in), torch.uint8, W.device, stream)
+    scales = _empty((*lead, ng, d_out), torch.float32, W.device, stream)
+    zeros = _empty((*lead, ng, d_out), torch.uint8, W.device, stream)
+    g_idx = _empty((*lead, d_in), torch.int32, W.device, stream)
     ws = _workspace(workspace_size(WS_QUANTIZE, batch, d_out, d_in, 0, params), W.device, workspace, stream)
     p = params.c()
     _check(lib().gptq_quantize_layer(batch, d_out, d_in, _DT[W.dtype], Wb.data_ptr(), Wb.stride(1),
@@ -311,11 +317,10 @@ def quantize_layer_noalloc(W: torch.Tensor, U: torch.Tensor, perm: torch.Tensor,
     ng = params.n_groups(d_in)
     lead = W.shape[:-2]
     if out is None:
-        out = (torch.empty(*lead, d_out, d_in, dtype=torch.uint8, device=W.device),
-               torch.empty(*lead, ng, d_out, dtype=torch.float32, device=W.device),
-               torch.empty(*lead, ng, d_out, dtype=torch.uint8, device=W.device),
-               torch.empty(*lead, d_in, dtype=torch.int32, device=W.device))
-        _keep_for(stream, *out)
+        out = (_empty((*lead, d_out, d_in), torch.uint8, W.device, stream),
+               _empty((*lead, ng, d_out), torch.float32, W.device, stream),
+               _empty((*lead, ng, d_out), torch.uint8, W.device, stream),
+               _empty((*lead, d_in), torch.int32, W.device, stream))
     codes, scales, zeros, g_idx = out
     want = [((*lead, d_out, d_in), torch.uint8), ((*lead, ng, d_out), torch.float32),
             ((*lead, ng, d_out), torch.uint8), ((*lead, d_in), torch.int32)]
@@ -340,10 +345,9 @@ def pack_int4(codes: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor, st
     if not (codes.is_contiguous() and scales.is_contiguous() and zeros.is_contiguous()):
         raise ValueError("codes, scales and zeros must be contiguous")
     lead = codes.shape[:-2]
-    qweight = torch.empty(*lead, d_in // 8, d_out, dtype=torch.int32, device=codes.device)
-    qzeros = torch.empty(*lead, ng, d_out // 8, dtype=torch.int32, device=codes.device)
-    sf16 = torch.empty(*lead, ng, d_out, dtype=torch.float16, device=codes.device)
-    _keep_for(stream, qweight, qzeros, sf16)
+    qweight = _empty((*lead, d_in // 8, d_out), torch.int32, codes.device, stream)
+    qzeros = _empty((*lead, ng, d_out // 8), torch.int32, codes.device, stream)
+    sf16 = _empty((*lead, ng, d_out), torch.float16, codes.device, stream)
     _check(lib().gptq_pack_int4(batch, d_out, d_in, ng, codes.data_ptr(), scales.data_ptr(), zeros.data_ptr(),
                                 qweight.data_ptr(), qzeros.data_ptr(), sf16.data_ptr(), _stream(stream)),
            "gptq_pack_int4")
@@ -364,9 +368,8 @@ def w4a16_repack(qweight: torch.Tensor, g_idx: torch.Tensor, n_groups: int, work
         raise TypeError("qweight and g_idx must be int32, g_idx [(b,) d_in]")
     if not qweight.is_contiguous() or not g_idx.is_contiguous():
         raise ValueError("qweight and g_idx must be contiguous")
-    qs = torch.empty_like(qweight)
-    order = torch.empty_like(g_idx)
-    _keep_for(stream, qs, order)
+    qs = _empty(qweight.shape, torch.int32, qweight.device, stream)
+    order = _empty(g_idx.shape, torch.int32, g_idx.device, stream)
     ws = _workspace(workspace_size(WS_W4A16_REPACK, batch, d_out, d_in), qweight.device, workspace, stream)
     _check(lib().gptq_w4a16_repack(batch, d_out, d_in, n_groups, qweight.data_ptr(), g_idx.data_ptr(), qs.data_ptr(),
                                    order.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream)), "gptq_w4a16_repack")
@@ -390,9 +393,7 @@ def w4a16_matmul(X: torch.Tensor, qweight_s: torch.Tensor, qzeros: torch.Tensor,
         raise ValueError("packed tensors must be contiguous")
     if order is not None and (order.dtype != torch.int32 or order.numel() != d_in or not order.is_contiguous()):
         raise ValueError("order must be contiguous int32 [d_in]")
-    Y = out if out is not None else torch.empty(m, d_out, dtype=torch.float32, device=X.device)
-    if out is None:
-        _keep_for(stream, Y)
+    Y = out if out is not None else _empty((m, d_out), torch.float32, X.device, stream)
     gsz = -1 if n_groups == 1 else d_in // n_groups
     ws = _workspace(workspace_size(WS_W4A16, 1, d_out, d_in, m, Params(group_size=gsz)), X.device, workspace, stream)
     _check(lib().gptq_w4a16_matmul(m, d_out, d_in, n_groups, _DT[X.dtype], X.data_ptr(), X.stride(0),
@@ -427,8 +428,8 @@ def _run(what: str, stream, tensors, *args) -> None:
         with torch.cuda.device(device):
             status = fn(*args, _stream(stream))
         if stream is not None and stream != torch.cuda.current_stream(stream.device):
-            # also the caller's tensors: they may be freed on the current stream before a call
-            # on another one is done with them
+            # the caller's tensors too may be freed on the current stream before a call on
+            # another one is done with them
             for t in tensors:
                 if t is not None:
                     t.record_stream(stream)
@@ -441,7 +442,7 @@ def _workspace_bytes(which: int, batch: int, d_out: int, d_in: int, hint: int) -
     return workspace_size(which, batch, d_out, d_in, hint)
 
 
-def _scratch(which, batch, d_out, d_in, hint, device, workspace) -> torch.Tensor | None:
+def _scratch(which, batch, d_out, d_in, hint, device, workspace, stream) -> torch.Tensor | None:
     """The caller's workspace if it is large enough, else a new one; None where the call needs none."""
     nbytes = _workspace_bytes(which, batch, d_out, d_in, hint)
     if nbytes <= 256:   # the size of a workspace that nothing is kept in
@@ -451,7 +452,7 @@ def _scratch(which, batch, d_out, d_in, hint, device, workspace) -> torch.Tensor
             raise ValueError("workspace must be contiguous")
         if _bytes(workspace) >= nbytes:
             return workspace
-    return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    return _empty(nbytes, torch.uint8, device, stream)
 
 
 def _ptr(t):
@@ -467,12 +468,12 @@ def _route_params(*values) -> _RouteParams:
     return _RouteParams(*values)
 
 
-def _out(out, shape, dtype, device, name="out"):
+def _out(out, shape, dtype, device, stream):
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return _empty(shape, dtype, device, stream)
     if tuple(out.shape) != tuple(shape) or out.dtype != dtype or out.stride(-1) != 1 or (
             len(shape) > 1 and shape[0] > 1 and out.stride(0) < shape[-1]):
-        raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)} with contiguous rows")
+        raise ValueError(f"out must be {dtype} of shape {tuple(shape)} with contiguous rows")
     return out
 
 
@@ -501,11 +502,11 @@ def fp8_quantize(X: torch.Tensor, block_rows: int = 1, scale_dtype: torch.dtype 
         raise ValueError("X rows must be contiguous")
     rb, cb = -(-rows // block_rows), -(-cols // _FP8_BLOCK)
     ld_row, ld_block = (1, max(rb, 1)) if block_rows == 1 else (cb, 1)
-    q = torch.empty(X.shape, dtype=torch.float8_e4m3fn, device=X.device)
+    q = _empty(X.shape, torch.float8_e4m3fn, X.device, stream)
     if X.dim() == 2:
-        S = torch.empty_strided((rb, cb), (ld_row, ld_block), dtype=scale_dtype, device=X.device)
+        S = _empty((rb, cb), scale_dtype, X.device, stream, (ld_row, ld_block))
     else:
-        S = torch.empty_strided((batch, rb, cb), (rb * cb, ld_row, ld_block), dtype=scale_dtype, device=X.device)
+        S = _empty((batch, rb, cb), scale_dtype, X.device, stream, (rb * cb, ld_row, ld_block))
     _run("gptq_fp8_quantize", stream, (X, q, S), batch, rows, cols, _DT[X.dtype], X.data_ptr(), _row_stride(Xb),
          Xb.stride(0), block_rows, _SDT[scale_dtype], q.data_ptr(), S.data_ptr(), ld_row, ld_block, rb * cb)
     return q, S
@@ -559,8 +560,9 @@ def fp8_matmul(X: torch.Tensor, qweight: torch.Tensor, w_scales: torch.Tensor, x
         raise ValueError("qweight must be [d_out, d_in]")
     sdt = _fp8_operands(X, x_scales, qweight, w_scales, out_dtype)
     (m, d_in), d_out = X.shape, qweight.shape[0]
-    Y = _out(out, (m, d_out), out_dtype, X.device)
-    ws = None if X.dtype == torch.float8_e4m3fn else _scratch(WS_FP8_MATMUL, 1, d_out, d_in, m, X.device, workspace)
+    Y = _out(out, (m, d_out), out_dtype, X.device, stream)
+    ws = None if X.dtype == torch.float8_e4m3fn else _scratch(WS_FP8_MATMUL, 1, d_out, d_in, m, X.device, workspace,
+                                                              stream)
     _run("gptq_fp8_matmul", stream, (X, qweight, w_scales, x_scales, Y, ws), m, d_out, d_in, _DT.get(X.dtype, E4M3),
          X.data_ptr(), _row_stride(X), sdt, *_fp8_scales(x_scales), qweight.data_ptr(), w_scales.data_ptr(),
          _DT[out_dtype], Y.data_ptr(), _row_stride(Y), _ptr(ws),
@@ -587,9 +589,9 @@ def fp8_matmul_grouped(X: torch.Tensor, qweight: torch.Tensor, w_scales: torch.T
                                   not row_index.is_contiguous()):
         raise ValueError("row_index must be contiguous int32 [n_rows]")
     n_rows = x_rows if row_index is None else row_index.numel()
-    Y = _out(out, (n_rows, d_out), out_dtype, X.device)
+    Y = _out(out, (n_rows, d_out), out_dtype, X.device, stream)
     ws = None if X.dtype == torch.float8_e4m3fn else _scratch(WS_FP8_GROUPED, experts, d_out, d_in, x_rows, X.device,
-                                                              workspace)
+                                                              workspace, stream)
     _run("gptq_fp8_matmul_grouped", stream, (X, qweight, w_scales, token_offsets, row_index, x_scales, Y, ws), experts,
          x_rows, n_rows, d_out, d_in, _DT.get(X.dtype, E4M3), X.data_ptr(), _row_stride(X), sdt,
          *_fp8_scales(x_scales), qweight.data_ptr(), w_scales.data_ptr(), token_offsets.data_ptr(),
@@ -622,8 +624,8 @@ def moe_route(logits: torch.Tensor, top_k: int, bias: torch.Tensor | None = None
         raise ValueError("scoring must be 'softmax' or 'sigmoid', group_score 'max' or 'top2'")
     p = _route_params(_SCORING[scoring], n_groups, n_groups if top_groups is None else top_groups,
                       _GROUP_SCORE[group_score], top_k, int(renormalize), scale)
-    ids = torch.empty((tokens, max(top_k, 0)), dtype=torch.int32, device=logits.device)
-    weights = torch.empty_like(ids, dtype=torch.float32)
+    ids = _empty((tokens, max(top_k, 0)), torch.int32, logits.device, stream)
+    weights = _empty(ids.shape, torch.float32, logits.device, stream)
     _run("gptq_moe_route", stream, (logits, bias, ids, weights), tokens, experts, _DT[logits.dtype], logits.data_ptr(),
          _row_stride(logits), _ptr(bias), ctypes.byref(p), ids.data_ptr(),
          weights.data_ptr())
@@ -641,10 +643,10 @@ def moe_group_tokens(ids: torch.Tensor, n_experts: int, workspace: torch.Tensor 
     if ids.dim() != 2 or not ids.is_contiguous() or ids.shape[1] < 1 or not 1 <= n_experts <= 1024:
         raise ValueError("ids must be contiguous [tokens, top_k], n_experts 1..1024")
     tokens, k = ids.shape
-    offsets = torch.empty(n_experts + 1, dtype=torch.int64, device=ids.device)
-    rows = torch.empty(tokens * k, dtype=torch.int32, device=ids.device)
-    place = torch.empty_like(ids)
-    ws = _scratch(WS_MOE_GROUP, 1, n_experts, k, tokens, ids.device, workspace)
+    offsets = _empty(n_experts + 1, torch.int64, ids.device, stream)
+    rows = _empty(tokens * k, torch.int32, ids.device, stream)
+    place = _empty(ids.shape, torch.int32, ids.device, stream)
+    ws = _scratch(WS_MOE_GROUP, 1, n_experts, k, tokens, ids.device, workspace, stream)
     _run("gptq_moe_group_tokens", stream, (ids, offsets, rows, place, ws), tokens, k, n_experts, ids.data_ptr(),
          offsets.data_ptr(), rows.data_ptr(), place.data_ptr(), _ptr(ws), _bytes(ws))
     return offsets, rows, place
@@ -663,7 +665,7 @@ def moe_combine(Y: torch.Tensor, place: torch.Tensor, weights: torch.Tensor, out
             place.is_contiguous() and weights.is_contiguous()):
         raise ValueError("place and weights must be contiguous [tokens, top_k]")
     (tokens, k), (rows, d) = place.shape, Y.shape
-    res = _out(out, (tokens, d), Y.dtype, Y.device)
+    res = _out(out, (tokens, d), Y.dtype, Y.device, stream)
     _run("gptq_moe_combine", stream, (Y, place, weights, res), tokens, k, rows, d, _DT[Y.dtype], Y.data_ptr(),
          _row_stride(Y), place.data_ptr(), weights.data_ptr(), res.data_ptr(), _row_stride(res))
     return res

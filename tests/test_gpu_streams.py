@@ -1,0 +1,81 @@
+"""Calls on another stream than the current one, while blocks that were freed on the current
+stream still have work queued there: the calls' outputs and scratch must not be such blocks."""
+import pytest
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+
+
+def lib():
+    from post_weight_quantization_03_amd import gptq
+    return gptq
+
+
+def flat(out):
+    return list(out) if isinstance(out, tuple) else [out]
+
+
+def raw(t):
+    return t.view(torch.uint8) if t.dtype.itemsize == 1 else t
+
+
+def calls():
+    g = lib()
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn(300, 256, generator=gen, device="cuda").to(torch.bfloat16)
+    W, WS = g.fp8_quantize(torch.randn(3, 192, 256, generator=gen, device="cuda"), 128)
+    ids, w = g.moe_route(torch.randn(6000, 3, generator=gen, device="cuda"), 2)
+    few = (ids[:300] % 3).contiguous()
+    off, rows, place = g.moe_group_tokens(few, 3)
+    y = torch.randn(600, 192, generator=gen, device="cuda")
+    logits = torch.randn(300, 64, generator=gen, device="cuda")
+    p = g.Params(group_size=128, act_order=True)
+    H, key, n = g.new_hessian(256)
+    g.accumulate_hessian(x, H, key, n)
+    U, perm, dead = g.prepare_hinv(H, key, p)
+    wf = W[0].float()
+    codes, scales, zeros, g_idx = g.quantize_layer(wf, U, perm, dead, p)
+    c4 = codes & 15
+    qw, qz, sf = g.pack_int4(c4, scales, zeros)
+    qs, order = g.w4a16_repack(qw, g_idx, 2)
+
+    torch.cuda.synchronize()
+    return {
+        "fp8_quantize": lambda st: g.fp8_quantize(x, stream=st),
+        "fp8_matmul": lambda st: g.fp8_matmul(x, W[0], WS[0], stream=st),
+        "fp8_matmul_grouped": lambda st: g.fp8_matmul_grouped(x, W, WS, off, rows, stream=st),
+        "moe_route": lambda st: g.moe_route(logits, 6, stream=st),
+        "moe_group_tokens": lambda st: g.moe_group_tokens(ids, 3, stream=st),
+        "moe_combine": lambda st: g.moe_combine(y, place, w[:300], stream=st),
+        "quantize_layer": lambda st: g.quantize_layer(wf, U, perm, dead, p, stream=st),
+        "pack_int4": lambda st: g.pack_int4(c4, scales, zeros, stream=st),
+        "w4a16_repack": lambda st: g.w4a16_repack(qw, g_idx, 2, stream=st),
+        "w4a16_matmul": lambda st: g.w4a16_matmul(x, qs, qz, sf, order, stream=st),
+        "prepare_hinv": lambda st: g.prepare_hinv(H, key, p, stream=st),
+    }
+
+
+NAMES = ["fp8_quantize", "fp8_matmul", "fp8_matmul_grouped", "moe_route", "moe_group_tokens", "moe_combine",
+         "quantize_layer", "pack_int4", "w4a16_repack", "w4a16_matmul", "prepare_hinv"]
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_blocks_with_work_queued_elsewhere_are_left_alone(name):
+    print(f"\n[gpu-case] {name}", flush=True)
+    call = calls()[name]
+    want = [t.clone() for t in flat(call(None))]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    # blocks of the outputs' and of scratch's sizes, read on the current stream after a pause and freed now
+    sizes = [t.numel() * t.element_size() for t in want] + [300 * 256 + 4 * 600, 1 << 16, 1 << 20]
+    kept = []
+    torch.cuda._sleep(40_000_000)
+    for size in sizes:
+        block = torch.full((size,), 7, dtype=torch.uint8, device="cuda")
+        kept.append(torch.empty_like(block))
+        kept[-1].copy_(block)
+        del block
+    got = flat(call(side))
+    torch.cuda.synchronize()
+    assert all(bool((k == 7).all()) for k in kept)
+    assert len(got) == len(want) and all(torch.equal(raw(a), raw(b)) for a, b in zip(got, want))

@@ -1,0 +1,102 @@
+"""Where the binding's own tensors come from when a call runs on another stream than the
+current one: from that stream, and known to the current one.  A block freed on the current
+stream may have work queued there that the other stream does not wait for.  Streams and
+kernels are stand-ins here, so that no GPU is needed."""
+import contextlib
+
+import pytest
+
+from post_weight_quantization_03_amd import gptq
+
+torch = pytest.importorskip("torch")
+
+
+class Stream:
+    def __init__(self, name):
+        self.name, self.cuda_stream = name, 0
+        self.device = torch.device("cuda", 0)
+
+
+class Library:
+    """Every call succeeds; sizes as the library gives them."""
+
+    def __init__(self, real):
+        self.gptq_workspace_size = real.gptq_workspace_size
+
+    def __getattr__(self, name):
+        return lambda *args: gptq.GPTQ_OK
+
+
+@pytest.fixture
+def streams(monkeypatch):
+    main, side, now = Stream("main"), Stream("side"), []
+    made, known = {}, {}
+    now.append(main)
+
+    @contextlib.contextmanager
+    def on(s):
+        now.append(s)
+        yield
+        now.pop()
+
+    def logged(real):
+        def make(*args, **kw):
+            t = real(*args, **kw)
+            made[id(t)] = (now[-1].name, t)
+            return t
+        return make
+
+    library = Library(gptq.lib())
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: now[-1])
+    monkeypatch.setattr(torch.cuda, "stream", on)
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: known.setdefault(id(t), set()).add(s.name),
+                        raising=False)
+    monkeypatch.setattr(gptq, "lib", lambda: library)
+    monkeypatch.setattr(gptq, "_run", lambda *args: None)
+    gptq._workspace_bytes.cache_clear()
+    for name in ("empty", "empty_like", "empty_strided"):
+        monkeypatch.setattr(torch, name, logged(getattr(torch, name)))
+    yield side, made, known
+    gptq._workspace_bytes.cache_clear()
+
+
+def calls():
+    i32 = dict(dtype=torch.int32)
+    x, w = torch.zeros(40, 128, dtype=torch.bfloat16), torch.zeros(64, 128).to(torch.float8_e4m3fn)
+    s, off = torch.ones(1, 1), torch.zeros(2, dtype=torch.int64)
+    H, key, n = torch.zeros(128, 128), torch.zeros(128, dtype=torch.float64), torch.zeros(1, dtype=torch.int64)
+    perm, dead, p = torch.zeros(128, **i32), torch.zeros(128, dtype=torch.uint8), gptq.Params()
+    codes = torch.zeros(64, 128, dtype=torch.uint8)
+    qw, qz = torch.zeros(16, 64, **i32), torch.zeros(1, 8, **i32)
+    return {
+        "fp8_quantize": lambda st: gptq.fp8_quantize(x, stream=st),
+        "fp8_quantize batch": lambda st: gptq.fp8_quantize(x[None], 128, stream=st),
+        "fp8_matmul": lambda st: gptq.fp8_matmul(x, w, s, stream=st),
+        "fp8_matmul_grouped": lambda st: gptq.fp8_matmul_grouped(x, w[None], s[None], off, stream=st),
+        "moe_route": lambda st: gptq.moe_route(torch.zeros(4, 8), 2, stream=st),
+        "moe_group_tokens": lambda st: gptq.moe_group_tokens(torch.zeros(9000, 2, **i32), 8, stream=st),
+        "moe_combine": lambda st: gptq.moe_combine(x, torch.zeros(4, 2, **i32), torch.zeros(4, 2), stream=st),
+        "accumulate_hessian": lambda st: gptq.accumulate_hessian(x, H, key, n, stream=st),
+        "accumulate_hessian_grouped": lambda st: gptq.accumulate_hessian_grouped(x, off, H[None], key, n, 40, stream=st),
+        "prepare_hinv": lambda st: gptq.prepare_hinv(H, key, p, stream=st),
+        "quantize_layer": lambda st: gptq.quantize_layer(x, H, perm, dead, p, stream=st),
+        "quantize_layer_noalloc": lambda st: gptq.quantize_layer_noalloc(x, H, perm, dead, p, stream=st),
+        "pack_int4": lambda st: gptq.pack_int4(codes, torch.ones(1, 64), torch.zeros(1, 64, dtype=torch.uint8), stream=st),
+        "w4a16_repack": lambda st: gptq.w4a16_repack(qw, perm, 1, stream=st),
+        "w4a16_matmul": lambda st: gptq.w4a16_matmul(x, qw, qz, torch.ones(1, 64, dtype=torch.float16), stream=st),
+    }
+
+
+@pytest.mark.parametrize("name", list(calls()))
+def test_tensors_come_from_the_stream_that_writes_them(name, streams):
+    side, made, known = streams
+    call = calls()[name]
+    made.clear()
+    call(side)
+    assert made
+    for i, (where, _) in made.items():
+        assert where == "side" and known.get(i) == {"main"}
+    made.clear()
+    known.clear()
+    call(None)
+    assert made and all(where == "main" for where, _ in made.values()) and not known
