@@ -424,3 +424,20 @@ def test_group_few_experts_many_slots(experts, slots):
         assert np.array_equal(off.cpu().numpy(), want_off)
         assert np.array_equal(rows.cpu().numpy(), want_rows)
         assert np.array_equal(place.cpu().numpy()[:, 0], want_place)
+
+
+def test_combine_past_32_bit_threads():
+    # one thread a token: more than 2^32 of them, in a grid whose second dimension is in use
+    tokens = 2 ** 32 + 600
+    y = torch.arange(1, 5, device="cuda").to(torch.bfloat16)[:, None].contiguous()
+    place = torch.full((tokens, 1), -1, dtype=torch.int32, device="cuda")
+    at = [0, 255, 2 ** 30 - 1, 2 ** 30, 2 ** 31, 2 ** 32 - 1, 2 ** 32, tokens - 1]
+    for n, i in enumerate(at):
+        place[i, 0] = n % 4
+    out = lib().moe_combine(y, place, torch.ones(tokens, 1, device="cuda"), out=torch.full(
+        (tokens, 1), 7.0, dtype=torch.bfloat16, device="cuda"))
+    for n, i in enumerate(at):
+        assert float(out[i, 0]) == 1 + n % 4
+    assert int(out.count_nonzero()) == len(at)
+    del place, out
+    torch.cuda.empty_cache()
