@@ -394,7 +394,9 @@ typedef struct {
  *   descending order; equal values (of groups and of experts): the lower index first
  *   ids[t, j]     int32 [n_tokens, top_k]   the chosen experts
  *   weights[t, j] fp32  [n_tokens, top_k]   scale * s, or scale * s / sum of the chosen s
- *                                           (0 where that sum is 0)
+ *                                           (0 where that sum is 0), in fp64 and rounded once;
+ *                                           the sum under a softmax is of fp32 exponentials
+ *                                           (scale * s within 2^-20 of its value)
  * An expert whose logit is -inf or NaN, or whose bias is -inf or NaN, is never chosen (a
  * masked logit also adds nothing to the softmax); where fewer than top_k experts can be
  * chosen the remaining ids are -1 with weight 0.  Softmax over logits of +inf shares the

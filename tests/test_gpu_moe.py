@@ -441,3 +441,18 @@ def test_combine_past_32_bit_threads():
     assert int(out.count_nonzero()) == len(at)
     del place, out
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("experts,k", [(64, 6), (256, 8), (96, 16), (384, 8)])
+def test_route_weights_are_rounded_once(experts, k):
+    # half a step of fp32, and what the fp64 values behind the two sides differ by (a few times
+    # 2^-53), except for the softmax's own sum: exponentials within 3 roundings of 2^-24, their
+    # arguments rounded by |l - m| 2^-24 (weighted by the scores at most 4.5 for 1024 experts)
+    rng = np.random.default_rng(experts)
+    logits = torch.from_numpy(3 * rng.standard_normal((500, experts))).float().cuda()
+    for scoring, renorm in itertools.product(("softmax", "sigmoid"), (False, True)):
+        ids, w = lib().moe_route(logits, k, scoring=scoring, renormalize=renorm)
+        want, ww = M.ref_route(logits.double().cpu().numpy(), k, scoring=scoring, renormalize=renorm)
+        assert np.array_equal(ids.cpu().numpy(), want)
+        err = np.abs(w.double().cpu().numpy() - ww) / ww
+        assert err.max() <= (1 + 2.0 ** -20 + (7.5 if scoring == "softmax" and not renorm else 0)) * 2.0 ** -24
