@@ -595,13 +595,15 @@ __global__ __launch_bounds__(WM* WN * 64) void fp8_tile_kernel(MmArgs a) {
   }
 }
 
+// Tiles of tm rows that a launch has workgroups for: grouped, as many as any ranges can make.
+int64_t tile_rows(const MmArgs& a, int tm) {
+  return a.off == nullptr ? (a.m + tm - 1) / tm : a.m / tm + std::min<int64_t>(a.experts, a.m);
+}
+
 template <int TM, int TN, int WM, int WN>
 gptq_status launch_tile(MmArgs a, hipStream_t stream) {
   a.tiles_n = (a.n + TN - 1) / TN;
-  const int64_t tiles = a.off == nullptr ? (a.m + TM - 1) / TM : a.m / TM + std::min<int64_t>(a.experts, a.m);
-  const int64_t grid = tiles * a.tiles_n;
-  if (grid > (1 << 22)) return GPTQ_ERR_UNSUPPORTED;
-  const dim3 g(static_cast<unsigned>(grid)), b(WM * WN * 64);
+  const dim3 g(static_cast<unsigned>(tile_rows(a, TM) * a.tiles_n)), b(WM * WN * 64);
   if (a.y_dtype == GPTQ_F32) GPTQ_LAUNCH((fp8_tile_kernel<TM, TN, WM, WN, kMmaExact>), g, b, 0, stream, a);
   else if (a.e8) GPTQ_LAUNCH((fp8_tile_kernel<TM, TN, WM, WN, kMmaE8M0>), g, b, 0, stream, a);
   else GPTQ_LAUNCH((fp8_tile_kernel<TM, TN, WM, WN, kMmaF32Scale>), g, b, 0, stream, a);
@@ -891,10 +893,8 @@ __global__ __launch_bounds__(NW * 64) void fp8_big_kernel(MmArgs a) {
 }
 
 gptq_status launch_big(MmArgs a, hipStream_t stream) {
-  a.order = {(a.n + 255) / 256, a.off == nullptr ? (a.m + 255) / 256 : a.m / 256 + std::min<int64_t>(a.experts, a.m)};
-  const int64_t grid = order_grid(a.order);
-  if (grid > (1 << 22)) return GPTQ_ERR_UNSUPPORTED;
-  const dim3 g(static_cast<unsigned>(grid));
+  a.order = {(a.n + 255) / 256, tile_rows(a, 256)};
+  const dim3 g(static_cast<unsigned>(order_grid(a.order)));
   const size_t lds = 2 * static_cast<size_t>(a.kb) * sizeof(float);
   if (a.e8) GPTQ_LAUNCH((fp8_big_kernel<kMmaE8M0, 4>), g, dim3(256), lds, stream, a);
   else GPTQ_LAUNCH((fp8_big_kernel<kMmaF32Scale, 8>), g, dim3(512), lds, stream, a);
@@ -1041,9 +1041,8 @@ gptq_status launch_mid_groups(const MmArgs& a, unsigned grid, hipStream_t stream
 }
 
 gptq_status launch_mid(MmArgs a, hipStream_t stream) {
-  a.order = {(a.n + 63) / 64, a.off == nullptr ? (a.m + 63) / 64 : a.m / 64 + std::min<int64_t>(a.experts, a.m)};
+  a.order = {(a.n + 63) / 64, tile_rows(a, 64)};
   const int64_t grid = order_grid(a.order);
-  if (grid > (1 << 22)) return GPTQ_ERR_UNSUPPORTED;
   if (mid_groups(a.kb, static_cast<double>(grid)) == 2) return launch_mid_groups<2>(a, static_cast<unsigned>(grid), stream);
   return launch_mid_groups<1>(a, static_cast<unsigned>(grid), stream);
 }
@@ -1175,10 +1174,7 @@ template <int FM, int WK, typename T>
 gptq_status launch_rows(MmArgs a, hipStream_t stream) {
   constexpr int TM = 16 * FM;
   a.tiles_n = (a.n + 15) / 16;
-  const int64_t tiles = a.off == nullptr ? (a.m + TM - 1) / TM : a.m / TM + std::min<int64_t>(a.experts, a.m);
-  const int64_t grid = tiles * a.tiles_n;
-  if (grid > (1 << 22)) return GPTQ_ERR_UNSUPPORTED;
-  const dim3 g(static_cast<unsigned>(grid)), b(WK * 64);
+  const dim3 g(static_cast<unsigned>(tile_rows(a, TM) * a.tiles_n)), b(WK * 64);
   const size_t lds = std::is_void_v<T> ? 0 : raw_lds(a, TM);
   if (a.y_dtype == GPTQ_F32) GPTQ_LAUNCH((fp8_rows_kernel<FM, WK, kMmaExact, T>), g, b, lds, stream, a);
   else if (a.e8) GPTQ_LAUNCH((fp8_rows_kernel<FM, WK, kMmaE8M0, T>), g, b, lds, stream, a);
@@ -1233,15 +1229,24 @@ Product choose_product(const MmArgs& a) {
   return best == t_tile ? kTile : best == t_big ? kBig : kRows;
 }
 
+// Rows of fp8_rows_kernel's tiles: 16 for grouped rows.
+int rows_tile(const MmArgs& a) { return a.off != nullptr || a.m <= 16 ? 16 : a.m <= 32 ? 32 : 64; }
+
+// Whether the launch is one the kernels number their tiles for (asked before anything is enqueued).
+bool launchable(const MmArgs& a, Product kind) {
+  const int tm = kind == kBig ? 256 : kind == kTile ? 128 : kind == kMid ? 64 : rows_tile(a);
+  const int tn = kind == kRows ? 16 : tm;
+  return tile_rows(a, tm) <= (1 << 22) / ((a.n + tn - 1) / tn);
+}
+
 gptq_status launch_product(const MmArgs& a, Product kind, hipStream_t stream) {
   if (kind == kMid) return launch_mid(a, stream);
   if (kind == kTile) return launch_tile<128, 128, 2, 2>(a, stream);
   if (kind == kBig) return launch_big(a, stream);
-  const bool grouped = a.off != nullptr;
-  // 16-row tiles for grouped rows; 8 waves along the inputs while each has 3 blocks or more
+  // 8 waves along the inputs while each has 3 blocks or more
   // (4096 x 4096 at 1 row: 5.5 us with 8, 6.5 with 4; 64 experts of 1408 x 2048, 96 rows: 35 and 24)
-  if (!grouped && a.m > 32) return launch_rows<4, 8, void>(a, stream);
-  if (!grouped && a.m > 16) return launch_rows<2, 8, void>(a, stream);
+  if (rows_tile(a) == 64) return launch_rows<4, 8, void>(a, stream);
+  if (rows_tile(a) == 32) return launch_rows<2, 8, void>(a, stream);
   return a.kb >= 24 ? launch_rows<1, 8, void>(a, stream) : launch_rows<1, 4, void>(a, stream);
 }
 
@@ -1293,11 +1298,15 @@ gptq_status fp8_matmul_enqueue(const Fp8Problem& p, hipStream_t stream) {
   if (a.off != nullptr && (a.m / 16 + 1) * a.experts > INT32_MAX) return GPTQ_ERR_UNSUPPORTED;
   a.X = static_cast<const uint8_t*>(p.X);
   a.ldx = p.ldx; a.xs = p.xs; a.xsr = p.xsr; a.xsb = p.xsb;
-  if (p.x_dtype == GPTQ_E4M3) return launch_product(a, choose_product(a), stream);
+  if (p.x_dtype == GPTQ_E4M3) {
+    const Product kind = choose_product(a);
+    return launchable(a, kind) ? launch_product(a, kind, stream) : GPTQ_ERR_UNSUPPORTED;
+  }
   const Fp8Layout l = fp8_layout(p.x_rows, p.k);
   if (p.x_rows > 0 && (p.workspace == nullptr || p.workspace_bytes < l.total)) return GPTQ_ERR_WORKSPACE;
   a.ldx = p.k;   // as the product will read them
   const Product kind = choose_product(a);
+  if (!launchable(a, kind)) return GPTQ_ERR_UNSUPPORTED;
   if (kind == kRows && rounds_itself(a)) {
     a.ldx = p.ldx;
     return p.x_dtype == GPTQ_BF16 ? launch_raw<BF16>(a, stream) : launch_raw<F16>(a, stream);

@@ -190,3 +190,15 @@ def test_group_workspace_tells_whether_it_is_used():
             assert need > 256
             assert gptq.lib().gptq_moe_group_tokens(slots, 1, experts, 16, 16, 16, 16, None, 0, None) == WS
             assert gptq.lib().gptq_moe_group_tokens(slots, 1, experts, 16, 16, 16, 16, 16, need - 1, None) == WS
+
+
+def test_too_many_tiles_are_refused_before_anything_is_enqueued():
+    # 16-bit rows are rounded by a launch of its own: without a GPU it would fail with another error
+    UNS, big = gptq.GPTQ_ERR_UNSUPPORTED, 1 << 62
+    for x, y in ((E4M3, BF16), (BF16, BF16), (F16, F32)):
+        for m in (1 << 25, 1 << 40):
+            a = {**MATMUL, "m": m, "n": 1 << 20, "k": 16, "ldx": 16, "xt": x, "yt": y, "ldy": 1 << 20, "wsp": 16, "wsb": big}
+            assert gptq.lib().gptq_fp8_matmul(*a.values()) == UNS
+    a = dict(batch=1024, xr=1 << 20, rows=1 << 20, n=1 << 24, k=16, xt=BF16, X=16, ldx=16, st=F32, xs=None, xsr=0,
+             xsb=0, W=16, ws=16, off=16, idx=None, yt=BF16, Y=16, ldy=1 << 24, wsp=16, wsb=big, stream=None)
+    assert gptq.lib().gptq_fp8_matmul_grouped(*a.values()) == UNS
