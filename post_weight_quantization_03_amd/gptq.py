@@ -143,26 +143,37 @@ def _check(status: int, what: str):
 _DT = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 
 
-def _stream(stream) -> int:
-    s = torch.cuda.current_stream() if stream is None else stream
-    return s.cuda_stream
+def _stream() -> int:
+    return torch.cuda.current_stream().cuda_stream
 
 
-def _empty(shape, dtype: torch.dtype, device, stream=None, strides=None) -> torch.Tensor:
-    """A new tensor that kernels on ``stream`` (None: the current one) write.  On another stream
-    than the current one its memory comes from that stream's blocks: one freed on the current
-    stream may still have work queued there, which that stream would not wait for.  The current
-    stream is told to the caching allocator, since the caller goes on to use the tensor there."""
-    if stream is not None:
-        current = torch.cuda.current_stream(stream.device)
-        if stream != current:
-            with torch.cuda.stream(stream):
-                t = _empty(shape, dtype, device, None, strides)
-            t.record_stream(current)
-            return t
-    if strides is not None:
-        return torch.empty_strided(shape, strides, dtype=dtype, device=device)
-    return torch.empty(shape, dtype=dtype, device=device)
+def _tensors(v):
+    if isinstance(v, torch.Tensor):
+        yield v
+    elif isinstance(v, (tuple, list, dict)):
+        for x in v.values() if isinstance(v, dict) else v:
+            yield from _tensors(x)
+
+
+def _on(stream, call, *args):
+    """``call(*args)`` with ``stream`` as the current one, so that also the call's own tensors come
+    from that stream's memory: a block freed on the caller's stream may still have work queued
+    there, which the other stream would not wait for.  The caching allocator is told that the
+    caller's tensors are in use on that stream and the results on the caller's: they may be freed
+    before the work queued there is done."""
+    current = torch.cuda.current_stream(stream.device)
+    if stream == current:
+        return call(*args)
+    used = list(_tensors(args))
+    if any(t.device != stream.device for t in used):
+        raise ValueError("stream and tensors must be on one GPU")
+    with torch.cuda.stream(stream):
+        result = call(*args)
+    for t in used:
+        t.record_stream(stream)
+    for t in _tensors(result):
+        t.record_stream(current)
+    return result
 
 
 def _batched(t: torch.Tensor, nd: int) -> torch.Tensor:
@@ -175,10 +186,10 @@ def workspace_size(which: int, batch: int, d_out: int, d_in: int, n_tokens_hint:
     return int(lib().gptq_workspace_size(which, batch, d_out, d_in, n_tokens_hint, ctypes.byref(p)))
 
 
-def _workspace(nbytes: int, device, workspace: torch.Tensor | None, stream=None) -> torch.Tensor:
+def _workspace(nbytes: int, device, workspace: torch.Tensor | None) -> torch.Tensor:
     if workspace is not None and workspace.numel() >= nbytes:
         return workspace
-    return _empty(max(nbytes, 1), torch.uint8, device, stream)
+    return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
 
 
 def new_hessian(d_in: int, batch: int | None = None, device="cuda"):
@@ -192,6 +203,8 @@ def new_hessian(d_in: int, batch: int | None = None, device="cuda"):
 def accumulate_hessian(X: torch.Tensor, H: torch.Tensor, diag_key: torch.Tensor, n_seen: torch.Tensor,
                        workspace: torch.Tensor | None = None, stream=None) -> None:
     """H += 2 X^T X, diag_key += 2 sum x^2 (fp64), n_seen += n for token-major X [(batch,) n, d_in]."""
+    if stream is not None:
+        return _on(stream, accumulate_hessian, X, H, diag_key, n_seen, workspace)
     Xb = _batched(X, 2)
     Hb = _batched(H, 2)
     batch, n, d_in = Xb.shape
@@ -201,11 +214,11 @@ def accumulate_hessian(X: torch.Tensor, H: torch.Tensor, diag_key: torch.Tensor,
         raise ValueError("shape mismatch between X, H, diag_key, n_seen")
     if Xb.stride(2) != 1 or not Hb.is_contiguous() or not diag_key.is_contiguous():
         raise ValueError("X rows must be contiguous; H and diag_key contiguous")
-    ws = _workspace(workspace_size(WS_HESSIAN, batch, 0, d_in, n), X.device, workspace, stream)
+    ws = _workspace(workspace_size(WS_HESSIAN, batch, 0, d_in, n), X.device, workspace)
     _check(lib().gptq_accumulate_hessian(batch, d_in, n, _DT[X.dtype], Xb.data_ptr(), Xb.stride(1),
                                          Xb.stride(0) if batch > 1 else n * Xb.stride(1), Hb.data_ptr(),
                                          d_in * d_in, diag_key.data_ptr(), n_seen.data_ptr(), ws.data_ptr(),
-                                         ws.numel(), _stream(stream)), "gptq_accumulate_hessian")
+                                         ws.numel(), _stream()), "gptq_accumulate_hessian")
 
 
 def accumulate_hessian_grouped(X: torch.Tensor, token_offsets: torch.Tensor, H: torch.Tensor, diag_key: torch.Tensor,
@@ -214,6 +227,8 @@ def accumulate_hessian_grouped(X: torch.Tensor, token_offsets: torch.Tensor, H: 
     """Per-problem token ranges of one buffer: problem e accumulates rows token_offsets[e] ..
     token_offsets[e + 1] - 1 of token-major X [total, d_in] (at most ``max_tokens`` rows each,
     the largest count the caller expects); n_seen[e] += the rows it took."""
+    if stream is not None:
+        return _on(stream, accumulate_hessian_grouped, X, token_offsets, H, diag_key, n_seen, max_tokens, workspace)
     total, d_in = X.shape
     batch = token_offsets.numel() - 1
     Hb = _batched(H, 2)
@@ -225,11 +240,11 @@ def accumulate_hessian_grouped(X: torch.Tensor, token_offsets: torch.Tensor, H: 
         raise ValueError("shape mismatch between token_offsets, H, diag_key, n_seen")
     if X.stride(1) != 1 or not Hb.is_contiguous() or not diag_key.is_contiguous():
         raise ValueError("X rows must be contiguous; H and diag_key contiguous")
-    ws = _workspace(workspace_size(WS_HESSIAN, batch, 0, d_in, max_tokens), X.device, workspace, stream)
+    ws = _workspace(workspace_size(WS_HESSIAN, batch, 0, d_in, max_tokens), X.device, workspace)
     _check(lib().gptq_accumulate_hessian_grouped(batch, d_in, total, max_tokens, _DT[X.dtype], X.data_ptr(),
                                                  X.stride(0), token_offsets.data_ptr(), Hb.data_ptr(), d_in * d_in,
                                                  diag_key.data_ptr(), n_seen.data_ptr(), ws.data_ptr(), ws.numel(),
-                                                 _stream(stream)), "gptq_accumulate_hessian_grouped")
+                                                 _stream()), "gptq_accumulate_hessian_grouped")
 
 
 class HessianHook:
@@ -260,19 +275,21 @@ def prepare_hinv(H: torch.Tensor, diag_key: torch.Tensor, params: Params, worksp
                  stream=None):
     """-> (U fp32 [(batch,) d_in, d_in], perm int32 [(batch,) d_in], dead uint8 [(batch,) d_in]).
     Raises NotSPDError if the damped Hessian has no Cholesky factor."""
+    if stream is not None:
+        return _on(stream, prepare_hinv, H, diag_key, params, workspace)
     Hb = _batched(H, 2)
     batch, d_in, _ = Hb.shape
     if not Hb.is_contiguous() or not diag_key.is_contiguous():
         raise ValueError("H and diag_key must be contiguous")
     shp = H.shape[:-1]
-    U = _empty(H.shape, torch.float32, H.device, stream)
-    perm = _empty(shp, torch.int32, H.device, stream)
-    dead = _empty(shp, torch.uint8, H.device, stream)
-    ws = _workspace(workspace_size(WS_PREPARE, batch, 0, d_in, 0, params), H.device, workspace, stream)
+    U = torch.empty(*H.shape, dtype=torch.float32, device=H.device)
+    perm = torch.empty(*shp, dtype=torch.int32, device=H.device)
+    dead = torch.empty(*shp, dtype=torch.uint8, device=H.device)
+    ws = _workspace(workspace_size(WS_PREPARE, batch, 0, d_in, 0, params), H.device, workspace)
     p = params.c()
     _check(lib().gptq_prepare_hinv(batch, d_in, Hb.data_ptr(), d_in * d_in, diag_key.data_ptr(), ctypes.byref(p),
                                    U.data_ptr(), d_in * d_in, perm.data_ptr(), dead.data_ptr(), ws.data_ptr(),
-                                   ws.numel(), _stream(stream)), "gptq_prepare_hinv")
+                                   ws.numel(), _stream()), "gptq_prepare_hinv")
     return U, perm, dead
 
 
@@ -280,6 +297,8 @@ def quantize_layer(W: torch.Tensor, U: torch.Tensor, perm: torch.Tensor, dead: t
                    workspace: torch.Tensor | None = None, stream=None):
     """-> (codes uint8 [(b,) d_out, d_in] original order, scales fp32 [(b,) n_groups, d_out],
     zeros uint8 [(b,) n_groups, d_out], g_idx int32 [(b,) d_in])."""
+    if stream is not None:
+        return _on(stream, quantize_layer, W, U, perm, dead, params, workspace)
     Wb = _batched(W, 2)
     batch, d_out, d_in = Wb.shape
     if W.dtype not in _DT:
@@ -288,17 +307,17 @@ def quantize_layer(W: torch.Tensor, U: torch.Tensor, perm: torch.Tensor, dead: t
         raise ValueError("W rows, U, perm and dead must be contiguous")
     ng = params.n_groups(d_in)
     lead = W.shape[:-2]
-    codes = _empty((*lead, d_out, d_in), torch.uint8, W.device, stream)
-    scales = _empty((*lead, ng, d_out), torch.float32, W.device, stream)
-    zeros = _empty((*lead, ng, d_out), torch.uint8, W.device, stream)
-    g_idx = _empty((*lead, d_in), torch.int32, W.device, stream)
-    ws = _workspace(workspace_size(WS_QUANTIZE, batch, d_out, d_in, 0, params), W.device, workspace, stream)
+    codes = torch.empty(*lead, d_out, d_in, dtype=torch.uint8, device=W.device)
+    scales = torch.empty(*lead, ng, d_out, dtype=torch.float32, device=W.device)
+    zeros = torch.empty(*lead, ng, d_out, dtype=torch.uint8, device=W.device)
+    g_idx = torch.empty(*lead, d_in, dtype=torch.int32, device=W.device)
+    ws = _workspace(workspace_size(WS_QUANTIZE, batch, d_out, d_in, 0, params), W.device, workspace)
     p = params.c()
     _check(lib().gptq_quantize_layer(batch, d_out, d_in, _DT[W.dtype], Wb.data_ptr(), Wb.stride(1),
                                      Wb.stride(0) if batch > 1 else d_out * Wb.stride(1), U.data_ptr(),
                                      d_in * d_in, perm.data_ptr(), dead.data_ptr(), ctypes.byref(p),
                                      codes.data_ptr(), scales.data_ptr(), zeros.data_ptr(), g_idx.data_ptr(),
-                                     ws.data_ptr(), ws.numel(), _stream(stream)), "gptq_quantize_layer")
+                                     ws.data_ptr(), ws.numel(), _stream()), "gptq_quantize_layer")
     return codes, scales, zeros, g_idx
 
 
@@ -308,6 +327,8 @@ def quantize_layer_noalloc(W: torch.Tensor, U: torch.Tensor, perm: torch.Tensor,
     library's fixed device scratch instead of a workspace.  ``out`` = (codes, scales,
     zeros, g_idx) preallocated by the caller (shapes as returned by quantize_layer);
     without it they are allocated here, but the C call itself never allocates."""
+    if stream is not None:
+        return _on(stream, quantize_layer_noalloc, W, U, perm, dead, params, out)
     Wb = _batched(W, 2)
     batch, d_out, d_in = Wb.shape
     if W.dtype not in _DT:
@@ -317,10 +338,10 @@ def quantize_layer_noalloc(W: torch.Tensor, U: torch.Tensor, perm: torch.Tensor,
     ng = params.n_groups(d_in)
     lead = W.shape[:-2]
     if out is None:
-        out = (_empty((*lead, d_out, d_in), torch.uint8, W.device, stream),
-               _empty((*lead, ng, d_out), torch.float32, W.device, stream),
-               _empty((*lead, ng, d_out), torch.uint8, W.device, stream),
-               _empty((*lead, d_in), torch.int32, W.device, stream))
+        out = (torch.empty(*lead, d_out, d_in, dtype=torch.uint8, device=W.device),
+               torch.empty(*lead, ng, d_out, dtype=torch.float32, device=W.device),
+               torch.empty(*lead, ng, d_out, dtype=torch.uint8, device=W.device),
+               torch.empty(*lead, d_in, dtype=torch.int32, device=W.device))
     codes, scales, zeros, g_idx = out
     want = [((*lead, d_out, d_in), torch.uint8), ((*lead, ng, d_out), torch.float32),
             ((*lead, ng, d_out), torch.uint8), ((*lead, d_in), torch.int32)]
@@ -332,24 +353,26 @@ def quantize_layer_noalloc(W: torch.Tensor, U: torch.Tensor, perm: torch.Tensor,
                                              Wb.stride(0) if batch > 1 else d_out * Wb.stride(1), U.data_ptr(),
                                              d_in * d_in, perm.data_ptr(), dead.data_ptr(), ctypes.byref(p),
                                              codes.data_ptr(), scales.data_ptr(), zeros.data_ptr(), g_idx.data_ptr(),
-                                             _stream(stream)), "gptq_quantize_layer_noalloc")
+                                             _stream()), "gptq_quantize_layer_noalloc")
     return codes, scales, zeros, g_idx
 
 
 def pack_int4(codes: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor, stream=None):
     """-> (qweight int32 [(b,) d_in/8, d_out], qzeros int32 [(b,) n_groups, d_out/8],
     scales fp16 [(b,) n_groups, d_out])."""
+    if stream is not None:
+        return _on(stream, pack_int4, codes, scales, zeros)
     cb = _batched(codes, 2)
     batch, d_out, d_in = cb.shape
     ng = scales.shape[-2]
     if not (codes.is_contiguous() and scales.is_contiguous() and zeros.is_contiguous()):
         raise ValueError("codes, scales and zeros must be contiguous")
     lead = codes.shape[:-2]
-    qweight = _empty((*lead, d_in // 8, d_out), torch.int32, codes.device, stream)
-    qzeros = _empty((*lead, ng, d_out // 8), torch.int32, codes.device, stream)
-    sf16 = _empty((*lead, ng, d_out), torch.float16, codes.device, stream)
+    qweight = torch.empty(*lead, d_in // 8, d_out, dtype=torch.int32, device=codes.device)
+    qzeros = torch.empty(*lead, ng, d_out // 8, dtype=torch.int32, device=codes.device)
+    sf16 = torch.empty(*lead, ng, d_out, dtype=torch.float16, device=codes.device)
     _check(lib().gptq_pack_int4(batch, d_out, d_in, ng, codes.data_ptr(), scales.data_ptr(), zeros.data_ptr(),
-                                qweight.data_ptr(), qzeros.data_ptr(), sf16.data_ptr(), _stream(stream)),
+                                qweight.data_ptr(), qzeros.data_ptr(), sf16.data_ptr(), _stream()),
            "gptq_pack_int4")
     return qweight, qzeros, sf16
 
@@ -361,6 +384,8 @@ def w4a16_repack(qweight: torch.Tensor, g_idx: torch.Tensor, n_groups: int, work
                  stream=None):
     """Serving layout of a packed layer: (qweight_s int32 [(b,) d_in/8, d_out], order int32
     [(b,) d_in]) with the inputs sorted by group.  Raises GptqError on a malformed g_idx."""
+    if stream is not None:
+        return _on(stream, w4a16_repack, qweight, g_idx, n_groups, workspace)
     qb = _batched(qweight, 2)
     batch, rows8, d_out = qb.shape
     d_in = rows8 * 8
@@ -368,11 +393,11 @@ def w4a16_repack(qweight: torch.Tensor, g_idx: torch.Tensor, n_groups: int, work
         raise TypeError("qweight and g_idx must be int32, g_idx [(b,) d_in]")
     if not qweight.is_contiguous() or not g_idx.is_contiguous():
         raise ValueError("qweight and g_idx must be contiguous")
-    qs = _empty(qweight.shape, torch.int32, qweight.device, stream)
-    order = _empty(g_idx.shape, torch.int32, g_idx.device, stream)
-    ws = _workspace(workspace_size(WS_W4A16_REPACK, batch, d_out, d_in), qweight.device, workspace, stream)
+    qs = torch.empty_like(qweight)
+    order = torch.empty_like(g_idx)
+    ws = _workspace(workspace_size(WS_W4A16_REPACK, batch, d_out, d_in), qweight.device, workspace)
     _check(lib().gptq_w4a16_repack(batch, d_out, d_in, n_groups, qweight.data_ptr(), g_idx.data_ptr(), qs.data_ptr(),
-                                   order.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream)), "gptq_w4a16_repack")
+                                   order.data_ptr(), ws.data_ptr(), ws.numel(), _stream()), "gptq_w4a16_repack")
     return qs, order
 
 
@@ -382,6 +407,8 @@ def w4a16_matmul(X: torch.Tensor, qweight_s: torch.Tensor, qzeros: torch.Tensor,
     """Y fp32 [m, d_out] = X What^T from the packed tensors (X [m, d_in] bf16 / fp16).
     ``order`` from :func:`w4a16_repack`, or None when qweight is in input order with
     contiguous groups."""
+    if stream is not None:
+        return _on(stream, w4a16_matmul, X, qweight_s, qzeros, scales_f16, order, out, workspace)
     m, d_in = X.shape
     d_out = qweight_s.shape[-1]
     n_groups = scales_f16.shape[0]
@@ -393,13 +420,13 @@ def w4a16_matmul(X: torch.Tensor, qweight_s: torch.Tensor, qzeros: torch.Tensor,
         raise ValueError("packed tensors must be contiguous")
     if order is not None and (order.dtype != torch.int32 or order.numel() != d_in or not order.is_contiguous()):
         raise ValueError("order must be contiguous int32 [d_in]")
-    Y = out if out is not None else _empty((m, d_out), torch.float32, X.device, stream)
+    Y = out if out is not None else torch.empty(m, d_out, dtype=torch.float32, device=X.device)
     gsz = -1 if n_groups == 1 else d_in // n_groups
-    ws = _workspace(workspace_size(WS_W4A16, 1, d_out, d_in, m, Params(group_size=gsz)), X.device, workspace, stream)
+    ws = _workspace(workspace_size(WS_W4A16, 1, d_out, d_in, m, Params(group_size=gsz)), X.device, workspace)
     _check(lib().gptq_w4a16_matmul(m, d_out, d_in, n_groups, _DT[X.dtype], X.data_ptr(), X.stride(0),
                                    qweight_s.data_ptr(), None if order is None else order.data_ptr(), qzeros.data_ptr(),
                                    scales_f16.data_ptr(), Y.data_ptr(), Y.stride(0), ws.data_ptr(), ws.numel(),
-                                   _stream(stream)), "gptq_w4a16_matmul")
+                                   _stream()), "gptq_w4a16_matmul")
     return Y
 
 
@@ -408,11 +435,11 @@ _SDT = {torch.float32: 0, torch.float8_e8m0fnu: E8M0}
 _FP8_BLOCK = 128
 
 
-def _run(what: str, stream, tensors, *args) -> None:
+def _run(what: str, tensors, *args) -> None:
     """The library's call ``what`` with ``args`` and a stream handle, for tensors (or None) of
-    one GPU, with that GPU as the current device: on ``stream``, or on its current stream.
-    The first of ``tensors`` is not None.  Small calls last a few microseconds, so this path
-    creates no Stream object (2.8 us of a 12.9 us call)."""
+    one GPU, with that GPU as the current device, on its current stream.  The first of
+    ``tensors`` is not None.  Small calls last a few microseconds, so this path creates no Stream
+    object (2.8 us of a 12.9 us call)."""
     device = tensors[0].get_device()
     if device < 0:
         raise ValueError("tensors must be on a GPU")
@@ -420,19 +447,11 @@ def _run(what: str, stream, tensors, *args) -> None:
         if t is not None and t.get_device() != device:
             raise ValueError("tensors must be on one GPU")
     fn = getattr(_lib or lib(), what)
-    if stream is None and device == torch._C._cuda_getDevice():
+    if device == torch._C._cuda_getDevice():
         status = fn(*args, torch._C._cuda_getCurrentRawStream(device))
     else:
-        if stream is not None and stream.device.index != device:
-            raise ValueError("stream and tensors must be on one GPU")
         with torch.cuda.device(device):
-            status = fn(*args, _stream(stream))
-        if stream is not None and stream != torch.cuda.current_stream(stream.device):
-            # the caller's tensors too may be freed on the current stream before a call on
-            # another one is done with them
-            for t in tensors:
-                if t is not None:
-                    t.record_stream(stream)
+            status = fn(*args, _stream())
     if status != GPTQ_OK:
         _check(status, what)
 
@@ -442,7 +461,7 @@ def _workspace_bytes(which: int, batch: int, d_out: int, d_in: int, hint: int) -
     return workspace_size(which, batch, d_out, d_in, hint)
 
 
-def _scratch(which, batch, d_out, d_in, hint, device, workspace, stream) -> torch.Tensor | None:
+def _scratch(which, batch, d_out, d_in, hint, device, workspace) -> torch.Tensor | None:
     """The caller's workspace if it is large enough, else a new one; None where the call needs none."""
     nbytes = _workspace_bytes(which, batch, d_out, d_in, hint)
     if nbytes <= 256:   # the size of a workspace that nothing is kept in
@@ -452,7 +471,7 @@ def _scratch(which, batch, d_out, d_in, hint, device, workspace, stream) -> torc
             raise ValueError("workspace must be contiguous")
         if _bytes(workspace) >= nbytes:
             return workspace
-    return _empty(nbytes, torch.uint8, device, stream)
+    return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
 def _ptr(t):
@@ -468,9 +487,9 @@ def _route_params(*values) -> _RouteParams:
     return _RouteParams(*values)
 
 
-def _out(out, shape, dtype, device, stream):
+def _out(out, shape, dtype, device):
     if out is None:
-        return _empty(shape, dtype, device, stream)
+        return torch.empty(shape, dtype=dtype, device=device)
     if tuple(out.shape) != tuple(shape) or out.dtype != dtype or out.stride(-1) != 1 or (
             len(shape) > 1 and shape[0] > 1 and out.stride(0) < shape[-1]):
         raise ValueError(f"out must be {dtype} of shape {tuple(shape)} with contiguous rows")
@@ -490,6 +509,8 @@ def fp8_quantize(X: torch.Tensor, block_rows: int = 1, scale_dtype: torch.dtype 
     (``scale_dtype`` float8_e8m0fnu).  block_rows 1 for activations, 128 for weights.  The
     scales of activations are stored block by block (stride 1 along the rows), as the products
     read them."""
+    if stream is not None:
+        return _on(stream, fp8_quantize, X, block_rows, scale_dtype)
     if X.dtype not in _DT or scale_dtype not in _SDT:
         raise TypeError("X must be fp32/bf16/fp16, scale_dtype float32 or float8_e8m0fnu")
     if block_rows not in (1, _FP8_BLOCK) or X.dim() not in (2, 3):
@@ -502,12 +523,12 @@ def fp8_quantize(X: torch.Tensor, block_rows: int = 1, scale_dtype: torch.dtype 
         raise ValueError("X rows must be contiguous")
     rb, cb = -(-rows // block_rows), -(-cols // _FP8_BLOCK)
     ld_row, ld_block = (1, max(rb, 1)) if block_rows == 1 else (cb, 1)
-    q = _empty(X.shape, torch.float8_e4m3fn, X.device, stream)
+    q = torch.empty(X.shape, dtype=torch.float8_e4m3fn, device=X.device)
     if X.dim() == 2:
-        S = _empty((rb, cb), scale_dtype, X.device, stream, (ld_row, ld_block))
+        S = torch.empty_strided((rb, cb), (ld_row, ld_block), dtype=scale_dtype, device=X.device)
     else:
-        S = _empty((batch, rb, cb), scale_dtype, X.device, stream, (rb * cb, ld_row, ld_block))
-    _run("gptq_fp8_quantize", stream, (X, q, S), batch, rows, cols, _DT[X.dtype], X.data_ptr(), _row_stride(Xb),
+        S = torch.empty_strided((batch, rb, cb), (rb * cb, ld_row, ld_block), dtype=scale_dtype, device=X.device)
+    _run("gptq_fp8_quantize", (X, q, S), batch, rows, cols, _DT[X.dtype], X.data_ptr(), _row_stride(Xb),
          Xb.stride(0), block_rows, _SDT[scale_dtype], q.data_ptr(), S.data_ptr(), ld_row, ld_block, rb * cb)
     return q, S
 
@@ -556,14 +577,15 @@ def fp8_matmul(X: torch.Tensor, qweight: torch.Tensor, w_scales: torch.Tensor, x
     blocks (:func:`fp8_quantize` with block_rows 128).  X [m, d_in] is float8_e4m3fn with
     ``x_scales`` [m, ceil(d_in / 128)], or bf16 / fp16, then rounded first as
     :func:`fp8_quantize` does."""
+    if stream is not None:
+        return _on(stream, fp8_matmul, X, qweight, w_scales, x_scales, out_dtype, out, workspace)
     if qweight.dim() != 2:
         raise ValueError("qweight must be [d_out, d_in]")
     sdt = _fp8_operands(X, x_scales, qweight, w_scales, out_dtype)
     (m, d_in), d_out = X.shape, qweight.shape[0]
-    Y = _out(out, (m, d_out), out_dtype, X.device, stream)
-    ws = None if X.dtype == torch.float8_e4m3fn else _scratch(WS_FP8_MATMUL, 1, d_out, d_in, m, X.device, workspace,
-                                                              stream)
-    _run("gptq_fp8_matmul", stream, (X, qweight, w_scales, x_scales, Y, ws), m, d_out, d_in, _DT.get(X.dtype, E4M3),
+    Y = _out(out, (m, d_out), out_dtype, X.device)
+    ws = None if X.dtype == torch.float8_e4m3fn else _scratch(WS_FP8_MATMUL, 1, d_out, d_in, m, X.device, workspace)
+    _run("gptq_fp8_matmul", (X, qweight, w_scales, x_scales, Y, ws), m, d_out, d_in, _DT.get(X.dtype, E4M3),
          X.data_ptr(), _row_stride(X), sdt, *_fp8_scales(x_scales), qweight.data_ptr(), w_scales.data_ptr(),
          _DT[out_dtype], Y.data_ptr(), _row_stride(Y), _ptr(ws),
          _bytes(ws))
@@ -579,6 +601,9 @@ def fp8_matmul_grouped(X: torch.Tensor, qweight: torch.Tensor, w_scales: torch.T
     expert e's weights qweight [experts, d_out, d_in]; operands otherwise as in
     :func:`fp8_matmul`.  ``token_offsets`` int64 [experts + 1] and ``row_index`` int32 [n_rows]
     come from :func:`moe_group_tokens`.  Rows outside every range are not written."""
+    if stream is not None:
+        return _on(stream, fp8_matmul_grouped, X, qweight, w_scales, token_offsets, row_index, x_scales,
+                   out_dtype, out, workspace)
     if qweight.dim() != 3 or qweight.shape[0] < 1:
         raise ValueError("qweight must be [experts, d_out, d_in]")
     sdt = _fp8_operands(X, x_scales, qweight, w_scales, out_dtype)
@@ -589,10 +614,10 @@ def fp8_matmul_grouped(X: torch.Tensor, qweight: torch.Tensor, w_scales: torch.T
                                   not row_index.is_contiguous()):
         raise ValueError("row_index must be contiguous int32 [n_rows]")
     n_rows = x_rows if row_index is None else row_index.numel()
-    Y = _out(out, (n_rows, d_out), out_dtype, X.device, stream)
+    Y = _out(out, (n_rows, d_out), out_dtype, X.device)
     ws = None if X.dtype == torch.float8_e4m3fn else _scratch(WS_FP8_GROUPED, experts, d_out, d_in, x_rows, X.device,
-                                                              workspace, stream)
-    _run("gptq_fp8_matmul_grouped", stream, (X, qweight, w_scales, token_offsets, row_index, x_scales, Y, ws), experts,
+                                                              workspace)
+    _run("gptq_fp8_matmul_grouped", (X, qweight, w_scales, token_offsets, row_index, x_scales, Y, ws), experts,
          x_rows, n_rows, d_out, d_in, _DT.get(X.dtype, E4M3), X.data_ptr(), _row_stride(X), sdt,
          *_fp8_scales(x_scales), qweight.data_ptr(), w_scales.data_ptr(), token_offsets.data_ptr(),
          _ptr(row_index), _DT[out_dtype], Y.data_ptr(), _row_stride(Y),
@@ -613,6 +638,9 @@ def moe_route(logits: torch.Tensor, top_k: int, bias: torch.Tensor | None = None
     equal values by index; weights are ``scale`` times the scores without bias, divided by
     their sum with ``renormalize``.  Logits or biases of -inf or NaN take an expert out; ids
     are -1 (weight 0) where none is left."""
+    if stream is not None:
+        return _on(stream, moe_route, logits, top_k, bias, scoring, n_groups, top_groups, group_score,
+                   renormalize, scale)
     if logits.dtype not in _DT or (bias is not None and bias.dtype != torch.float32):
         raise TypeError("logits must be fp32/bf16/fp16, bias fp32")
     if logits.dim() != 2 or logits.shape[1] < 1 or (logits.stride(1) != 1 and logits.shape[1] > 1):
@@ -624,11 +652,10 @@ def moe_route(logits: torch.Tensor, top_k: int, bias: torch.Tensor | None = None
         raise ValueError("scoring must be 'softmax' or 'sigmoid', group_score 'max' or 'top2'")
     p = _route_params(_SCORING[scoring], n_groups, n_groups if top_groups is None else top_groups,
                       _GROUP_SCORE[group_score], top_k, int(renormalize), scale)
-    ids = _empty((tokens, max(top_k, 0)), torch.int32, logits.device, stream)
-    weights = _empty(ids.shape, torch.float32, logits.device, stream)
-    _run("gptq_moe_route", stream, (logits, bias, ids, weights), tokens, experts, _DT[logits.dtype], logits.data_ptr(),
-         _row_stride(logits), _ptr(bias), ctypes.byref(p), ids.data_ptr(),
-         weights.data_ptr())
+    ids = torch.empty((tokens, max(top_k, 0)), dtype=torch.int32, device=logits.device)
+    weights = torch.empty_like(ids, dtype=torch.float32)
+    _run("gptq_moe_route", (logits, bias, ids, weights), tokens, experts, _DT[logits.dtype], logits.data_ptr(),
+         _row_stride(logits), _ptr(bias), ctypes.byref(p), ids.data_ptr(), weights.data_ptr())
     return ids, weights
 
 
@@ -638,16 +665,18 @@ def moe_group_tokens(ids: torch.Tensor, n_experts: int, workspace: torch.Tensor 
     expert.  ``token_offsets`` are the experts' ranges that accumulate_hessian_grouped and
     fp8_matmul_grouped take, ``row_index`` the token at each position (-1 behind the last
     range), ``place`` the position of each choice (-1 for an id outside [0, n_experts))."""
+    if stream is not None:
+        return _on(stream, moe_group_tokens, ids, n_experts, workspace)
     if ids.dtype != torch.int32:
         raise TypeError("ids must be int32")
     if ids.dim() != 2 or not ids.is_contiguous() or ids.shape[1] < 1 or not 1 <= n_experts <= 1024:
         raise ValueError("ids must be contiguous [tokens, top_k], n_experts 1..1024")
     tokens, k = ids.shape
-    offsets = _empty(n_experts + 1, torch.int64, ids.device, stream)
-    rows = _empty(tokens * k, torch.int32, ids.device, stream)
-    place = _empty(ids.shape, torch.int32, ids.device, stream)
-    ws = _scratch(WS_MOE_GROUP, 1, n_experts, k, tokens, ids.device, workspace, stream)
-    _run("gptq_moe_group_tokens", stream, (ids, offsets, rows, place, ws), tokens, k, n_experts, ids.data_ptr(),
+    offsets = torch.empty(n_experts + 1, dtype=torch.int64, device=ids.device)
+    rows = torch.empty(tokens * k, dtype=torch.int32, device=ids.device)
+    place = torch.empty_like(ids)
+    ws = _scratch(WS_MOE_GROUP, 1, n_experts, k, tokens, ids.device, workspace)
+    _run("gptq_moe_group_tokens", (ids, offsets, rows, place, ws), tokens, k, n_experts, ids.data_ptr(),
          offsets.data_ptr(), rows.data_ptr(), place.data_ptr(), _ptr(ws), _bytes(ws))
     return offsets, rows, place
 
@@ -657,6 +686,8 @@ def moe_combine(Y: torch.Tensor, place: torch.Tensor, weights: torch.Tensor, out
     """out [tokens, d] (Y's type) = sum over j of weights[:, j] * Y[place[:, j]]: every token's
     expert outputs, summed in fp32 in the order of its choices; a place outside Y adds
     nothing."""
+    if stream is not None:
+        return _on(stream, moe_combine, Y, place, weights, out)
     if Y.dtype not in _DT or place.dtype != torch.int32 or weights.dtype != torch.float32:
         raise TypeError("Y must be fp32/bf16/fp16, place int32, weights fp32")
     if Y.dim() != 2 or Y.shape[1] < 1 or Y.stride(1) != 1:
@@ -665,8 +696,8 @@ def moe_combine(Y: torch.Tensor, place: torch.Tensor, weights: torch.Tensor, out
             place.is_contiguous() and weights.is_contiguous()):
         raise ValueError("place and weights must be contiguous [tokens, top_k]")
     (tokens, k), (rows, d) = place.shape, Y.shape
-    res = _out(out, (tokens, d), Y.dtype, Y.device, stream)
-    _run("gptq_moe_combine", stream, (Y, place, weights, res), tokens, k, rows, d, _DT[Y.dtype], Y.data_ptr(),
+    res = _out(out, (tokens, d), Y.dtype, Y.device)
+    _run("gptq_moe_combine", (Y, place, weights, res), tokens, k, rows, d, _DT[Y.dtype], Y.data_ptr(),
          _row_stride(Y), place.data_ptr(), weights.data_ptr(), res.data_ptr(), _row_stride(res))
     return res
 
@@ -688,13 +719,16 @@ def timing_read(which: int = TIME_SYRK):
 
 
 def gptq_layer(W: torch.Tensor, X_chunks, params: Params, stream=None):
-    """Whole layer: accumulate H over the chunks, prepare U, quantize.  Returns a dict."""
+    """Whole layer: accumulate H over the chunks (taken from X_chunks with ``stream`` as the current
+    one), prepare U, quantize.  Returns a dict."""
+    if stream is not None:
+        return _on(stream, gptq_layer, W, X_chunks, params)
     lead = W.shape[:-2]
     d_in = W.shape[-1]
     H, key, n = new_hessian(d_in, lead[0] if lead else None, W.device)
     for Xc in X_chunks:
-        accumulate_hessian(Xc, H, key, n, stream=stream)
-    U, perm, dead = prepare_hinv(H, key, params, stream=stream)
-    codes, scales, zeros, g_idx = quantize_layer(W, U, perm, dead, params, stream=stream)
+        accumulate_hessian(Xc, H, key, n)
+    U, perm, dead = prepare_hinv(H, key, params)
+    codes, scales, zeros, g_idx = quantize_layer(W, U, perm, dead, params)
     return dict(H=H, diag_key=key, n_seen=n, U=U, perm=perm, dead=dead, codes=codes, scales=scales,
                 zeros=zeros, g_idx=g_idx)

@@ -14,7 +14,7 @@ torch = pytest.importorskip("torch")
 class Stream:
     def __init__(self, name):
         self.name, self.cuda_stream = name, 0
-        self.device = torch.device("cuda", 0)
+        self.device = torch.device("cpu")
 
 
 class Library:
@@ -54,7 +54,7 @@ def streams(monkeypatch):
     monkeypatch.setattr(gptq, "lib", lambda: library)
     monkeypatch.setattr(gptq, "_run", lambda *args: None)
     gptq._workspace_bytes.cache_clear()
-    for name in ("empty", "empty_like", "empty_strided"):
+    for name in ("empty", "empty_like", "empty_strided", "zeros"):
         monkeypatch.setattr(torch, name, logged(getattr(torch, name)))
     yield side, made, known
     gptq._workspace_bytes.cache_clear()
@@ -67,22 +67,24 @@ def calls():
     H, key, n = torch.zeros(128, 128), torch.zeros(128, dtype=torch.float64), torch.zeros(1, dtype=torch.int64)
     perm, dead, p = torch.zeros(128, **i32), torch.zeros(128, dtype=torch.uint8), gptq.Params()
     codes = torch.zeros(64, 128, dtype=torch.uint8)
-    qw, qz = torch.zeros(16, 64, **i32), torch.zeros(1, 8, **i32)
+    qw, qz, zeros = torch.zeros(16, 64, **i32), torch.zeros(1, 8, **i32), torch.zeros(1, 64, dtype=torch.uint8)
+    logits, ids, place, cw = torch.zeros(4, 8), torch.zeros(9000, 2, **i32), torch.zeros(4, 2, **i32), torch.zeros(4, 2)
     return {
         "fp8_quantize": lambda st: gptq.fp8_quantize(x, stream=st),
         "fp8_quantize batch": lambda st: gptq.fp8_quantize(x[None], 128, stream=st),
         "fp8_matmul": lambda st: gptq.fp8_matmul(x, w, s, stream=st),
         "fp8_matmul_grouped": lambda st: gptq.fp8_matmul_grouped(x, w[None], s[None], off, stream=st),
-        "moe_route": lambda st: gptq.moe_route(torch.zeros(4, 8), 2, stream=st),
-        "moe_group_tokens": lambda st: gptq.moe_group_tokens(torch.zeros(9000, 2, **i32), 8, stream=st),
-        "moe_combine": lambda st: gptq.moe_combine(x, torch.zeros(4, 2, **i32), torch.zeros(4, 2), stream=st),
+        "moe_route": lambda st: gptq.moe_route(logits, 2, stream=st),
+        "moe_group_tokens": lambda st: gptq.moe_group_tokens(ids, 8, stream=st),
+        "moe_combine": lambda st: gptq.moe_combine(x, place, cw, stream=st),
         "accumulate_hessian": lambda st: gptq.accumulate_hessian(x, H, key, n, stream=st),
         "accumulate_hessian_grouped": lambda st: gptq.accumulate_hessian_grouped(x, off, H[None], key, n, 40, stream=st),
         "prepare_hinv": lambda st: gptq.prepare_hinv(H, key, p, stream=st),
         "quantize_layer": lambda st: gptq.quantize_layer(x, H, perm, dead, p, stream=st),
         "quantize_layer_noalloc": lambda st: gptq.quantize_layer_noalloc(x, H, perm, dead, p, stream=st),
-        "pack_int4": lambda st: gptq.pack_int4(codes, torch.ones(1, 64), torch.zeros(1, 64, dtype=torch.uint8), stream=st),
+        "pack_int4": lambda st: gptq.pack_int4(codes, torch.ones(1, 64), zeros, stream=st),
         "w4a16_repack": lambda st: gptq.w4a16_repack(qw, perm, 1, stream=st),
+        "gptq_layer": lambda st: gptq.gptq_layer(x, [x, x], p, stream=st),
         "w4a16_matmul": lambda st: gptq.w4a16_matmul(x, qw, qz, torch.ones(1, 64, dtype=torch.float16), stream=st),
     }
 
@@ -92,11 +94,16 @@ def test_tensors_come_from_the_stream_that_writes_them(name, streams):
     side, made, known = streams
     call = calls()[name]
     made.clear()
-    call(side)
-    assert made
-    for i, (where, _) in made.items():
-        assert where == "side" and known.get(i) == {"main"}
+    results = call(side)
+    assert made and all(where == "side" for where, _ in made.values())
+    for t in gptq._tensors(results):
+        assert id(t) in made and known[id(t)] == {"main"}
     made.clear()
     known.clear()
     call(None)
     assert made and all(where == "main" for where, _ in made.values()) and not known
+    # the caller's tensors are known to the stream that reads them
+    made.clear()
+    call(side)
+    theirs = set(known) - set(made)
+    assert theirs and all(known[i] == {"side"} for i in theirs)
