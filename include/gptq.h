@@ -24,7 +24,8 @@
  *     gptq_prepare_hinv, which waits for its own kernels to read the factorisation
  *     status.  Outputs are valid once the stream reaches the end of the call's work.
  *   - Arrays are dense row-major; "stride" arguments count ELEMENTS of the array's own
- *     type.  `batch` independent problems are addressed by the batch strides.
+ *     type.  `batch` independent problems are addressed by the batch strides.  An array that
+ *     a call writes may not share elements with another of its arrays.
  *   - Errors are returned, never printed; on an error the outputs are unspecified.
  *     Argument errors are detected before anything is enqueued.
  *   - Calls on different streams that share a workspace race; calls on one stream do
@@ -329,13 +330,16 @@ gptq_status gptq_fp8_quantize(int batch, int64_t rows, int cols, gptq_dtype x_dt
  *   GPTQ_BF16, GPTQ_F16 rounded first as gptq_fp8_quantize does with block_rows = 1 and
  *                       scales of s_dtype; x_scales and its strides are ignored
  * Y [m, d_out] fp32, bf16 or fp16, row stride ldy (>= d_out).  Products are exact.  For fp32 Y
- * sums are fp32; for 16-bit Y the chip's 8-bit matrix instructions cut products at 2^-13 of
- * the largest among 8 consecutive inputs, and sums of blocks are fp32, rounded once.  The
+ * sums are fp32.  For 16-bit Y the chip's 8-bit matrix instructions cut products at 2^-13 of
+ * the largest among 8 consecutive inputs (at most 7 * 2^-13 of the sum of magnitudes: below
+ * bf16's half step of that sum, up to 1.7 times fp16's), and sums of blocks are fp32, rounded
+ * once; ask for fp32 Y where an fp16 result has to come from fp32 sums.  The
  * product xs * ws of any two scales has to be a normal fp32 number (or its block's products
  * zero).  workspace: gptq_workspace_size(GPTQ_WS_FP8_MATMUL, batch = 1, d_out, d_in,
  * n_tokens_hint = m, NULL) bytes, 16-byte aligned; it serves one call at a time.  Requires
  * d_in % 16 == 0, d_out >= 1; m may be 0 (no-op); more than 2^22 tiles of the kernel that fits the
- * sizes (16 x 16 to 256 x 256 outputs) are refused (GPTQ_ERR_UNSUPPORTED).
+ * sizes (16 x 16 to 256 x 256 outputs), and more 16-bit rows than gptq_fp8_quantize takes, are
+ * refused (GPTQ_ERR_UNSUPPORTED).
  */
 gptq_status gptq_fp8_matmul(int64_t m, int d_out, int d_in, gptq_dtype x_dtype, const void* X,
                             int64_t ldx, gptq_dtype s_dtype, const void* x_scales,
