@@ -79,3 +79,36 @@ def test_blocks_with_work_queued_elsewhere_are_left_alone(name):
     torch.cuda.synchronize()
     assert all(bool((k == 7).all()) for k in kept)
     assert len(got) == len(want) and all(torch.equal(raw(a), raw(b)) for a, b in zip(got, want))
+
+
+def test_captured_on_a_forked_stream():
+    # a graph whose calls run on a stream forked from the captured one and joined again
+    g = lib()
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    x = torch.zeros(200, 256, dtype=torch.bfloat16, device="cuda")
+    logits = torch.zeros(200, 8, device="cuda")
+    W, WS = g.fp8_quantize(torch.randn(8, 192, 256, generator=gen, device="cuda"), 128)
+
+    def block(st):
+        ids, w = g.moe_route(logits, 2, stream=st)
+        off, rows, place = g.moe_group_tokens(ids, 8, stream=st)
+        y = g.fp8_matmul_grouped(x, W, WS, off, rows, stream=st)
+        return ids, w, off, rows, place, y, g.moe_combine(y, place, w, stream=st)
+
+    side = torch.cuda.Stream()
+    block(None)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        held = block(side)
+        main.wait_stream(side)
+    for i in range(4):
+        x.copy_(torch.randn(200, 256, generator=gen, device="cuda"))
+        logits.copy_(torch.randn(200, 8, generator=gen, device="cuda"))
+        want = block(None)
+        graph.replay()
+        again = block(None)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) and torch.equal(a, c) for a, b, c in zip(held, want, again))
