@@ -56,8 +56,12 @@ typedef enum {
 
 /* GPTQ_E4M3 (4 exponent bits, 3 mantissa bits, largest value 448, no infinity) and
  * GPTQ_E8M0 (a scale 2^(b - 127), b = 255: NaN) are the 8-bit types of the block-scaled
- * calls at the end of this file; no other call takes them. */
-typedef enum { GPTQ_F32 = 0, GPTQ_BF16 = 1, GPTQ_F16 = 2, GPTQ_E4M3 = 3, GPTQ_E8M0 = 4 } gptq_dtype;
+ * calls at the end of this file, GPTQ_E2M1 (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives as
+ * codes 0..7 and 8..15, two to a byte, the first in the low half) the 4-bit type of the
+ * microscaled ones; no other call takes them. */
+typedef enum {
+  GPTQ_F32 = 0, GPTQ_BF16 = 1, GPTQ_F16 = 2, GPTQ_E4M3 = 3, GPTQ_E8M0 = 4, GPTQ_E2M1 = 5
+} gptq_dtype;
 
 /* Quantizer knobs ("GPTQ Architecture, in depth", "The algorithm in code" and
  * "Groups, act-order and other knobs"; damping: "Same Ruler, Smarter Placement:
@@ -101,7 +105,9 @@ typedef enum {
   GPTQ_WS_W4A16 = 4,
   GPTQ_WS_FP8_MATMUL = 5,
   GPTQ_WS_FP8_GROUPED = 6,
-  GPTQ_WS_MOE_GROUP = 7
+  GPTQ_WS_MOE_GROUP = 7,
+  GPTQ_WS_MXFP4_MATMUL = 8,
+  GPTQ_WS_MXFP4_MOE_MLP = 9
 } gptq_ws_call;
 
 /*
@@ -442,13 +448,107 @@ gptq_status gptq_moe_combine(int64_t n_tokens, int top_k, int64_t n_rows, int d,
                              const void* Y, int64_t ldy, const int32_t* place, const float* weights,
                              void* out, int64_t ldo, hipStream_t stream);
 
+/*
+ * Rounding to the 4-bit microscaled form: e2m1 codes with one E8M0 scale per 32 consecutive inputs
+ * of a row.  For every problem e < batch and block b of a row of X[e] [rows, cols]:
+ *   top_b   = max |x| over the block
+ *   scale_b = max(2^(floor(log2(top_b)) - 2), 2^-126)    scaling 0: values above 6 scale_b are cut
+ *                                                        to it (the microscaling formats' own rule)
+ *             max(2^ceil(log2(top_b / 6)), 2^-126)       scaling 1: none is cut
+ *   Q       = the e2m1 value nearest to x / scale_b, ties to even, at most 6
+ * A block that holds an infinity or a NaN gets scale NaN (255) and codes 0.  X is bf16, fp16 or fp32
+ * with row stride ldx (>= cols) and batch stride batch_stride_x; Q uint8 [batch, rows, cols / 2]
+ * (16-byte aligned) and scales uint8 [batch, rows, cols / 32] are dense.  Requires cols % 32 == 0;
+ * rows may be 0 (no-op); more than 2^24 - 1 rows of 64 or more blocks (64 times as many of one),
+ * or more than 65535 problems, are refused (GPTQ_ERR_UNSUPPORTED).
+ */
+gptq_status gptq_mxfp4_quantize(int batch, int64_t rows, int cols, gptq_dtype x_dtype, const void* X,
+                                int64_t ldx, int64_t batch_stride_x, int scaling, uint8_t* Q,
+                                uint8_t* scales, hipStream_t stream);
+
+/*
+ * The values that such codes stand for: Y[r, c] = scale[r, c / 32] * q[r, c], rounded once to bf16,
+ * fp16 or fp32 (fp32 holds all of them, bf16 all up to 2^128; a scale of 255 gives NaN).  Q
+ * (16-byte aligned), scales and Y (16-byte aligned) are dense, [rows, cols / 2], [rows, cols / 32] and
+ * [rows, cols].  The same sizes as gptq_mxfp4_quantize.
+ */
+gptq_status gptq_mxfp4_dequantize(int64_t rows, int cols, const uint8_t* Q, const uint8_t* scales,
+                                  gptq_dtype y_dtype, void* Y, hipStream_t stream);
+
+/*
+ * Product with 4-bit microscaled weights:
+ *   Y[r, o] = sum over blocks b of 32 inputs of  ws[o, b] * sum_{c in b} x[r, c] * q[o, c]
+ * qweight: e2m1 [d_out, d_in / 2] bytes, 16-byte aligned, and w_scales E8M0 [d_out, d_in / 32],
+ * dense (as written by gptq_mxfp4_quantize).  X [m, d_in], 16-byte aligned:
+ *   GPTQ_E2M1           x = xs[r, b] * xq[r, c]; ldx counts bytes (>= d_in / 2, ldx % 16 == 0), row r's
+ *                       scales start at x_scales + r * ld_xs_row (>= d_in / 32)
+ *   GPTQ_BF16, GPTQ_F16 x itself, not rounded; ldx % 8 == 0, ldx >= d_in; x_scales and its stride are
+ *                       ignored.  fp16 takes two matrix products where bf16 takes one
+ * Y [m, d_out] fp32, bf16 or fp16, row stride ldy (>= d_out).  Products are exact and sums fp32 for
+ * every type of Y.  A product of two scales, and with 16-bit X a weight, has to lie in fp32's normal
+ * range to count in full (a weight of 2^128 or more is infinite).  workspace:
+ * gptq_workspace_size(GPTQ_WS_MXFP4_MATMUL, batch = 1, d_out, d_in, n_tokens_hint = m, NULL) bytes,
+ * 16-byte aligned (sums of parts of the inputs; where that is 256 the call keeps nothing there and
+ * takes NULL); it serves one call at a time.  Requires d_in % 32 == 0, d_out >= 1; m may be 0 (no-op); more
+ * than 2^22 tiles of the kernel that fits the sizes (16 x 16 to 256 x 256 outputs) are refused
+ * (GPTQ_ERR_UNSUPPORTED).
+ */
+gptq_status gptq_mxfp4_matmul(int64_t m, int d_out, int d_in, gptq_dtype x_dtype, const void* X,
+                              int64_t ldx, const uint8_t* x_scales, int64_t ld_xs_row,
+                              const uint8_t* qweight, const uint8_t* w_scales, gptq_dtype y_dtype,
+                              void* Y, int64_t ldy, void* workspace, size_t workspace_bytes,
+                              hipStream_t stream);
+
+/*
+ * The same product for the experts of a mixture-of-experts block: `batch` weights qweight [batch,
+ * d_out, d_in / 2] with scales [batch, d_out, d_in / 32], and rows grouped by expert as in
+ * gptq_fp8_matmul_grouped: row p of expert e's range token_offsets[e] .. token_offsets[e + 1] - 1
+ * (clamped to [0, n_rows]) is row row_index[p] of X (row_index NULL: row p, n_rows <= x_rows) times
+ * expert e's weights; an index outside [0, x_rows) gives a row of zeros; rows of Y outside every
+ * range are left as they were.  It takes no workspace.  Requires (n_rows / 16 + 1) * batch < 2^31
+ * (GPTQ_ERR_UNSUPPORTED).
+ */
+gptq_status gptq_mxfp4_matmul_grouped(int batch, int64_t x_rows, int64_t n_rows, int d_out, int d_in,
+                                      gptq_dtype x_dtype, const void* X, int64_t ldx,
+                                      const uint8_t* x_scales, int64_t ld_xs_row,
+                                      const uint8_t* qweight, const uint8_t* w_scales,
+                                      const int64_t* token_offsets, const int32_t* row_index,
+                                      gptq_dtype y_dtype, void* Y, int64_t ldy, hipStream_t stream);
+
+/*
+ * The expert layer of a mixture-of-experts block for few tokens, in two launches:
+ *   g, u      = the first and the last `inner` of W1[e] x[t]
+ *   out[t, :] = sum over j of weights[t, j] * W2[e] (act(g) * u),   e = ids[t, j]
+ * with act 0: g / (1 + exp(-g)); 1: 0.5 g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))).
+ * X [n_tokens, d_in] bf16 or fp16, row stride ldx; ids int32 and weights fp32 [n_tokens, top_k],
+ * dense (as written by gptq_moe_route; an id outside [0, n_experts) is no choice, an expert named
+ * twice by a token counts with both weights); W1 e2m1 [n_experts, 2 inner, d_in / 2] (gate rows, then
+ * up rows) with scales [n_experts, 2 inner, d_in / 32], W2 [n_experts, d_in, inner / 2] with scales
+ * [n_experts, d_in, inner / 32], dense, W1 and W2 16-byte aligned; out [n_tokens, d_in] of X's type,
+ * row stride ldo, zeros for a token without choices.  X is not rounded, sums are fp32, and the
+ * activations between the products, which carry the weights, keep 16 significant bits.  workspace:
+ * gptq_workspace_size(GPTQ_WS_MXFP4_MOE_MLP, 1, inner, d_in, n_tokens * top_k, NULL) bytes, 16-byte
+ * aligned; it serves one call at a time.  Requires d_in % 32 == 0, inner % 32 == 0, 1 <= n_experts <=
+ * 1024, 1 <= top_k <= 32; n_tokens may be 0 (no-op).  More than GPTQ_MOE_MLP_CHOICES
+ * (4096) choices (n_tokens * top_k) are
+ * refused (GPTQ_ERR_UNSUPPORTED): group them and use gptq_mxfp4_matmul_grouped.
+ */
+#define GPTQ_MOE_MLP_CHOICES 4096
+gptq_status gptq_mxfp4_moe_mlp(int64_t n_tokens, int top_k, int n_experts, int d_in, int inner,
+                               gptq_dtype x_dtype, const void* X, int64_t ldx, const int32_t* ids,
+                               const float* weights, const uint8_t* W1, const uint8_t* w1_scales,
+                               const uint8_t* W2, const uint8_t* w2_scales, int activation, void* out,
+                               int64_t ldo, void* workspace, size_t workspace_bytes,
+                               hipStream_t stream);
+
 /* Bytes of workspace the given call needs (0 on invalid arguments).  For
  * GPTQ_WS_HESSIAN `d_out` is ignored and `n_tokens_hint` is the largest n_tokens per call
  * (it only sizes the split over tokens); for GPTQ_WS_W4A16 `n_tokens_hint` is the number
  * of activation rows m and p->group_size the group size (-1: one grid per row); for
  * GPTQ_WS_FP8_MATMUL and GPTQ_WS_FP8_GROUPED `n_tokens_hint` is the number of rows of X; for
- * GPTQ_WS_MOE_GROUP `d_out` is n_experts and `d_in` is top_k; for the other calls it is
- * ignored. */
+ * GPTQ_WS_MOE_GROUP `d_out` is n_experts and `d_in` is top_k; for GPTQ_WS_MXFP4_MATMUL
+ * `n_tokens_hint` is m, and for GPTQ_WS_MXFP4_MOE_MLP `d_out` is inner and `n_tokens_hint` the number
+ * of choices; for the other calls it is ignored. */
 size_t gptq_workspace_size(gptq_ws_call which, int batch, int d_out, int d_in,
                            int64_t n_tokens_hint, const gptq_params* p);
 

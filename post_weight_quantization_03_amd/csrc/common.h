@@ -156,6 +156,43 @@ struct Fp8Problem {
 size_t fp8_workspace(int64_t x_rows, int k);
 gptq_status fp8_matmul_enqueue(const Fp8Problem& p, hipStream_t stream);
 
+// The 4-bit microscaled form (mx.hip) and the expert layer of few tokens (mx_moe.hip).
+gptq_status mx_quantize_enqueue(int batch, int64_t rows, int cols, gptq_dtype x_dtype, const void* X, int64_t ldx,
+                                int64_t bsx, bool ceil, uint8_t* Q, uint8_t* S, hipStream_t stream);
+gptq_status mx_dequantize_enqueue(int64_t rows, int cols, const uint8_t* Q, const uint8_t* S, gptq_dtype y_dtype,
+                                  void* Y, hipStream_t stream);
+struct MxProblem {
+  int batch;                    // experts; 1 without offsets
+  int64_t x_rows, n_rows;
+  int n, k;
+  gptq_dtype x_dtype;
+  const void* X; int64_t ldx;
+  const uint8_t* xs; int64_t xsr;
+  const uint8_t* W;
+  const uint8_t* ws;
+  const int64_t* offsets;       // null: one dense product
+  const int32_t* row_index;
+  gptq_dtype y_dtype;
+  void* Y; int64_t ldy;
+  void* workspace; size_t workspace_bytes;
+};
+size_t mx_workspace(int64_t m, int n, int k);
+gptq_status mx_matmul_enqueue(const MxProblem& p, hipStream_t stream);
+struct MxMlp {
+  int tokens, top_k, experts, d, inner;
+  bool bf16;                    // X and out, else fp16
+  const void* X; int64_t ldx;
+  const int32_t* ids;
+  const float* weights;
+  const uint8_t* W1; const uint8_t* s1;
+  const uint8_t* W2; const uint8_t* s2;
+  int activation;
+  void* out; int64_t ldo;
+  void* workspace; size_t workspace_bytes;
+};
+size_t mx_mlp_workspace(int64_t pairs, int inner);
+gptq_status mx_mlp_enqueue(const MxMlp& p, hipStream_t stream);
+
 // Routing, grouping and combination of experts (moe.hip).
 gptq_status route_enqueue(int64_t n_tokens, int n_experts, gptq_dtype l_dtype, const void* logits, int64_t ldl,
                           const float* bias, const gptq_route_params& p, int32_t* ids, float* weights,

@@ -386,6 +386,95 @@ gptq_status gptq_moe_combine(int64_t n_tokens, int top_k, int64_t n_rows, int d,
   return gptq::combine_enqueue(n_tokens, top_k, n_rows, d, y_dtype, Y, ldy, place, weights, out, ldo, stream);
 }
 
+gptq_status gptq_mxfp4_quantize(int batch, int64_t rows, int cols, gptq_dtype x_dtype, const void* X, int64_t ldx,
+                                int64_t batch_stride_x, int scaling, uint8_t* Q, uint8_t* scales, hipStream_t stream) {
+  if (batch < 1 || rows < 0 || cols < 32 || cols % 32 != 0 || !real_dtype(x_dtype) || scaling < 0 || scaling > 1)
+    return GPTQ_ERR_INVALID_ARG;
+  if (rows == 0) return GPTQ_OK;
+  if (X == nullptr || Q == nullptr || scales == nullptr) return GPTQ_ERR_INVALID_ARG;
+  if (ldx < cols || !aligned(Q, 16) || !aligned(X, dtype_bytes(x_dtype))) return GPTQ_ERR_INVALID_ARG;
+  if (batch > 1 && batch_stride_x < ldx * (rows - 1) + cols) return GPTQ_ERR_INVALID_ARG;
+  return gptq::mx_quantize_enqueue(batch, rows, cols, x_dtype, X, ldx, batch > 1 ? batch_stride_x : 0, scaling == 1, Q,
+                                   scales, stream);
+}
+
+gptq_status gptq_mxfp4_dequantize(int64_t rows, int cols, const uint8_t* Q, const uint8_t* scales, gptq_dtype y_dtype,
+                                  void* Y, hipStream_t stream) {
+  if (rows < 0 || cols < 32 || cols % 32 != 0 || !real_dtype(y_dtype)) return GPTQ_ERR_INVALID_ARG;
+  if (rows == 0) return GPTQ_OK;
+  if (Q == nullptr || scales == nullptr || Y == nullptr || !aligned(Q, 16) || !aligned(Y, 16))
+    return GPTQ_ERR_INVALID_ARG;
+  return gptq::mx_dequantize_enqueue(rows, cols, Q, scales, y_dtype, Y, stream);
+}
+
+namespace {
+// Arguments shared by the dense and the grouped 4-bit product.
+gptq_status check_mx(const gptq::MxProblem& p) {
+  if (p.batch < 1 || p.n < 1 || p.k < 32 || p.k % 32 != 0 || p.x_rows < 0 || p.n_rows < 0) return GPTQ_ERR_INVALID_ARG;
+  if (p.x_dtype != GPTQ_E2M1 && p.x_dtype != GPTQ_BF16 && p.x_dtype != GPTQ_F16) return GPTQ_ERR_INVALID_ARG;
+  if (!real_dtype(p.y_dtype)) return GPTQ_ERR_INVALID_ARG;
+  if (p.n_rows == 0) return GPTQ_OK;
+  if (p.W == nullptr || p.ws == nullptr || p.Y == nullptr || (p.X == nullptr && p.x_rows > 0)) return GPTQ_ERR_INVALID_ARG;
+  if (p.ldy < p.n || !aligned(p.W, 16) || !aligned(p.X, 16) || !aligned(p.Y, dtype_bytes(p.y_dtype)) ||
+      !aligned(p.workspace, 16))
+    return GPTQ_ERR_INVALID_ARG;
+  if (p.x_dtype == GPTQ_E2M1) {
+    if (p.ldx < p.k / 2 || p.ldx % 16 != 0 || (p.xs == nullptr && p.x_rows > 0) || p.xsr < p.k / 32)
+      return GPTQ_ERR_INVALID_ARG;
+  } else if (p.ldx < p.k || p.ldx % 8 != 0) {
+    return GPTQ_ERR_INVALID_ARG;
+  }
+  return GPTQ_OK;
+}
+}  // namespace
+
+gptq_status gptq_mxfp4_matmul(int64_t m, int d_out, int d_in, gptq_dtype x_dtype, const void* X, int64_t ldx,
+                              const uint8_t* x_scales, int64_t ld_xs_row, const uint8_t* qweight,
+                              const uint8_t* w_scales, gptq_dtype y_dtype, void* Y, int64_t ldy, void* workspace,
+                              size_t workspace_bytes, hipStream_t stream) {
+  const gptq::MxProblem p{1, m, m, d_out, d_in, x_dtype, X, ldx, x_scales, ld_xs_row, qweight, w_scales, nullptr,
+                          nullptr, y_dtype, Y, ldy, workspace, workspace_bytes};
+  const gptq_status st = check_mx(p);
+  if (st != GPTQ_OK || m == 0) return st;
+  return gptq::mx_matmul_enqueue(p, stream);
+}
+
+gptq_status gptq_mxfp4_matmul_grouped(int batch, int64_t x_rows, int64_t n_rows, int d_out, int d_in,
+                                      gptq_dtype x_dtype, const void* X, int64_t ldx, const uint8_t* x_scales,
+                                      int64_t ld_xs_row, const uint8_t* qweight, const uint8_t* w_scales,
+                                      const int64_t* token_offsets, const int32_t* row_index, gptq_dtype y_dtype,
+                                      void* Y, int64_t ldy, hipStream_t stream) {
+  const gptq::MxProblem p{batch, x_rows, n_rows, d_out, d_in, x_dtype, X, ldx, x_scales, ld_xs_row, qweight, w_scales,
+                          token_offsets, row_index, y_dtype, Y, ldy, nullptr, 0};
+  const gptq_status st = check_mx(p);
+  if (st != GPTQ_OK || n_rows == 0) return st;
+  if (token_offsets == nullptr || !aligned(token_offsets, 8) || !aligned(row_index, 4)) return GPTQ_ERR_INVALID_ARG;
+  if (row_index == nullptr && n_rows > x_rows) return GPTQ_ERR_INVALID_ARG;   // row p of X for every p
+  return gptq::mx_matmul_enqueue(p, stream);
+}
+
+gptq_status gptq_mxfp4_moe_mlp(int64_t n_tokens, int top_k, int n_experts, int d_in, int inner, gptq_dtype x_dtype,
+                               const void* X, int64_t ldx, const int32_t* ids, const float* weights,
+                               const uint8_t* W1, const uint8_t* w1_scales, const uint8_t* W2,
+                               const uint8_t* w2_scales, int activation, void* out, int64_t ldo, void* workspace,
+                               size_t workspace_bytes, hipStream_t stream) {
+  if (n_tokens < 0 || top_k < 1 || top_k > 32 || n_experts < 1 || n_experts > 1024 || d_in < 32 || d_in % 32 != 0 ||
+      inner < 32 || inner % 32 != 0 || inner > (1 << 30) || activation < 0 || activation > 1 ||
+      (x_dtype != GPTQ_BF16 && x_dtype != GPTQ_F16))
+    return GPTQ_ERR_INVALID_ARG;
+  if (n_tokens == 0) return GPTQ_OK;
+  if (n_tokens > GPTQ_MOE_MLP_CHOICES / top_k) return GPTQ_ERR_UNSUPPORTED;
+  if (X == nullptr || ids == nullptr || weights == nullptr || W1 == nullptr || w1_scales == nullptr || W2 == nullptr ||
+      w2_scales == nullptr || out == nullptr || ldx < d_in || ldo < d_in)
+    return GPTQ_ERR_INVALID_ARG;
+  if (!aligned(X, 2) || !aligned(out, 2) || !aligned(ids, 4) || !aligned(weights, 4) || !aligned(W1, 16) ||
+      !aligned(W2, 16) || !aligned(workspace, 16))
+    return GPTQ_ERR_INVALID_ARG;
+  const gptq::MxMlp p{static_cast<int>(n_tokens), top_k, n_experts, d_in, inner, x_dtype == GPTQ_BF16, X, ldx, ids,
+                      weights, W1, w1_scales, W2, w2_scales, activation, out, ldo, workspace, workspace_bytes};
+  return gptq::mx_mlp_enqueue(p, stream);
+}
+
 size_t gptq_workspace_size(gptq_ws_call which, int batch, int d_out, int d_in, int64_t n_tokens_hint,
                            const gptq_params* p) {
   switch (which) {
@@ -413,6 +502,12 @@ size_t gptq_workspace_size(gptq_ws_call which, int batch, int d_out, int d_in, i
     case GPTQ_WS_MOE_GROUP:
       if (d_out < 1 || d_out > 1024 || d_in < 1 || n_tokens_hint < 0 || n_tokens_hint > INT32_MAX / d_in) return 0;
       return gptq::group_workspace(d_out, n_tokens_hint * d_in);
+    case GPTQ_WS_MXFP4_MATMUL:
+      if (batch != 1 || d_out < 1 || d_in < 32 || d_in % 32 != 0 || n_tokens_hint < 0) return 0;
+      return gptq::mx_workspace(n_tokens_hint, d_out, d_in);
+    case GPTQ_WS_MXFP4_MOE_MLP:
+      if (d_out < 32 || d_out % 32 != 0 || n_tokens_hint < 0 || n_tokens_hint > GPTQ_MOE_MLP_CHOICES) return 0;
+      return gptq::mx_mlp_workspace(n_tokens_hint, d_out);
   }
   return 0;
 }
@@ -430,6 +525,6 @@ const char* gptq_status_string(gptq_status s) {
   return "unknown status";
 }
 
-const char* gptq_version(void) { return "0.3.0"; }
+const char* gptq_version(void) { return "0.4.0"; }
 
 }  // extern "C"

@@ -7,8 +7,8 @@ library has not been built: there is no fallback path.
 
 Names follow the C ABI: ``accumulate_hessian``, ``prepare_hinv``, ``quantize_layer``,
 ``pack_int4``.  Tensors may carry a leading batch dimension (independent problems, e.g.
-mixture-of-experts layers).  ``moe_*`` route tokens to experts and ``fp8_*`` serve layers in
-8 bits; no call records a gradient.
+mixture-of-experts layers).  ``moe_*`` route tokens to experts, ``fp8_*`` serve layers in
+8 bits and ``mxfp4_*`` in 4; no call records a gradient.
 
 ``stream`` is the torch stream a call runs on (None: the current one).  Its inputs have to be
 ready there; what the call allocates comes from that stream's memory.
@@ -31,11 +31,14 @@ GPTQ_ERR_TOO_LARGE = -6
 NOALLOC_SCRATCH_BYTES = 64 << 20
 WS_HESSIAN, WS_PREPARE, WS_QUANTIZE, WS_W4A16_REPACK, WS_W4A16 = 0, 1, 2, 3, 4
 WS_FP8_MATMUL, WS_FP8_GROUPED, WS_MOE_GROUP = 5, 6, 7
+WS_MXFP4_MATMUL, WS_MXFP4_MOE_MLP = 8, 9
 
 EXPORTED = ("gptq_accumulate_hessian", "gptq_prepare_hinv", "gptq_quantize_layer", "gptq_quantize_layer_noalloc",
             "gptq_accumulate_hessian_grouped", "gptq_pack_int4", "gptq_w4a16_repack", "gptq_w4a16_matmul",
             "gptq_fp8_quantize", "gptq_fp8_matmul", "gptq_fp8_matmul_grouped", "gptq_moe_route",
             "gptq_moe_group_tokens", "gptq_moe_combine",
+            "gptq_mxfp4_quantize", "gptq_mxfp4_dequantize", "gptq_mxfp4_matmul", "gptq_mxfp4_matmul_grouped",
+            "gptq_mxfp4_moe_mlp",
             "gptq_workspace_size", "gptq_status_string", "gptq_version", "gptq_timing_enable", "gptq_timing_read")
 
 
@@ -112,6 +115,13 @@ def lib() -> ctypes.CDLL:
     L.gptq_moe_route.argtypes = [i64, i32, i32, vp, i64, vp, ctypes.POINTER(_RouteParams), vp, vp, vp]
     L.gptq_moe_group_tokens.argtypes = [i64, i32, i32, vp, vp, vp, vp, vp, sz, vp]
     L.gptq_moe_combine.argtypes = [i64, i32, i64, i32, i32, vp, i64, vp, vp, vp, i64, vp]
+    L.gptq_mxfp4_quantize.argtypes = [i32, i64, i32, i32, vp, i64, i64, i32, vp, vp, vp]
+    L.gptq_mxfp4_dequantize.argtypes = [i64, i32, vp, vp, i32, vp, vp]
+    L.gptq_mxfp4_matmul.argtypes = [i64, i32, i32, i32, vp, i64, vp, i64, vp, vp, i32, vp, i64, vp, sz, vp]
+    L.gptq_mxfp4_matmul_grouped.argtypes = [i32, i64, i64, i32, i32, i32, vp, i64, vp, i64, vp, vp, vp, vp, i32, vp,
+                                            i64, vp]
+    L.gptq_mxfp4_moe_mlp.argtypes = [i64, i32, i32, i32, i32, i32, vp, i64, vp, vp, vp, vp, vp, vp, i32, vp, i64, vp,
+                                     sz, vp]
     L.gptq_workspace_size.argtypes = [i32, i32, i32, i32, i64, ctypes.POINTER(_Params)]
     L.gptq_workspace_size.restype = sz
     L.gptq_status_string.argtypes = [i32]
@@ -123,7 +133,8 @@ def lib() -> ctypes.CDLL:
     for name in ("gptq_accumulate_hessian", "gptq_accumulate_hessian_grouped", "gptq_prepare_hinv", "gptq_quantize_layer", "gptq_quantize_layer_noalloc",
                  "gptq_pack_int4", "gptq_w4a16_repack", "gptq_w4a16_matmul", "gptq_timing_enable",
                  "gptq_timing_read", "gptq_fp8_quantize", "gptq_fp8_matmul", "gptq_fp8_matmul_grouped",
-                 "gptq_moe_route", "gptq_moe_group_tokens", "gptq_moe_combine"):
+                 "gptq_moe_route", "gptq_moe_group_tokens", "gptq_moe_combine", "gptq_mxfp4_quantize",
+                 "gptq_mxfp4_dequantize", "gptq_mxfp4_matmul", "gptq_mxfp4_matmul_grouped", "gptq_mxfp4_moe_mlp"):
         getattr(L, name).restype = i32
     _lib = L
     return L
@@ -700,6 +711,183 @@ def moe_combine(Y: torch.Tensor, place: torch.Tensor, weights: torch.Tensor, out
     res = _out(out, (tokens, d), Y.dtype, Y.device)
     _run("gptq_moe_combine", (Y, place, weights, res), tokens, k, rows, d, _DT[Y.dtype], Y.data_ptr(),
          _row_stride(Y), place.data_ptr(), weights.data_ptr(), res.data_ptr(), _row_stride(res))
+    return res
+
+
+E2M1 = 5
+_MX_BLOCK = 32
+_MX_CODES, _MX_SCALES = (torch.float4_e2m1fn_x2, torch.uint8), (torch.float8_e8m0fnu, torch.uint8)
+_MX_SCALING, _ACTIVATIONS = {"floor": 0, "ceil": 1}, {"silu": 0, "gelu_tanh": 1}
+
+
+def mxfp4_quantize(X: torch.Tensor, scaling: str = "floor", stream=None):
+    """-> (q float4_e2m1fn_x2 [(b,) rows, cols / 2], scales float8_e8m0fnu [(b,) rows, cols / 32]):
+    X [(b,) rows, cols] fp32/bf16/fp16 as 4-bit codes with a power-of-two scale per 32 inputs of a
+    row, q = X / scale rounded to nearest even.  ``scaling`` "floor": scale 2^(floor(log2 max|x|)
+    - 2), which cuts values above 6 scales (the microscaling formats' own rule); "ceil": the
+    smallest power of two that cuts none."""
+    if stream is not None:
+        return _on(stream, mxfp4_quantize, X, scaling)
+    if X.dtype not in _DT:
+        raise TypeError("X must be fp32/bf16/fp16")
+    if scaling not in _MX_SCALING or X.dim() not in (2, 3):
+        raise ValueError("X must be [(batch,) rows, cols], scaling 'floor' or 'ceil'")
+    Xb = _batched(X, 2)
+    batch, rows, cols = Xb.shape
+    if cols < _MX_BLOCK or cols % _MX_BLOCK or batch < 1:
+        raise ValueError("cols must be a positive multiple of 32")
+    if Xb.stride(2) != 1:
+        raise ValueError("X rows must be contiguous")
+    q = torch.empty((*X.shape[:-1], cols // 2), dtype=torch.float4_e2m1fn_x2, device=X.device)
+    S = torch.empty((*X.shape[:-1], cols // _MX_BLOCK), dtype=torch.float8_e8m0fnu, device=X.device)
+    _run("gptq_mxfp4_quantize", (X, q, S), batch, rows, cols, _DT[X.dtype], X.data_ptr(), _row_stride(Xb),
+         Xb.stride(0), _MX_SCALING[scaling], q.data_ptr(), S.data_ptr())
+    return q, S
+
+
+def _mx_pair(q, scales, what: str):
+    """Checks codes and their scales; -> the number of inputs of a row."""
+    if q.dtype not in _MX_CODES or scales.dtype not in _MX_SCALES:
+        raise TypeError(f"{what} must be float4_e2m1fn_x2 (or uint8) with float8_e8m0fnu (or uint8) scales")
+    k = 2 * q.shape[-1]
+    if k < _MX_BLOCK or k % _MX_BLOCK or scales.shape != (*q.shape[:-1], k // _MX_BLOCK):
+        raise ValueError(f"{what} must be [.., inputs / 2] with scales [.., inputs / 32]")
+    return k
+
+
+def mxfp4_dequantize(q: torch.Tensor, scales: torch.Tensor, dtype: torch.dtype = torch.bfloat16,
+                     stream=None) -> torch.Tensor:
+    """The values that codes q [.., cols / 2] and scales [.., cols / 32] stand for, [.., cols], in
+    ``dtype`` (fp32 and, below 2^128, bf16 hold all of them)."""
+    if stream is not None:
+        return _on(stream, mxfp4_dequantize, q, scales, dtype)
+    if dtype not in _DT:
+        raise TypeError("dtype must be fp32/bf16/fp16")
+    if q.dim() < 1:
+        raise ValueError("q must be [.., cols / 2]")
+    cols = _mx_pair(q, scales, "q")
+    if not (q.is_contiguous() and scales.is_contiguous()):
+        raise ValueError("q and scales must be contiguous")
+    Y = torch.empty((*q.shape[:-1], cols), dtype=dtype, device=q.device)
+    _run("gptq_mxfp4_dequantize", (q, scales, Y), Y.numel() // cols, cols, q.data_ptr(), scales.data_ptr(), _DT[dtype],
+         Y.data_ptr())
+    return Y
+
+
+def _mx_operands(X, x_scales, qweight, w_scales, out_dtype):
+    """Checks shared by the dense and the grouped product; -> (X, its type code, inputs), X in rows
+    that start at multiples of 16 bytes."""
+    d_in = _mx_pair(qweight, w_scales, "qweight")
+    if out_dtype not in _DT:
+        raise TypeError("out_dtype must be fp32/bf16/fp16")
+    if not (qweight.is_contiguous() and w_scales.is_contiguous()):
+        raise ValueError("qweight and w_scales must be contiguous")
+    if X.dim() != 2 or X.stride(1) != 1:
+        raise ValueError("X must be [rows, inputs] with contiguous rows")
+    if x_scales is None:
+        if X.dtype not in (torch.bfloat16, torch.float16):
+            raise TypeError("X must be bf16 or fp16, or 4-bit codes with x_scales")
+        code, width, step = _DT[X.dtype], d_in, 8
+    else:
+        _mx_pair(X, x_scales, "X")
+        if x_scales.stride(1) != 1 and x_scales.shape[1] > 1 or (x_scales.shape[0] > 1 and
+                                                                 x_scales.stride(0) < x_scales.shape[1]):
+            raise ValueError("x_scales must have contiguous rows that do not overlap")
+        code, width, step = E2M1, d_in // 2, 16
+    if X.shape[1] != width:
+        raise ValueError("X and qweight must have the same number of inputs")
+    if X.data_ptr() % 16 or _row_stride(X) % step:
+        X = X.clone(memory_format=torch.contiguous_format)
+    return X, code, d_in
+
+
+def mxfp4_matmul(X: torch.Tensor, qweight: torch.Tensor, w_scales: torch.Tensor, x_scales: torch.Tensor | None = None,
+                 out_dtype: torch.dtype = torch.bfloat16, out: torch.Tensor | None = None,
+                 workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Y [m, d_out] = X What^T with 4-bit microscaled weights [d_out, d_in / 2] and their scales
+    [d_out, d_in / 32] (:func:`mxfp4_quantize`; uint8 tensors are taken as their bits).  X [m, d_in] is
+    bf16 or fp16 and multiplied as it is, or [m, d_in / 2] codes with ``x_scales`` [m, d_in / 32].
+    Sums are fp32.  X whose rows do not start at multiples of 16 bytes is copied first."""
+    if stream is not None:
+        return _on(stream, mxfp4_matmul, X, qweight, w_scales, x_scales, out_dtype, out, workspace)
+    if qweight.dim() != 2 or qweight.shape[0] < 1:
+        raise ValueError("qweight must be [d_out, d_in / 2]")
+    X, code, d_in = _mx_operands(X, x_scales, qweight, w_scales, out_dtype)
+    m, d_out = X.shape[0], qweight.shape[0]
+    Y = _out(out, (m, d_out), out_dtype, X.device)
+    ws = _scratch(WS_MXFP4_MATMUL, 1, d_out, d_in, m, X.device, workspace)
+    _run("gptq_mxfp4_matmul", (X, qweight, w_scales, x_scales, Y, ws), m, d_out, d_in, code, X.data_ptr(),
+         _row_stride(X), _ptr(x_scales), 0 if x_scales is None else _row_stride(x_scales), qweight.data_ptr(),
+         w_scales.data_ptr(), _DT[out_dtype], Y.data_ptr(), _row_stride(Y), _ptr(ws), _bytes(ws))
+    return Y
+
+
+def mxfp4_matmul_grouped(X: torch.Tensor, qweight: torch.Tensor, w_scales: torch.Tensor, token_offsets: torch.Tensor,
+                         row_index: torch.Tensor | None = None, x_scales: torch.Tensor | None = None,
+                         out_dtype: torch.dtype = torch.bfloat16, out: torch.Tensor | None = None,
+                         stream=None) -> torch.Tensor:
+    """The experts' products: row p of Y [n_rows, d_out], token_offsets[e] <= p <
+    token_offsets[e + 1], is row row_index[p] of X (row p without ``row_index``) times
+    expert e's weights qweight [experts, d_out, d_in / 2]; operands otherwise as in
+    :func:`mxfp4_matmul`, ranges and indexes as in :func:`fp8_matmul_grouped`."""
+    if stream is not None:
+        return _on(stream, mxfp4_matmul_grouped, X, qweight, w_scales, token_offsets, row_index, x_scales, out_dtype,
+                   out)
+    if qweight.dim() != 3 or qweight.shape[0] < 1 or qweight.shape[1] < 1:
+        raise ValueError("qweight must be [experts, d_out, d_in / 2]")
+    X, code, d_in = _mx_operands(X, x_scales, qweight, w_scales, out_dtype)
+    x_rows, (experts, d_out) = X.shape[0], qweight.shape[:2]
+    if token_offsets.dtype != torch.int64 or not token_offsets.is_contiguous() or token_offsets.shape != (experts + 1,):
+        raise ValueError("token_offsets must be contiguous int64 [experts + 1]")
+    if row_index is not None and (row_index.dtype != torch.int32 or row_index.dim() != 1 or
+                                  not row_index.is_contiguous()):
+        raise ValueError("row_index must be contiguous int32 [n_rows]")
+    n_rows = x_rows if row_index is None else row_index.numel()
+    Y = _out(out, (n_rows, d_out), out_dtype, X.device)
+    _run("gptq_mxfp4_matmul_grouped", (X, qweight, w_scales, token_offsets, row_index, x_scales, Y), experts, x_rows,
+         n_rows, d_out, d_in, code, X.data_ptr(), _row_stride(X), _ptr(x_scales),
+         0 if x_scales is None else _row_stride(x_scales), qweight.data_ptr(), w_scales.data_ptr(),
+         token_offsets.data_ptr(), _ptr(row_index), _DT[out_dtype], Y.data_ptr(), _row_stride(Y))
+    return Y
+
+
+def mxfp4_moe_mlp(X: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, w1: torch.Tensor, w1_scales: torch.Tensor,
+                  w2: torch.Tensor, w2_scales: torch.Tensor, activation: str = "silu", out: torch.Tensor | None = None,
+                  workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The expert layer of few tokens in two launches: out [tokens, d] (X's type) = sum over j of
+    weights[:, j] * W2[e] (act(gate) * up), e = ids[:, j], with gate and up the first and second half
+    of W1[e] x.  X [tokens, d] bf16 or fp16, multiplied as it is; ids int32 and weights fp32 [tokens,
+    top_k] from :func:`moe_route` (ids outside the experts are no choice); w1 [experts, 2 inner,
+    d / 2] and w2 [experts, d, inner / 2] with their scales from :func:`mxfp4_quantize`;
+    ``activation`` "silu" or "gelu_tanh".  At most 4096 choices (tokens * top_k); for more, group the
+    tokens and use :func:`mxfp4_matmul_grouped`."""
+    if stream is not None:
+        return _on(stream, mxfp4_moe_mlp, X, ids, weights, w1, w1_scales, w2, w2_scales, activation, out, workspace)
+    if X.dtype not in (torch.bfloat16, torch.float16) or ids.dtype != torch.int32 or weights.dtype != torch.float32:
+        raise TypeError("X must be bf16 or fp16, ids int32, weights fp32")
+    if activation not in _ACTIVATIONS:
+        raise ValueError("activation must be 'silu' or 'gelu_tanh'")
+    if w1.dim() != 3 or w2.dim() != 3:
+        raise ValueError("w1 must be [experts, 2 inner, d / 2], w2 [experts, d, inner / 2]")
+    d, inner = _mx_pair(w1, w1_scales, "w1"), _mx_pair(w2, w2_scales, "w2")
+    experts = w1.shape[0]
+    if w1.shape[1] != 2 * inner or w2.shape[:2] != (experts, d) or not 1 <= experts <= 1024:
+        raise ValueError("w1 must be [experts, 2 inner, d / 2], w2 [experts, d, inner / 2], experts 1..1024")
+    if not (w1.is_contiguous() and w1_scales.is_contiguous() and w2.is_contiguous() and w2_scales.is_contiguous()):
+        raise ValueError("weights and their scales must be contiguous")
+    if X.dim() != 2 or X.shape[1] != d or X.stride(1) != 1:
+        raise ValueError("X must be [tokens, d] with contiguous rows")
+    tokens = X.shape[0]
+    if ids.dim() != 2 or ids.shape[0] != tokens or not 1 <= ids.shape[1] <= 32 or weights.shape != ids.shape or not (
+            ids.is_contiguous() and weights.is_contiguous()):
+        raise ValueError("ids and weights must be contiguous [tokens, top_k], top_k 1..32")
+    k = ids.shape[1]
+    res = _out(out, (tokens, d), X.dtype, X.device)
+    ws = _scratch(WS_MXFP4_MOE_MLP, 1, inner, d, tokens * k, X.device, workspace)
+    _run("gptq_mxfp4_moe_mlp", (X, ids, weights, w1, w1_scales, w2, w2_scales, res, ws), tokens, k, experts, d, inner,
+         _DT[X.dtype], X.data_ptr(), _row_stride(X), ids.data_ptr(), weights.data_ptr(), w1.data_ptr(),
+         w1_scales.data_ptr(), w2.data_ptr(), w2_scales.data_ptr(), _ACTIVATIONS[activation], res.data_ptr(),
+         _row_stride(res), _ptr(ws), _bytes(ws))
     return res
 
 
