@@ -520,18 +520,18 @@ gptq_status gptq_mxfp4_matmul_grouped(int batch, int64_t x_rows, int64_t n_rows,
  *   g, u      = the first and the last `inner` of W1[e] x[t]
  *   out[t, :] = sum over j of weights[t, j] * W2[e] (act(g) * u),   e = ids[t, j]
  * with act 0: g / (1 + exp(-g)); 1: 0.5 g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))).
- * X [n_tokens, d_in] bf16 or fp16, row stride ldx; ids int32 and weights fp32 [n_tokens, top_k],
+ * X [n_tokens, d_in] bf16 or fp16, 16-byte aligned, row stride ldx (a multiple of 8); ids int32 and weights fp32 [n_tokens, top_k],
  * dense (as written by gptq_moe_route; an id outside [0, n_experts) is no choice, an expert named
  * twice by a token counts with both weights); W1 e2m1 [n_experts, 2 inner, d_in / 2] (gate rows, then
  * up rows) with scales [n_experts, 2 inner, d_in / 32], W2 [n_experts, d_in, inner / 2] with scales
- * [n_experts, d_in, inner / 32], dense, W1 and W2 16-byte aligned; out [n_tokens, d_in] of X's type,
+ * [n_experts, d_in, inner / 32], dense and all four 16-byte aligned; out [n_tokens, d_in] of X's type,
  * row stride ldo, zeros for a token without choices.  X is not rounded, sums are fp32, and the
  * activations between the products, which carry the weights, keep 16 significant bits.  workspace:
  * gptq_workspace_size(GPTQ_WS_MXFP4_MOE_MLP, 1, inner, d_in, n_tokens * top_k, NULL) bytes, 16-byte
  * aligned; it serves one call at a time.  Requires d_in % 32 == 0, inner % 32 == 0, 1 <= n_experts <=
  * 1024, 1 <= top_k <= 32; n_tokens may be 0 (no-op).  More than GPTQ_MOE_MLP_CHOICES
- * (4096) choices (n_tokens * top_k) are
- * refused (GPTQ_ERR_UNSUPPORTED): group them and use gptq_mxfp4_matmul_grouped.
+ * (4096) choices (n_tokens * top_k), or more than 16384 inputs or inner values, are refused
+ * (GPTQ_ERR_UNSUPPORTED): group the tokens and use gptq_mxfp4_matmul_grouped.
  */
 #define GPTQ_MOE_MLP_CHOICES 4096
 gptq_status gptq_mxfp4_moe_mlp(int64_t n_tokens, int top_k, int n_experts, int d_in, int inner,

@@ -190,7 +190,7 @@ struct MxMlp {
   void* out; int64_t ldo;
   void* workspace; size_t workspace_bytes;
 };
-size_t mx_mlp_workspace(int64_t pairs, int inner);
+size_t mx_mlp_workspace(int64_t pairs, int inner, int d);
 gptq_status mx_mlp_enqueue(const MxMlp& p, hipStream_t stream);
 
 // Routing, grouping and combination of experts (moe.hip).

@@ -459,15 +459,15 @@ gptq_status gptq_mxfp4_moe_mlp(int64_t n_tokens, int top_k, int n_experts, int d
                                const uint8_t* w2_scales, int activation, void* out, int64_t ldo, void* workspace,
                                size_t workspace_bytes, hipStream_t stream) {
   if (n_tokens < 0 || top_k < 1 || top_k > 32 || n_experts < 1 || n_experts > 1024 || d_in < 32 || d_in % 32 != 0 ||
-      inner < 32 || inner % 32 != 0 || inner > (1 << 30) || activation < 0 || activation > 1 ||
+      inner < 32 || inner % 32 != 0 || activation < 0 || activation > 1 ||
       (x_dtype != GPTQ_BF16 && x_dtype != GPTQ_F16))
     return GPTQ_ERR_INVALID_ARG;
   if (n_tokens == 0) return GPTQ_OK;
-  if (n_tokens > GPTQ_MOE_MLP_CHOICES / top_k) return GPTQ_ERR_UNSUPPORTED;
+  if (n_tokens > GPTQ_MOE_MLP_CHOICES / top_k || d_in > 16384 || inner > 16384) return GPTQ_ERR_UNSUPPORTED;
   if (X == nullptr || ids == nullptr || weights == nullptr || W1 == nullptr || w1_scales == nullptr || W2 == nullptr ||
       w2_scales == nullptr || out == nullptr || ldx < d_in || ldo < d_in)
     return GPTQ_ERR_INVALID_ARG;
-  if (!aligned(X, 2) || !aligned(out, 2) || !aligned(ids, 4) || !aligned(weights, 4) || !aligned(W1, 16) ||
+  if (ldx % 8 != 0 || !aligned(X, 16) || !aligned(out, 2) || !aligned(w1_scales, 16) || !aligned(w2_scales, 16) || !aligned(ids, 4) || !aligned(weights, 4) || !aligned(W1, 16) ||
       !aligned(W2, 16) || !aligned(workspace, 16))
     return GPTQ_ERR_INVALID_ARG;
   const gptq::MxMlp p{static_cast<int>(n_tokens), top_k, n_experts, d_in, inner, x_dtype == GPTQ_BF16, X, ldx, ids,
@@ -506,8 +506,10 @@ size_t gptq_workspace_size(gptq_ws_call which, int batch, int d_out, int d_in, i
       if (batch != 1 || d_out < 1 || d_in < 32 || d_in % 32 != 0 || n_tokens_hint < 0) return 0;
       return gptq::mx_workspace(n_tokens_hint, d_out, d_in);
     case GPTQ_WS_MXFP4_MOE_MLP:
-      if (d_out < 32 || d_out % 32 != 0 || n_tokens_hint < 0 || n_tokens_hint > GPTQ_MOE_MLP_CHOICES) return 0;
-      return gptq::mx_mlp_workspace(n_tokens_hint, d_out);
+      if (d_out < 32 || d_out % 32 != 0 || d_in < 32 || d_in % 32 != 0 || n_tokens_hint < 0 ||
+          n_tokens_hint > GPTQ_MOE_MLP_CHOICES)
+        return 0;
+      return gptq::mx_mlp_workspace(n_tokens_hint, d_out, d_in);
   }
   return 0;
 }

@@ -168,8 +168,10 @@ __global__ __launch_bounds__(WK * 64) void mx_rows_kernel(MxArgs a) {
     for (int i = 0; i < FM; ++i) {
       const bool ok = in && have[i];
 #pragma unroll
-      for (int p = 0; p < XR; ++p)
-        __builtin_memcpy(&xv[u][i][p], ok ? x[i] + 16 * XR * b + 16 * p : zeros, 16);
+      for (int p = 0; p < XR; ++p) xv[u][i][p] = i32x4{0, 0, 0, 0};
+      if (ok)
+#pragma unroll
+        for (int p = 0; p < XR; ++p) __builtin_memcpy(&xv[u][i][p], x[i] + 16 * XR * b + 16 * p, 16);
       if constexpr (KIND == kMx4) sx[u][i] = ok ? xs[i][b] : 127u;
     }
   };
@@ -416,23 +418,23 @@ __global__ __launch_bounds__(256) void mx_tile_kernel(MxArgs a) {
   }
 }
 
-// Y from the sums of the parts, in their order.
+// Y from the sums of the parts, in their order, all loads at once.
+template <int SPLITS>
 __global__ __launch_bounds__(256) void mx_sum_kernel(MxArgs a) {
-  const int64_t g = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  const int per_row = (a.n + 3) / 4;
-  const int64_t row = g / per_row;
-  const int o = static_cast<int>(g - row * per_row) * 4, n = min(4, a.n - o);
-  if (row >= a.m) return;
-  float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int z = 0; z < a.splits; ++z) {
-    const float* p = a.part + (static_cast<int64_t>(z) * a.m + row) * a.n + o;
-    float u[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (n == 4) __builtin_memcpy(u, p, 16);
-    else
-      for (int i = 0; i < n; ++i) u[i] = p[i];
+  const int row = blockIdx.y, o = (blockIdx.x * 256 + threadIdx.x) * 4, n = min(4, a.n - o);
+  if (n <= 0) return;
+  const float* p = a.part + static_cast<int64_t>(row) * a.n + o;
+  f32x4 u[SPLITS];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] += u[i];
+  for (int z = 0; z < SPLITS; ++z, p += a.m * a.n) {
+    u[z] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    if (n == 4) __builtin_memcpy(&u[z], p, 16);
+    else
+      for (int i = 0; i < n; ++i) u[z][i] = p[i];
   }
+#pragma unroll
+  for (int z = 1; z < SPLITS; ++z) u[0] += u[z];
+  const float v[4] = {u[0][0], u[0][1], u[0][2], u[0][3]};
   store_y(a, row, o, v);
 }
 
@@ -504,8 +506,10 @@ gptq_status launch_mx(MxArgs a, const MxPlan& p, void* workspace, hipStream_t st
   }
   st = p.kind == kMxTile64 ? launch_mx_tile<64, KIND>(a, stream) : launch_mx_tile<128, KIND>(a, stream);
   if (st != GPTQ_OK || p.splits == 1) return st;
-  const int64_t groups = a.m * ((a.n + 3) / 4);
-  GPTQ_LAUNCH(mx_sum_kernel, dim3(static_cast<unsigned>((groups + 255) / 256)), dim3(256), 0, stream, a);
+  const dim3 g((a.n + 1023) / 1024, static_cast<unsigned>(a.m));   // parts are of few tiles: m is small
+  if (p.splits == 2) GPTQ_LAUNCH(mx_sum_kernel<2>, g, dim3(256), 0, stream, a);
+  else if (p.splits == 4) GPTQ_LAUNCH(mx_sum_kernel<4>, g, dim3(256), 0, stream, a);
+  else GPTQ_LAUNCH(mx_sum_kernel<8>, g, dim3(256), 0, stream, a);
   return GPTQ_OK;
 }
 

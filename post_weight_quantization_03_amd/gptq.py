@@ -859,8 +859,9 @@ def mxfp4_moe_mlp(X: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, w1:
     of W1[e] x.  X [tokens, d] bf16 or fp16, multiplied as it is; ids int32 and weights fp32 [tokens,
     top_k] from :func:`moe_route` (ids outside the experts are no choice); w1 [experts, 2 inner,
     d / 2] and w2 [experts, d, inner / 2] with their scales from :func:`mxfp4_quantize`;
-    ``activation`` "silu" or "gelu_tanh".  At most 4096 choices (tokens * top_k); for more, group the
-    tokens and use :func:`mxfp4_matmul_grouped`."""
+    ``activation`` "silu" or "gelu_tanh".  X whose rows do not start at multiples of 16 bytes is copied
+    first.  At most 4096 choices (tokens * top_k); for more, group the tokens and use
+    :func:`mxfp4_matmul_grouped`."""
     if stream is not None:
         return _on(stream, mxfp4_moe_mlp, X, ids, weights, w1, w1_scales, w2, w2_scales, activation, out, workspace)
     if X.dtype not in (torch.bfloat16, torch.float16) or ids.dtype != torch.int32 or weights.dtype != torch.float32:
@@ -877,6 +878,10 @@ def mxfp4_moe_mlp(X: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, w1:
         raise ValueError("weights and their scales must be contiguous")
     if X.dim() != 2 or X.shape[1] != d or X.stride(1) != 1:
         raise ValueError("X must be [tokens, d] with contiguous rows")
+    if X.data_ptr() % 16 or _row_stride(X) % 8:
+        X = X.clone(memory_format=torch.contiguous_format)
+    if w1_scales.data_ptr() % 16 or w2_scales.data_ptr() % 16:
+        raise ValueError("scales must start at a multiple of 16 bytes")
     tokens = X.shape[0]
     if ids.dim() != 2 or ids.shape[0] != tokens or not 1 <= ids.shape[1] <= 32 or weights.shape != ids.shape or not (
             ids.is_contiguous() and weights.is_contiguous()):

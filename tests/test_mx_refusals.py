@@ -87,14 +87,14 @@ def test_grouped_empty_and_too_large():
     assert gptq.lib().gptq_mxfp4_matmul_grouped(*a.values()) == UNS
 
 
-MLP = dict(tokens=4, k=2, experts=8, d=64, inner=96, xt=BF16, X=16, ldx=64, ids=16, w=16, W1=16, s1=3, W2=16, s2=3, act=0,
+MLP = dict(tokens=4, k=2, experts=8, d=64, inner=96, xt=BF16, X=16, ldx=64, ids=16, w=16, W1=16, s1=16, W2=16, s2=16, act=0,
            out=16, ldo=64, wsp=16, wsb=1 << 20, stream=None)
 
 
 @pytest.mark.parametrize("change", [
     dict(tokens=-1), dict(k=0), dict(k=33), dict(experts=0), dict(experts=1025), dict(d=0), dict(d=80), dict(inner=0),
-    dict(inner=48), dict(xt=F32), dict(xt=E2M1), dict(X=None), dict(X=17), dict(ldx=63), dict(ids=None), dict(ids=18),
-    dict(w=None), dict(w=18), dict(W1=None), dict(W1=8), dict(s1=None), dict(W2=None), dict(W2=8), dict(s2=None),
+    dict(inner=48), dict(xt=F32), dict(xt=E2M1), dict(X=None), dict(X=24), dict(ldx=56), dict(ldx=68), dict(ids=None), dict(ids=18),
+    dict(w=None), dict(w=18), dict(W1=None), dict(W1=8), dict(s1=None), dict(s1=8), dict(W2=None), dict(W2=8), dict(s2=None), dict(s2=4),
     dict(act=2), dict(act=-1), dict(out=None), dict(out=17), dict(ldo=63), dict(wsp=8)])
 def test_mlp_refusals(change):
     assert gptq.lib().gptq_mxfp4_moe_mlp(*{**MLP, **change}.values()) == BAD
