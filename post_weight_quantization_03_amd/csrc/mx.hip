@@ -125,99 +125,158 @@ struct MxArgs : MmArgs {
   int stages;     // of the LDS kernels
   int splits, per;   // parts of the inputs, and their stages
   float* part;       // [splits][m][n] sums, where there is more than one
+  int cap, slots;    // of the kernel for few rows: rows of a tile, units in a wave's ring
 };
 
-// Few rows: 16 outputs x 16 FM rows per workgroup, whose WK waves take every WK-th pair of chunks of
-// 128 inputs straight from memory to registers (a block of 32 per lane and chunk), U chunks in
-// flight per wave; their sums meet in LDS and are added in wave order.
-template <int FM, int WK, int KIND>
-__global__ __launch_bounds__(WK * 64) void mx_rows_kernel(MxArgs a) {
-  constexpr int U = FM == 1 ? 4 : 2, TM = 16 * FM, XR = KIND == kMx4 ? 1 : 4;   // 16-byte pieces of X a block
-  __shared__ __attribute__((aligned(16))) float part[WK][TM][16];
-  __shared__ bool lost[TM];
-  const int tid = threadIdx.x, lane = tid & 63, wk = uniform(tid >> 6);
+// Few rows, at most `cap` (up to 16) of one expert or of the one problem: a workgroup has NW / KS tiles
+// of 16 NM outputs, KS waves of it share a tile's inputs.  All comes by copies to LDS: the rows at once,
+// and weights in units of 256 inputs, up to DEPTH of them in a ring of each wave's own, so that nothing but
+// the matrix instruction's own reads goes through registers.  The waves' sums are added in their order.
+constexpr int UNIT = 2048;   // bytes of a unit of 16 outputs: 8 blocks each
+template <int NW, int KS, int NM, int DEPTH, int KIND>
+__global__ __launch_bounds__(NW * 64) void mx_few_kernel(MxArgs a) {
+  constexpr int GROUPS = NW / KS, COPIES = 2 * NM, XP = KIND == kMx4 ? 1 : 4;   // 16-byte pieces of a block of X
+  extern __shared__ __attribute__((aligned(128))) uint8_t few_lds[];
+  __shared__ f32x4 part[KS == 1 ? 1 : NW][NM][64];
+  const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
   const int64_t mt = blockIdx.x / a.tiles_n;
-  const int n0 = static_cast<int>(blockIdx.x - mt * a.tiles_n) * 16;
-  const Tile t = find_tile<TM>(a, mt);
+  const int tile0 = static_cast<int>(blockIdx.x - mt * a.tiles_n) * GROUPS;
+  const Tile t = find_tile(a, mt, a.cap);
   if (t.count <= 0) return;
+  const int kb = a.kb, group = wave / KS, wk = wave % KS;
   const int j = lane & 15, q = lane >> 4;
-  const uint8_t* zeros = reinterpret_cast<const uint8_t*>(&zero16);
-  const int64_t wrow = static_cast<int64_t>(t.e) * a.n + min(n0 + j, a.n - 1);
-  const uint8_t* w = a.W + wrow * (a.k / 2);
-  const uint8_t* ws = static_cast<const uint8_t*>(a.ws) + wrow * a.kb;
-  const uint8_t* x[FM];
-  const uint8_t* xs[FM];
-  bool have[FM];
+  // the rings, the tiles' scales, zeros, rows of X and their scales
+  const int scale_bytes = (16 * NM * kb + 15) / 16 * 16, pitch = 16 * XP * kb + 16, xs_pitch = (kb + 3) / 4 * 4;
+  uint8_t* const ring = few_lds + wave * a.slots * NM * UNIT;
+  uint8_t* const scales = few_lds + NW * a.slots * NM * UNIT;
+  uint8_t* const zeros = scales + GROUPS * scale_bytes;
+  uint8_t* const xrows = zeros + 64;
+  uint8_t* const xscales = xrows + a.cap * pitch;
+  const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(
+      (__attribute__((address_space(3))) uint8_t*)few_lds));
+  const uint32_t ring0 = lds0 + wave * a.slots * NM * UNIT;
+  const int n0 = 16 * NM * (tile0 + group);   // this wave's outputs
+  const int64_t w0 = static_cast<int64_t>(t.e) * a.n + min(n0, a.n - 1);
+  const uint8_t* const w = a.W + w0 * (16 * kb);
+  const int units = (kb + 7) / 8, mine = (units + KS - 1) / KS;   // of this wave: wk, wk + KS, ..
+  // Piece c of row r of a unit lies at c ^ (r / 2 % 8), so that 16 lanes reading the same piece of 16 rows
+  // cover all banks.  Behind the last block or output the last one is copied again.
+  auto issue = [&](int k) {
+    const int unit = wk + KS * k;
 #pragma unroll
-  for (int i = 0; i < FM; ++i) {
-    const int64_t row = source_row(a, t.p0 + min(16 * i + j, t.count - 1));
-    if (tid < 16) lost[16 * i + j] = row < 0;
-    have[i] = row >= 0 && 16 * i + j < t.count;
-    x[i] = a.X + max(row, static_cast<int64_t>(0)) * a.ldx;
-    if constexpr (KIND == kMx4) xs[i] = static_cast<const uint8_t*>(a.xs) + max(row, static_cast<int64_t>(0)) * a.xsr;
-  }
-  const int chunks = (a.kb + 3) / 4;
-  i32x4 wv[U], xv[U][FM][XR];
-  uint32_t sw[U], sx[U][FM];
-  auto load = [&](int u, int c) {
-    const int b = 4 * c + q;
-    const bool in = b < a.kb;
-    wv[u] = *reinterpret_cast<const i32x4*>(in ? w + 16 * b : zeros);
-    sw[u] = in ? ws[b] : 127u;
-#pragma unroll
-    for (int i = 0; i < FM; ++i) {
-      const bool ok = in && have[i];
-#pragma unroll
-      for (int p = 0; p < XR; ++p) xv[u][i][p] = i32x4{0, 0, 0, 0};
-      if (ok)
-#pragma unroll
-        for (int p = 0; p < XR; ++p) __builtin_memcpy(&xv[u][i][p], x[i] + 16 * XR * b + 16 * p, 16);
-      if constexpr (KIND == kMx4) sx[u][i] = ok ? xs[i][b] : 127u;
+    for (int i = 0; i < COPIES; ++i) {
+      const int r = 8 * i + (lane >> 3), c = (lane & 7) ^ ((r >> 1) & 7);
+      const uint32_t off = 16 * (min(r, max(a.n - 1 - n0, 0)) * kb + min(8 * unit + c, kb - 1));
+      copy16_at(w, off, ring0 + (k % DEPTH) * NM * UNIT + 1024 * i);
     }
   };
-  auto chunk = [&](int g, int u) { return 2 * (wk + WK * (g + u / 2)) + (u & 1); };
-  f32x4 y[FM];
+  // rows and first weights, then the scales through registers: they may start at any byte
+  if (tid < 16) reinterpret_cast<uint32_t*>(zeros)[tid] = 0;
+  const int chunks = (XP * kb + 63) / 64;
+  for (int i = wave; i < t.count * chunks; i += NW) {
+    const int r = i / chunks, c = i - r * chunks;
+    const int64_t row = uniform(source_row(a, t.p0 + r));
+    if (row >= 0 && 64 * c + lane < XP * kb)
+      copy16_at(a.X + row * a.ldx, 1024 * c + 16 * lane,
+                lds0 + static_cast<uint32_t>(xrows - few_lds) + r * pitch + 1024 * c);
+  }
+  for (int k = 0; k < min(DEPTH, mine); ++k) issue(k);
+  {
+    // the outputs' scales are one piece of memory a tile
+    const int g = tid / (NW * 64 / GROUPS), at = tid % (NW * 64 / GROUPS);   // this wave's own tile
+    const int have = max(0, min(16 * NM, a.n - 16 * NM * (tile0 + g))) * kb;
+    const uint8_t* from = static_cast<const uint8_t*>(a.ws) + (static_cast<int64_t>(t.e) * a.n + 16 * NM * (tile0 + g)) * kb;
+    for (int i = 16 * at; i < have; i += 16 * (NW * 64 / GROUPS)) {
+      uint8_t v[16];
+      if (i + 16 <= have) {
+        __builtin_memcpy(v, from + i, 16);
+      } else {
 #pragma unroll
-  for (int i = 0; i < FM; ++i) y[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-  for (int u = 0; u < U; ++u)
-    if (chunk(0, u) < chunks) load(u, chunk(0, u));
-  for (int g = 0; chunk(g, 0) < chunks; g += U / 2) {
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (chunk(g, u) < chunks) {
-        if constexpr (KIND == kMx4) {
-#pragma unroll
-          for (int i = 0; i < FM; ++i)
-            y[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(widen(wv[u]), widen(xv[u][i][0]), y[i], 4, 4, 0,
-                                                                    static_cast<int>(sw[u]), 0, static_cast<int>(sx[u][i]));
-        } else {
-#pragma unroll
-          for (int p = 0; p < 4; ++p) {
-            const bf16x8 wf = mx_bf16(static_cast<uint32_t>(wv[u][p]), sw[u]);
-#pragma unroll
-            for (int i = 0; i < FM; ++i) y[i] = mx_mma16<KIND>(wf, XValues<KIND>(xv[u][i][p]), y[i]);
-          }
+        for (int b = 0; b < 16; ++b) v[b] = i + b < have ? from[i + b] : 127;
+      }
+      *reinterpret_cast<uint4*>(scales + g * scale_bytes + i) = *reinterpret_cast<const uint4*>(v);
+    }
+    if constexpr (KIND == kMx4)
+      for (int i = tid; i < t.count * (xs_pitch / 4); i += NW * 64) {
+        const int r = i / (xs_pitch / 4), b0 = 4 * (i - r * (xs_pitch / 4));
+        const int64_t row = source_row(a, t.p0 + r);
+        uint8_t v[4] = {127, 127, 127, 127};
+        if (row >= 0) {
+          const uint8_t* s = static_cast<const uint8_t*>(a.xs) + row * a.xsr + b0;
+          if (b0 + 4 <= kb) __builtin_memcpy(v, s, 4);
+          else
+            for (int b = 0; b < kb - b0; ++b) v[b] = s[b];
         }
-        if (chunk(g + U / 2, u) < chunks) load(u, chunk(g + U / 2, u));
+        *reinterpret_cast<uint32_t*>(xscales + r * xs_pitch + b0) = *reinterpret_cast<const uint32_t*>(v);
+      }
+  }
+  wait_copies();   // the first units too: they were asked for before
+  __syncthreads();
+  const int jr = min(j, t.count - 1);   // columns behind the last row repeat it; nothing reads them
+  const bool lost = source_row(a, t.p0 + jr) < 0;
+  const uint8_t* const x = xrows + jr * pitch;
+  const uint8_t* const scale = scales + group * scale_bytes;
+  f32x4 y[NM];
+#pragma unroll
+  for (int g = 0; g < NM; ++g) y[g] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  for (int k = 0; k < mine; ++k) {
+    // this unit's copies are the oldest of those of up to DEPTH units
+    if (k + DEPTH <= mine) wait_vmcnt<(DEPTH - 1) * COPIES>();
+    else wait_copies();
+    asm volatile("" ::: "memory");
+    const uint8_t* const at = ring + (k % DEPTH) * NM * UNIT + j * 128;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int b = 8 * (wk + KS * k) + q + 4 * h;   // this lane's block
+      const bool in = b < kb;
+      i32x4 v[XP], wv[NM];
+      uint32_t s[NM];
+#pragma unroll
+      for (int g = 0; g < NM; ++g) {
+        wv[g] = *reinterpret_cast<const i32x4*>(at + g * UNIT + 16 * ((q + 4 * h) ^ ((j >> 1) & 7)));
+        s[g] = scale[(16 * g + j) * kb + min(b, kb - 1)];
+      }
+      const uint8_t* from = in && !lost ? x + 16 * XP * b : zeros;
+#pragma unroll
+      for (int p = 0; p < XP; ++p) v[p] = *reinterpret_cast<const i32x4*>(from + 16 * p);
+#pragma unroll
+      for (int g = 0; g < NM; ++g) s[g] = in ? s[g] : 127u;
+      if constexpr (KIND == kMx4) {
+        int sx = xscales[jr * xs_pitch + min(b, kb - 1)];
+        sx = in ? sx : 127;
+#pragma unroll
+        for (int g = 0; g < NM; ++g)
+          y[g] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(widen(wv[g]), widen(v[0]), y[g], 4, 4, 0,
+                                                                  static_cast<int>(s[g]), 0, sx);
+      } else {
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+          const XValues<KIND> xv(v[p]);
+#pragma unroll
+          for (int g = 0; g < NM; ++g) y[g] = mx_mma16<KIND>(mx_bf16(static_cast<uint32_t>(wv[g][p]), s[g]), xv, y[g]);
+        }
       }
     }
-  }
-#pragma unroll
-  for (int i = 0; i < FM; ++i) *reinterpret_cast<f32x4*>(&part[wk][16 * i + j][4 * q]) = y[i];
-  __syncthreads();
-  for (int g = tid; g < min(TM, t.count) * 4; g += WK * 64) {
-    const int c = g & 3, r = g >> 2;
-    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-    for (int h = 0; h < WK; ++h) {
-      const f32x4 o = *reinterpret_cast<const f32x4*>(&part[h][r][4 * c]);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] += o[e];
+    if (k + DEPTH < mine) {
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the unit has been read
+      issue(k + DEPTH);
     }
-    const bool none = lost[r];
-    const float f[4] = {none ? 0.0f : v[0], none ? 0.0f : v[1], none ? 0.0f : v[2], none ? 0.0f : v[3]};
-    store_y(a, t.p0 + r, n0 + 4 * c, f);
+  }
+  if constexpr (KS > 1) {
+#pragma unroll
+    for (int g = 0; g < NM; ++g) part[wave][g][lane] = y[g];
+    __syncthreads();
+    if (wk != 0) return;
+#pragma unroll
+    for (int h = 1; h < KS; ++h)
+#pragma unroll
+      for (int g = 0; g < NM; ++g) y[g] += part[wave + h][g][lane];
+  }
+  if (j >= t.count) return;
+#pragma unroll
+  for (int g = 0; g < NM; ++g) {
+    const float f[4] = {lost ? 0.0f : y[g][0], lost ? 0.0f : y[g][1], lost ? 0.0f : y[g][2], lost ? 0.0f : y[g][3]};
+    store_y(a, t.p0 + j, n0 + 16 * g + 4 * q, f);
   }
 }
 
@@ -440,45 +499,68 @@ __global__ __launch_bounds__(256) void mx_sum_kernel(MxArgs a) {
 
 // ---------------------------------------------------------------------------- host side
 
-enum MxProduct { kMxRows, kMxTile64, kMxTile128 };
+enum MxProduct { kMxFew, kMxTile64, kMxTile128 };
 struct MxPlan {
   MxProduct kind;
   int splits;
+  int cap;     // kMxFew: rows of a tile
+  bool wide;   // kMxFew: 4 tiles of 32 outputs a workgroup, else one of 16
 };
 
 int stage_blocks(int kind) { return kind == kMx4 ? MxStage<kMx4>::BLOCKS : MxStage<kMxBf16>::BLOCKS; }
 
-// Rows of a tile of the kernel for few rows: 16 for grouped rows.
-int mx_rows_tile(int64_t m, bool grouped) { return grouped || m <= 16 ? 16 : m <= 32 ? 32 : 64; }
+// The kernel for few rows: 8 waves sharing one tile of 16 outputs, or 4 waves with one of 32 each.
+constexpr int FEW_DEPTH = 4, WIDE_DEPTH = 2;
+constexpr int FEW_LDS = 78 * 1024, FEW_MOST_LDS = 150 * 1024;   // two workgroups on a CU, and one
+int few_slots(int kb, bool wide) { return std::min((kb + 7) / 8 / (wide ? 1 : 8) + 1, wide ? WIDE_DEPTH : FEW_DEPTH); }
+// LDS without rows of X, and of a row.
+int64_t few_fixed(int kb, bool wide) {
+  const int64_t scales = wide ? 4 * ((32 * static_cast<int64_t>(kb) + 15) / 16 * 16) : 16 * static_cast<int64_t>(kb);
+  return (wide ? 4 * 2 : 8) * few_slots(kb, wide) * UNIT + scales + 64;
+}
+int64_t few_row(int kb, int kind) {
+  return kind == kMx4 ? 16 * static_cast<int64_t>(kb) + 16 + (kb + 3) / 4 * 4 : 64 * static_cast<int64_t>(kb) + 16;
+}
 
 // Which kernel, by sizes alone (the workspace's size goes by the same rule).
 MxPlan mx_plan(int64_t m, int n, int k, int kind, bool grouped, int experts) {
   const double used = grouped ? static_cast<double>(std::min<int64_t>(experts, m)) : 1.0;
   const double rows = static_cast<double>(m) / used;
-  if (rows <= 16) return {kMxRows, 1};
+  const int kb = k / MXB;
+  const bool wide = kb <= 128 && used * ((n + 15) / 16) > 1024;
+  const int64_t most = std::min<int64_t>(16, m);
+  const int64_t want = std::min<int64_t>(most, static_cast<int64_t>(grouped ? 1.5 * rows + 2 : m));
+  const int64_t fit = (FEW_LDS - few_fixed(kb, wide)) / few_row(kb, kind);
+  const int64_t cap = std::min(most, std::max(fit, std::min(want, (FEW_MOST_LDS - few_fixed(kb, wide)) / few_row(kb, kind))));
+  if (cap >= 1 && rows <= 16 && (grouped ? cap * 2 >= rows : (m + cap - 1) / cap <= 2))
+    return {kMxFew, 1, static_cast<int>(cap), wide};
   auto tiles = [&](int t) {
     const double r = grouped ? static_cast<double>(m) / t + 0.5 * used : static_cast<double>((m + t - 1) / t);
     return r * ((n + t - 1) / t);
   };
-  const int stages = (k / MXB + stage_blocks(kind) - 1) / stage_blocks(kind);
-  if (tiles(128) >= 384) return {kMxTile128, 1};
+  const int stages = (kb + stage_blocks(kind) - 1) / stage_blocks(kind);
+  if (tiles(128) >= 384) return {kMxTile128, 1, 0, false};
   int splits = 1;
   if (!grouped) {
     while (splits < 8 && tiles(64) * splits < 384 && stages / (2 * splits) >= 8) splits *= 2;
     while (splits > 1 && static_cast<double>(splits) * static_cast<double>(m) * n * 4 > 64e6) splits /= 2;
   }
-  return {kMxTile64, splits};
+  return {kMxTile64, splits, 0, false};
 }
 
 size_t mx_part_bytes(const MxPlan& p, int64_t m, int n) {
   return p.splits > 1 ? static_cast<size_t>(p.splits) * static_cast<size_t>(m) * n * sizeof(float) : 0;
 }
 
-template <int FM, int WK, int KIND>
-gptq_status launch_mx_rows(MxArgs a, hipStream_t stream) {
-  a.tiles_n = (a.n + 15) / 16;
-  const dim3 g(static_cast<unsigned>(tile_rows(a, 16 * FM) * a.tiles_n));
-  GPTQ_LAUNCH((mx_rows_kernel<FM, WK, KIND>), g, dim3(WK * 64), 0, stream, a);
+template <int NW, int KS, int NM, int DEPTH, int KIND>
+gptq_status launch_mx_few(MxArgs a, const MxPlan& p, hipStream_t stream) {
+  constexpr int OUTPUTS = NW / KS * NM * 16;
+  a.tiles_n = (a.n + OUTPUTS - 1) / OUTPUTS;
+  a.cap = p.cap;
+  a.slots = few_slots(a.kb, p.wide);
+  const dim3 g(static_cast<unsigned>(tile_rows(a, a.cap) * a.tiles_n));
+  GPTQ_LAUNCH((mx_few_kernel<NW, KS, NM, DEPTH, KIND>), g, dim3(NW * 64),
+              static_cast<size_t>(few_fixed(a.kb, p.wide) + a.cap * few_row(a.kb, KIND)), stream, a);
   return GPTQ_OK;
 }
 
@@ -498,12 +580,8 @@ gptq_status launch_mx(MxArgs a, const MxPlan& p, void* workspace, hipStream_t st
   a.per = (a.stages + p.splits - 1) / p.splits;
   a.part = static_cast<float*>(workspace);
   gptq_status st;
-  if (p.kind == kMxRows) {
-    const int tm = mx_rows_tile(a.m, a.off != nullptr);
-    if (tm == 64) return launch_mx_rows<4, 8, KIND>(a, stream);
-    if (tm == 32) return launch_mx_rows<2, 8, KIND>(a, stream);
-    return a.kb >= 96 ? launch_mx_rows<1, 8, KIND>(a, stream) : launch_mx_rows<1, 4, KIND>(a, stream);
-  }
+  if (p.kind == kMxFew)
+    return p.wide ? launch_mx_few<4, 1, 2, WIDE_DEPTH, KIND>(a, p, stream) : launch_mx_few<8, 8, 1, FEW_DEPTH, KIND>(a, p, stream);
   st = p.kind == kMxTile64 ? launch_mx_tile<64, KIND>(a, stream) : launch_mx_tile<128, KIND>(a, stream);
   if (st != GPTQ_OK || p.splits == 1) return st;
   const dim3 g((a.n + 1023) / 1024, static_cast<unsigned>(a.m));   // parts are of few tiles: m is small
@@ -515,8 +593,8 @@ gptq_status launch_mx(MxArgs a, const MxPlan& p, void* workspace, hipStream_t st
 
 // Whether the launch is one the kernels number their tiles for.
 bool mx_launchable(const MxArgs& a, const MxPlan& p) {
-  const int tm = p.kind == kMxTile128 ? 128 : p.kind == kMxTile64 ? 64 : mx_rows_tile(a.m, a.off != nullptr);
-  const int tn = p.kind == kMxRows ? 16 : tm;
+  const int tm = p.kind == kMxTile128 ? 128 : p.kind == kMxTile64 ? 64 : p.cap;
+  const int tn = p.kind == kMxFew ? 16 : tm;
   return tile_rows(a, tm) <= (1 << 22) / ((a.n + tn - 1) / tn);
 }
 

@@ -112,8 +112,7 @@ __device__ __forceinline__ int64_t uniform(int64_t v) {
 
 // The mt-th tile of TM rows: of the one problem, or counting tiles expert by expert.  Every wave
 // finds it for itself, 64 experts at a time.
-template <int TM>
-__device__ __forceinline__ Tile find_tile(const MmArgs& a, int64_t mt) {
+__device__ __forceinline__ Tile find_tile(const MmArgs& a, int64_t mt, int TM) {
   if (a.off == nullptr) {
     const int64_t p0 = mt * TM;
     return {0, p0, static_cast<int>(min(static_cast<int64_t>(TM), a.m - p0))};
@@ -144,6 +143,8 @@ __device__ __forceinline__ Tile find_tile(const MmArgs& a, int64_t mt) {
   }
   return {0, 0, 0};
 }
+template <int TM>
+__device__ __forceinline__ Tile find_tile(const MmArgs& a, int64_t mt) { return find_tile(a, mt, TM); }
 
 // The row of X behind output row p, -1 for none.
 __device__ __forceinline__ int64_t source_row(const MmArgs& a, int64_t p) {
