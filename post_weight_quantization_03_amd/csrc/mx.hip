@@ -280,81 +280,35 @@ __global__ __launch_bounds__(NW * 64) void mx_few_kernel(MxArgs a) {
   }
 }
 
-// The LDS kernels' stage is 128 bytes of every row of X: 256 inputs of 4-bit rows, 64 of 16-bit
-// ones, whose weights are 32 bytes a row.  Two instructions each use one half: with 4 bits the 16-byte
-// pieces q and q + 4 of a row are the lane's blocks of the first and the second, and with 16 bits
-// its 8 inputs of the stage's first and second block.
-constexpr int ROW = 128;   // bytes of a row of X a stage
-template <int KIND>
+// The tile kernel's stage is XB bytes of every row of X: XB / 64 instructions for each 16 outputs x 16
+// rows, the h-th of which takes the row's 16-byte pieces 4 h + q, q = 0..3 by lane: with 4 bits a block of
+// 32 inputs each, with 16 bits 8 inputs of one block, whose 8 codes are word q of piece h of the weights.
+template <int KIND, int XB>
 struct MxStage {
-  static constexpr int WBYTES = KIND == kMx4 ? 128 : 32;   // bytes of a row of W
-  static constexpr int BLOCKS = KIND == kMx4 ? 8 : 2;      // scales of a row
+  static constexpr int WB = KIND == kMx4 ? XB : XB / 4;            // bytes of a row of W
+  static constexpr int BLOCKS = KIND == kMx4 ? XB / 16 : XB / 64;  // scales of a row
+  // where piece c of row r lies: 16 lanes reading the same piece (of W in 16 bits: word of one) of 16 rows
+  // cover all banks
+  static __device__ __forceinline__ int x_at(int r, int c) { return XB == 128 ? c ^ ((r >> 1) & 7) : c ^ (r & 15); }
+  static __device__ __forceinline__ int w_at(int r, int c) {
+    return KIND == kMx4 ? x_at(r, c) : WB == 32 ? c ^ ((r >> 3) & 1) : c ^ ((r >> 2) & 3);
+  }
 };
 
-// A lane's operands of a stage: 16 outputs' weights and 16 rows' activations.
-template <int KIND>
-struct MxW {
-  bf16x8 v[2];
-};
-template <>
-struct MxW<kMx4> {
-  i32x4 v[2];
-  int s;   // the scales of both halves in its two low bytes
-};
-template <int KIND>
-struct MxX {
-  XValues<KIND> v[2];
-};
-template <>
-struct MxX<kMx4> {
-  i32x4 v[2];
-  int s;
-};
-template <int KIND>
-__device__ __forceinline__ void mx_mma(const MxW<KIND>& w, const MxX<KIND>& x, f32x4& acc) {
-  if constexpr (KIND == kMx4) {
-    acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(widen(w.v[0]), widen(x.v[0]), acc, 4, 4, 0, w.s, 0, x.s);
-    acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(widen(w.v[1]), widen(x.v[1]), acc, 4, 4, 1, w.s, 1, x.s);
-  } else {
-    acc = mx_mma16<KIND>(w.v[0], x.v[0], acc);
-    acc = mx_mma16<KIND>(w.v[1], x.v[1], acc);
-  }
-}
-
-// The scale codes of stage s of a row (those behind the last block count as 1), 4-bit operands' in
-// the order 0 4 1 5 2 6 3 7, so that a lane's two are neighbours.
-template <int KIND>
-__device__ __forceinline__ uint2 stage_scales(const uint8_t* row, int s, int kb) {
-  constexpr int N = MxStage<KIND>::BLOCKS;
-  uint8_t b[8];
-  if (N * (s + 1) <= kb) {
-    __builtin_memcpy(b, row + N * s, N);
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i) b[i] = N * s + i < kb ? row[N * s + i] : 127;
-  }
-  if constexpr (KIND == kMx4) {
-    uint2 v;
-    __builtin_memcpy(&v, b, 8);
-    return make_uint2(__builtin_amdgcn_perm(v.y, v.x, 0x05010400u), __builtin_amdgcn_perm(v.y, v.x, 0x07030602u));
-  } else {
-    return make_uint2(b[0] | static_cast<uint32_t>(b[1]) << 8, 0);
-  }
-}
-
-// Tiles of TM rows x TN outputs, 2 x 2 waves, two buffers, the next stage's copies in flight during
-// this one's products.  The 16-byte piece c of a row r of 128 bytes lies at c ^ (r / 2 % 8), so that
-// 16 lanes reading the same piece of 16 rows cover all 64 banks.  gridDim.y parts of the inputs:
-// few tiles would leave most of the chip idle (sums of parts are added by mx_sum_kernel).
-template <int TM, int TN, int KIND>
+// Tiles of TM rows x TN outputs, 2 x 2 waves, NB buffers, NB - 1 stages of copies on the way.  The
+// scales of up to PB blocks are in LDS before their first stage, so that the loop has no loads but copies
+// and can wait for them by their number.  gridDim.y parts of the inputs: few tiles would leave most of the
+// chip idle (sums of parts are added by mx_sum_kernel).
+template <int TM, int TN, int XB, int NB, int KIND>
 __global__ __launch_bounds__(256) void mx_tile_kernel(MxArgs a) {
-  constexpr int NW = 4, FM = TM / 32, FN = TN / 32;
-  constexpr int WB = MxStage<KIND>::WBYTES, STAGE = TM * ROW + TN * WB;
-  constexpr int LX = TM / 8 / NW, WC = TN * WB / 1024, LW = (WC + NW - 1) / NW;   // copies of 1 KB: per wave, in all, per wave
-  constexpr int SROWS = KIND == kMx4 ? TM + TN : TN;
-  static_assert(SROWS <= 256 && TM <= 256 && TM % 32 == 0 && TN % 32 == 0, "tile shape");
-  __shared__ __attribute__((aligned(128))) uint8_t lds[2 * STAGE];
-  __shared__ uint2 scales[2][SROWS];
+  typedef MxStage<KIND, XB> St;
+  constexpr int NW = 4, FM = TM / 32, FN = TN / 32, H = XB / 64;
+  constexpr int STAGE = TM * XB + TN * St::WB, XROWS = 1024 / XB, WROWS = 1024 / St::WB;   // rows of one copy
+  constexpr int LX = TM * XB / 1024 / NW, LW = TN * St::WB / 1024 / NW, LD = LX + LW;
+  constexpr int SROWS = KIND == kMx4 ? TM + TN : TN, PB = KIND != kMx4 ? 256 : TM == 64 ? 128 : 48, PITCH = PB + 4;
+  static_assert(LW >= 1 && TM % 32 == 0 && TN % 32 == 0 && SROWS <= 256 && PB % St::BLOCKS == 0, "tile shape");
+  __shared__ __attribute__((aligned(128))) uint8_t lds[NB * STAGE];
+  __shared__ __attribute__((aligned(16))) uint8_t scales[SROWS * PITCH];
   __shared__ bool lost[TM];
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
   int64_t mt;
@@ -368,93 +322,114 @@ __global__ __launch_bounds__(256) void mx_tile_kernel(MxArgs a) {
   const uint8_t* zeros = reinterpret_cast<const uint8_t*>(&zero16);
   const int64_t xbytes = KIND == kMx4 ? a.k / 2 : 2 * static_cast<int64_t>(a.k);
 
-  const int c = (lane & 7) ^ ((4 * wave + lane / 16) & 7);   // this lane's piece of a 128-byte row: the same in every copy
   const uint8_t* xsrc[LX];
+  const uint8_t* wsrc[LW];
+  int xc[LX], wc[LW];   // this lane's pieces
 #pragma unroll
   for (int i = 0; i < LX; ++i) {
-    const int64_t row = source_row(a, t.p0 + min((wave + NW * i) * 8 + lane / 8, t.count - 1));
-    xsrc[i] = row >= 0 ? a.X + row * a.ldx + 16 * c : nullptr;
+    const int r = (wave + NW * i) * XROWS + lane / (XB / 16);
+    const int64_t row = source_row(a, t.p0 + min(r, t.count - 1));
+    xc[i] = St::x_at(r, lane % (XB / 16));
+    xsrc[i] = row >= 0 ? a.X + row * a.ldx + 16 * xc[i] : nullptr;
   }
-  const uint8_t* wsrc[LW];
-  const int wc = KIND == kMx4 ? c : lane & 1;
 #pragma unroll
   for (int i = 0; i < LW; ++i) {
-    const int r = KIND == kMx4 ? (wave + NW * i) * 8 + lane / 8 : (wave + NW * i) * 32 + lane / 2;
-    wsrc[i] = We + static_cast<int64_t>(min(n0 + r, a.n - 1)) * (a.k / 2) + 16 * wc;
+    const int r = (wave + NW * i) * WROWS + lane / (St::WB / 16);
+    wc[i] = St::w_at(r, lane % (St::WB / 16));
+    wsrc[i] = We + static_cast<int64_t>(min(n0 + r, a.n - 1)) * (a.k / 2) + 16 * wc[i];
   }
   if (tid < TM) lost[tid] = source_row(a, t.p0 + min(tid, t.count - 1)) < 0;
-  const uint8_t* srow = nullptr;   // this thread's row of scales; null: no such row
-  if (tid < SROWS) {
-    const int o = KIND == kMx4 ? tid - TM : tid;
-    if (o >= 0) {
-      srow = static_cast<const uint8_t*>(a.ws) + (static_cast<int64_t>(t.e) * a.n + min(n0 + o, a.n - 1)) * a.kb;
-    } else {
-      const int64_t row = source_row(a, t.p0 + min(tid, t.count - 1));
-      if (row >= 0) srow = static_cast<const uint8_t*>(a.xs) + row * a.xsr;
-    }
-  }
-  uint2 s_next = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
   const unsigned lds0 = static_cast<unsigned>(reinterpret_cast<uintptr_t>(
       (__attribute__((address_space(3))) uint8_t*)lds));
-  auto issue = [&](int s) {
-    if (srow != nullptr) s_next = stage_scales<KIND>(srow, s, a.kb);
-    const unsigned to = lds0 + (s & 1) * STAGE;
-    const bool xin = static_cast<int64_t>(s) * ROW + 16 * c < xbytes, win = s * WB + 16 * wc < a.k / 2;
+  auto issue = [&](int s, int buffer) {
+    const unsigned to = lds0 + buffer * STAGE + wave * 1024;
 #pragma unroll
     for (int i = 0; i < LX; ++i)
-      copy16(xin && xsrc[i] != nullptr ? xsrc[i] + static_cast<int64_t>(s) * ROW : zeros, to + (wave + NW * i) * 1024);
+      copy16(static_cast<int64_t>(s) * XB + 16 * xc[i] < xbytes && xsrc[i] != nullptr ? xsrc[i] + static_cast<int64_t>(s) * XB : zeros,
+             to + NW * i * 1024);
 #pragma unroll
     for (int i = 0; i < LW; ++i)
-      if (wave + NW * i < WC) copy16(win ? wsrc[i] + s * WB : zeros, to + TM * ROW + (wave + NW * i) * 1024);
+      copy16(static_cast<int64_t>(s) * St::WB + 16 * wc[i] < a.k / 2 ? wsrc[i] + static_cast<int64_t>(s) * St::WB : zeros,
+             to + TM * XB + NW * i * 1024);
   };
 
   const int wm = wave / 2, wn = wave % 2;
   const int j = lane & 15, q = lane >> 4;
-  const int swz = (j >> 1) & 7;
-  const int at0 = j * ROW + 16 * (q ^ swz), at1 = j * ROW + 16 * ((q + 4) ^ swz);
   f32x4 y[FM][FN];
 #pragma unroll
   for (int i = 0; i < FM; ++i)
 #pragma unroll
     for (int h = 0; h < FN; ++h) y[i][h] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  if (first < end) issue(first);
-  for (int s = first; s < end; ++s) {
-    wait_copies();
-    if (tid < SROWS) scales[s & 1][tid] = s_next;
-    __syncthreads();
-    if (s + 1 < end) issue(s + 1);
-    const uint8_t* xb = lds + (s & 1) * STAGE + wm * (TM / 2) * ROW;
-    const uint8_t* wb = lds + (s & 1) * STAGE + TM * ROW + wn * (TN / 2) * WB;
-    MxW<KIND> wf[FN];
-#pragma unroll
-    for (int h = 0; h < FN; ++h) {
-      const int o = wn * (TN / 2) + 16 * h + j;
-      if constexpr (KIND == kMx4) {
-        wf[h].v[0] = *reinterpret_cast<const i32x4*>(wb + 16 * h * ROW + at0);
-        wf[h].v[1] = *reinterpret_cast<const i32x4*>(wb + 16 * h * ROW + at1);
-        wf[h].s = reinterpret_cast<const uint16_t*>(&scales[s & 1][TM + o])[q];
+  for (int p0 = first; p0 < end; p0 += PB / St::BLOCKS) {
+    const int p1 = min(p0 + PB / St::BLOCKS, end);
+    if (p0 > first) __syncthreads();   // everyone is done with the scales and buffers before
+    for (int i = tid; i < SROWS * (PB / 16); i += 256) {
+      const int r = i % SROWS, b0 = p0 * St::BLOCKS + 16 * (i / SROWS);
+      const int o = KIND == kMx4 ? r - TM : r;
+      const uint8_t* row = nullptr;
+      if (o >= 0) {
+        row = static_cast<const uint8_t*>(a.ws) + (static_cast<int64_t>(t.e) * a.n + min(n0 + o, a.n - 1)) * a.kb;
       } else {
-        const uint32_t* p = reinterpret_cast<const uint32_t*>(wb + (16 * h + j) * WB) + q;
-        const uint32_t sc = scales[s & 1][o].x;
-        wf[h].v[0] = mx_bf16(p[0], sc & 255);
-        wf[h].v[1] = mx_bf16(p[4], sc >> 8);
+        const int64_t x = source_row(a, t.p0 + min(r, t.count - 1));
+        if (x >= 0) row = static_cast<const uint8_t*>(a.xs) + x * a.xsr;
       }
+      uint32_t v[4] = {0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu};   // behind the last block: 1
+      if (row != nullptr && b0 + 16 <= a.kb) {
+        __builtin_memcpy(v, row + b0, 16);
+      } else if (row != nullptr && b0 < a.kb) {
+        uint8_t b[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) b[e] = b0 + e < a.kb ? row[b0 + e] : 127;
+        __builtin_memcpy(v, b, 16);
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) *reinterpret_cast<uint32_t*>(scales + r * PITCH + 16 * (i / SROWS) + 4 * e) = v[e];
     }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // the loop counts copies alone
 #pragma unroll
-    for (int i = 0; i < FM; ++i) {
-      const i32x4 lo = *reinterpret_cast<const i32x4*>(xb + 16 * i * ROW + at0);
-      const i32x4 hi = *reinterpret_cast<const i32x4*>(xb + 16 * i * ROW + at1);
-      MxX<KIND> xf;
-      if constexpr (KIND == kMx4) {
-        xf.v[0] = lo;
-        xf.v[1] = hi;
-        xf.s = reinterpret_cast<const uint16_t*>(&scales[s & 1][wm * (TM / 2) + 16 * i + j])[q];
-      } else {
-        xf.v[0] = XValues<KIND>(lo);
-        xf.v[1] = XValues<KIND>(hi);
+    for (int s = 0; s < NB - 1; ++s)
+      if (p0 + s < p1) issue(p0 + s, s);
+    for (int s = p0; s < p1; ++s) {
+      // this stage's copies are the oldest of those of up to NB - 1 stages
+      if (NB >= 4 && s + 2 < p1) wait_vmcnt<2 * LD>();
+      else if (NB >= 3 && s + 1 < p1) wait_vmcnt<LD>();
+      else wait_vmcnt<0>();
+      __syncthreads();   // everyone's copies have landed, and everyone is done with the stage before
+      if (s + NB - 1 < p1) issue(s + NB - 1, (s - p0 + NB - 1) % NB);
+      const uint8_t* xb = lds + (s - p0) % NB * STAGE + wm * (TM / 2) * XB;
+      const uint8_t* wb = lds + (s - p0) % NB * STAGE + TM * XB + wn * (TN / 2) * St::WB;
+      const uint8_t* sc = scales + (s - p0) * St::BLOCKS;
+      const uint8_t* ws = sc + ((KIND == kMx4 ? TM : 0) + wn * (TN / 2) + j) * PITCH;
+#pragma unroll
+      for (int h = 0; h < H; ++h) {
+        i32x4 w4[FN];
+        bf16x8 w16[FN];
+        int sw[FN];
+#pragma unroll
+        for (int f = 0; f < FN; ++f) {
+          const uint8_t* row = wb + (16 * f + j) * St::WB;
+          if constexpr (KIND == kMx4) {
+            w4[f] = *reinterpret_cast<const i32x4*>(row + 16 * St::w_at(j, 4 * h + q));
+            sw[f] = ws[16 * f * PITCH + 4 * h + q];
+          } else {
+            w16[f] = mx_bf16(*reinterpret_cast<const uint32_t*>(row + 16 * St::w_at(j, h) + 4 * q), ws[16 * f * PITCH + h]);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < FM; ++i) {
+          const i32x4 v = *reinterpret_cast<const i32x4*>(xb + (16 * i + j) * XB + 16 * St::x_at(j, 4 * h + q));
+          if constexpr (KIND == kMx4) {
+            const int sx = sc[(wm * (TM / 2) + 16 * i + j) * PITCH + 4 * h + q];
+#pragma unroll
+            for (int f = 0; f < FN; ++f)
+              y[i][f] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(widen(w4[f]), widen(v), y[i][f], 4, 4, 0, sw[f], 0, sx);
+          } else {
+            const XValues<KIND> xv(v);
+#pragma unroll
+            for (int f = 0; f < FN; ++f) y[i][f] = mx_mma16<KIND>(w16[f], xv, y[i][f]);
+          }
+        }
       }
-#pragma unroll
-      for (int h = 0; h < FN; ++h) mx_mma<KIND>(wf[h], xf, y[i][h]);
     }
   }
   MxArgs out = a;
@@ -507,7 +482,10 @@ struct MxPlan {
   bool wide;   // kMxFew: 4 tiles of 32 outputs a workgroup, else one of 16
 };
 
-int stage_blocks(int kind) { return kind == kMx4 ? MxStage<kMx4>::BLOCKS : MxStage<kMxBf16>::BLOCKS; }
+// The tile kernel's stages: 256 inputs of 4-bit rows; of 16-bit ones 128 in the small tiles, else 64.
+constexpr int tile_xb(int kind, int tile) { return kind != kMx4 && tile == 64 ? 256 : 128; }
+constexpr int tile_blocks(int kind, int tile) { return kind == kMx4 ? tile_xb(kind, tile) / 16 : tile_xb(kind, tile) / 64; }
+constexpr int tile_buffers(int kind, int tile) { return tile == 64 ? 3 : 2; }
 
 // The kernel for few rows: 8 waves sharing one tile of 16 outputs, or 4 waves with one of 32 each.
 constexpr int FEW_DEPTH = 4, WIDE_DEPTH = 2;
@@ -538,11 +516,11 @@ MxPlan mx_plan(int64_t m, int n, int k, int kind, bool grouped, int experts) {
     const double r = grouped ? static_cast<double>(m) / t + 0.5 * used : static_cast<double>((m + t - 1) / t);
     return r * ((n + t - 1) / t);
   };
-  const int stages = (kb + stage_blocks(kind) - 1) / stage_blocks(kind);
+  const int stages = (kb + tile_blocks(kind, 64) - 1) / tile_blocks(kind, 64);
   if (tiles(128) >= 384) return {kMxTile128, 1, 0, false};
   int splits = 1;
   if (!grouped) {
-    while (splits < 8 && tiles(64) * splits < 384 && stages / (2 * splits) >= 8) splits *= 2;
+    while (splits < 8 && tiles(64) * splits < 384 && stages / (2 * splits) >= 4) splits *= 2;
     while (splits > 1 && static_cast<double>(splits) * static_cast<double>(m) * n * 4 > 64e6) splits /= 2;
   }
   return {kMxTile64, splits, 0, false};
@@ -565,30 +543,29 @@ gptq_status launch_mx_few(MxArgs a, const MxPlan& p, hipStream_t stream) {
 }
 
 template <int T, int KIND>
-gptq_status launch_mx_tile(MxArgs a, hipStream_t stream) {
+gptq_status launch_mx_tile(MxArgs a, const MxPlan& p, void* workspace, hipStream_t stream) {
+  constexpr int BLOCKS = tile_blocks(KIND, T);
   a.order = {(a.n + T - 1) / T, tile_rows(a, T)};
+  a.stages = (a.kb + BLOCKS - 1) / BLOCKS;
+  a.splits = p.splits;
+  a.per = (a.stages + p.splits - 1) / p.splits;
+  a.part = static_cast<float*>(workspace);
   const dim3 g(static_cast<unsigned>(order_grid(a.order)), static_cast<unsigned>(a.splits));
-  GPTQ_LAUNCH((mx_tile_kernel<T, T, KIND>), g, dim3(256), 0, stream, a);
+  GPTQ_LAUNCH((mx_tile_kernel<T, T, tile_xb(KIND, T), tile_buffers(KIND, T), KIND>), g, dim3(256), 0, stream, a);
+  if (p.splits == 1) return GPTQ_OK;
+  const dim3 s((a.n + 1023) / 1024, static_cast<unsigned>(a.m));   // parts are of few tiles: m is small
+  if (p.splits == 2) GPTQ_LAUNCH(mx_sum_kernel<2>, s, dim3(256), 0, stream, a);
+  else if (p.splits == 4) GPTQ_LAUNCH(mx_sum_kernel<4>, s, dim3(256), 0, stream, a);
+  else GPTQ_LAUNCH(mx_sum_kernel<8>, s, dim3(256), 0, stream, a);
   return GPTQ_OK;
 }
 
 template <int KIND>
-gptq_status launch_mx(MxArgs a, const MxPlan& p, void* workspace, hipStream_t stream) {
-  const int blocks = stage_blocks(KIND);
-  a.stages = (a.kb + blocks - 1) / blocks;
-  a.splits = p.splits;
-  a.per = (a.stages + p.splits - 1) / p.splits;
-  a.part = static_cast<float*>(workspace);
-  gptq_status st;
+gptq_status launch_mx(const MxArgs& a, const MxPlan& p, void* workspace, hipStream_t stream) {
   if (p.kind == kMxFew)
     return p.wide ? launch_mx_few<4, 1, 2, WIDE_DEPTH, KIND>(a, p, stream) : launch_mx_few<8, 8, 1, FEW_DEPTH, KIND>(a, p, stream);
-  st = p.kind == kMxTile64 ? launch_mx_tile<64, KIND>(a, stream) : launch_mx_tile<128, KIND>(a, stream);
-  if (st != GPTQ_OK || p.splits == 1) return st;
-  const dim3 g((a.n + 1023) / 1024, static_cast<unsigned>(a.m));   // parts are of few tiles: m is small
-  if (p.splits == 2) GPTQ_LAUNCH(mx_sum_kernel<2>, g, dim3(256), 0, stream, a);
-  else if (p.splits == 4) GPTQ_LAUNCH(mx_sum_kernel<4>, g, dim3(256), 0, stream, a);
-  else GPTQ_LAUNCH(mx_sum_kernel<8>, g, dim3(256), 0, stream, a);
-  return GPTQ_OK;
+  return p.kind == kMxTile64 ? launch_mx_tile<64, KIND>(a, p, workspace, stream)
+                             : launch_mx_tile<128, KIND>(a, p, workspace, stream);
 }
 
 // Whether the launch is one the kernels number their tiles for.
