@@ -107,7 +107,8 @@ typedef enum {
   GPTQ_WS_FP8_GROUPED = 6,
   GPTQ_WS_MOE_GROUP = 7,
   GPTQ_WS_MXFP4_MATMUL = 8,
-  GPTQ_WS_MXFP4_MOE_MLP = 9
+  GPTQ_WS_MXFP4_MOE_MLP = 9,
+  GPTQ_WS_MXFP4_GROUPED = 10
 } gptq_ws_call;
 
 /*
@@ -488,8 +489,8 @@ gptq_status gptq_mxfp4_dequantize(int64_t rows, int cols, const uint8_t* Q, cons
  * every type of Y.  A product of two scales, and with 16-bit X a weight, has to lie in fp32's normal
  * range to count in full (a weight of 2^128 or more is infinite).  workspace:
  * gptq_workspace_size(GPTQ_WS_MXFP4_MATMUL, batch = 1, d_out, d_in, n_tokens_hint = m, NULL) bytes,
- * 16-byte aligned (sums of parts of the inputs; where that is 256 the call keeps nothing there and
- * takes NULL); it serves one call at a time.  Requires d_in % 32 == 0, d_out >= 1; m may be 0 (no-op); more
+ * 16-byte aligned (sums of parts of the inputs, or 4-bit operands' scales in the order of the largest
+ * tiles; where that is 256 the call keeps nothing there and takes NULL); it serves one call at a time.  Requires d_in % 32 == 0, d_out >= 1; m may be 0 (no-op); more
  * than 2^22 tiles of the kernel that fits the sizes (16 x 16 to 256 x 256 outputs) are refused
  * (GPTQ_ERR_UNSUPPORTED).
  */
@@ -505,15 +506,17 @@ gptq_status gptq_mxfp4_matmul(int64_t m, int d_out, int d_in, gptq_dtype x_dtype
  * gptq_fp8_matmul_grouped: row p of expert e's range token_offsets[e] .. token_offsets[e + 1] - 1
  * (clamped to [0, n_rows]) is row row_index[p] of X (row_index NULL: row p, n_rows <= x_rows) times
  * expert e's weights; an index outside [0, x_rows) gives a row of zeros; rows of Y outside every
- * range are left as they were.  It takes no workspace.  Requires (n_rows / 16 + 1) * batch < 2^31
- * (GPTQ_ERR_UNSUPPORTED).
+ * range are left as they were.  workspace: gptq_workspace_size(GPTQ_WS_MXFP4_GROUPED, batch, d_out,
+ * d_in, n_tokens_hint = n_rows, NULL) bytes, as for gptq_mxfp4_matmul.  Requires (n_rows / 16 + 1) *
+ * batch < 2^31 (GPTQ_ERR_UNSUPPORTED).
  */
 gptq_status gptq_mxfp4_matmul_grouped(int batch, int64_t x_rows, int64_t n_rows, int d_out, int d_in,
                                       gptq_dtype x_dtype, const void* X, int64_t ldx,
                                       const uint8_t* x_scales, int64_t ld_xs_row,
                                       const uint8_t* qweight, const uint8_t* w_scales,
                                       const int64_t* token_offsets, const int32_t* row_index,
-                                      gptq_dtype y_dtype, void* Y, int64_t ldy, hipStream_t stream);
+                                      gptq_dtype y_dtype, void* Y, int64_t ldy, void* workspace,
+                                      size_t workspace_bytes, hipStream_t stream);
 
 /*
  * The expert layer of a mixture-of-experts block for few tokens, in two launches:
@@ -547,7 +550,7 @@ gptq_status gptq_mxfp4_moe_mlp(int64_t n_tokens, int top_k, int n_experts, int d
  * of activation rows m and p->group_size the group size (-1: one grid per row); for
  * GPTQ_WS_FP8_MATMUL and GPTQ_WS_FP8_GROUPED `n_tokens_hint` is the number of rows of X; for
  * GPTQ_WS_MOE_GROUP `d_out` is n_experts and `d_in` is top_k; for GPTQ_WS_MXFP4_MATMUL
- * `n_tokens_hint` is m, and for GPTQ_WS_MXFP4_MOE_MLP `d_out` is inner and `n_tokens_hint` the number
+ * `n_tokens_hint` is m, for GPTQ_WS_MXFP4_GROUPED n_rows, and for GPTQ_WS_MXFP4_MOE_MLP `d_out` is inner and `n_tokens_hint` the number
  * of choices; for the other calls it is ignored. */
 size_t gptq_workspace_size(gptq_ws_call which, int batch, int d_out, int d_in,
                            int64_t n_tokens_hint, const gptq_params* p);

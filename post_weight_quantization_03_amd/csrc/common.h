@@ -176,7 +176,7 @@ struct MxProblem {
   void* Y; int64_t ldy;
   void* workspace; size_t workspace_bytes;
 };
-size_t mx_workspace(int64_t m, int n, int k);
+size_t mx_workspace(int batch, bool grouped, int64_t m, int n, int k);
 gptq_status mx_matmul_enqueue(const MxProblem& p, hipStream_t stream);
 struct MxMlp {
   int tokens, top_k, experts, d, inner;

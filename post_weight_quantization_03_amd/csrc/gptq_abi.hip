@@ -443,9 +443,10 @@ gptq_status gptq_mxfp4_matmul_grouped(int batch, int64_t x_rows, int64_t n_rows,
                                       gptq_dtype x_dtype, const void* X, int64_t ldx, const uint8_t* x_scales,
                                       int64_t ld_xs_row, const uint8_t* qweight, const uint8_t* w_scales,
                                       const int64_t* token_offsets, const int32_t* row_index, gptq_dtype y_dtype,
-                                      void* Y, int64_t ldy, hipStream_t stream) {
+                                      void* Y, int64_t ldy, void* workspace, size_t workspace_bytes,
+                                      hipStream_t stream) {
   const gptq::MxProblem p{batch, x_rows, n_rows, d_out, d_in, x_dtype, X, ldx, x_scales, ld_xs_row, qweight, w_scales,
-                          token_offsets, row_index, y_dtype, Y, ldy, nullptr, 0};
+                          token_offsets, row_index, y_dtype, Y, ldy, workspace, workspace_bytes};
   const gptq_status st = check_mx(p);
   if (st != GPTQ_OK || n_rows == 0) return st;
   if (token_offsets == nullptr || !aligned(token_offsets, 8) || !aligned(row_index, 4)) return GPTQ_ERR_INVALID_ARG;
@@ -503,8 +504,11 @@ size_t gptq_workspace_size(gptq_ws_call which, int batch, int d_out, int d_in, i
       if (d_out < 1 || d_out > 1024 || d_in < 1 || n_tokens_hint < 0 || n_tokens_hint > INT32_MAX / d_in) return 0;
       return gptq::group_workspace(d_out, n_tokens_hint * d_in);
     case GPTQ_WS_MXFP4_MATMUL:
-      if (batch != 1 || d_out < 1 || d_in < 32 || d_in % 32 != 0 || n_tokens_hint < 0) return 0;
-      return gptq::mx_workspace(n_tokens_hint, d_out, d_in);
+    case GPTQ_WS_MXFP4_GROUPED:
+      if (batch < 1 || (which == GPTQ_WS_MXFP4_MATMUL && batch != 1) || d_out < 1 || d_in < 32 || d_in % 32 != 0 ||
+          n_tokens_hint < 0)
+        return 0;
+      return gptq::mx_workspace(batch, which == GPTQ_WS_MXFP4_GROUPED, n_tokens_hint, d_out, d_in);
     case GPTQ_WS_MXFP4_MOE_MLP:
       if (d_out < 32 || d_out % 32 != 0 || d_in < 32 || d_in % 32 != 0 || n_tokens_hint < 0 ||
           n_tokens_hint > GPTQ_MOE_MLP_CHOICES)

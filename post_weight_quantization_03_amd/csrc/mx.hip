@@ -126,6 +126,10 @@ struct MxArgs : MmArgs {
   int splits, per;   // parts of the inputs, and their stages
   float* part;       // [splits][m][n] sums, where there is more than one
   int cap, slots;    // of the kernel for few rows: rows of a tile, units in a wave's ring
+  uint2* xst;        // of the largest tiles: scales by stage
+  uint2* wst;
+  int64_t mp;        // and their rows
+  int np;
 };
 
 // Few rows, at most `cap` (up to 16) of one expert or of the one problem: a workgroup has NW / KS tiles
@@ -452,6 +456,333 @@ __global__ __launch_bounds__(256) void mx_tile_kernel(MxArgs a) {
   }
 }
 
+// The same product for large problems: 256 x 256 tiles, 4 waves of 128 x 128 (8 x 8 blocks of 16 x 16),
+// one workgroup per CU.  Bound by the matrix cores.  Two buffers; a stage is 128 bytes of every row of X,
+// two instructions for a block (four for fp16), here together called a product.  Operands go global -> LDS
+// with a scalar base that moves by a stage and one 32-bit offset per lane and copy.  Before a wave's last
+// three rows of blocks it has read all it needs of the stage: there the workgroup waits for the next stage's
+// copies, and the products of these rows cover the first reads of the next stage and half of the copies
+// of the one after it; the other half goes out with the next stage's first products.
+// A tile of up to 128 rows or outputs (the last of a ragged problem or expert) goes the same way with half
+// the work per wave.
+constexpr int BIG = 256;
+template <int KIND>
+struct BigW {
+  bf16x8 v[2];
+};
+template <>
+struct BigW<kMx4> {
+  i32x4 v[2];
+  int s;   // the scales of both halves in its two low bytes
+};
+template <int KIND>
+struct BigX {
+  i32x4 v[2];
+  int s;
+};
+template <int KIND>
+__device__ __forceinline__ void big_product(const BigW<KIND>& w, const BigX<KIND>& x, f32x4& acc) {
+  if constexpr (KIND == kMx4) {
+    acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(widen(w.v[0]), widen(x.v[0]), acc, 4, 4, 0, w.s, 0, x.s);
+    acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(widen(w.v[1]), widen(x.v[1]), acc, 4, 4, 1, w.s, 1, x.s);
+  } else {
+    acc = mx_mma16<KIND>(w.v[0], XValues<KIND>(x.v[0]), acc);
+    acc = mx_mma16<KIND>(w.v[1], XValues<KIND>(x.v[1]), acc);
+  }
+}
+
+// The scales of 4-bit operands stage by stage, for this kernel: 8 codes of every output row [stages][mp]
+// and of every output [experts][stages][np], those behind the last block 1, in the order 0 4 1 5 2 6 3 7, so
+// that a lane's two are neighbours.  (Read where they are, 8 bytes a stage come out of lines of 128, which
+// doubles what a CU reads: 8192 x 4096 x 14336 286 us, 221 so, this kernel in it.)
+constexpr int GATHER = 8;   // stages of a thread
+__global__ __launch_bounds__(256) void mx_gather_scales_kernel(MxArgs a) {
+  const int64_t g = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  const uint8_t* row = nullptr;
+  uint2* to;
+  int64_t step;
+  if (g < a.mp) {
+    const int64_t x = g < a.m ? source_row(a, g) : -1;
+    if (x >= 0) row = static_cast<const uint8_t*>(a.xs) + x * a.xsr;
+    to = a.xst + g;
+    step = a.mp;
+  } else {
+    const int64_t w = g - a.mp, e = w / a.np;
+    const int o = static_cast<int>(w - e * a.np);
+    if (e >= a.experts) return;
+    if (o < a.n) row = static_cast<const uint8_t*>(a.ws) + (e * a.n + o) * a.kb;
+    to = a.wst + e * a.stages * a.np + o;
+    step = a.np;
+  }
+  for (int s = blockIdx.y * GATHER; s < min(static_cast<int>(blockIdx.y + 1) * GATHER, a.stages); ++s) {
+    uint32_t v[2] = {0x7F7F7F7Fu, 0x7F7F7F7Fu};
+    if (row != nullptr && 8 * s + 8 <= a.kb) {
+      __builtin_memcpy(v, row + 8 * s, 8);
+    } else if (row != nullptr) {
+#pragma unroll 1
+      for (int i = 0; i < a.kb - 8 * s; ++i) {
+        const uint32_t c = static_cast<uint32_t>(row[8 * s + i] ^ 0x7F) << (8 * (i & 3));
+        if (i < 4) v[0] ^= c;
+        else v[1] ^= c;
+      }
+    }
+    to[s * step] = make_uint2(__builtin_amdgcn_perm(v[1], v[0], 0x05010400u), __builtin_amdgcn_perm(v[1], v[0], 0x07030602u));
+  }
+}
+
+// Outputs n0 .. of the rows of t: XR rows of X and WR of W, waves_n waves beside each other.
+template <int KIND, int XR, int WR, int FM, int FN>
+__device__ __forceinline__ void big_tile(const MxArgs& a, const Tile& t, int n0, int waves_n, uint8_t* lds, uint2* scs,
+                                         bool* lost) {
+  typedef MxStage<KIND, 128> St;
+  constexpr bool F4 = KIND == kMx4;
+  constexpr int NW = 4, STAGE = XR * 128 + WR * St::WB, WROWS = 1024 / St::WB;
+  constexpr int LX = XR / 8 / NW, LW = WR / WROWS / NW, LD = LX + LW;
+  constexpr int SROWS = F4 ? 2 * BIG : BIG;   // rows of scales: of X, then of W
+  const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+  const int stages = a.stages;
+  const uint8_t* xbase = a.X + (a.rows == nullptr ? t.p0 * a.ldx : 0);
+  const uint8_t* wbase = a.W + (static_cast<int64_t>(t.e) * a.n + n0) * (a.k / 2);
+  // this lane's pieces: the same in every copy of X, and of W; whether they lie past K in the last stage
+  const int cx = St::x_at(8 * wave + lane / 8, lane & 7), cw = St::w_at(WROWS * wave + lane / (St::WB / 16), lane % (St::WB / 16));
+  const bool cut_x = (stages - 1) * 128 + 16 * cx >= (F4 ? a.k / 2 : 2 * a.k), cut_w = (stages - 1) * St::WB + 16 * cw >= a.k / 2;
+  uint32_t off[LD];
+#pragma unroll
+  for (int i = 0; i < LD; ++i) {
+    if (i < LX) {
+      const int r = (wave + NW * i) * 8 + lane / 8;
+      const int64_t row = source_row(a, t.p0 + min(r, t.count - 1));   // none: row 0, and zeros at the end
+      off[i] = static_cast<uint32_t>(max(a.rows == nullptr ? row - t.p0 : row, static_cast<int64_t>(0)) * a.ldx) + 16 * cx;
+    } else {
+      const int r = (wave + NW * (i - LX)) * WROWS + lane / (St::WB / 16);
+      off[i] = static_cast<uint32_t>(min(r, a.n - 1 - n0)) * static_cast<uint32_t>(a.k / 2) + 16 * cw;
+    }
+  }
+  const int64_t own = source_row(a, t.p0 + min(tid, t.count - 1));
+  lost[tid] = own < 0;
+  // 4-bit operands' scales are copied; those of the weights of 16-bit rows go through a register, 2 in
+  // 4 bytes that end with the row at the latest
+  const uint8_t* const wsrow =
+      static_cast<const uint8_t*>(a.ws) + (static_cast<int64_t>(t.e) * a.n + min(n0 + tid, a.n - 1)) * a.kb;
+  uint32_t sw_next = 0;
+  const unsigned scs0 = static_cast<unsigned>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint2*)scs));
+  const unsigned lds0 = static_cast<unsigned>(reinterpret_cast<uintptr_t>(
+      (__attribute__((address_space(3))) uint8_t*)lds));
+  auto issue_scales = [&](int s) {
+    if constexpr (F4) {
+      const uint2* x = a.xst + static_cast<int64_t>(s) * a.mp + t.p0;
+      const uint2* w = a.wst + (static_cast<int64_t>(t.e) * a.stages + s) * a.np + n0;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int at = 512 * wave + 256 * i;   // bytes
+        copy4(reinterpret_cast<const uint8_t*>(x) + at + 4 * lane, scs0 + (s & 1) * SROWS * 8 + at);
+        copy4(reinterpret_cast<const uint8_t*>(w) + at + 4 * lane, scs0 + (s & 1) * SROWS * 8 + BIG * 8 + at);
+      }
+    } else {
+      __builtin_memcpy(&sw_next, wsrow + min(2 * s, a.kb - 4), 4);
+    }
+  };
+  auto issue_copies = [&](int s, int from, int to) {
+    const uint8_t* xb = xbase + static_cast<int64_t>(s) * 128;
+    const uint8_t* wb = wbase + static_cast<int64_t>(s) * St::WB;
+    const unsigned dst = lds0 + (s & 1) * STAGE + wave * 1024;
+    // past K the row's first piece instead; zeroed below
+    const uint32_t back_x = s == stages - 1 && cut_x ? 16 * cx : 0, back_w = s == stages - 1 && cut_w ? 16 * cw : 0;
+#pragma unroll
+    for (int i = from; i < to; ++i) {
+      if (i < LX) copy16_at(xb, off[i] - back_x, dst + NW * i * 1024);
+      else copy16_at(wb, off[i] - back_w, dst + XR * 128 + NW * (i - LX) * 1024);
+    }
+  };
+  // the copies and scales of stage s have landed; the next barrier makes them visible
+  auto land = [&](int s, bool last) {
+    wait_copies();
+    if (last) {
+#pragma unroll
+      for (int i = 0; i < LD; ++i)
+        if (i < LX ? cut_x : cut_w)
+          *reinterpret_cast<uint4*>(lds + (s & 1) * STAGE + wave * 1024 +
+                                    (i < LX ? NW * i * 1024 : XR * 128 + NW * (i - LX) * 1024) + 16 * lane) = make_uint4(0, 0, 0, 0);
+    }
+    if constexpr (!F4)
+      reinterpret_cast<uint16_t*>(scs)[(s & 1) * BIG + tid] =
+          static_cast<uint16_t>(sw_next >> (8 * (2 * s - min(2 * s, a.kb - 4))));
+  };
+  auto barrier = [&] {
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  };
+
+  const int wm = wave / waves_n, wn = wave % waves_n;
+  const int j = lane & 15, q = lane >> 4;
+  const int xr = wm * 16 * FM, wr = wn * 16 * FN;
+  const int at0 = j * 128 + 16 * St::x_at(j, q), at1 = j * 128 + 16 * St::x_at(j, q + 4);
+  auto half_x = [&](int s, int i, int half, BigX<KIND>& o) {
+    o.v[half] = *reinterpret_cast<const i32x4*>(lds + (s & 1) * STAGE + (xr + 16 * i) * 128 + (half ? at1 : at0));
+  };
+  auto scale_x = [&](int s, int i, BigX<KIND>& o) {
+    if constexpr (F4) o.s = reinterpret_cast<const uint16_t*>(&scs[(s & 1) * SROWS + xr + 16 * i + j])[q];
+  };
+  auto read_w = [&](int s, int h, BigW<KIND>& o) {
+    const uint8_t* base = lds + (s & 1) * STAGE + XR * 128 + (wr + 16 * h) * St::WB;
+    if constexpr (F4) {
+      o.v[0] = *reinterpret_cast<const i32x4*>(base + at0);
+      o.v[1] = *reinterpret_cast<const i32x4*>(base + at1);
+      o.s = reinterpret_cast<const uint16_t*>(&scs[(s & 1) * SROWS + BIG + wr + 16 * h + j])[q];
+    } else {
+      const uint32_t sc = reinterpret_cast<const uint16_t*>(scs)[(s & 1) * BIG + wr + 16 * h + j];
+      const uint8_t* row = base + j * St::WB + 4 * q;
+      o.v[0] = mx_bf16(*reinterpret_cast<const uint32_t*>(row + 16 * St::w_at(j, 0)), sc & 255);
+      o.v[1] = mx_bf16(*reinterpret_cast<const uint32_t*>(row + 16 * St::w_at(j, 1)), sc >> 8);
+    }
+  };
+
+  f32x4 y[FM][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int h = 0; h < FN; ++h) y[i][h] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  BigX<KIND> xf[4];   // row of blocks i in xf[i % 4]
+  BigW<KIND> wf[FN];
+  // Products of a stage: rows of blocks one after another, then the last three together, output block by
+  // output block.
+  constexpr int LAST = 3, SPLIT = (FM - LAST) * FN;   // rows taken together, products before them
+  constexpr int EARLY = LAST * FN / 2 < LD ? LAST * FN / 2 : LD;   // copies issued with them, one after every second product
+  // the barrier keeps everything in the order written
+  auto product = [&](auto P) {
+    constexpr int p = P, i = p < SPLIT ? p / FN : FM - LAST + (p - SPLIT) % LAST, h = p < SPLIT ? p % FN : (p - SPLIT) / LAST;
+    big_product<KIND>(wf[h], xf[i % 4], y[i][h]);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  // one stage; kMore: another follows, kIssue: and one after that (constants, so that the loop's body has no
+  // branch)
+  auto stage = [&](int s, auto kMore, auto kIssue) {
+    // all rows but the last three; row i + 3 is read meanwhile, one access after each product
+    static_for(std::make_integer_sequence<int, SPLIT>{}, [&](auto P) {
+      constexpr int p = P, i = p / FN, h = p % FN;
+      product(P);
+      if constexpr (h == 0) half_x(s, i + 3, 0, xf[(i + 3) % 4]);
+      if constexpr (h == 1) half_x(s, i + 3, 1, xf[(i + 3) % 4]);
+      if constexpr (h == 2) scale_x(s, i + 3, xf[(i + 3) % 4]);
+      // the rest of the next stage's copies
+      if constexpr (kMore && p % 2 == 1 && EARLY + p / 2 < LD) issue_copies(s + 1, EARLY + p / 2, EARLY + p / 2 + 1);
+      __builtin_amdgcn_sched_barrier(0);
+    });
+    if constexpr (kMore) {
+      land(s + 1, !kIssue);
+      barrier();
+      if constexpr (kIssue) issue_scales(s + 2);
+      // operand 0 is free: the next stage's first
+      half_x(s + 1, 0, 0, xf[0]);
+      half_x(s + 1, 0, 1, xf[0]);
+      scale_x(s + 1, 0, xf[0]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    // the last three rows: a weight operand makes room for the next stage's after its third product
+    static_for(std::make_integer_sequence<int, LAST * FN>{}, [&](auto Q) {
+      constexpr int n = Q, h = n / LAST;
+      product(std::integral_constant<int, SPLIT + n>{});
+      if constexpr (kMore && n % LAST == LAST - 1) read_w(s + 1, h, wf[h]);
+      if constexpr (kIssue && n % 2 == 1 && n / 2 < EARLY) issue_copies(s + 2, n / 2, n / 2 + 1);
+      __builtin_amdgcn_sched_barrier(0);
+    });
+    if constexpr (kMore) {
+#pragma unroll
+      for (int i = 1; i < 3; ++i) {
+        half_x(s + 1, i, 0, xf[i]);
+        half_x(s + 1, i, 1, xf[i]);
+        scale_x(s + 1, i, xf[i]);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+
+  issue_scales(0);
+  issue_copies(0, 0, LD);
+  land(0, stages == 1);
+  barrier();
+  if (stages > 1) {
+    issue_scales(1);
+    issue_copies(1, 0, EARLY);
+  }
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    half_x(0, i, 0, xf[i]);
+    half_x(0, i, 1, xf[i]);
+    scale_x(0, i, xf[i]);
+  }
+#pragma unroll
+  for (int h = 0; h < FN; ++h) read_w(0, h, wf[h]);
+  const std::true_type yes;
+  const std::false_type no;
+  for (int s = 0; s + 2 < stages; ++s) stage(s, yes, yes);
+  if (stages > 1) stage(stages - 2, yes, no);
+  stage(stages - 1, no, no);
+
+  if (a.y_dtype == GPTQ_F32) {
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      const int r = xr + 16 * i + j;
+      if (r >= t.count) continue;
+      const bool none = lost[r];
+#pragma unroll
+      for (int h = 0; h < FN; ++h) {
+        const float v[4] = {none ? 0.0f : y[i][h][0], none ? 0.0f : y[i][h][1], none ? 0.0f : y[i][h][2],
+                            none ? 0.0f : y[i][h][3]};
+        store_y(a, t.p0 + r, n0 + wr + 16 * h + 4 * q, v);
+      }
+    }
+    return;
+  }
+  // Of outputs 16 h + 4 q .. of two neighbouring h, lanes of odd and even q exchange one each (they are of one
+  // row): a lane then stores 8 in 16 bytes, and four lanes 64 bytes of a row in one piece.
+  const int o0 = n0 + wr + 16 * (q & 1) + 8 * (q >> 1);
+  const bool whole = n0 + wr + 16 * FN <= a.n;
+  auto store = [&](auto kBf16, auto kWhole) {
+    uint16_t* out = static_cast<uint16_t*>(a.Y) + (t.p0 + xr + j) * a.ldy + o0;
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      if (xr + 16 * i + j < t.count) {
+        const bool none = lost[xr + 16 * i + j];
+#pragma unroll
+        for (int h = 0; h < FN; h += 2) {
+          const uint2 u = pack16<kBf16>(y[i][h]), v = pack16<kBf16>(y[i][h + 1]);
+          const auto lo = __builtin_amdgcn_permlane16_swap(u.x, v.x, false, false);
+          const auto hi = __builtin_amdgcn_permlane16_swap(u.y, v.y, false, false);
+          const uint4 w = none ? make_uint4(0, 0, 0, 0) : make_uint4(lo[0], hi[0], lo[1], hi[1]);
+          if constexpr (kWhole) __builtin_memcpy(out + 16 * h, &w, sizeof(w));
+          else store_narrow(a, out + 16 * h, o0 + 16 * h, w);
+        }
+      }
+      out += 16 * a.ldy;
+    }
+  };
+  if (a.y_dtype == GPTQ_BF16) {
+    if (whole) store(yes, yes);
+    else store(yes, no);
+  } else {
+    if (whole) store(no, yes);
+    else store(no, no);
+  }
+}
+
+template <int KIND>
+__global__ __launch_bounds__(256) void mx_big_kernel(MxArgs a) {
+  __shared__ __attribute__((aligned(128))) uint8_t lds[2 * BIG * (128 + MxStage<KIND, 128>::WB)];
+  __shared__ uint2 scs[KIND == kMx4 ? 4 * BIG : BIG / 2];
+  __shared__ bool lost[BIG];
+  int64_t mt;
+  int nt;
+  if (!ordered_tile(a.order, blockIdx.x, &mt, &nt)) return;
+  const int n0 = nt * BIG;
+  const Tile t = find_tile<BIG>(a, mt);
+  if (t.count <= 0) return;
+  if (t.count <= BIG / 2) big_tile<KIND, BIG / 2, BIG, 8, 4>(a, t, n0, 4, lds, scs, lost);
+  else if (a.n - n0 <= BIG / 2) big_tile<KIND, BIG, BIG / 2, 8, 4>(a, t, n0, 2, lds, scs, lost);
+  else big_tile<KIND, BIG, BIG, 8, 8>(a, t, n0, 2, lds, scs, lost);
+}
+
 // Y from the sums of the parts, in their order, all loads at once.
 template <int SPLITS>
 __global__ __launch_bounds__(256) void mx_sum_kernel(MxArgs a) {
@@ -474,7 +805,7 @@ __global__ __launch_bounds__(256) void mx_sum_kernel(MxArgs a) {
 
 // ---------------------------------------------------------------------------- host side
 
-enum MxProduct { kMxFew, kMxTile64, kMxTile128 };
+enum MxProduct { kMxFew, kMxTile64, kMxTile128, kMxBig };
 struct MxPlan {
   MxProduct kind;
   int splits;
@@ -517,6 +848,7 @@ MxPlan mx_plan(int64_t m, int n, int k, int kind, bool grouped, int experts) {
     return r * ((n + t - 1) / t);
   };
   const int stages = (kb + tile_blocks(kind, 64) - 1) / tile_blocks(kind, 64);
+  if (tiles(256) >= 192 && kb >= 8 && (!grouped || rows >= 384)) return {kMxBig, 1, 0, false};
   if (tiles(128) >= 384) return {kMxTile128, 1, 0, false};
   int splits = 1;
   if (!grouped) {
@@ -526,7 +858,14 @@ MxPlan mx_plan(int64_t m, int n, int k, int kind, bool grouped, int experts) {
   return {kMxTile64, splits, 0, false};
 }
 
-size_t mx_part_bytes(const MxPlan& p, int64_t m, int n) {
+// The largest tiles' scales: rows and outputs that a tile may read behind the last.
+int64_t big_rows(int64_t m) { return m + BIG; }
+int big_outputs(int n) { return (n + BIG - 1) / BIG * BIG; }
+
+// Workspace: sums of parts, or scales by stage.
+size_t mx_plan_bytes(const MxPlan& p, int64_t m, int n, int k, int kind, int experts) {
+  if (p.kind == kMxBig && kind == kMx4)
+    return static_cast<size_t>((k / MXB + 7) / 8) * 8 * (big_rows(m) + static_cast<size_t>(experts) * big_outputs(n));
   return p.splits > 1 ? static_cast<size_t>(p.splits) * static_cast<size_t>(m) * n * sizeof(float) : 0;
 }
 
@@ -561,16 +900,35 @@ gptq_status launch_mx_tile(MxArgs a, const MxPlan& p, void* workspace, hipStream
 }
 
 template <int KIND>
+gptq_status launch_mx_big(MxArgs a, void* workspace, hipStream_t stream) {
+  constexpr int BLOCKS = MxStage<KIND, 128>::BLOCKS;
+  a.stages = (a.kb + BLOCKS - 1) / BLOCKS;
+  a.order = {(a.n + BIG - 1) / BIG, tile_rows(a, BIG)};
+  if constexpr (KIND == kMx4) {
+    a.mp = big_rows(a.m);
+    a.np = big_outputs(a.n);
+    a.xst = static_cast<uint2*>(workspace);
+    a.wst = a.xst + a.stages * a.mp;
+    const int64_t rows = a.mp + static_cast<int64_t>(a.experts) * a.np;
+    GPTQ_LAUNCH(mx_gather_scales_kernel, dim3(static_cast<unsigned>((rows + 255) / 256), (a.stages + GATHER - 1) / GATHER),
+                dim3(256), 0, stream, a);
+  }
+  GPTQ_LAUNCH(mx_big_kernel<KIND>, dim3(static_cast<unsigned>(order_grid(a.order))), dim3(256), 0, stream, a);
+  return GPTQ_OK;
+}
+
+template <int KIND>
 gptq_status launch_mx(const MxArgs& a, const MxPlan& p, void* workspace, hipStream_t stream) {
   if (p.kind == kMxFew)
     return p.wide ? launch_mx_few<4, 1, 2, WIDE_DEPTH, KIND>(a, p, stream) : launch_mx_few<8, 8, 1, FEW_DEPTH, KIND>(a, p, stream);
+  if (p.kind == kMxBig) return launch_mx_big<KIND>(a, workspace, stream);
   return p.kind == kMxTile64 ? launch_mx_tile<64, KIND>(a, p, workspace, stream)
                              : launch_mx_tile<128, KIND>(a, p, workspace, stream);
 }
 
 // Whether the launch is one the kernels number their tiles for.
 bool mx_launchable(const MxArgs& a, const MxPlan& p) {
-  const int tm = p.kind == kMxTile128 ? 128 : p.kind == kMxTile64 ? 64 : p.cap;
+  const int tm = p.kind == kMxBig ? BIG : p.kind == kMxTile128 ? 128 : p.kind == kMxTile64 ? 64 : p.cap;
   const int tn = p.kind == kMxFew ? 16 : tm;
   return tile_rows(a, tm) <= (1 << 22) / ((a.n + tn - 1) / tn);
 }
@@ -600,10 +958,11 @@ gptq_status mx_dequantize_enqueue(int64_t rows, int cols, const uint8_t* Q, cons
   return GPTQ_OK;
 }
 
-size_t mx_workspace(int64_t m, int n, int k) {
-  const size_t parts = std::max(mx_part_bytes(mx_plan(m, n, k, kMx4, false, 1), m, n),
-                                mx_part_bytes(mx_plan(m, n, k, kMxBf16, false, 1), m, n));
-  return std::max<size_t>(256, parts);
+size_t mx_workspace(int batch, bool grouped, int64_t m, int n, int k) {
+  size_t most = 256;
+  for (const int kind : {kMx4, kMxBf16})
+    most = std::max(most, mx_plan_bytes(mx_plan(m, n, k, kind, grouped, batch), m, n, k, kind, batch));
+  return most;
 }
 
 gptq_status mx_matmul_enqueue(const MxProblem& p, hipStream_t stream) {
@@ -616,10 +975,14 @@ gptq_status mx_matmul_enqueue(const MxProblem& p, hipStream_t stream) {
   const int kind = p.x_dtype == GPTQ_E2M1 ? kMx4 : p.x_dtype == GPTQ_BF16 ? kMxBf16 : kMxF16;
   a.ldx = kind == kMx4 ? p.ldx : 2 * p.ldx;
   if (a.off != nullptr && (a.m / 16 + 1) * a.experts > INT32_MAX) return GPTQ_ERR_UNSUPPORTED;
-  const MxPlan plan = mx_plan(a.m, a.n, a.k, kind, a.off != nullptr, a.experts);
+  MxPlan plan = mx_plan(a.m, a.n, a.k, kind, a.off != nullptr, a.experts);
+  // the largest tiles address a tile's rows by 32-bit offsets
+  const int64_t span = a.rows == nullptr ? BIG * a.ldx : a.x_rows * a.ldx;
+  if (plan.kind == kMxBig && (span > INT32_MAX || BIG * static_cast<int64_t>(a.k / 2) > INT32_MAX || a.x_rows == 0))
+    plan.kind = kMxTile128;
   if (!mx_launchable(a, plan)) return GPTQ_ERR_UNSUPPORTED;
-  if (plan.splits > 1 && (p.workspace == nullptr || p.workspace_bytes < mx_part_bytes(plan, a.m, a.n)))
-    return GPTQ_ERR_WORKSPACE;
+  const size_t need = mx_plan_bytes(plan, a.m, a.n, a.k, kind, a.experts);
+  if (need > 0 && (p.workspace == nullptr || p.workspace_bytes < need)) return GPTQ_ERR_WORKSPACE;
   if (kind == kMx4) return launch_mx<kMx4>(a, plan, p.workspace, stream);
   if (kind == kMxBf16) return launch_mx<kMxBf16>(a, plan, p.workspace, stream);
   return launch_mx<kMxF16>(a, plan, p.workspace, stream);

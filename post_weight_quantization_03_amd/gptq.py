@@ -31,7 +31,7 @@ GPTQ_ERR_TOO_LARGE = -6
 NOALLOC_SCRATCH_BYTES = 64 << 20
 WS_HESSIAN, WS_PREPARE, WS_QUANTIZE, WS_W4A16_REPACK, WS_W4A16 = 0, 1, 2, 3, 4
 WS_FP8_MATMUL, WS_FP8_GROUPED, WS_MOE_GROUP = 5, 6, 7
-WS_MXFP4_MATMUL, WS_MXFP4_MOE_MLP = 8, 9
+WS_MXFP4_MATMUL, WS_MXFP4_MOE_MLP, WS_MXFP4_GROUPED = 8, 9, 10
 
 EXPORTED = ("gptq_accumulate_hessian", "gptq_prepare_hinv", "gptq_quantize_layer", "gptq_quantize_layer_noalloc",
             "gptq_accumulate_hessian_grouped", "gptq_pack_int4", "gptq_w4a16_repack", "gptq_w4a16_matmul",
@@ -119,7 +119,7 @@ def lib() -> ctypes.CDLL:
     L.gptq_mxfp4_dequantize.argtypes = [i64, i32, vp, vp, i32, vp, vp]
     L.gptq_mxfp4_matmul.argtypes = [i64, i32, i32, i32, vp, i64, vp, i64, vp, vp, i32, vp, i64, vp, sz, vp]
     L.gptq_mxfp4_matmul_grouped.argtypes = [i32, i64, i64, i32, i32, i32, vp, i64, vp, i64, vp, vp, vp, vp, i32, vp,
-                                            i64, vp]
+                                            i64, vp, sz, vp]
     L.gptq_mxfp4_moe_mlp.argtypes = [i64, i32, i32, i32, i32, i32, vp, i64, vp, vp, vp, vp, vp, vp, i32, vp, i64, vp,
                                      sz, vp]
     L.gptq_workspace_size.argtypes = [i32, i32, i32, i32, i64, ctypes.POINTER(_Params)]
@@ -825,14 +825,14 @@ def mxfp4_matmul(X: torch.Tensor, qweight: torch.Tensor, w_scales: torch.Tensor,
 def mxfp4_matmul_grouped(X: torch.Tensor, qweight: torch.Tensor, w_scales: torch.Tensor, token_offsets: torch.Tensor,
                          row_index: torch.Tensor | None = None, x_scales: torch.Tensor | None = None,
                          out_dtype: torch.dtype = torch.bfloat16, out: torch.Tensor | None = None,
-                         stream=None) -> torch.Tensor:
+                         workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """The experts' products: row p of Y [n_rows, d_out], token_offsets[e] <= p <
     token_offsets[e + 1], is row row_index[p] of X (row p without ``row_index``) times
     expert e's weights qweight [experts, d_out, d_in / 2]; operands otherwise as in
     :func:`mxfp4_matmul`, ranges and indexes as in :func:`fp8_matmul_grouped`."""
     if stream is not None:
         return _on(stream, mxfp4_matmul_grouped, X, qweight, w_scales, token_offsets, row_index, x_scales, out_dtype,
-                   out)
+                   out, workspace)
     if qweight.dim() != 3 or qweight.shape[0] < 1 or qweight.shape[1] < 1:
         raise ValueError("qweight must be [experts, d_out, d_in / 2]")
     X, code, d_in = _mx_operands(X, x_scales, qweight, w_scales, out_dtype)
@@ -844,10 +844,11 @@ def mxfp4_matmul_grouped(X: torch.Tensor, qweight: torch.Tensor, w_scales: torch
         raise ValueError("row_index must be contiguous int32 [n_rows]")
     n_rows = x_rows if row_index is None else row_index.numel()
     Y = _out(out, (n_rows, d_out), out_dtype, X.device)
-    _run("gptq_mxfp4_matmul_grouped", (X, qweight, w_scales, token_offsets, row_index, x_scales, Y), experts, x_rows,
+    ws = _scratch(WS_MXFP4_GROUPED, experts, d_out, d_in, n_rows, X.device, workspace)
+    _run("gptq_mxfp4_matmul_grouped", (X, qweight, w_scales, token_offsets, row_index, x_scales, Y, ws), experts, x_rows,
          n_rows, d_out, d_in, code, X.data_ptr(), _row_stride(X), _ptr(x_scales),
          0 if x_scales is None else _row_stride(x_scales), qweight.data_ptr(), w_scales.data_ptr(),
-         token_offsets.data_ptr(), _ptr(row_index), _DT[out_dtype], Y.data_ptr(), _row_stride(Y))
+         token_offsets.data_ptr(), _ptr(row_index), _DT[out_dtype], Y.data_ptr(), _row_stride(Y), _ptr(ws), _bytes(ws))
     return Y
 
 

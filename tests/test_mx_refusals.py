@@ -58,7 +58,8 @@ def test_matmul_workspace_and_empty():
         a = {**MATMUL, "m": 64, "n": 4096, "k": 14336, "xt": xt, "ldx": ldx, "xsr": 448, "ldy": 4096}
         assert L.gptq_mxfp4_matmul(*a.values()) == WS
         assert L.gptq_mxfp4_matmul(*{**a, "wsp": 16, "wsb": 255}.values()) == WS
-    assert gptq.workspace_size(gptq.WS_MXFP4_MATMUL, 1, 4096, 14336, 8192) == 256
+    assert gptq.workspace_size(gptq.WS_MXFP4_MATMUL, 1, 4096, 14336, 8192) > 256       # scales by stage
+    assert gptq.workspace_size(gptq.WS_MXFP4_MATMUL, 1, 4096, 14336, 1) == 256
     assert gptq.workspace_size(gptq.WS_MXFP4_MATMUL, 1, 4096, 14336, 0) == 256
     for bad in ((2, 64, 128, 4), (1, 0, 128, 4), (1, 64, 100, 4), (1, 64, 128, -1)):
         assert gptq.workspace_size(gptq.WS_MXFP4_MATMUL, *bad) == 0
@@ -72,7 +73,7 @@ def test_too_many_tiles_are_refused():
 
 
 GROUPED = dict(batch=2, xr=8, rows=5, n=64, k=128, xt=E2M1, X=16, ldx=64, xs=3, xsr=4, W=16, ws=3, off=16, idx=None,
-               yt=BF16, Y=16, ldy=64, stream=None)
+               yt=BF16, Y=16, ldy=64, wsp=None, wsb=0, stream=None)
 
 
 @pytest.mark.parametrize("change", [dict(batch=0), dict(xr=-1), dict(rows=-1), dict(off=None), dict(off=12), dict(idx=6),
@@ -85,6 +86,12 @@ def test_grouped_empty_and_too_large():
     assert gptq.lib().gptq_mxfp4_matmul_grouped(*{**GROUPED, "rows": 0}.values()) == OK
     a = {**GROUPED, "batch": 1 << 20, "xr": 1 << 16, "rows": 1 << 16}
     assert gptq.lib().gptq_mxfp4_matmul_grouped(*a.values()) == UNS
+    need = gptq.workspace_size(gptq.WS_MXFP4_GROUPED, 4, 4096, 2048, 8192)
+    a = {**GROUPED, "batch": 4, "xr": 8192, "rows": 8192, "n": 4096, "k": 2048, "ldx": 1024, "xsr": 64, "ldy": 4096}
+    assert need > 256 and gptq.lib().gptq_mxfp4_matmul_grouped(*a.values()) == WS
+    assert gptq.lib().gptq_mxfp4_matmul_grouped(*{**a, "wsp": 16, "wsb": need - 1}.values()) == WS
+    for bad in ((0, 64, 128, 4), (2, 0, 128, 4), (2, 64, 100, 4), (2, 64, 128, -1)):
+        assert gptq.workspace_size(gptq.WS_MXFP4_GROUPED, *bad) == 0
 
 
 MLP = dict(tokens=4, k=2, experts=8, d=64, inner=96, xt=BF16, X=16, ldx=64, ids=16, w=16, W1=16, s1=16, W2=16, s2=16, act=0,
