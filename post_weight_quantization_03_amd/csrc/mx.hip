@@ -223,48 +223,62 @@ __global__ __launch_bounds__(NW * 64) void mx_few_kernel(MxArgs a) {
   f32x4 y[NM];
 #pragma unroll
   for (int g = 0; g < NM; ++g) y[g] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  for (int k = 0; k < mine; ++k) {
-    // this unit's copies are the oldest of those of up to DEPTH units
-    if (k + DEPTH <= mine) wait_vmcnt<(DEPTH - 1) * COPIES>();
-    else wait_copies();
-    asm volatile("" ::: "memory");
-    const uint8_t* const at = ring + (k % DEPTH) * NM * UNIT + j * 128;
+  auto sum = [&](auto kKind) {
+    for (int k = 0; k < mine; ++k) {
+      // this unit's copies are the oldest of those of up to DEPTH units
+      if (k + DEPTH <= mine) wait_vmcnt<(DEPTH - 1) * COPIES>();
+      else wait_copies();
+      asm volatile("" ::: "memory");
+      const uint8_t* const at = ring + (k % DEPTH) * NM * UNIT + j * 128;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int b = 8 * (wk + KS * k) + q + 4 * h;   // this lane's block
-      const bool in = b < kb;
-      i32x4 v[XP], wv[NM];
-      uint32_t s[NM];
+      for (int h = 0; h < 2; ++h) {
+        const int b = 8 * (wk + KS * k) + q + 4 * h;   // this lane's block
+        const bool in = b < kb;
+        i32x4 v[XP], wv[NM];
+        uint32_t s[NM];
 #pragma unroll
-      for (int g = 0; g < NM; ++g) {
-        wv[g] = *reinterpret_cast<const i32x4*>(at + g * UNIT + 16 * ((q + 4 * h) ^ ((j >> 1) & 7)));
-        s[g] = scale[(16 * g + j) * kb + min(b, kb - 1)];
-      }
-      const uint8_t* from = in && !lost ? x + 16 * XP * b : zeros;
+        for (int g = 0; g < NM; ++g) {
+          wv[g] = *reinterpret_cast<const i32x4*>(at + g * UNIT + 16 * ((q + 4 * h) ^ ((j >> 1) & 7)));
+          s[g] = scale[(16 * g + j) * kb + min(b, kb - 1)];
+        }
+        const uint8_t* from = in && !lost ? x + 16 * XP * b : zeros;
 #pragma unroll
-      for (int p = 0; p < XP; ++p) v[p] = *reinterpret_cast<const i32x4*>(from + 16 * p);
+        for (int p = 0; p < XP; ++p) v[p] = *reinterpret_cast<const i32x4*>(from + 16 * p);
 #pragma unroll
-      for (int g = 0; g < NM; ++g) s[g] = in ? s[g] : 127u;
-      if constexpr (KIND == kMx4) {
-        int sx = xscales[jr * xs_pitch + min(b, kb - 1)];
-        sx = in ? sx : 127;
+        for (int g = 0; g < NM; ++g) s[g] = in ? s[g] : 127u;
+        if constexpr (KIND == kMx4) {
+          int sx = xscales[jr * xs_pitch + min(b, kb - 1)];
+          sx = in ? sx : 127;
 #pragma unroll
-        for (int g = 0; g < NM; ++g)
-          y[g] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(widen(wv[g]), widen(v[0]), y[g], 4, 4, 0,
-                                                                  static_cast<int>(s[g]), 0, sx);
-      } else {
+          for (int g = 0; g < NM; ++g)
+            y[g] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(widen(wv[g]), widen(v[0]), y[g], 4, 4, 0,
+                                                                    static_cast<int>(s[g]), 0, sx);
+        } else {
 #pragma unroll
-        for (int p = 0; p < 4; ++p) {
-          const XValues<KIND> xv(v[p]);
+          for (int p = 0; p < 4; ++p) {
+            const XValues<kKind> xv(v[p]);
 #pragma unroll
-          for (int g = 0; g < NM; ++g) y[g] = mx_mma16<KIND>(mx_bf16(static_cast<uint32_t>(wv[g][p]), s[g]), xv, y[g]);
+            for (int g = 0; g < NM; ++g)
+              y[g] = mx_mma16<kKind>(mx_weights16<kKind>(static_cast<uint32_t>(wv[g][p]), s[g]), xv, y[g]);
+          }
         }
       }
+      if (k + DEPTH < mine) {
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the unit has been read
+        issue(k + DEPTH);
+      }
     }
-    if (k + DEPTH < mine) {
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the unit has been read
-      issue(k + DEPTH);
+  };
+  if constexpr (KIND == kMxF16) {
+    ScaleRange range;   // of this wave's tile
+    for (int i = 16 * lane, have = max(0, min(16 * NM, a.n - n0)) * kb; i < have; i += 1024) {
+      const uint4 v = *reinterpret_cast<const uint4*>(scale + i);
+      range.add(v.x), range.add(v.y), range.add(v.z), range.add(v.w);
     }
+    if (__all(range.f16())) sum(MxConst<kMxF16Direct>{});
+    else sum(MxConst<kMxF16>{});
+  } else {
+    sum(MxConst<KIND>{});
   }
   if constexpr (KS > 1) {
 #pragma unroll
@@ -299,18 +313,19 @@ struct MxStage {
   }
 };
 
-// Tiles of TM rows x TN outputs, 2 x 2 waves, NB buffers, NB - 1 stages of copies on the way.  The
+// Tiles of TM rows x TN outputs, 2 x 2 waves (of 32 rows 1 x 4), NB buffers, NB - 1 stages of copies on the way.  The
 // scales of up to PB blocks are in LDS before their first stage, so that the loop has no loads but copies
 // and can wait for them by their number.  gridDim.y parts of the inputs: few tiles would leave most of the
 // chip idle (sums of parts are added by mx_sum_kernel).
 template <int TM, int TN, int XB, int NB, int KIND>
 __global__ __launch_bounds__(256) void mx_tile_kernel(MxArgs a) {
   typedef MxStage<KIND, XB> St;
-  constexpr int NW = 4, FM = TM / 32, FN = TN / 32, H = XB / 64;
+  constexpr int NW = 4, WM = TM == 32 ? 1 : 2, WN = NW / WM, XW = TM / WM, WW = TN / WN;   // waves, and their tiles
+  constexpr int FM = XW / 16, FN = WW / 16, H = XB / 64;
   constexpr int STAGE = TM * XB + TN * St::WB, XROWS = 1024 / XB, WROWS = 1024 / St::WB;   // rows of one copy
   constexpr int LX = TM * XB / 1024 / NW, LW = TN * St::WB / 1024 / NW, LD = LX + LW;
-  constexpr int SROWS = KIND == kMx4 ? TM + TN : TN, PB = KIND != kMx4 ? 256 : TM == 64 ? 128 : 48, PITCH = PB + 4;
-  static_assert(LW >= 1 && TM % 32 == 0 && TN % 32 == 0 && SROWS <= 256 && PB % St::BLOCKS == 0, "tile shape");
+  constexpr int SROWS = KIND == kMx4 ? TM + TN : TN, PB = KIND != kMx4 ? (TM == 32 ? 128 : 256) : TM == 32 ? 96 : TM == 64 ? 128 : 48, PITCH = PB + 4;
+  static_assert(LX >= 1 && LW >= 1 && TM % 32 == 0 && TN % (16 * WN) == 0 && SROWS <= 256 && PB % St::BLOCKS == 0, "tile shape");
   __shared__ __attribute__((aligned(128))) uint8_t lds[NB * STAGE];
   __shared__ __attribute__((aligned(16))) uint8_t scales[SROWS * PITCH];
   __shared__ bool lost[TM];
@@ -357,7 +372,7 @@ __global__ __launch_bounds__(256) void mx_tile_kernel(MxArgs a) {
              to + TM * XB + NW * i * 1024);
   };
 
-  const int wm = wave / 2, wn = wave % 2;
+  const int wm = wave / WN, wn = wave % WN;
   const int j = lane & 15, q = lane >> 4;
   f32x4 y[FM][FN];
 #pragma unroll
@@ -367,6 +382,7 @@ __global__ __launch_bounds__(256) void mx_tile_kernel(MxArgs a) {
   for (int p0 = first; p0 < end; p0 += PB / St::BLOCKS) {
     const int p1 = min(p0 + PB / St::BLOCKS, end);
     if (p0 > first) __syncthreads();   // everyone is done with the scales and buffers before
+    ScaleRange range;
     for (int i = tid; i < SROWS * (PB / 16); i += 256) {
       const int r = i % SROWS, b0 = p0 * St::BLOCKS + 16 * (i / SROWS);
       const int o = KIND == kMx4 ? r - TM : r;
@@ -387,53 +403,65 @@ __global__ __launch_bounds__(256) void mx_tile_kernel(MxArgs a) {
         __builtin_memcpy(v, b, 16);
       }
 #pragma unroll
-      for (int e = 0; e < 4; ++e) *reinterpret_cast<uint32_t*>(scales + r * PITCH + 16 * (i / SROWS) + 4 * e) = v[e];
+      for (int e = 0; e < 4; ++e) {
+        *reinterpret_cast<uint32_t*>(scales + r * PITCH + 16 * (i / SROWS) + 4 * e) = v[e];
+        if constexpr (KIND == kMxF16) range.add(v[e]);
+      }
     }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // the loop counts copies alone
 #pragma unroll
     for (int s = 0; s < NB - 1; ++s)
       if (p0 + s < p1) issue(p0 + s, s);
-    for (int s = p0; s < p1; ++s) {
-      // this stage's copies are the oldest of those of up to NB - 1 stages
-      if (NB >= 4 && s + 2 < p1) wait_vmcnt<2 * LD>();
-      else if (NB >= 3 && s + 1 < p1) wait_vmcnt<LD>();
-      else wait_vmcnt<0>();
-      __syncthreads();   // everyone's copies have landed, and everyone is done with the stage before
-      if (s + NB - 1 < p1) issue(s + NB - 1, (s - p0 + NB - 1) % NB);
-      const uint8_t* xb = lds + (s - p0) % NB * STAGE + wm * (TM / 2) * XB;
-      const uint8_t* wb = lds + (s - p0) % NB * STAGE + TM * XB + wn * (TN / 2) * St::WB;
-      const uint8_t* sc = scales + (s - p0) * St::BLOCKS;
-      const uint8_t* ws = sc + ((KIND == kMx4 ? TM : 0) + wn * (TN / 2) + j) * PITCH;
+    auto sum = [&](auto kKind) {
+      for (int s = p0; s < p1; ++s) {
+        // this stage's copies are the oldest of those of up to NB - 1 stages
+        if (NB >= 4 && s + 2 < p1) wait_vmcnt<2 * LD>();
+        else if (NB >= 3 && s + 1 < p1) wait_vmcnt<LD>();
+        else wait_vmcnt<0>();
+        __syncthreads();   // everyone's copies have landed, and everyone is done with the stage before
+        if (s + NB - 1 < p1) issue(s + NB - 1, (s - p0 + NB - 1) % NB);
+        const uint8_t* xb = lds + (s - p0) % NB * STAGE + wm * XW * XB;
+        const uint8_t* wb = lds + (s - p0) % NB * STAGE + TM * XB + wn * WW * St::WB;
+        const uint8_t* sc = scales + (s - p0) * St::BLOCKS;
+        const uint8_t* ws = sc + ((KIND == kMx4 ? TM : 0) + wn * WW + j) * PITCH;
 #pragma unroll
-      for (int h = 0; h < H; ++h) {
-        i32x4 w4[FN];
-        bf16x8 w16[FN];
-        int sw[FN];
+        for (int h = 0; h < H; ++h) {
+          i32x4 w4[FN];
+          decltype(mx_weights16<kKind>(0u, 0u)) w16[FN];
+          int sw[FN];
 #pragma unroll
-        for (int f = 0; f < FN; ++f) {
-          const uint8_t* row = wb + (16 * f + j) * St::WB;
-          if constexpr (KIND == kMx4) {
-            w4[f] = *reinterpret_cast<const i32x4*>(row + 16 * St::w_at(j, 4 * h + q));
-            sw[f] = ws[16 * f * PITCH + 4 * h + q];
-          } else {
-            w16[f] = mx_bf16(*reinterpret_cast<const uint32_t*>(row + 16 * St::w_at(j, h) + 4 * q), ws[16 * f * PITCH + h]);
+          for (int f = 0; f < FN; ++f) {
+            const uint8_t* row = wb + (16 * f + j) * St::WB;
+            if constexpr (KIND == kMx4) {
+              w4[f] = *reinterpret_cast<const i32x4*>(row + 16 * St::w_at(j, 4 * h + q));
+              sw[f] = ws[16 * f * PITCH + 4 * h + q];
+            } else {
+              w16[f] = mx_weights16<kKind>(*reinterpret_cast<const uint32_t*>(row + 16 * St::w_at(j, h) + 4 * q),
+                                           ws[16 * f * PITCH + h]);
+            }
           }
-        }
 #pragma unroll
-        for (int i = 0; i < FM; ++i) {
-          const i32x4 v = *reinterpret_cast<const i32x4*>(xb + (16 * i + j) * XB + 16 * St::x_at(j, 4 * h + q));
-          if constexpr (KIND == kMx4) {
-            const int sx = sc[(wm * (TM / 2) + 16 * i + j) * PITCH + 4 * h + q];
+          for (int i = 0; i < FM; ++i) {
+            const i32x4 v = *reinterpret_cast<const i32x4*>(xb + (16 * i + j) * XB + 16 * St::x_at(j, 4 * h + q));
+            if constexpr (KIND == kMx4) {
+              const int sx = sc[(wm * XW + 16 * i + j) * PITCH + 4 * h + q];
 #pragma unroll
-            for (int f = 0; f < FN; ++f)
-              y[i][f] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(widen(w4[f]), widen(v), y[i][f], 4, 4, 0, sw[f], 0, sx);
-          } else {
-            const XValues<KIND> xv(v);
+              for (int f = 0; f < FN; ++f)
+                y[i][f] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(widen(w4[f]), widen(v), y[i][f], 4, 4, 0, sw[f], 0, sx);
+            } else {
+              const XValues<kKind> xv(v);
 #pragma unroll
-            for (int f = 0; f < FN; ++f) y[i][f] = mx_mma16<KIND>(w16[f], xv, y[i][f]);
+              for (int f = 0; f < FN; ++f) y[i][f] = mx_mma16<kKind>(w16[f], xv, y[i][f]);
+            }
           }
         }
       }
+    };
+    if constexpr (KIND == kMxF16) {
+      if (__syncthreads_and(range.f16())) sum(MxConst<kMxF16Direct>{});
+      else sum(MxConst<kMxF16>{});
+    } else {
+      sum(MxConst<KIND>{});
     }
   }
   MxArgs out = a;
@@ -444,14 +472,14 @@ __global__ __launch_bounds__(256) void mx_tile_kernel(MxArgs a) {
   }
 #pragma unroll
   for (int i = 0; i < FM; ++i) {
-    const int r = wm * (TM / 2) + 16 * i + j;
+    const int r = wm * XW + 16 * i + j;
     if (r >= t.count) continue;
     const bool none = lost[r];
 #pragma unroll
     for (int h = 0; h < FN; ++h) {
       const f32x4 s = y[i][h];
       const float v[4] = {none ? 0.0f : s[0], none ? 0.0f : s[1], none ? 0.0f : s[2], none ? 0.0f : s[3]};
-      store_y(out, t.p0 + r, n0 + wn * (TN / 2) + 16 * h + 4 * q, v);
+      store_y(out, t.p0 + r, n0 + wn * WW + 16 * h + 4 * q, v);
     }
   }
 }
@@ -468,7 +496,7 @@ __global__ __launch_bounds__(256) void mx_tile_kernel(MxArgs a) {
 constexpr int BIG = 256;
 template <int KIND>
 struct BigW {
-  bf16x8 v[2];
+  decltype(mx_weights16<KIND>(0u, 0u)) v[2];
 };
 template <>
 struct BigW<kMx4> {
@@ -633,8 +661,8 @@ __device__ __forceinline__ void big_tile(const MxArgs& a, const Tile& t, int n0,
     } else {
       const uint32_t sc = reinterpret_cast<const uint16_t*>(scs)[(s & 1) * BIG + wr + 16 * h + j];
       const uint8_t* row = base + j * St::WB + 4 * q;
-      o.v[0] = mx_bf16(*reinterpret_cast<const uint32_t*>(row + 16 * St::w_at(j, 0)), sc & 255);
-      o.v[1] = mx_bf16(*reinterpret_cast<const uint32_t*>(row + 16 * St::w_at(j, 1)), sc >> 8);
+      o.v[0] = mx_weights16<KIND>(*reinterpret_cast<const uint32_t*>(row + 16 * St::w_at(j, 0)), sc & 255);
+      o.v[1] = mx_weights16<KIND>(*reinterpret_cast<const uint32_t*>(row + 16 * St::w_at(j, 1)), sc >> 8);
     }
   };
 
@@ -778,9 +806,25 @@ __global__ __launch_bounds__(256) void mx_big_kernel(MxArgs a) {
   const int n0 = nt * BIG;
   const Tile t = find_tile<BIG>(a, mt);
   if (t.count <= 0) return;
-  if (t.count <= BIG / 2) big_tile<KIND, BIG / 2, BIG, 8, 4>(a, t, n0, 4, lds, scs, lost);
-  else if (a.n - n0 <= BIG / 2) big_tile<KIND, BIG, BIG / 2, 8, 4>(a, t, n0, 2, lds, scs, lost);
-  else big_tile<KIND, BIG, BIG, 8, 8>(a, t, n0, 2, lds, scs, lost);
+  auto tile = [&](auto kKind) {
+    if (t.count <= BIG / 2) big_tile<kKind, BIG / 2, BIG, 8, 4>(a, t, n0, 4, lds, scs, lost);
+    else if (a.n - n0 <= BIG / 2) big_tile<kKind, BIG, BIG / 2, 8, 4>(a, t, n0, 2, lds, scs, lost);
+    else big_tile<kKind, BIG, BIG, 8, 8>(a, t, n0, 2, lds, scs, lost);
+  };
+  if constexpr (KIND == kMxF16) {
+    const uint8_t* row = static_cast<const uint8_t*>(a.ws) +
+                         (static_cast<int64_t>(t.e) * a.n + min(n0 + static_cast<int>(threadIdx.x), a.n - 1)) * a.kb;
+    ScaleRange range;
+    for (int b = 0; b < a.kb; b += 4) {
+      uint32_t v;
+      __builtin_memcpy(&v, row + min(b, a.kb - 4), 4);
+      range.add(v);
+    }
+    if (__syncthreads_and(range.f16())) tile(MxConst<kMxF16Direct>{});
+    else tile(MxConst<kMxF16>{});
+  } else {
+    tile(MxConst<KIND>{});
+  }
 }
 
 // Y from the sums of the parts, in their order, all loads at once.
@@ -805,7 +849,7 @@ __global__ __launch_bounds__(256) void mx_sum_kernel(MxArgs a) {
 
 // ---------------------------------------------------------------------------- host side
 
-enum MxProduct { kMxFew, kMxTile64, kMxTile128, kMxBig };
+enum MxProduct { kMxFew, kMxTile32, kMxTile64, kMxTile128, kMxBig };
 struct MxPlan {
   MxProduct kind;
   int splits;
@@ -814,9 +858,11 @@ struct MxPlan {
 };
 
 // The tile kernel's stages: 256 inputs of 4-bit rows; of 16-bit ones 128 in the small tiles, else 64.
-constexpr int tile_xb(int kind, int tile) { return kind != kMx4 && tile == 64 ? 256 : 128; }
+constexpr int tile_xb(int kind, int tile) { return kind != kMx4 && tile <= 64 ? 256 : 128; }
 constexpr int tile_blocks(int kind, int tile) { return kind == kMx4 ? tile_xb(kind, tile) / 16 : tile_xb(kind, tile) / 64; }
-constexpr int tile_buffers(int kind, int tile) { return tile == 64 ? 3 : 2; }
+constexpr int tile_buffers(int tile) { return tile <= 64 ? 3 : 2; }
+constexpr int tile_outputs(int tile) { return tile == 32 ? 128 : tile; }
+constexpr int tile_rows_of(MxProduct p) { return p == kMxBig ? BIG : p == kMxTile128 ? 128 : p == kMxTile64 ? 64 : 32; }
 
 // The kernel for few rows: 8 waves sharing one tile of 16 outputs, or 4 waves with one of 32 each.
 constexpr int FEW_DEPTH = 4, WIDE_DEPTH = 2;
@@ -831,31 +877,80 @@ int64_t few_row(int kb, int kind) {
   return kind == kMx4 ? 16 * static_cast<int64_t>(kb) + 16 + (kb + 3) / 4 * 4 : 64 * static_cast<int64_t>(kb) + 16;
 }
 
-// Which kernel, by sizes alone (the workspace's size goes by the same rule).
+// What a kernel takes, in us, as measured on the card (two sides of each choice below): the start of a launch
+// and its loop, and its stages of 128 inputs of 16-bit rows or 256 of 4-bit ones where a CU has one workgroup
+// and where it has as many as it holds.
+struct MxCost {
+  double start, one, full;
+  int held;   // workgroups of a CU
+};
+constexpr MxCost mx_cost(MxProduct kind, bool four) {
+  return kind == kMxTile32   ? MxCost{4.0, 0.57, 0.82, 2}
+         : kind == kMxTile64 ? (four ? MxCost{2.5, 0.51, 0.72, 2} : MxCost{3.0, 0.59, 0.83, 2})
+         : kind == kMxTile128 ? (four ? MxCost{4.0, 1.02, 1.68, 2} : MxCost{5.0, 1.36, 2.14, 2})
+                              : (four ? MxCost{10.0, 1.9, 1.9, 1} : MxCost{8.0, 3.1, 3.1, 1});
+}
+constexpr double FEW_START = 2.0;
+// a CU's bytes in 1 us of the kernel for few rows, weights and rows of X (conversions slow 16-bit ones)
+constexpr double few_rate(int kind) { return kind == kMx4 ? 21e3 : 18e3; }
+constexpr double SUM_START = 2.5, SUM_RATE = 4e6;   // of adding parts: bytes written and read in 1 us
+// experts differ, and few large tiles do not even that out (16-bit rows, 4096 tokens: 232 us, 128 x 128 196)
+constexpr double BIG_UNEVEN = 0.6;
+constexpr int CUS = 256;
+
+// Which kernel, by sizes alone (the workspace's size goes by the same rule): the one with the least estimate.
+// With them (us, in brackets the best of the other kernels; 64 experts of 1408 x 2048):
+//   16-bit rows   4096 x 14336       14336 x 4096      experts
+//      2          few 10 (15)        few 11 (14)
+//      16         32 x 128 15 (18)   32 x 128 15 (18)  16 tokens: few 14 (33)
+//      64         64 x 64 21 (21)    32 x 128 21 (22)  256: 32 x 128 36 (54)
+//      256        64 x 64 56 (152)   128 x 128 51 (54) 1024: 128 x 128 84 (85)
+//      2048       128 x 128 239 (341)                  256 x 256 207 (245)
+//   4-bit rows 8: few 10 (12), 32: 32 x 128 13 (14), 512: 64 x 64 41 (59), 1024: 128 x 128 62 (75) of 4096 x 14336
 MxPlan mx_plan(int64_t m, int n, int k, int kind, bool grouped, int experts) {
+  const bool four = kind == kMx4;
   const double used = grouped ? static_cast<double>(std::min<int64_t>(experts, m)) : 1.0;
   const double rows = static_cast<double>(m) / used;
   const int kb = k / MXB;
+  MxPlan best{kMxTile64, 1, 0, false};
+  double least = 1e30;
+  auto take = [&](const MxPlan& p, double t) {
+    if (t < least) least = t, best = p;
+  };
+  // few rows: as many a tile as LDS holds with two workgroups on a CU, or one if that spares reading weights twice
   const bool wide = kb <= 128 && used * ((n + 15) / 16) > 1024;
   const int64_t most = std::min<int64_t>(16, m);
   const int64_t want = std::min<int64_t>(most, static_cast<int64_t>(grouped ? 1.5 * rows + 2 : m));
   const int64_t fit = (FEW_LDS - few_fixed(kb, wide)) / few_row(kb, kind);
   const int64_t cap = std::min(most, std::max(fit, std::min(want, (FEW_MOST_LDS - few_fixed(kb, wide)) / few_row(kb, kind))));
-  if (cap >= 1 && rows <= 16 && (grouped ? cap * 2 >= rows : (m + cap - 1) / cap <= 2))
-    return {kMxFew, 1, static_cast<int>(cap), wide};
-  auto tiles = [&](int t) {
-    const double r = grouped ? static_cast<double>(m) / t + 0.5 * used : static_cast<double>((m + t - 1) / t);
-    return r * ((n + t - 1) / t);
-  };
-  const int stages = (kb + tile_blocks(kind, 64) - 1) / tile_blocks(kind, 64);
-  if (tiles(256) >= 192 && kb >= 8 && (!grouped || rows >= 384)) return {kMxBig, 1, 0, false};
-  if (tiles(128) >= 384) return {kMxTile128, 1, 0, false};
-  int splits = 1;
-  if (!grouped) {
-    while (splits < 8 && tiles(64) * splits < 384 && stages / (2 * splits) >= 4) splits *= 2;
-    while (splits > 1 && static_cast<double>(splits) * static_cast<double>(m) * n * 4 > 64e6) splits /= 2;
+  if (cap >= 1 && rows <= 16) {
+    const int outputs = wide ? 128 : 16;
+    const double groups = std::max(1.0, used * ((n + outputs - 1) / outputs) / CUS);
+    const double passes = std::ceil(rows / static_cast<double>(cap));
+    const double bytes = passes * 17.0 * outputs * kb + rows * few_row(kb, kind);
+    take({kMxFew, 1, static_cast<int>(cap), wide}, FEW_START + groups * bytes / few_rate(kind));
   }
-  return {kMxTile64, splits, 0, false};
+  for (const MxProduct p : {kMxTile32, kMxTile64, kMxTile128, kMxBig}) {
+    if (p == kMxBig && kb < 8) continue;
+    const MxCost c = mx_cost(p, four);
+    const int tm = tile_rows_of(p), tn = tile_outputs(tm);
+    // experts' last tiles are half full on average, and one has at least one
+    const double mts = grouped ? used * std::max(1.0, rows / tm + 0.5) : static_cast<double>((m + tm - 1) / tm);
+    const double tiles = mts * ((n + tn - 1) / tn);
+    const int units = (kb + (four ? 7 : 3)) / (four ? 8 : 4);
+    for (int splits = 1; splits <= 16; splits *= 2) {
+      if (splits > 1 && (grouped || p == kMxTile128 || p == kMxBig || units < 2 * splits ||
+                         static_cast<double>(splits) * static_cast<double>(m) * n * 4 > 64e6))
+        break;
+      const double groups = tiles * splits, full = std::floor(groups / (c.held * CUS));
+      const double rest = groups - full * c.held * CUS;
+      const double round = full * c.full + (rest == 0 ? 0.0 : rest <= CUS ? c.one : c.full) +
+                           (grouped && p == kMxBig ? BIG_UNEVEN * c.full : 0.0);
+      const double parts = splits == 1 ? 0.0 : SUM_START + 8.0 * splits * static_cast<double>(m) * n / SUM_RATE;
+      take({p, splits, 0, false}, c.start + (units + splits - 1) / splits * round + parts);
+    }
+  }
+  return best;
 }
 
 // The largest tiles' scales: rows and outputs that a tile may read behind the last.
@@ -884,18 +979,20 @@ gptq_status launch_mx_few(MxArgs a, const MxPlan& p, hipStream_t stream) {
 template <int T, int KIND>
 gptq_status launch_mx_tile(MxArgs a, const MxPlan& p, void* workspace, hipStream_t stream) {
   constexpr int BLOCKS = tile_blocks(KIND, T);
-  a.order = {(a.n + T - 1) / T, tile_rows(a, T)};
+  constexpr int TN = tile_outputs(T);
+  a.order = {(a.n + TN - 1) / TN, tile_rows(a, T)};
   a.stages = (a.kb + BLOCKS - 1) / BLOCKS;
   a.splits = p.splits;
   a.per = (a.stages + p.splits - 1) / p.splits;
   a.part = static_cast<float*>(workspace);
   const dim3 g(static_cast<unsigned>(order_grid(a.order)), static_cast<unsigned>(a.splits));
-  GPTQ_LAUNCH((mx_tile_kernel<T, T, tile_xb(KIND, T), tile_buffers(KIND, T), KIND>), g, dim3(256), 0, stream, a);
+  GPTQ_LAUNCH((mx_tile_kernel<T, TN, tile_xb(KIND, T), tile_buffers(T), KIND>), g, dim3(256), 0, stream, a);
   if (p.splits == 1) return GPTQ_OK;
   const dim3 s((a.n + 1023) / 1024, static_cast<unsigned>(a.m));   // parts are of few tiles: m is small
   if (p.splits == 2) GPTQ_LAUNCH(mx_sum_kernel<2>, s, dim3(256), 0, stream, a);
   else if (p.splits == 4) GPTQ_LAUNCH(mx_sum_kernel<4>, s, dim3(256), 0, stream, a);
-  else GPTQ_LAUNCH(mx_sum_kernel<8>, s, dim3(256), 0, stream, a);
+  else if (p.splits == 8) GPTQ_LAUNCH(mx_sum_kernel<8>, s, dim3(256), 0, stream, a);
+  else GPTQ_LAUNCH(mx_sum_kernel<16>, s, dim3(256), 0, stream, a);
   return GPTQ_OK;
 }
 
@@ -922,14 +1019,15 @@ gptq_status launch_mx(const MxArgs& a, const MxPlan& p, void* workspace, hipStre
   if (p.kind == kMxFew)
     return p.wide ? launch_mx_few<4, 1, 2, WIDE_DEPTH, KIND>(a, p, stream) : launch_mx_few<8, 8, 1, FEW_DEPTH, KIND>(a, p, stream);
   if (p.kind == kMxBig) return launch_mx_big<KIND>(a, workspace, stream);
+  if (p.kind == kMxTile32) return launch_mx_tile<32, KIND>(a, p, workspace, stream);
   return p.kind == kMxTile64 ? launch_mx_tile<64, KIND>(a, p, workspace, stream)
                              : launch_mx_tile<128, KIND>(a, p, workspace, stream);
 }
 
 // Whether the launch is one the kernels number their tiles for.
 bool mx_launchable(const MxArgs& a, const MxPlan& p) {
-  const int tm = p.kind == kMxBig ? BIG : p.kind == kMxTile128 ? 128 : p.kind == kMxTile64 ? 64 : p.cap;
-  const int tn = p.kind == kMxFew ? 16 : tm;
+  const int tm = p.kind == kMxFew ? p.cap : tile_rows_of(p.kind);
+  const int tn = p.kind == kMxFew ? 16 : tile_outputs(tm);
   return tile_rows(a, tm) <= (1 << 22) / ((a.n + tn - 1) / tn);
 }
 

@@ -251,49 +251,61 @@ __global__ __launch_bounds__(MLP_NT) void mlp_kernel(MlpArgs a) {
     f32x4 y[NM];
 #pragma unroll
     for (int g = 0; g < NM; ++g) y[g] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    for (int k = 0; k < mine; ++k) {
-      // this unit's copies are the oldest of those of up to DEPTH units
-      if (k + DEPTH <= mine) wait_vmcnt<(DEPTH - 1) * COPIES>();
-      else wait_copies();
-      asm volatile("" ::: "memory");
-      const uint8_t* const at = ring + (k % DEPTH) * NM * UNIT + j * 128;
+    auto sum = [&](auto kKind) {
+      for (int k = 0; k < mine; ++k) {
+        // this unit's copies are the oldest of those of up to DEPTH units
+        if (k + DEPTH <= mine) wait_vmcnt<(DEPTH - 1) * COPIES>();
+        else wait_copies();
+        asm volatile("" ::: "memory");
+        const uint8_t* const at = ring + (k % DEPTH) * NM * UNIT + j * 128;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int b = 8 * (wk + KS * k) + q + 4 * h;   // this lane's block
-        const bool in = b < kb;
-        i32x4 v[PLANES][4], wv[NM];
-        uint32_t s[NM];
-#pragma unroll
-        for (int g = 0; g < NM; ++g) {
-          wv[g] = *reinterpret_cast<const i32x4*>(at + g * UNIT + 16 * ((q + 4 * h) ^ ((j >> 1) & 7)));
-          s[g] = scale[g * scale_bytes + j * kb + min(b, kb - 1)];
-        }
-#pragma unroll
-        for (int l = 0; l < PLANES; ++l) {
-          const uint8_t* from = in ? x + l * pitch + 64 * b : zeros;
-#pragma unroll
-          for (int p = 0; p < 4; ++p) v[l][p] = *reinterpret_cast<const i32x4*>(from + 16 * p);
-        }
-#pragma unroll
-        for (int g = 0; g < NM; ++g) s[g] = in ? s[g] : 127u;
-#pragma unroll
-        for (int p = 0; p < 4; ++p) {
+        for (int h = 0; h < 2; ++h) {
+          const int b = 8 * (wk + KS * k) + q + 4 * h;   // this lane's block
+          const bool in = b < kb;
+          i32x4 v[PLANES][4], wv[NM];
+          uint32_t s[NM];
 #pragma unroll
           for (int g = 0; g < NM; ++g) {
-            const bf16x8 wf = mx_bf16(static_cast<uint32_t>(wv[g][p]), s[g]);
-            if constexpr (UP) {
-              y[g] = mx_mma16<KIND>(wf, XValues<KIND>(v[0][p]), y[g]);
-            } else {
-              y[g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf, __builtin_bit_cast(bf16x8, v[1][p]), y[g], 0, 0, 0);
-              y[g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf, __builtin_bit_cast(bf16x8, v[0][p]), y[g], 0, 0, 0);
+            wv[g] = *reinterpret_cast<const i32x4*>(at + g * UNIT + 16 * ((q + 4 * h) ^ ((j >> 1) & 7)));
+            s[g] = scale[g * scale_bytes + j * kb + min(b, kb - 1)];
+          }
+#pragma unroll
+          for (int l = 0; l < PLANES; ++l) {
+            const uint8_t* from = in ? x + l * pitch + 64 * b : zeros;
+#pragma unroll
+            for (int p = 0; p < 4; ++p) v[l][p] = *reinterpret_cast<const i32x4*>(from + 16 * p);
+          }
+#pragma unroll
+          for (int g = 0; g < NM; ++g) s[g] = in ? s[g] : 127u;
+#pragma unroll
+          for (int p = 0; p < 4; ++p) {
+#pragma unroll
+            for (int g = 0; g < NM; ++g) {
+              const auto wf = mx_weights16<kKind>(static_cast<uint32_t>(wv[g][p]), s[g]);
+              if constexpr (UP) {
+                y[g] = mx_mma16<kKind>(wf, XValues<kKind>(v[0][p]), y[g]);
+              } else {
+                y[g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf, __builtin_bit_cast(bf16x8, v[1][p]), y[g], 0, 0, 0);
+                y[g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf, __builtin_bit_cast(bf16x8, v[0][p]), y[g], 0, 0, 0);
+              }
             }
           }
         }
+        if (k + DEPTH < mine) {
+          asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the unit has been read
+          issue(k + DEPTH);
+        }
       }
-      if (k + DEPTH < mine) {
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the unit has been read
-        issue(k + DEPTH);
-      }
+    };
+    if constexpr (UP && KIND == kMxF16) {
+      ScaleRange range;   // of this wave's tile
+      for (int i = 4 * lane; i < 16 * kb; i += 256)
+#pragma unroll
+        for (int g = 0; g < NM; ++g) range.add(*reinterpret_cast<const uint32_t*>(scale + g * scale_bytes + i));
+      if (__all(range.f16())) sum(MxConst<kMxF16Direct>{});
+      else sum(MxConst<kMxF16>{});
+    } else {
+      sum(MxConst<UP ? KIND : kMxBf16>{});
     }
     if constexpr (KS > 1) {
       if (r0 > 0) lds_barrier();   // the sums before have been read

@@ -9,8 +9,8 @@ operands are exact.
             it adds four of them and the accumulator, each addition good to 2^-23 of B at the worst
             (cut, not rounded): c = (5 ceil(k / 128) + 16) 2^-23, the 16 for parts of the inputs that
             waves or workgroups add.
-  16-bit X  32 products and the accumulator an instruction, twice for fp16, whose values are two bf16
-            numbers: c = (33 p ceil(k / 32) + 16) 2^-23, p = 1 or 2.
+  16-bit X  32 products and the accumulator an instruction, twice for fp16, whose values may go as two
+            bf16 numbers: c = (33 p ceil(k / 32) + 16) 2^-23, p = 1 or 2.
 These bounds grow with k as if every error had one sign; so the norm of Y - Y_ref is held too: within
 h / sqrt(3) (roundings even over half a step) and 8 sqrt(n) 2^-24 for n additions of independent
 errors, of the norm of Y_ref, with a factor of 2 for both.
@@ -316,6 +316,26 @@ def test_matmul_extreme_scales():
             assert bool((lib().mxfp4_matmul(X, W, ws, out_dtype=torch.float32).double() == want).all()), a
 
 
+@pytest.mark.parametrize("codes", [(104, 140), (103, 140), (104, 141), (0, 150)])
+@pytest.mark.parametrize("m,n,k", [(3, 50, 4096), (3, 17000, 96), (30, 1100, 2080), (200, 300, 1056), (1000, 4096, 544),
+                                   (3600, 4180, 1056)])
+def test_matmul_fp16_rows_and_scales_at_its_ends(m, n, k, codes):
+    # weights that are fp16 values, its smallest among them, and weights that are not, in one product; rows of
+    # fp16's smallest and largest numbers
+    g = torch.Generator(device="cuda")
+    g.manual_seed(m + k)
+    W = torch.randint(0, 256, (n, k // 2), generator=g, device="cuda", dtype=torch.uint8)
+    ws = torch.randint(104, 141, (n, k // 32), generator=g, device="cuda", dtype=torch.uint8)
+    ws[n // 3, k // 32 - 1], ws[n - 1, 0] = codes
+    X = torch.randn(m, k, generator=g, device="cuda")
+    X[m // 2] *= 2.0 ** -20
+    X[m - 1] = X[m - 1].clamp(-2, 2) * 3e4
+    X = X.half()
+    Y = lib().mxfp4_matmul(X, W, ws, out_dtype=torch.float32)
+    print("worst / bound", check_large(Y, wide(X, None), wide(W, ws), k, "f16", "f32"), flush=True)
+    assert torch.equal(Y, lib().mxfp4_matmul(X, W, ws, out_dtype=torch.float32))
+
+
 def test_matmul_empty():
     (W, ws), _ = weights(np.random.default_rng(1), 64, 128)
     x = torch.zeros(0, 128, dtype=torch.bfloat16, device="cuda")
@@ -389,7 +409,8 @@ def check_large(Y, x, w, k, kind, out):
     (4090, 4095, 1056, "bf16"), (3900, 4000, 416, "f32"), (8192, 8192, 256, "bf16"), (8192, 8192, 128, "bf16"),
     (8192, 8100, 96, "f16"), (2050, 2050, 672, "f32"), (4096, 4096, 288, "f32"), (1027, 4096, 2080, "bf16"),
     (513, 2304, 1056, "f32"), (65, 200, 1056, "f32"), (300, 640, 896, "bf16"), (64, 4096, 14336, "bf16"),
-    (300, 4096, 7808, "f32"), (4353, 4225, 704, "bf16"), (8200, 8256, 32, "bf16"), (20, 16000, 512, "f32")])
+    (300, 4096, 7808, "f32"), (4353, 4225, 704, "bf16"), (8200, 8256, 32, "bf16"), (20, 16000, 512, "f32"), (3600, 4180, 1056, "bf16"), (3601, 4177, 1312, "f32"),
+    (3583, 4225, 1024, "f16"), (30, 4160, 4128, "f32"), (24, 1000, 14336, "bf16")])
 def test_large_products(m, n, k, out, x):
     # sizes at which the larger tiles are taken, with short last tiles, and shared inputs
     q, s = random_operand(m + k, m, k, x)
@@ -629,6 +650,28 @@ def test_layer_same_expert_twice_and_no_expert(tokens):
     assert bool((out[1] == 0).all())
     ids[:] = -1
     assert bool((lib().mxfp4_moe_mlp(x, cuda(ids), cuda(p), *w) == 0).all())
+
+
+@pytest.mark.parametrize("code", [104, 140, 103, 141, 0])
+@pytest.mark.parametrize("tokens,experts,d,inner", [(2, 4, 4096, 32), (12, 60, 96, 288)])
+def test_layer_fp16_scales_at_its_ends(tokens, experts, d, inner, code):
+    # gates whose weights are fp16's smallest values and below: their expert's own results only
+    rng = np.random.default_rng(code)
+    x, ids, p, w, xv, wv = layer(rng, tokens, 2, experts, d, inner, "f16", spare=0)
+    ids[0, 0], ids[0, 1] = 1, 2
+    w[1].view(torch.uint8)[1, :inner, 1] = code
+    scale = 2.0 ** (code - 127)
+    if code > 127:      # one output, of small weights otherwise: the result must stay in fp16's range
+        w[1].view(torch.uint8)[1, :inner, 1] = 120
+        w[1].view(torch.uint8)[1, inner // 2, 1] = code
+        x[:, 32:64] *= 2.0 ** -14
+        xv[:] = x.double().cpu().numpy()
+    s1 = w[1].view(torch.uint8).cpu().numpy()
+    codes = M.unpack(w[0].view(torch.uint8).cpu().numpy())
+    wv[0] = M.dequantize(codes, s1)
+    assert scale in 2.0 ** (s1[1].astype(np.float64) - 127)
+    out = lib().mxfp4_moe_mlp(x, cuda(ids), cuda(p), *w, activation="silu")
+    print("worst / bound", check_layer(out, xv, ids, p, *wv, "silu", "f16"), flush=True)
 
 
 @pytest.mark.parametrize("tokens", [3, 20, 70])
