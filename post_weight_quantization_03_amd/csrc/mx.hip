@@ -313,19 +313,21 @@ struct MxStage {
   }
 };
 
-// Tiles of TM rows x TN outputs, 2 x 2 waves (of 32 rows 1 x 4), NB buffers, NB - 1 stages of copies on the way.  The
+// Tiles of TM rows x TN outputs, 2 x 2 waves (1 x 4 where it is wider than high), NB buffers, NB - 1 stages of copies on the way.  The
 // scales of up to PB blocks are in LDS before their first stage, so that the loop has no loads but copies
 // and can wait for them by their number.  gridDim.y parts of the inputs: few tiles would leave most of the
 // chip idle (sums of parts are added by mx_sum_kernel).
 template <int TM, int TN, int XB, int NB, int KIND>
 __global__ __launch_bounds__(256) void mx_tile_kernel(MxArgs a) {
   typedef MxStage<KIND, XB> St;
-  constexpr int NW = 4, WM = TM == 32 ? 1 : 2, WN = NW / WM, XW = TM / WM, WW = TN / WN;   // waves, and their tiles
+  constexpr int NW = 4, WM = TM < TN ? 1 : 2, WN = NW / WM, XW = TM / WM, WW = TN / WN;   // waves, and their tiles
   constexpr int FM = XW / 16, FN = WW / 16, H = XB / 64;
   constexpr int STAGE = TM * XB + TN * St::WB, XROWS = 1024 / XB, WROWS = 1024 / St::WB;   // rows of one copy
   constexpr int LX = TM * XB / 1024 / NW, LW = TN * St::WB / 1024 / NW, LD = LX + LW;
-  constexpr int SROWS = KIND == kMx4 ? TM + TN : TN, PB = KIND != kMx4 ? (TM == 32 ? 128 : 256) : TM == 32 ? 96 : TM == 64 ? 128 : 48, PITCH = PB + 4;
-  static_assert(LX >= 1 && LW >= 1 && TM % 32 == 0 && TN % (16 * WN) == 0 && SROWS <= 256 && PB % St::BLOCKS == 0, "tile shape");
+  // two workgroups on a CU: what the buffers leave of half its LDS is for scales
+  constexpr int SROWS = KIND == kMx4 ? TM + TN : TN;
+  constexpr int PB = std::min(256, ((80 * 1024 - 256 - NB * STAGE) / SROWS - 4) / 16 * 16), PITCH = PB + 4;
+  static_assert(LX >= 1 && PB >= 16 && LW >= 1 && TM % 32 == 0 && TN % (16 * WN) == 0 && SROWS <= 256 && PB % St::BLOCKS == 0, "tile shape");
   __shared__ __attribute__((aligned(128))) uint8_t lds[NB * STAGE];
   __shared__ __attribute__((aligned(16))) uint8_t scales[SROWS * PITCH];
   __shared__ bool lost[TM];
@@ -383,7 +385,7 @@ __global__ __launch_bounds__(256) void mx_tile_kernel(MxArgs a) {
     const int p1 = min(p0 + PB / St::BLOCKS, end);
     if (p0 > first) __syncthreads();   // everyone is done with the scales and buffers before
     ScaleRange range;
-    for (int i = tid; i < SROWS * (PB / 16); i += 256) {
+    for (int i = tid; i < SROWS * (((p1 - p0) * St::BLOCKS + 15) / 16); i += 256) {
       const int r = i % SROWS, b0 = p0 * St::BLOCKS + 16 * (i / SROWS);
       const int o = KIND == kMx4 ? r - TM : r;
       const uint8_t* row = nullptr;
@@ -849,7 +851,7 @@ __global__ __launch_bounds__(256) void mx_sum_kernel(MxArgs a) {
 
 // ---------------------------------------------------------------------------- host side
 
-enum MxProduct { kMxFew, kMxTile32, kMxTile64, kMxTile128, kMxBig };
+enum MxProduct { kMxFew, kMxTile32, kMxWide64, kMxTile64, kMxTile128, kMxBig };
 struct MxPlan {
   MxProduct kind;
   int splits;
@@ -858,11 +860,13 @@ struct MxPlan {
 };
 
 // The tile kernel's stages: 256 inputs of 4-bit rows; of 16-bit ones 128 in the small tiles, else 64.
-constexpr int tile_xb(int kind, int tile) { return kind != kMx4 && tile <= 64 ? 256 : 128; }
-constexpr int tile_blocks(int kind, int tile) { return kind == kMx4 ? tile_xb(kind, tile) / 16 : tile_xb(kind, tile) / 64; }
-constexpr int tile_buffers(int tile) { return tile <= 64 ? 3 : 2; }
-constexpr int tile_outputs(int tile) { return tile == 32 ? 128 : tile; }
-constexpr int tile_rows_of(MxProduct p) { return p == kMxBig ? BIG : p == kMxTile128 ? 128 : p == kMxTile64 ? 64 : 32; }
+constexpr int tile_rows_of(MxProduct p) {
+  return p == kMxBig ? BIG : p == kMxTile128 ? 128 : p == kMxTile32 ? 32 : 64;
+}
+constexpr int tile_outputs(MxProduct p) { return p == kMxBig ? BIG : p == kMxTile64 ? 64 : 128; }
+constexpr int tile_xb(MxProduct p, int kind) { return kind != kMx4 && p != kMxTile128 ? 256 : 128; }
+constexpr int tile_blocks(MxProduct p, int kind) { return tile_xb(p, kind) / (kind == kMx4 ? 16 : 64); }
+constexpr int tile_buffers(MxProduct p) { return p == kMxTile128 ? 2 : 3; }
 
 // The kernel for few rows: 8 waves sharing one tile of 16 outputs, or 4 waves with one of 32 each.
 constexpr int FEW_DEPTH = 4, WIDE_DEPTH = 2;
@@ -886,6 +890,7 @@ struct MxCost {
 };
 constexpr MxCost mx_cost(MxProduct kind, bool four) {
   return kind == kMxTile32   ? MxCost{4.0, 0.57, 0.82, 2}
+         : kind == kMxWide64 ? MxCost{3.5, 0.85, 1.18, 2}   // of 16-bit rows
          : kind == kMxTile64 ? (four ? MxCost{2.5, 0.51, 0.72, 2} : MxCost{3.0, 0.59, 0.83, 2})
          : kind == kMxTile128 ? (four ? MxCost{4.0, 1.02, 1.68, 2} : MxCost{5.0, 1.36, 2.14, 2})
                               : (four ? MxCost{10.0, 1.9, 1.9, 1} : MxCost{8.0, 3.1, 3.1, 1});
@@ -900,12 +905,12 @@ constexpr int CUS = 256;
 
 // Which kernel, by sizes alone (the workspace's size goes by the same rule): the one with the least estimate.
 // With them (us, in brackets the best of the other kernels; 64 experts of 1408 x 2048):
-//   16-bit rows   4096 x 14336       14336 x 4096      experts
-//      2          few 10 (15)        few 11 (14)
-//      16         32 x 128 15 (18)   32 x 128 15 (18)  16 tokens: few 14 (33)
-//      64         64 x 64 21 (21)    32 x 128 21 (22)  256: 32 x 128 36 (54)
-//      256        64 x 64 56 (152)   128 x 128 51 (54) 1024: 128 x 128 84 (85)
-//      2048       128 x 128 239 (341)                  256 x 256 207 (245)
+//   16-bit rows   4096 x 14336         14336 x 4096          experts, tokens
+//      2          few 10 (15)          few 11 (14)           16: few 14 (33)
+//      16         32 x 128 15 (18)     32 x 128 15 (18)      256: 32 x 128 38 (45)
+//      256        64 x 128 47 (52)     64 x 128 42 (51)      1024: 64 x 128 78 (85)
+//      512        64 x 128 78 (88)     128 x 128 68 (81)     4096: 128 x 128 196 (232)
+//      2048       128 x 128 227 (341)  256 x 256 207 (245)   16384: 256 x 256 575 (650)
 //   4-bit rows 8: few 10 (12), 32: 32 x 128 13 (14), 512: 64 x 64 41 (59), 1024: 128 x 128 62 (75) of 4096 x 14336
 MxPlan mx_plan(int64_t m, int n, int k, int kind, bool grouped, int experts) {
   const bool four = kind == kMx4;
@@ -930,10 +935,10 @@ MxPlan mx_plan(int64_t m, int n, int k, int kind, bool grouped, int experts) {
     const double bytes = passes * 17.0 * outputs * kb + rows * few_row(kb, kind);
     take({kMxFew, 1, static_cast<int>(cap), wide}, FEW_START + groups * bytes / few_rate(kind));
   }
-  for (const MxProduct p : {kMxTile32, kMxTile64, kMxTile128, kMxBig}) {
-    if (p == kMxBig && kb < 8) continue;
+  for (const MxProduct p : {kMxTile32, kMxTile64, kMxWide64, kMxTile128, kMxBig}) {
+    if ((p == kMxBig && kb < 8) || (p == kMxWide64 && four)) continue;
     const MxCost c = mx_cost(p, four);
-    const int tm = tile_rows_of(p), tn = tile_outputs(tm);
+    const int tm = tile_rows_of(p), tn = tile_outputs(p);
     // experts' last tiles are half full on average, and one has at least one
     const double mts = grouped ? used * std::max(1.0, rows / tm + 0.5) : static_cast<double>((m + tm - 1) / tm);
     const double tiles = mts * ((n + tn - 1) / tn);
@@ -976,17 +981,16 @@ gptq_status launch_mx_few(MxArgs a, const MxPlan& p, hipStream_t stream) {
   return GPTQ_OK;
 }
 
-template <int T, int KIND>
+template <MxProduct P, int KIND>
 gptq_status launch_mx_tile(MxArgs a, const MxPlan& p, void* workspace, hipStream_t stream) {
-  constexpr int BLOCKS = tile_blocks(KIND, T);
-  constexpr int TN = tile_outputs(T);
-  a.order = {(a.n + TN - 1) / TN, tile_rows(a, T)};
+  constexpr int TM = tile_rows_of(P), TN = tile_outputs(P), BLOCKS = tile_blocks(P, KIND);
+  a.order = {(a.n + TN - 1) / TN, tile_rows(a, TM)};
   a.stages = (a.kb + BLOCKS - 1) / BLOCKS;
   a.splits = p.splits;
   a.per = (a.stages + p.splits - 1) / p.splits;
   a.part = static_cast<float*>(workspace);
   const dim3 g(static_cast<unsigned>(order_grid(a.order)), static_cast<unsigned>(a.splits));
-  GPTQ_LAUNCH((mx_tile_kernel<T, TN, tile_xb(KIND, T), tile_buffers(T), KIND>), g, dim3(256), 0, stream, a);
+  GPTQ_LAUNCH((mx_tile_kernel<TM, TN, tile_xb(P, KIND), tile_buffers(P), KIND>), g, dim3(256), 0, stream, a);
   if (p.splits == 1) return GPTQ_OK;
   const dim3 s((a.n + 1023) / 1024, static_cast<unsigned>(a.m));   // parts are of few tiles: m is small
   if (p.splits == 2) GPTQ_LAUNCH(mx_sum_kernel<2>, s, dim3(256), 0, stream, a);
@@ -1019,15 +1023,17 @@ gptq_status launch_mx(const MxArgs& a, const MxPlan& p, void* workspace, hipStre
   if (p.kind == kMxFew)
     return p.wide ? launch_mx_few<4, 1, 2, WIDE_DEPTH, KIND>(a, p, stream) : launch_mx_few<8, 8, 1, FEW_DEPTH, KIND>(a, p, stream);
   if (p.kind == kMxBig) return launch_mx_big<KIND>(a, workspace, stream);
-  if (p.kind == kMxTile32) return launch_mx_tile<32, KIND>(a, p, workspace, stream);
-  return p.kind == kMxTile64 ? launch_mx_tile<64, KIND>(a, p, workspace, stream)
-                             : launch_mx_tile<128, KIND>(a, p, workspace, stream);
+  if (p.kind == kMxTile32) return launch_mx_tile<kMxTile32, KIND>(a, p, workspace, stream);
+  if constexpr (KIND != kMx4)
+    if (p.kind == kMxWide64) return launch_mx_tile<kMxWide64, KIND>(a, p, workspace, stream);
+  if (p.kind == kMxTile64) return launch_mx_tile<kMxTile64, KIND>(a, p, workspace, stream);
+  return launch_mx_tile<kMxTile128, KIND>(a, p, workspace, stream);
 }
 
 // Whether the launch is one the kernels number their tiles for.
 bool mx_launchable(const MxArgs& a, const MxPlan& p) {
   const int tm = p.kind == kMxFew ? p.cap : tile_rows_of(p.kind);
-  const int tn = p.kind == kMxFew ? 16 : tile_outputs(tm);
+  const int tn = p.kind == kMxFew ? 16 : tile_outputs(p.kind);
   return tile_rows(a, tm) <= (1 << 22) / ((a.n + tn - 1) / tn);
 }
 
