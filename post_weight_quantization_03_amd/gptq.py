@@ -730,18 +730,18 @@ def mxfp4_quantize(X: torch.Tensor, scaling: str = "floor", stream=None):
         return _on(stream, mxfp4_quantize, X, scaling)
     if X.dtype not in _DT:
         raise TypeError("X must be fp32/bf16/fp16")
-    if scaling not in _MX_SCALING or X.dim() not in (2, 3):
+    shape, strides = X.shape, X.stride()
+    if scaling not in _MX_SCALING or len(shape) not in (2, 3):
         raise ValueError("X must be [(batch,) rows, cols], scaling 'floor' or 'ceil'")
-    Xb = _batched(X, 2)
-    batch, rows, cols = Xb.shape
+    (*lead, rows, cols), batch = shape, 1 if len(shape) == 2 else shape[0]
     if cols < _MX_BLOCK or cols % _MX_BLOCK or batch < 1:
         raise ValueError("cols must be a positive multiple of 32")
-    if Xb.stride(2) != 1:
+    if strides[-1] != 1:
         raise ValueError("X rows must be contiguous")
-    q = torch.empty((*X.shape[:-1], cols // 2), dtype=torch.float4_e2m1fn_x2, device=X.device)
-    S = torch.empty((*X.shape[:-1], cols // _MX_BLOCK), dtype=torch.float8_e8m0fnu, device=X.device)
-    _run("gptq_mxfp4_quantize", (X, q, S), batch, rows, cols, _DT[X.dtype], X.data_ptr(), _row_stride(Xb),
-         Xb.stride(0), _MX_SCALING[scaling], q.data_ptr(), S.data_ptr())
+    q = X.new_empty((*lead, rows, cols // 2), dtype=torch.float4_e2m1fn_x2)
+    S = X.new_empty((*lead, rows, cols // _MX_BLOCK), dtype=torch.float8_e8m0fnu)
+    _run("gptq_mxfp4_quantize", (X, q, S), batch, rows, cols, _DT[X.dtype], X.data_ptr(),
+         strides[-2] if rows > 1 else cols, strides[0], _MX_SCALING[scaling], q.data_ptr(), S.data_ptr())
     return q, S
 
 
@@ -749,8 +749,9 @@ def _mx_pair(q, scales, what: str):
     """Checks codes and their scales; -> the number of inputs of a row."""
     if q.dtype not in _MX_CODES or scales.dtype not in _MX_SCALES:
         raise TypeError(f"{what} must be float4_e2m1fn_x2 (or uint8) with float8_e8m0fnu (or uint8) scales")
-    k = 2 * q.shape[-1]
-    if k < _MX_BLOCK or k % _MX_BLOCK or scales.shape != (*q.shape[:-1], k // _MX_BLOCK):
+    (*rows, half), (*scale_rows, blocks) = q.shape, scales.shape
+    k = 2 * half
+    if k < _MX_BLOCK or blocks * _MX_BLOCK != k or rows != scale_rows:
         raise ValueError(f"{what} must be [.., inputs / 2] with scales [.., inputs / 32]")
     return k
 
