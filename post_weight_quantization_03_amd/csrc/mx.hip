@@ -130,6 +130,7 @@ struct MxArgs : MmArgs {
   uint2* wst;
   int64_t mp;        // and their rows
   int np;
+  int parts;         // 2 or 4: workgroups of a tile that is behind the last whole round of them
 };
 
 // Few rows, at most `cap` (up to 16) of one expert or of the one problem: a workgroup has NW / KS tiles
@@ -603,9 +604,13 @@ __device__ __forceinline__ void big_tile(const MxArgs& a, const Tile& t, int n0,
       const uint2* x = a.xst + static_cast<int64_t>(s) * a.mp + t.p0;
       const uint2* w = a.wst + (static_cast<int64_t>(t.e) * a.stages + s) * a.np + n0;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int at = 512 * wave + 256 * i;   // bytes
+      for (int i = 0; i < XR / 128; ++i) {
+        const int at = 2 * XR * wave + 256 * i;   // bytes
         copy4(reinterpret_cast<const uint8_t*>(x) + at + 4 * lane, scs0 + (s & 1) * SROWS * 8 + at);
+      }
+#pragma unroll
+      for (int i = 0; i < WR / 128; ++i) {
+        const int at = 2 * WR * wave + 256 * i;
         copy4(reinterpret_cast<const uint8_t*>(w) + at + 4 * lane, scs0 + (s & 1) * SROWS * 8 + BIG * 8 + at);
       }
     } else {
@@ -802,14 +807,31 @@ __global__ __launch_bounds__(256) void mx_big_kernel(MxArgs a) {
   __shared__ __attribute__((aligned(128))) uint8_t lds[2 * BIG * (128 + MxStage<KIND, 128>::WB)];
   __shared__ uint2 scs[KIND == kMx4 ? 4 * BIG : BIG / 2];
   __shared__ bool lost[BIG];
+  // Behind the last whole round of 256 tiles up to 128 go as halves of 128 rows and up to 64 as quarters,
+  // those of a tile on one XCD (4096 x 14336 x 4096, half a round left, 16-bit rows 416 us, 385 so; 4096 x 4608
+  // x 8192, an eighth, 390 and 285, 4-bit rows 110 and 97).
+  uint32_t id = blockIdx.x, part = 0;
+  const uint32_t whole = static_cast<uint32_t>(a.order.tiles_m) * static_cast<uint32_t>(a.order.tiles_n) & ~255u;
+  if (a.parts > 1 && id >= whole) {
+    const uint32_t i = (id - whole) / 8;
+    part = i % a.parts;
+    id = whole + i / a.parts * 8 + (id - whole) % 8;
+  }
   int64_t mt;
   int nt;
-  if (!ordered_tile(a.order, blockIdx.x, &mt, &nt)) return;
-  const int n0 = nt * BIG;
-  const Tile t = find_tile<BIG>(a, mt);
-  if (t.count <= 0) return;
+  if (!ordered_tile(a.order, id, &mt, &nt)) return;
+  Tile t = find_tile<BIG>(a, mt);
+  int n0 = nt * BIG;
+  const bool narrow = a.parts == 4 && id >= whole;
+  if (a.parts > 1 && id >= whole) {
+    t.p0 += BIG / 2 * (part & 1);
+    t.count = min(BIG / 2, t.count - BIG / 2 * static_cast<int>(part & 1));
+    n0 += BIG / 2 * static_cast<int>(part >> 1);
+  }
+  if (t.count <= 0 || n0 >= a.n) return;
   auto tile = [&](auto kKind) {
-    if (t.count <= BIG / 2) big_tile<kKind, BIG / 2, BIG, 8, 4>(a, t, n0, 4, lds, scs, lost);
+    if (narrow) big_tile<kKind, BIG / 2, BIG / 2, 4, 4>(a, t, n0, 2, lds, scs, lost);
+    else if (t.count <= BIG / 2) big_tile<kKind, BIG / 2, BIG, 8, 4>(a, t, n0, 4, lds, scs, lost);
     else if (a.n - n0 <= BIG / 2) big_tile<kKind, BIG, BIG / 2, 8, 4>(a, t, n0, 2, lds, scs, lost);
     else big_tile<kKind, BIG, BIG, 8, 8>(a, t, n0, 2, lds, scs, lost);
   };
@@ -901,6 +923,10 @@ constexpr double few_rate(int kind) { return kind == kMx4 ? 21e3 : 18e3; }
 constexpr double SUM_START = 2.5, SUM_RATE = 4e6;   // of adding parts: bytes written and read in 1 us
 // experts differ, and few large tiles do not even that out (16-bit rows, 4096 tokens: 232 us, 128 x 128 196)
 constexpr double BIG_UNEVEN = 0.6;
+// a round of halves or quarters, as a part of one of whole tiles: more is copied for as many products
+constexpr double big_rest(bool quarters, bool four) {
+  return quarters ? (four ? 0.78 : 0.5) : four ? 0.95 : 0.62;
+}
 constexpr int CUS = 256;
 
 // Which kernel, by sizes alone (the workspace's size goes by the same rule): the one with the least estimate.
@@ -910,7 +936,7 @@ constexpr int CUS = 256;
 //      16         32 x 128 15 (18)     32 x 128 15 (18)      256: 32 x 128 38 (45)
 //      256        64 x 128 47 (52)     64 x 128 42 (51)      1024: 64 x 128 78 (85)
 //      512        64 x 128 78 (88)     128 x 128 68 (81)     4096: 128 x 128 196 (232)
-//      2048       128 x 128 227 (341)  256 x 256 207 (245)   16384: 256 x 256 575 (650)
+//      2048       256 x 256 214 (227)  256 x 256 207 (245)   16384: 256 x 256 575 (650)
 //   4-bit rows 8: few 10 (12), 32: 32 x 128 13 (14), 512: 64 x 64 41 (59), 1024: 128 x 128 62 (75) of 4096 x 14336
 MxPlan mx_plan(int64_t m, int n, int k, int kind, bool grouped, int experts) {
   const bool four = kind == kMx4;
@@ -949,8 +975,9 @@ MxPlan mx_plan(int64_t m, int n, int k, int kind, bool grouped, int experts) {
         break;
       const double groups = tiles * splits, full = std::floor(groups / (c.held * CUS));
       const double rest = groups - full * c.held * CUS;
-      const double round = full * c.full + (rest == 0 ? 0.0 : rest <= CUS ? c.one : c.full) +
-                           (grouped && p == kMxBig ? BIG_UNEVEN * c.full : 0.0);
+      double round = full * c.full + (rest == 0 ? 0.0 : rest <= CUS ? c.one : c.full);
+      if (p == kMxBig && grouped) round += BIG_UNEVEN * c.full;
+      else if (p == kMxBig && rest > 0 && rest <= 128) round -= c.full * (1.0 - big_rest(rest <= 64, four));
       const double parts = splits == 1 ? 0.0 : SUM_START + 8.0 * splits * static_cast<double>(m) * n / SUM_RATE;
       take({p, splits, 0, false}, c.start + (units + splits - 1) / splits * round + parts);
     }
@@ -1014,7 +1041,10 @@ gptq_status launch_mx_big(MxArgs a, void* workspace, hipStream_t stream) {
     GPTQ_LAUNCH(mx_gather_scales_kernel, dim3(static_cast<unsigned>((rows + 255) / 256), (a.stages + GATHER - 1) / GATHER),
                 dim3(256), 0, stream, a);
   }
-  GPTQ_LAUNCH(mx_big_kernel<KIND>, dim3(static_cast<unsigned>(order_grid(a.order))), dim3(256), 0, stream, a);
+  const int64_t tiles = a.order.tiles_m * a.order.tiles_n, whole = tiles & ~static_cast<int64_t>(255);
+  a.parts = a.off != nullptr || tiles - whole > 128 ? 1 : tiles - whole > 64 ? 2 : 4;
+  const int64_t grid = whole + a.parts * (order_grid(a.order) - whole);
+  GPTQ_LAUNCH(mx_big_kernel<KIND>, dim3(static_cast<unsigned>(grid)), dim3(256), 0, stream, a);
   return GPTQ_OK;
 }
 
