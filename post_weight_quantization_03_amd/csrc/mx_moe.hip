@@ -359,21 +359,29 @@ gptq_status launch_half(MlpArgs a, hipStream_t stream) {
   const int fixed = MLP_NW * DEPTH * NM * UNIT + GROUPS * NM * ((16 * kb + 1023) / 1024 * 1024) + 64 +
                     2 * (a.tokens + pairs);
   const int row = PLANES * (64 * kb + 16), most = std::min(16, a.tokens);
-  // an expert's weights are read again for every `cap` of its tokens: half as many again as it has on
-  // average should fit, else as many as leave room for two workgroups on a CU
-  const int want = std::min(most, 3 * pairs / (2 * a.experts) + 2);
-  a.cap = std::min(most, std::max((MLP_LDS - fixed) / row, std::min(want, (MLP_MOST_LDS - fixed) / row)));
+  // An expert's weights are read again for every `cap` of its tokens.  Two workgroups on a CU are worth more
+  // than room for the few experts that have more tokens than the average and its square root (64 tokens, 6 of
+  // 64 experts, d = 2048: 9 at a time 117 us, 11 with one workgroup 133), but less than room for more of them
+  // (32 tokens, 2 of 8, d = 4096: 8 at a time 88 us, 14 80; 8 tokens, 2 of 8, inner = 2816: 3 28 us, 5 25).
+  const int fit = (MLP_LDS - fixed) / row, want = 3 * pairs / (2 * a.experts) + 2;
+  const double spare = fit - static_cast<double>(pairs) / a.experts;
+  const bool enough = spare >= 0 && spare * spare * a.experts >= pairs;
+  a.cap = std::min(most, enough ? fit : std::max(fit, std::min(want, (MLP_MOST_LDS - fixed) / row)));
   if (a.cap < 1) return GPTQ_ERR_UNSUPPORTED;
   GPTQ_LAUNCH((mlp_kernel<UP, KS, KIND>), dim3(static_cast<unsigned>(slots * ((tiles + GROUPS - 1) / GROUPS))), dim3(MLP_NT),
               static_cast<size_t>(fixed) + a.cap * row, stream, a);
   return GPTQ_OK;
 }
-// Waves share a tile's inputs where that many tiles would leave waves without one (4 workgroups of 4
-// waves for each CU), and where one tile's scales for each wave would take too much LDS.
+// Waves share a tile's inputs where there are fewer tiles than waves (4 workgroups of 4 for each CU), and
+// where one tile's scales for each wave would take too much LDS: 4 where an expert has one token, else 2, whose
+// tiles share the tokens' rows (16 tokens, 2 of 8 experts, 1408 x 2048: 28 us, 24 so; one token, 6 of 64: 17.5, 17).
 template <bool UP, int KIND>
 gptq_status launch_half(const MlpArgs& a, hipStream_t stream) {
-  const int64_t tiles = static_cast<int64_t>(std::min(a.experts, a.tokens * a.top_k)) * (UP ? a.inner / 16 : a.d / 32);
-  if (tiles <= 1024 || (UP ? a.d : a.inner) > 4096) return launch_half<UP, 4, KIND>(a, stream);
+  const int pairs = a.tokens * a.top_k;
+  const int64_t tiles = static_cast<int64_t>(std::min(a.experts, pairs)) * (UP ? a.inner / 16 : a.d / 32);
+  const bool long_rows = (UP ? a.d : a.inner) > 4096;
+  if (long_rows || tiles <= (pairs <= a.experts ? 1024 : 384)) return launch_half<UP, 4, KIND>(a, stream);
+  if (tiles <= 1024) return launch_half<UP, 2, KIND>(a, stream);
   return launch_half<UP, 1, KIND>(a, stream);
 }
 
