@@ -484,15 +484,16 @@ gptq_status gptq_mxfp4_dequantize(int64_t rows, int cols, const uint8_t* Q, cons
  *   GPTQ_E2M1           x = xs[r, b] * xq[r, c]; ldx counts bytes (>= d_in / 2, ldx % 16 == 0), row r's
  *                       scales start at x_scales + r * ld_xs_row (>= d_in / 32)
  *   GPTQ_BF16, GPTQ_F16 x itself, not rounded; ldx % 8 == 0, ldx >= d_in; x_scales and its stride are
- *                       ignored.  fp16 takes two matrix products where bf16 takes one
+ *                       ignored.  fp16 beside weight scales below 2^-23 or above 2^13 takes two
+ *                       matrix products where one does otherwise, with the same accuracy
  * Y [m, d_out] fp32, bf16 or fp16, row stride ldy (>= d_out).  Products are exact and sums fp32 for
  * every type of Y.  A product of two scales, and with 16-bit X a weight, has to lie in fp32's normal
  * range to count in full (a weight of 2^128 or more is infinite).  workspace:
  * gptq_workspace_size(GPTQ_WS_MXFP4_MATMUL, batch = 1, d_out, d_in, n_tokens_hint = m, NULL) bytes,
  * 16-byte aligned (sums of parts of the inputs, or 4-bit operands' scales in the order of the largest
- * tiles; where that is 256 the call keeps nothing there and takes NULL); it serves one call at a time.  Requires d_in % 32 == 0, d_out >= 1; m may be 0 (no-op); more
- * than 2^22 tiles of the kernel that fits the sizes (16 x 16 to 256 x 256 outputs) are refused
- * (GPTQ_ERR_UNSUPPORTED).
+ * tiles; where that is 256 the call keeps nothing there and takes NULL); it serves one call at a time.
+ * Requires d_in % 32 == 0, d_out >= 1; m may be 0 (no-op); more than 2^22 tiles of the kernel that fits
+ * the sizes (16 x 16 to 256 x 256 outputs) are refused (GPTQ_ERR_UNSUPPORTED).
  */
 gptq_status gptq_mxfp4_matmul(int64_t m, int d_out, int d_in, gptq_dtype x_dtype, const void* X,
                               int64_t ldx, const uint8_t* x_scales, int64_t ld_xs_row,
@@ -523,9 +524,9 @@ gptq_status gptq_mxfp4_matmul_grouped(int batch, int64_t x_rows, int64_t n_rows,
  *   g, u      = the first and the last `inner` of W1[e] x[t]
  *   out[t, :] = sum over j of weights[t, j] * W2[e] (act(g) * u),   e = ids[t, j]
  * with act 0: g / (1 + exp(-g)); 1: 0.5 g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))).
- * X [n_tokens, d_in] bf16 or fp16, 16-byte aligned, row stride ldx (a multiple of 8); ids int32 and weights fp32 [n_tokens, top_k],
- * dense (as written by gptq_moe_route; an id outside [0, n_experts) is no choice, an expert named
- * twice by a token counts with both weights); W1 e2m1 [n_experts, 2 inner, d_in / 2] (gate rows, then
+ * X [n_tokens, d_in] bf16 or fp16, 16-byte aligned, row stride ldx (a multiple of 8); ids int32 and
+ * weights fp32 [n_tokens, top_k], dense (as written by gptq_moe_route; an id outside [0, n_experts) is
+ * no choice, an expert named twice by a token counts with both weights); W1 e2m1 [n_experts, 2 inner, d_in / 2] (gate rows, then
  * up rows) with scales [n_experts, 2 inner, d_in / 32], W2 [n_experts, d_in, inner / 2] with scales
  * [n_experts, d_in, inner / 32], dense and all four 16-byte aligned; out [n_tokens, d_in] of X's type,
  * row stride ldo, zeros for a token without choices.  X is not rounded, sums are fp32, and the
@@ -550,8 +551,8 @@ gptq_status gptq_mxfp4_moe_mlp(int64_t n_tokens, int top_k, int n_experts, int d
  * of activation rows m and p->group_size the group size (-1: one grid per row); for
  * GPTQ_WS_FP8_MATMUL and GPTQ_WS_FP8_GROUPED `n_tokens_hint` is the number of rows of X; for
  * GPTQ_WS_MOE_GROUP `d_out` is n_experts and `d_in` is top_k; for GPTQ_WS_MXFP4_MATMUL
- * `n_tokens_hint` is m, for GPTQ_WS_MXFP4_GROUPED n_rows, and for GPTQ_WS_MXFP4_MOE_MLP `d_out` is inner and `n_tokens_hint` the number
- * of choices; for the other calls it is ignored. */
+ * `n_tokens_hint` is m, for GPTQ_WS_MXFP4_GROUPED n_rows, and for GPTQ_WS_MXFP4_MOE_MLP `d_out` is
+ * inner and `n_tokens_hint` the number of choices; for the other calls it is ignored. */
 size_t gptq_workspace_size(gptq_ws_call which, int batch, int d_out, int d_in,
                            int64_t n_tokens_hint, const gptq_params* p);
 

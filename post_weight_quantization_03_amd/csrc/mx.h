@@ -54,7 +54,8 @@ struct ScaleRange {
   typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
   u16x2 least = {127, 127}, most = {127, 127};
   __device__ __forceinline__ void add(uint32_t codes) {
-    const u16x2 even = __builtin_bit_cast(u16x2, codes & 0x00FF00FFu), odd = __builtin_bit_cast(u16x2, codes >> 8 & 0x00FF00FFu);
+    const u16x2 even = __builtin_bit_cast(u16x2, codes & 0x00FF00FFu);
+    const u16x2 odd = __builtin_bit_cast(u16x2, codes >> 8 & 0x00FF00FFu);
     least = __builtin_elementwise_min(least, __builtin_elementwise_min(even, odd));
     most = __builtin_elementwise_max(most, __builtin_elementwise_max(even, odd));
   }

@@ -10,7 +10,8 @@
 // 2^6 and their sums within a block are exact; with scales apart by up to 2^40 a result is within
 // 2^-23.3 of sum |x q| (by experiment): fp32 sums, for every type of Y.
 // 16-bit activations: the weights become bf16 in registers, exactly, in front of
-// v_mfma_f32_16x16x32_bf16 with fp32 sums.
+// v_mfma_f32_16x16x32_bf16 with fp32 sums; beside fp16 activations they become fp16 where their scales
+// allow it, else the activations go as two bf16 numbers each (333 x 1416 x 2016 25 us so, 14 as fp16).
 // Weights are the first operand and activations the second: a lane then holds one activation row
 // and 4 consecutive outputs, which are stored together.
 #include <algorithm>
@@ -43,7 +44,8 @@ __device__ __forceinline__ uint32_t mx_scale(uint32_t top) {
 
 // Four lanes per block, 8 values each; a workgroup takes 2^shift blocks of 64 >> shift rows.  The
 // conversion rounds x / scale to nearest even and cuts at 6 (by experiment at all ties, also where
-// the scale is 2^-126 and x subnormal).  Bound by memory.
+// the scale is 2^-126 and x subnormal).  Bound by memory: 32768 x 8192 bf16 132 us, 5.1 TB/s, which is a
+// large copy's rate; 16 x 4096 2.2 us, a launch.
 template <typename T, bool CEIL>
 __global__ __launch_bounds__(256) void mx_quant_kernel(MxQuantArgs a) {
   const int u = threadIdx.x >> 2, part = threadIdx.x & 3;
@@ -78,7 +80,7 @@ struct MxDequantArgs {
   int shift;
 };
 
-// The values back, split like the rounding.  Bound by memory.
+// The values back, split like the rounding.  Bound by memory: 32768 x 8192 to bf16 130 us, 5.2 TB/s.
 template <typename T>
 __global__ __launch_bounds__(256) void mx_dequant_kernel(MxDequantArgs a) {
   const int u = threadIdx.x >> 2, part = threadIdx.x & 3;
@@ -88,8 +90,9 @@ __global__ __launch_bounds__(256) void mx_dequant_kernel(MxDequantArgs a) {
   const int col = b * MXB + part * 8;
   const uint32_t w = *reinterpret_cast<const uint32_t*>(a.Q + row * (a.cols / 2) + col / 2);
   const float s = __uint_as_float(static_cast<uint32_t>(a.S[row * a.kb + b]) << 23);
-  const f32x2 v[4] = {__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, s, 0), __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, s, 1),
-                      __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, s, 2), __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, s, 3)};
+  const f32x2 v[4] = {
+      __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, s, 0), __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, s, 1),
+      __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, s, 2), __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, s, 3)};
   Vec<T, 8> o;
 #pragma unroll
   for (int i = 0; i < 8; ++i) o.v[i] = from_f32<T>(v[i / 2][i & 1]);
@@ -137,6 +140,11 @@ struct MxArgs : MmArgs {
 // of 16 NM outputs, KS waves of it share a tile's inputs.  All comes by copies to LDS: the rows at once,
 // and weights in units of 256 inputs, up to DEPTH of them in a ring of each wave's own, so that nothing but
 // the matrix instruction's own reads goes through registers.  The waves' sums are added in their order.
+// Bound by reading the weights: one row of 4096 x 14336 9.4 us (31 MB: 3.3 TB/s from the launch on; 12.7 with
+// loads to registers), 16 tokens with 6 of 64 experts of 1408 x 2048 13.8 us (5.6 TB/s, part of it from the
+// last-level cache; 26 with loads to registers).  8 waves share a tile of 16 outputs; where there are many
+// tiles 4 waves take one of 32 outputs each, so that 8 times the outputs share the rows of X (these 16 tokens:
+// 17 us with the fastest other form).
 constexpr int UNIT = 2048;   // bytes of a unit of 16 outputs: 8 blocks each
 template <int NW, int KS, int NM, int DEPTH, int KIND>
 __global__ __launch_bounds__(NW * 64) void mx_few_kernel(MxArgs a) {
@@ -190,7 +198,8 @@ __global__ __launch_bounds__(NW * 64) void mx_few_kernel(MxArgs a) {
     // the outputs' scales are one piece of memory a tile
     const int g = tid / (NW * 64 / GROUPS), at = tid % (NW * 64 / GROUPS);   // this wave's own tile
     const int have = max(0, min(16 * NM, a.n - 16 * NM * (tile0 + g))) * kb;
-    const uint8_t* from = static_cast<const uint8_t*>(a.ws) + (static_cast<int64_t>(t.e) * a.n + 16 * NM * (tile0 + g)) * kb;
+    const uint8_t* from =
+        static_cast<const uint8_t*>(a.ws) + (static_cast<int64_t>(t.e) * a.n + 16 * NM * (tile0 + g)) * kb;
     for (int i = 16 * at; i < have; i += 16 * (NW * 64 / GROUPS)) {
       uint8_t v[16];
       if (i + 16 <= have) {
@@ -314,10 +323,13 @@ struct MxStage {
   }
 };
 
-// Tiles of TM rows x TN outputs, 2 x 2 waves (1 x 4 where it is wider than high), NB buffers, NB - 1 stages of copies on the way.  The
-// scales of up to PB blocks are in LDS before their first stage, so that the loop has no loads but copies
-// and can wait for them by their number.  gridDim.y parts of the inputs: few tiles would leave most of the
-// chip idle (sums of parts are added by mx_sum_kernel).
+// Tiles of TM rows x TN outputs, 2 x 2 waves (1 x 4 where it is wider than high), NB buffers, NB - 1 stages of
+// copies on the way.  The scales of up to PB blocks are in LDS before their first stage, so that the loop has no
+// loads but copies and can wait for them by their number.  gridDim.y parts of the inputs: few tiles would leave
+// most of the chip idle (sums of parts are added by mx_sum_kernel).
+// Bound by the copies, which take two workgroups' 60 to 160 KB of LDS from L2 with a latency of 1 to 2 us: the
+// more outputs a tile has for its rows of 16 bits, the less is copied (4096 x 14336, 16-bit rows: 16 rows 32 x 128
+// 15 us, 64 x 64 18; 256 rows 64 x 128 45 us, 64 x 64 52; 1024 rows 64 x 128 132, 128 x 128 151).
 template <int TM, int TN, int XB, int NB, int KIND>
 __global__ __launch_bounds__(256) void mx_tile_kernel(MxArgs a) {
   typedef MxStage<KIND, XB> St;
@@ -328,7 +340,8 @@ __global__ __launch_bounds__(256) void mx_tile_kernel(MxArgs a) {
   // two workgroups on a CU: what the buffers leave of half its LDS is for scales
   constexpr int SROWS = KIND == kMx4 ? TM + TN : TN;
   constexpr int PB = std::min(256, ((80 * 1024 - 256 - NB * STAGE) / SROWS - 4) / 16 * 16), PITCH = PB + 4;
-  static_assert(LX >= 1 && PB >= 16 && LW >= 1 && TM % 32 == 0 && TN % (16 * WN) == 0 && SROWS <= 256 && PB % St::BLOCKS == 0, "tile shape");
+  static_assert(LX >= 1 && LW >= 1 && PB >= 16 && PB % St::BLOCKS == 0 && SROWS <= 256, "tile shape");
+  static_assert(TM % (16 * WM) == 0 && TN % (16 * WN) == 0, "tile shape");
   __shared__ __attribute__((aligned(128))) uint8_t lds[NB * STAGE];
   __shared__ __attribute__((aligned(16))) uint8_t scales[SROWS * PITCH];
   __shared__ bool lost[TM];
@@ -366,13 +379,15 @@ __global__ __launch_bounds__(256) void mx_tile_kernel(MxArgs a) {
   auto issue = [&](int s, int buffer) {
     const unsigned to = lds0 + buffer * STAGE + wave * 1024;
 #pragma unroll
-    for (int i = 0; i < LX; ++i)
-      copy16(static_cast<int64_t>(s) * XB + 16 * xc[i] < xbytes && xsrc[i] != nullptr ? xsrc[i] + static_cast<int64_t>(s) * XB : zeros,
-             to + NW * i * 1024);
+    for (int i = 0; i < LX; ++i) {
+      const int64_t at = static_cast<int64_t>(s) * XB;
+      copy16(at + 16 * xc[i] < xbytes && xsrc[i] != nullptr ? xsrc[i] + at : zeros, to + NW * i * 1024);
+    }
 #pragma unroll
-    for (int i = 0; i < LW; ++i)
-      copy16(static_cast<int64_t>(s) * St::WB + 16 * wc[i] < a.k / 2 ? wsrc[i] + static_cast<int64_t>(s) * St::WB : zeros,
-             to + TM * XB + NW * i * 1024);
+    for (int i = 0; i < LW; ++i) {
+      const int64_t at = static_cast<int64_t>(s) * St::WB;
+      copy16(at + 16 * wc[i] < a.k / 2 ? wsrc[i] + at : zeros, to + TM * XB + NW * i * 1024);
+    }
   };
 
   const int wm = wave / WN, wn = wave % WN;
@@ -450,7 +465,8 @@ __global__ __launch_bounds__(256) void mx_tile_kernel(MxArgs a) {
               const int sx = sc[(wm * XW + 16 * i + j) * PITCH + 4 * h + q];
 #pragma unroll
               for (int f = 0; f < FN; ++f)
-                y[i][f] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(widen(w4[f]), widen(v), y[i][f], 4, 4, 0, sw[f], 0, sx);
+                y[i][f] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(widen(w4[f]), widen(v), y[i][f], 4, 4, 0,
+                                                                           sw[f], 0, sx);
             } else {
               const XValues<kKind> xv(v);
 #pragma unroll
@@ -488,9 +504,12 @@ __global__ __launch_bounds__(256) void mx_tile_kernel(MxArgs a) {
 }
 
 // The same product for large problems: 256 x 256 tiles, 4 waves of 128 x 128 (8 x 8 blocks of 16 x 16),
-// one workgroup per CU.  Bound by the matrix cores.  Two buffers; a stage is 128 bytes of every row of X,
-// two instructions for a block (four for fp16), here together called a product.  Operands go global -> LDS
-// with a scalar base that moves by a stage and one 32-bit offset per lane and copy.  Before a wave's last
+// one workgroup per CU.  Bound by the matrix cores: 8192 x 4096 x 14336 of 4-bit rows 204 us, 4.7 PFLOP/s (on
+// another card 221, and 169 without copies, scales and stores; the cores are busy 55% of the time),
+// 4096 x 14336 x 4096 of 16-bit rows 370 us, 1.30 PFLOP/s, where the library's large bf16 product reaches
+// 1.36 (without the weights' conversion it is no faster).  Two buffers; a stage is 128 bytes of every row of
+// X, two instructions for a block (four for fp16 as two bf16), here together called a product.  Operands go
+// global -> LDS with a scalar base that moves by a stage and one 32-bit offset per lane and copy.  Before a wave's last
 // three rows of blocks it has read all it needs of the stage: there the workgroup waits for the next stage's
 // copies, and the products of these rows cover the first reads of the next stage and half of the copies
 // of the one after it; the other half goes out with the next stage's first products.
@@ -525,7 +544,7 @@ __device__ __forceinline__ void big_product(const BigW<KIND>& w, const BigX<KIND
 // The scales of 4-bit operands stage by stage, for this kernel: 8 codes of every output row [stages][mp]
 // and of every output [experts][stages][np], those behind the last block 1, in the order 0 4 1 5 2 6 3 7, so
 // that a lane's two are neighbours.  (Read where they are, 8 bytes a stage come out of lines of 128, which
-// doubles what a CU reads: 8192 x 4096 x 14336 286 us, 221 so, this kernel in it.)
+// doubles what a CU reads: 8192 x 4096 x 14336 286 us, 221 so, this kernel's 7 in it.)
 constexpr int GATHER = 8;   // stages of a thread
 __global__ __launch_bounds__(256) void mx_gather_scales_kernel(MxArgs a) {
   const int64_t g = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
@@ -557,7 +576,8 @@ __global__ __launch_bounds__(256) void mx_gather_scales_kernel(MxArgs a) {
         else v[1] ^= c;
       }
     }
-    to[s * step] = make_uint2(__builtin_amdgcn_perm(v[1], v[0], 0x05010400u), __builtin_amdgcn_perm(v[1], v[0], 0x07030602u));
+    to[s * step] =
+        make_uint2(__builtin_amdgcn_perm(v[1], v[0], 0x05010400u), __builtin_amdgcn_perm(v[1], v[0], 0x07030602u));
   }
 }
 
@@ -575,15 +595,18 @@ __device__ __forceinline__ void big_tile(const MxArgs& a, const Tile& t, int n0,
   const uint8_t* xbase = a.X + (a.rows == nullptr ? t.p0 * a.ldx : 0);
   const uint8_t* wbase = a.W + (static_cast<int64_t>(t.e) * a.n + n0) * (a.k / 2);
   // this lane's pieces: the same in every copy of X, and of W; whether they lie past K in the last stage
-  const int cx = St::x_at(8 * wave + lane / 8, lane & 7), cw = St::w_at(WROWS * wave + lane / (St::WB / 16), lane % (St::WB / 16));
-  const bool cut_x = (stages - 1) * 128 + 16 * cx >= (F4 ? a.k / 2 : 2 * a.k), cut_w = (stages - 1) * St::WB + 16 * cw >= a.k / 2;
+  const int cx = St::x_at(8 * wave + lane / 8, lane & 7);
+  const int cw = St::w_at(WROWS * wave + lane / (St::WB / 16), lane % (St::WB / 16));
+  const bool cut_x = (stages - 1) * 128 + 16 * cx >= (F4 ? a.k / 2 : 2 * a.k);
+  const bool cut_w = (stages - 1) * St::WB + 16 * cw >= a.k / 2;
   uint32_t off[LD];
 #pragma unroll
   for (int i = 0; i < LD; ++i) {
     if (i < LX) {
       const int r = (wave + NW * i) * 8 + lane / 8;
       const int64_t row = source_row(a, t.p0 + min(r, t.count - 1));   // none: row 0, and zeros at the end
-      off[i] = static_cast<uint32_t>(max(a.rows == nullptr ? row - t.p0 : row, static_cast<int64_t>(0)) * a.ldx) + 16 * cx;
+      const int64_t from = max(a.rows == nullptr ? row - t.p0 : row, static_cast<int64_t>(0));
+      off[i] = static_cast<uint32_t>(from * a.ldx) + 16 * cx;
     } else {
       const int r = (wave + NW * (i - LX)) * WROWS + lane / (St::WB / 16);
       off[i] = static_cast<uint32_t>(min(r, a.n - 1 - n0)) * static_cast<uint32_t>(a.k / 2) + 16 * cw;
@@ -596,7 +619,8 @@ __device__ __forceinline__ void big_tile(const MxArgs& a, const Tile& t, int n0,
   const uint8_t* const wsrow =
       static_cast<const uint8_t*>(a.ws) + (static_cast<int64_t>(t.e) * a.n + min(n0 + tid, a.n - 1)) * a.kb;
   uint32_t sw_next = 0;
-  const unsigned scs0 = static_cast<unsigned>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint2*)scs));
+  const unsigned scs0 = static_cast<unsigned>(reinterpret_cast<uintptr_t>(
+      (__attribute__((address_space(3))) uint2*)scs));
   const unsigned lds0 = static_cast<unsigned>(reinterpret_cast<uintptr_t>(
       (__attribute__((address_space(3))) uint8_t*)lds));
   auto issue_scales = [&](int s) {
@@ -635,9 +659,10 @@ __device__ __forceinline__ void big_tile(const MxArgs& a, const Tile& t, int n0,
     if (last) {
 #pragma unroll
       for (int i = 0; i < LD; ++i)
-        if (i < LX ? cut_x : cut_w)
-          *reinterpret_cast<uint4*>(lds + (s & 1) * STAGE + wave * 1024 +
-                                    (i < LX ? NW * i * 1024 : XR * 128 + NW * (i - LX) * 1024) + 16 * lane) = make_uint4(0, 0, 0, 0);
+        if (i < LX ? cut_x : cut_w) {
+          const int at = i < LX ? NW * i * 1024 : XR * 128 + NW * (i - LX) * 1024;
+          *reinterpret_cast<uint4*>(lds + (s & 1) * STAGE + wave * 1024 + at + 16 * lane) = make_uint4(0, 0, 0, 0);
+        }
     }
     if constexpr (!F4)
       reinterpret_cast<uint16_t*>(scs)[(s & 1) * BIG + tid] =
@@ -683,10 +708,12 @@ __device__ __forceinline__ void big_tile(const MxArgs& a, const Tile& t, int n0,
   // Products of a stage: rows of blocks one after another, then the last three together, output block by
   // output block.
   constexpr int LAST = 3, SPLIT = (FM - LAST) * FN;   // rows taken together, products before them
-  constexpr int EARLY = LAST * FN / 2 < LD ? LAST * FN / 2 : LD;   // copies issued with them, one after every second product
+  // copies issued with them, one after every second product
+  constexpr int EARLY = LAST * FN / 2 < LD ? LAST * FN / 2 : LD;
   // the barrier keeps everything in the order written
   auto product = [&](auto P) {
-    constexpr int p = P, i = p < SPLIT ? p / FN : FM - LAST + (p - SPLIT) % LAST, h = p < SPLIT ? p % FN : (p - SPLIT) / LAST;
+    constexpr int p = P, i = p < SPLIT ? p / FN : FM - LAST + (p - SPLIT) % LAST;
+    constexpr int h = p < SPLIT ? p % FN : (p - SPLIT) / LAST;
     big_product<KIND>(wf[h], xf[i % 4], y[i][h]);
     __builtin_amdgcn_sched_barrier(0);
   };
@@ -851,7 +878,8 @@ __global__ __launch_bounds__(256) void mx_big_kernel(MxArgs a) {
   }
 }
 
-// Y from the sums of the parts, in their order, all loads at once.
+// Y from the sums of the parts, in their order, all loads at once (8 parts of 64 x 4096: 4 us, mostly a
+// launch's; 18 with a loop of loads).
 template <int SPLITS>
 __global__ __launch_bounds__(256) void mx_sum_kernel(MxArgs a) {
   const int row = blockIdx.y, o = (blockIdx.x * 256 + threadIdx.x) * 4, n = min(4, a.n - o);
@@ -953,7 +981,8 @@ MxPlan mx_plan(int64_t m, int n, int k, int kind, bool grouped, int experts) {
   const int64_t most = std::min<int64_t>(16, m);
   const int64_t want = std::min<int64_t>(most, static_cast<int64_t>(grouped ? 1.5 * rows + 2 : m));
   const int64_t fit = (FEW_LDS - few_fixed(kb, wide)) / few_row(kb, kind);
-  const int64_t cap = std::min(most, std::max(fit, std::min(want, (FEW_MOST_LDS - few_fixed(kb, wide)) / few_row(kb, kind))));
+  const int64_t alone = (FEW_MOST_LDS - few_fixed(kb, wide)) / few_row(kb, kind);
+  const int64_t cap = std::min(most, std::max(fit, std::min(want, alone)));
   if (cap >= 1 && rows <= 16) {
     const int outputs = wide ? 128 : 16;
     const double groups = std::max(1.0, used * ((n + outputs - 1) / outputs) / CUS);
@@ -1038,8 +1067,8 @@ gptq_status launch_mx_big(MxArgs a, void* workspace, hipStream_t stream) {
     a.xst = static_cast<uint2*>(workspace);
     a.wst = a.xst + a.stages * a.mp;
     const int64_t rows = a.mp + static_cast<int64_t>(a.experts) * a.np;
-    GPTQ_LAUNCH(mx_gather_scales_kernel, dim3(static_cast<unsigned>((rows + 255) / 256), (a.stages + GATHER - 1) / GATHER),
-                dim3(256), 0, stream, a);
+    const dim3 g(static_cast<unsigned>((rows + 255) / 256), (a.stages + GATHER - 1) / GATHER);
+    GPTQ_LAUNCH(mx_gather_scales_kernel, g, dim3(256), 0, stream, a);
   }
   const int64_t tiles = a.order.tiles_m * a.order.tiles_n, whole = tiles & ~static_cast<int64_t>(255);
   a.parts = a.off != nullptr || tiles - whole > 128 ? 1 : tiles - whole > 64 ? 2 : 4;
@@ -1051,7 +1080,8 @@ gptq_status launch_mx_big(MxArgs a, void* workspace, hipStream_t stream) {
 template <int KIND>
 gptq_status launch_mx(const MxArgs& a, const MxPlan& p, void* workspace, hipStream_t stream) {
   if (p.kind == kMxFew)
-    return p.wide ? launch_mx_few<4, 1, 2, WIDE_DEPTH, KIND>(a, p, stream) : launch_mx_few<8, 8, 1, FEW_DEPTH, KIND>(a, p, stream);
+    return p.wide ? launch_mx_few<4, 1, 2, WIDE_DEPTH, KIND>(a, p, stream)
+                  : launch_mx_few<8, 8, 1, FEW_DEPTH, KIND>(a, p, stream);
   if (p.kind == kMxBig) return launch_mx_big<KIND>(a, workspace, stream);
   if (p.kind == kMxTile32) return launch_mx_tile<kMxTile32, KIND>(a, p, workspace, stream);
   if constexpr (KIND != kMx4)

@@ -846,8 +846,8 @@ def mxfp4_matmul_grouped(X: torch.Tensor, qweight: torch.Tensor, w_scales: torch
     n_rows = x_rows if row_index is None else row_index.numel()
     Y = _out(out, (n_rows, d_out), out_dtype, X.device)
     ws = _scratch(WS_MXFP4_GROUPED, experts, d_out, d_in, n_rows, X.device, workspace)
-    _run("gptq_mxfp4_matmul_grouped", (X, qweight, w_scales, token_offsets, row_index, x_scales, Y, ws), experts, x_rows,
-         n_rows, d_out, d_in, code, X.data_ptr(), _row_stride(X), _ptr(x_scales),
+    _run("gptq_mxfp4_matmul_grouped", (X, qweight, w_scales, token_offsets, row_index, x_scales, Y, ws), experts,
+         x_rows, n_rows, d_out, d_in, code, X.data_ptr(), _row_stride(X), _ptr(x_scales),
          0 if x_scales is None else _row_stride(x_scales), qweight.data_ptr(), w_scales.data_ptr(),
          token_offsets.data_ptr(), _ptr(row_index), _DT[out_dtype], Y.data_ptr(), _row_stride(Y), _ptr(ws), _bytes(ws))
     return Y

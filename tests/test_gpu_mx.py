@@ -409,7 +409,8 @@ def check_large(Y, x, w, k, kind, out):
     (4090, 4095, 1056, "bf16"), (3900, 4000, 416, "f32"), (8192, 8192, 256, "bf16"), (8192, 8192, 128, "bf16"),
     (8192, 8100, 96, "f16"), (2050, 2050, 672, "f32"), (4096, 4096, 288, "f32"), (1027, 4096, 2080, "bf16"),
     (513, 2304, 1056, "f32"), (65, 200, 1056, "f32"), (300, 640, 896, "bf16"), (64, 4096, 14336, "bf16"),
-    (300, 4096, 7808, "f32"), (4353, 4225, 704, "bf16"), (8200, 8256, 32, "bf16"), (20, 16000, 512, "f32"), (3600, 4180, 1056, "bf16"), (3601, 4177, 1312, "f32"),
+    (300, 4096, 7808, "f32"), (4353, 4225, 704, "bf16"), (8200, 8256, 32, "bf16"), (20, 16000, 512, "f32"),
+    (3600, 4180, 1056, "bf16"), (3601, 4177, 1312, "f32"),
     (3583, 4225, 1024, "f16"), (30, 4160, 4128, "f32"), (24, 1000, 14336, "bf16"),
     (1990, 4000, 2080, "bf16"), (1990, 4050, 2112, "f32"), (1000, 4000, 4128, "f16"), (1000, 3900, 4096, "bf16"),
     (4200, 4010, 1056, "bf16"), (129, 32700, 1056, "bf16"), (4300, 16500, 288, "bf16")])
