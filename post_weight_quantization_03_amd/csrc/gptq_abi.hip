@@ -468,8 +468,9 @@ gptq_status gptq_mxfp4_moe_mlp(int64_t n_tokens, int top_k, int n_experts, int d
   if (X == nullptr || ids == nullptr || weights == nullptr || W1 == nullptr || w1_scales == nullptr || W2 == nullptr ||
       w2_scales == nullptr || out == nullptr || ldx < d_in || ldo < d_in)
     return GPTQ_ERR_INVALID_ARG;
-  if (ldx % 8 != 0 || !aligned(X, 16) || !aligned(out, 2) || !aligned(w1_scales, 16) || !aligned(w2_scales, 16) || !aligned(ids, 4) || !aligned(weights, 4) || !aligned(W1, 16) ||
-      !aligned(W2, 16) || !aligned(workspace, 16))
+  if (ldx % 8 != 0 || !aligned(X, 16) || !aligned(out, 2) || !aligned(ids, 4) || !aligned(weights, 4) ||
+      !aligned(W1, 16) || !aligned(w1_scales, 16) || !aligned(W2, 16) || !aligned(w2_scales, 16) ||
+      !aligned(workspace, 16))
     return GPTQ_ERR_INVALID_ARG;
   const gptq::MxMlp p{static_cast<int>(n_tokens), top_k, n_experts, d_in, inner, x_dtype == GPTQ_BF16, X, ldx, ids,
                       weights, W1, w1_scales, W2, w2_scales, activation, out, ldo, workspace, workspace_bytes};

@@ -931,6 +931,14 @@ int64_t few_row(int kb, int kind) {
   return kind == kMx4 ? 16 * static_cast<int64_t>(kb) + 16 + (kb + 3) / 4 * 4 : 64 * static_cast<int64_t>(kb) + 16;
 }
 
+// Whether the launch is one the kernels number their tiles for; experts 0: not grouped.
+bool mx_launchable(int64_t m, int n, int experts, const MxPlan& p) {
+  const int tm = p.kind == kMxFew ? p.cap : tile_rows_of(p.kind);
+  const int tn = p.kind == kMxFew ? 16 : tile_outputs(p.kind);
+  const int64_t rows = experts == 0 ? (m + tm - 1) / tm : m / tm + std::min<int64_t>(experts, m);
+  return rows <= (1 << 22) / ((n + tn - 1) / tn);
+}
+
 // What a kernel takes, in us, as measured on the card (two sides of each choice below): the start of a launch
 // and its loop, and its stages of 128 inputs of 16-bit rows or 256 of 4-bit ones where a CU has one workgroup
 // and where it has as many as it holds.
@@ -974,7 +982,7 @@ MxPlan mx_plan(int64_t m, int n, int k, int kind, bool grouped, int experts) {
   MxPlan best{kMxTile64, 1, 0, false};
   double least = 1e30;
   auto take = [&](const MxPlan& p, double t) {
-    if (t < least) least = t, best = p;
+    if (t < least && mx_launchable(m, n, grouped ? experts : 0, p)) least = t, best = p;
   };
   // few rows: as many a tile as LDS holds with two workgroups on a CU, or one if that spares reading weights twice
   const bool wide = kb <= 128 && used * ((n + 15) / 16) > 1024;
@@ -1090,13 +1098,6 @@ gptq_status launch_mx(const MxArgs& a, const MxPlan& p, void* workspace, hipStre
   return launch_mx_tile<kMxTile128, KIND>(a, p, workspace, stream);
 }
 
-// Whether the launch is one the kernels number their tiles for.
-bool mx_launchable(const MxArgs& a, const MxPlan& p) {
-  const int tm = p.kind == kMxFew ? p.cap : tile_rows_of(p.kind);
-  const int tn = p.kind == kMxFew ? 16 : tile_outputs(p.kind);
-  return tile_rows(a, tm) <= (1 << 22) / ((a.n + tn - 1) / tn);
-}
-
 }  // namespace
 
 gptq_status mx_quantize_enqueue(int batch, int64_t rows, int cols, gptq_dtype x_dtype, const void* X, int64_t ldx,
@@ -1122,8 +1123,10 @@ gptq_status mx_dequantize_enqueue(int64_t rows, int cols, const uint8_t* Q, cons
   return GPTQ_OK;
 }
 
+constexpr int MX_OUTPUTS = 1 << 30;
 size_t mx_workspace(int batch, bool grouped, int64_t m, int n, int k) {
   size_t most = 256;
+  if (m < 1 || n > MX_OUTPUTS) return most;   // nothing is launched
   for (const int kind : {kMx4, kMxBf16})
     most = std::max(most, mx_plan_bytes(mx_plan(m, n, k, kind, grouped, batch), m, n, k, kind, batch));
   return most;
@@ -1138,13 +1141,13 @@ gptq_status mx_matmul_enqueue(const MxProblem& p, hipStream_t stream) {
   a.xs = p.xs; a.xsr = p.xsr;
   const int kind = p.x_dtype == GPTQ_E2M1 ? kMx4 : p.x_dtype == GPTQ_BF16 ? kMxBf16 : kMxF16;
   a.ldx = kind == kMx4 ? p.ldx : 2 * p.ldx;
-  if (a.off != nullptr && (a.m / 16 + 1) * a.experts > INT32_MAX) return GPTQ_ERR_UNSUPPORTED;
+  if (a.n > MX_OUTPUTS || (a.off != nullptr && (a.m / 16 + 1) * a.experts > INT32_MAX)) return GPTQ_ERR_UNSUPPORTED;
   MxPlan plan = mx_plan(a.m, a.n, a.k, kind, a.off != nullptr, a.experts);
   // the largest tiles address a tile's rows by 32-bit offsets
   const int64_t span = a.rows == nullptr ? BIG * a.ldx : a.x_rows * a.ldx;
   if (plan.kind == kMxBig && (span > INT32_MAX || BIG * static_cast<int64_t>(a.k / 2) > INT32_MAX || a.x_rows == 0))
     plan.kind = kMxTile128;
-  if (!mx_launchable(a, plan)) return GPTQ_ERR_UNSUPPORTED;
+  if (!mx_launchable(a.m, a.n, a.off != nullptr ? a.experts : 0, plan)) return GPTQ_ERR_UNSUPPORTED;
   const size_t need = mx_plan_bytes(plan, a.m, a.n, a.k, kind, a.experts);
   if (need > 0 && (p.workspace == nullptr || p.workspace_bytes < need)) return GPTQ_ERR_WORKSPACE;
   if (kind == kMx4) return launch_mx<kMx4>(a, plan, p.workspace, stream);

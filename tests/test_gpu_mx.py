@@ -580,6 +580,50 @@ def test_captured_and_replayed(m):
         assert all(torch.equal(a, b) for a, b in zip(got, want)), i
 
 
+@pytest.mark.parametrize("grouped", [False, True])
+def test_largest_tiles_workspaces_streams_and_graphs(grouped):
+    # scales in tile order: stale bytes in the workspace, a workspace too small, two streams at once, replays
+    m, n, k, experts = 12000 if grouped else 3600, 4180, 1056, 2
+    q, s = random_operand(5, m, k, "mx")
+    w, ws = random_operand(6, n, k, "mx", (experts,))
+    cut = 7000
+    offsets = torch.tensor([0, cut, m], device="cuda")
+    rows = torch.randperm(m, generator=torch.Generator("cuda").manual_seed(1), device="cuda").int()
+    rows[7], rows[m - 1] = -1, m
+
+    def call(**kw):
+        if grouped:
+            return lib().mxfp4_matmul_grouped(q, w, ws, offsets, rows, s, **kw)
+        return lib().mxfp4_matmul(q, w[1], ws[1], s, **kw)
+    which = lib().WS_MXFP4_GROUPED if grouped else lib().WS_MXFP4_MATMUL
+    need = lib().workspace_size(which, experts if grouped else 1, n, k, m)
+    assert need >= 5 * 8 * (m + n)      # a byte per 32 inputs of a row, in stages of 256
+    Y = call()
+    if grouped:
+        x = wide(q, s)[rows.clamp(0, m - 1).long()]
+        x[7] = x[m - 1] = 0
+        for e, (a, b) in enumerate(((0, cut), (cut, m))):
+            check_large(Y[a:b], x[a:b], wide(w[e], ws[e]), k, "mx", "bf16")
+    else:
+        check_large(Y, wide(q, s), wide(w[1], ws[1]), k, "mx", "bf16")
+    scratch = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+    assert torch.equal(call(workspace=scratch), Y) and torch.equal(call(workspace=scratch[:need - 8]), Y)
+    sides = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [call(stream=side) for _ in range(3) for side in sides]
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, Y) for y in got)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = call(workspace=scratch)
+    for i in range(3):
+        s.add_(1)
+        scratch.fill_(255)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, call()), i
+
+
 # -------------------------------------------------------------------------- expert layer
 
 
@@ -617,7 +661,7 @@ def check_layer(out, x, ids, p, w1, w2, act, dtype):
 @pytest.mark.parametrize("tokens,k,experts,d,inner", [
     (1, 1, 1, 32, 32), (1, 6, 64, 256, 96), (1, 2, 8, 2080, 64), (3, 4, 4, 320, 160), (15, 3, 5, 96, 288), (16, 1, 3, 64, 32),
     (17, 8, 9, 128, 64), (32, 6, 33, 160, 96), (33, 2, 2, 64, 64), (64, 4, 40, 96, 416), (65, 2, 7, 64, 32), (200, 1, 3, 32, 64),
-    (5, 32, 1024, 32, 32), (40, 9, 3, 64, 32)])
+    (5, 32, 1024, 32, 32), (40, 9, 3, 64, 32), (12, 2, 6, 2080, 1056), (40, 2, 20, 1056, 992)])
 def test_layer(tokens, k, experts, d, inner, dtype, act):
     rng = np.random.default_rng(tokens + experts)
     x, ids, p, w, xv, wv = layer(rng, tokens, k, experts, d, inner, dtype)

@@ -90,6 +90,10 @@ def test_grouped_empty_and_too_large():
     a = {**GROUPED, "batch": 4, "xr": 8192, "rows": 8192, "n": 4096, "k": 2048, "ldx": 1024, "xsr": 64, "ldy": 4096}
     assert need > 256 and gptq.lib().gptq_mxfp4_matmul_grouped(*a.values()) == WS
     assert gptq.lib().gptq_mxfp4_matmul_grouped(*{**a, "wsp": 16, "wsb": need - 1}.values()) == WS
+    assert gptq.workspace_size(gptq.WS_MXFP4_GROUPED, 4, 4096, 2048, 0) == 256
+    assert gptq.workspace_size(gptq.WS_MXFP4_MATMUL, 1, 2 ** 31 - 1, 2048, 4) == 256     # refused by the call
+    a = {**GROUPED, "n": 2 ** 31 - 1, "ldy": 2 ** 31}
+    assert gptq.lib().gptq_mxfp4_matmul_grouped(*a.values()) == UNS
     for bad in ((0, 64, 128, 4), (2, 0, 128, 4), (2, 64, 100, 4), (2, 64, 128, -1)):
         assert gptq.workspace_size(gptq.WS_MXFP4_GROUPED, *bad) == 0
 
