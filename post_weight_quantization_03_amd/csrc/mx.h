@@ -97,6 +97,13 @@ __device__ __forceinline__ f32x4 mx_mma16(W w, const XValues<KIND>& x, f32x4 acc
   }
 }
 
+// A barrier for LDS alone, which loads and copies cross.
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
 __device__ __forceinline__ i32x8 widen(i32x4 v) { return i32x8{v[0], v[1], v[2], v[3], 0, 0, 0, 0}; }
 
 }  // namespace

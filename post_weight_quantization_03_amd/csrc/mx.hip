@@ -129,6 +129,7 @@ struct MxArgs : MmArgs {
   int splits, per;   // parts of the inputs, and their stages
   float* part;       // [splits][m][n] sums, where there is more than one
   int cap, slots;    // of the kernel for few rows: rows of a tile, units in a wave's ring
+  bool copied;       // and whether scales lie so that they can be copied to LDS
   uint2* xst;        // of the largest tiles: scales by stage
   uint2* wst;
   int64_t mp;        // and their rows
@@ -183,23 +184,46 @@ __global__ __launch_bounds__(NW * 64) void mx_few_kernel(MxArgs a) {
       copy16_at(w, off, ring0 + (k % DEPTH) * NM * UNIT + 1024 * i);
     }
   };
-  // rows and first weights, then the scales through registers: they may start at any byte
+  const int64_t row_j = source_row(a, t.p0 + min(j, t.count - 1));   // columns behind the last row repeat it
+  const bool lost = row_j < 0;
+  auto row_of = [&](int r) {
+    const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(row_j), r);
+    return static_cast<int64_t>(static_cast<uint64_t>(static_cast<uint32_t>(
+               __builtin_amdgcn_readlane(static_cast<int>(row_j >> 32), r))) << 32 | lo);
+  };
+  // rows, scales and first weights, in this order: the loop starts when the scales are there.  Scales that do not
+  // start at multiples of 16 bytes (of X: 4) go through registers, and the first weights are waited for with them.
   if (tid < 16) reinterpret_cast<uint32_t*>(zeros)[tid] = 0;
   const int chunks = (XP * kb + 63) / 64;
   for (int i = wave; i < t.count * chunks; i += NW) {
     const int r = i / chunks, c = i - r * chunks;
-    const int64_t row = uniform(source_row(a, t.p0 + r));
+    const int64_t row = row_of(r);
     if (row >= 0 && 64 * c + lane < XP * kb)
       copy16_at(a.X + row * a.ldx, 1024 * c + 16 * lane,
                 lds0 + static_cast<uint32_t>(xrows - few_lds) + r * pitch + 1024 * c);
   }
+  // the outputs' scales are one piece of memory a tile
+  const int have = max(0, min(16 * NM, a.n - n0)) * kb;
+  const uint8_t* const from = static_cast<const uint8_t*>(a.ws) + (static_cast<int64_t>(t.e) * a.n + n0) * kb;
+  if (a.copied) {
+    for (int c = wk; 1024 * c < have; c += KS)
+      if (1024 * c + 16 * lane < have)
+        copy16_at(from, 1024 * c + 16 * lane,
+                  lds0 + static_cast<uint32_t>(scales - few_lds) + group * scale_bytes + 1024 * c);
+    if constexpr (KIND == kMx4) {
+      const int parts = (kb / 4 + 63) / 64;
+      for (int i = wave; i < t.count * parts; i += NW) {
+        const int r = i / parts, c = i - r * parts;
+        const int64_t row = row_of(r);
+        if (row >= 0 && 64 * c + lane < kb / 4)
+          copy4(static_cast<const uint8_t*>(a.xs) + row * a.xsr + 256 * c + 4 * lane,
+                lds0 + static_cast<uint32_t>(xscales - few_lds) + r * xs_pitch + 256 * c);
+      }
+    }
+  }
   for (int k = 0; k < min(DEPTH, mine); ++k) issue(k);
-  {
-    // the outputs' scales are one piece of memory a tile
-    const int g = tid / (NW * 64 / GROUPS), at = tid % (NW * 64 / GROUPS);   // this wave's own tile
-    const int have = max(0, min(16 * NM, a.n - 16 * NM * (tile0 + g))) * kb;
-    const uint8_t* from =
-        static_cast<const uint8_t*>(a.ws) + (static_cast<int64_t>(t.e) * a.n + 16 * NM * (tile0 + g)) * kb;
+  if (!a.copied) {
+    const int g = group, at = tid % (NW * 64 / GROUPS);
     for (int i = 16 * at; i < have; i += 16 * (NW * 64 / GROUPS)) {
       uint8_t v[16];
       if (i + 16 <= have) {
@@ -224,10 +248,10 @@ __global__ __launch_bounds__(NW * 64) void mx_few_kernel(MxArgs a) {
         *reinterpret_cast<uint32_t*>(xscales + r * xs_pitch + b0) = *reinterpret_cast<const uint32_t*>(v);
       }
   }
-  wait_copies();   // the first units too: they were asked for before
-  __syncthreads();
-  const int jr = min(j, t.count - 1);   // columns behind the last row repeat it; nothing reads them
-  const bool lost = source_row(a, t.p0 + jr) < 0;
+  if (a.copied && mine >= DEPTH) wait_vmcnt<DEPTH * COPIES>();
+  else wait_copies();
+  lds_barrier();
+  const int jr = min(j, t.count - 1);
   const uint8_t* const x = xrows + jr * pitch;
   const uint8_t* const scale = scales + group * scale_bytes;
   f32x4 y[NM];
@@ -281,7 +305,7 @@ __global__ __launch_bounds__(NW * 64) void mx_few_kernel(MxArgs a) {
   };
   if constexpr (KIND == kMxF16) {
     ScaleRange range;   // of this wave's tile
-    for (int i = 16 * lane, have = max(0, min(16 * NM, a.n - n0)) * kb; i < have; i += 1024) {
+    for (int i = 16 * lane; i < have; i += 1024) {
       const uint4 v = *reinterpret_cast<const uint4*>(scale + i);
       range.add(v.x), range.add(v.y), range.add(v.z), range.add(v.w);
     }
@@ -1038,6 +1062,8 @@ gptq_status launch_mx_few(MxArgs a, const MxPlan& p, hipStream_t stream) {
   constexpr int OUTPUTS = NW / KS * NM * 16;
   a.tiles_n = (a.n + OUTPUTS - 1) / OUTPUTS;
   a.cap = p.cap;
+  a.copied = reinterpret_cast<uintptr_t>(a.ws) % 16 == 0 && static_cast<int64_t>(a.n) * a.kb % 16 == 0 &&
+             (KIND != kMx4 || (reinterpret_cast<uintptr_t>(a.xs) % 4 == 0 && a.xsr % 4 == 0 && a.kb % 4 == 0));
   a.slots = few_slots(a.kb, p.wide);
   const dim3 g(static_cast<unsigned>(tile_rows(a, a.cap) * a.tiles_n));
   GPTQ_LAUNCH((mx_few_kernel<NW, KS, NM, DEPTH, KIND>), g, dim3(NW * 64),

@@ -49,13 +49,6 @@ __device__ __forceinline__ float mlp_act(float g, int act) {
   return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.4426950408889634f * z));
 }
 
-// A barrier for LDS alone, which loads to registers cross.
-__device__ __forceinline__ void lds_barrier() {
-  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
-}
-
 // A token that names an expert twice takes it once, at its first choice, with both weights.
 __device__ __forceinline__ bool first_choice(const int16_t* ids, int i, int top_k) {
   for (int k = i / top_k * top_k; k < i; ++k)
