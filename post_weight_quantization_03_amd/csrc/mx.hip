@@ -141,8 +141,8 @@ struct MxArgs : MmArgs {
 // of 16 NM outputs, KS waves of it share a tile's inputs.  All comes by copies to LDS: the rows at once,
 // and weights in units of 256 inputs, up to DEPTH of them in a ring of each wave's own, so that nothing but
 // the matrix instruction's own reads goes through registers.  The waves' sums are added in their order.
-// Bound by reading the weights: one row of 4096 x 14336 9.4 us (31 MB: 3.3 TB/s from the launch on; 12.7 with
-// loads to registers), 16 tokens with 6 of 64 experts of 1408 x 2048 13.8 us (5.6 TB/s, part of it from the
+// Bound by reading the weights: one row of 4096 x 14336 8.5 us (31 MB: 3.7 TB/s from the launch on; 12.7 with
+// loads to registers), 16 tokens with 6 of 64 experts of 1408 x 2048 13.4 us (5.8 TB/s, part of it from the
 // last-level cache; 26 with loads to registers).  8 waves share a tile of 16 outputs; where there are many
 // tiles 4 waves take one of 32 outputs each, so that 8 times the outputs share the rows of X (these 16 tokens:
 // 17 us with the fastest other form).
@@ -943,9 +943,10 @@ constexpr int tile_blocks(MxProduct p, int kind) { return tile_xb(p, kind) / (ki
 constexpr int tile_buffers(MxProduct p) { return p == kMxTile128 ? 2 : 3; }
 
 // The kernel for few rows: 8 waves sharing one tile of 16 outputs, or 4 waves with one of 32 each.
-constexpr int FEW_DEPTH = 4, WIDE_DEPTH = 2;
+// (units of a ring: 3 rows of 5120 x 5120 7.1 us with 2, 9.1 with 3, 9.5 with 4; one of 4096 x 14336 8.5, 8.9, 9.4)
+constexpr int FEW_DEPTH = 2;
 constexpr int FEW_LDS = 78 * 1024, FEW_MOST_LDS = 150 * 1024;   // two workgroups on a CU, and one
-int few_slots(int kb, bool wide) { return std::min((kb + 7) / 8 / (wide ? 1 : 8) + 1, wide ? WIDE_DEPTH : FEW_DEPTH); }
+int few_slots(int kb, bool wide) { return std::min((kb + 7) / 8 / (wide ? 1 : 8) + 1, FEW_DEPTH); }
 // LDS without rows of X, and of a row.
 int64_t few_fixed(int kb, bool wide) {
   const int64_t scales = wide ? 4 * ((32 * static_cast<int64_t>(kb) + 15) / 16 * 16) : 16 * static_cast<int64_t>(kb);
@@ -979,7 +980,7 @@ constexpr MxCost mx_cost(MxProduct kind, bool four) {
 }
 constexpr double FEW_START = 2.0;
 // a CU's bytes in 1 us of the kernel for few rows, weights and rows of X (conversions slow 16-bit ones)
-constexpr double few_rate(int kind) { return kind == kMx4 ? 21e3 : 18e3; }
+constexpr double few_rate(int kind) { return kind == kMx4 ? 23e3 : 18e3; }
 constexpr double SUM_START = 2.5, SUM_RATE = 4e6;   // of adding parts: bytes written and read in 1 us
 // experts differ, and few large tiles do not even that out (16-bit rows, 4096 tokens: 232 us, 128 x 128 196)
 constexpr double BIG_UNEVEN = 0.6;
@@ -992,12 +993,12 @@ constexpr int CUS = 256;
 // Which kernel, by sizes alone (the workspace's size goes by the same rule): the one with the least estimate.
 // With them (us, in brackets the best of the other kernels; 64 experts of 1408 x 2048):
 //   16-bit rows   4096 x 14336         14336 x 4096          experts, tokens
-//      2          few 10 (15)          few 11 (14)           16: few 14 (33)
+//      2          few 9 (15)           few 10 (14)           16: few 14 (33)
 //      16         32 x 128 15 (18)     32 x 128 15 (18)      256: 32 x 128 38 (45)
 //      256        64 x 128 47 (52)     64 x 128 42 (51)      1024: 64 x 128 78 (85)
 //      512        64 x 128 78 (88)     128 x 128 68 (81)     4096: 128 x 128 196 (232)
 //      2048       256 x 256 214 (227)  256 x 256 207 (245)   16384: 256 x 256 575 (650)
-//   4-bit rows 8: few 10 (12), 32: 32 x 128 13 (14), 512: 64 x 64 41 (59), 1024: 128 x 128 62 (75) of 4096 x 14336
+//   4-bit rows 8: few 9 (12), 32: 32 x 128 13 (14), 512: 64 x 64 41 (59), 1024: 128 x 128 62 (75) of 4096 x 14336
 MxPlan mx_plan(int64_t m, int n, int k, int kind, bool grouped, int experts) {
   const bool four = kind == kMx4;
   const double used = grouped ? static_cast<double>(std::min<int64_t>(experts, m)) : 1.0;
@@ -1114,7 +1115,7 @@ gptq_status launch_mx_big(MxArgs a, void* workspace, hipStream_t stream) {
 template <int KIND>
 gptq_status launch_mx(const MxArgs& a, const MxPlan& p, void* workspace, hipStream_t stream) {
   if (p.kind == kMxFew)
-    return p.wide ? launch_mx_few<4, 1, 2, WIDE_DEPTH, KIND>(a, p, stream)
+    return p.wide ? launch_mx_few<4, 1, 2, FEW_DEPTH, KIND>(a, p, stream)
                   : launch_mx_few<8, 8, 1, FEW_DEPTH, KIND>(a, p, stream);
   if (p.kind == kMxBig) return launch_mx_big<KIND>(a, workspace, stream);
   if (p.kind == kMxTile32) return launch_mx_tile<kMxTile32, KIND>(a, p, workspace, stream);
