@@ -361,9 +361,11 @@ __global__ __launch_bounds__(256) void mx_tile_kernel(MxArgs a) {
   constexpr int FM = XW / 16, FN = WW / 16, H = XB / 64;
   constexpr int STAGE = TM * XB + TN * St::WB, XROWS = 1024 / XB, WROWS = 1024 / St::WB;   // rows of one copy
   constexpr int LX = TM * XB / 1024 / NW, LW = TN * St::WB / 1024 / NW, LD = LX + LW;
-  // two workgroups on a CU: what the buffers leave of half its LDS is for scales
+  // two workgroups on a CU, of 32 rows three: what the buffers leave of their LDS is for scales (experts of 1408 x
+  // 2048, 64 tokens with 6 of 64: 22 us, 28 with three buffers and two workgroups)
+  constexpr int SPACE = (TM == 32 ? 52 : 80) * 1024 - 256;
   constexpr int SROWS = KIND == kMx4 ? TM + TN : TN;
-  constexpr int PB = std::min(256, ((80 * 1024 - 256 - NB * STAGE) / SROWS - 4) / 16 * 16), PITCH = PB + 4;
+  constexpr int PB = std::min(256, ((SPACE - NB * STAGE) / SROWS - 4) / 16 * 16), PITCH = PB + 4;
   static_assert(LX >= 1 && LW >= 1 && PB >= 16 && PB % St::BLOCKS == 0 && SROWS <= 256, "tile shape");
   static_assert(TM % (16 * WM) == 0 && TN % (16 * WN) == 0, "tile shape");
   __shared__ __attribute__((aligned(128))) uint8_t lds[NB * STAGE];
@@ -940,7 +942,7 @@ constexpr int tile_rows_of(MxProduct p) {
 constexpr int tile_outputs(MxProduct p) { return p == kMxBig ? BIG : p == kMxTile64 ? 64 : 128; }
 constexpr int tile_xb(MxProduct p, int kind) { return kind != kMx4 && p != kMxTile128 ? 256 : 128; }
 constexpr int tile_blocks(MxProduct p, int kind) { return tile_xb(p, kind) / (kind == kMx4 ? 16 : 64); }
-constexpr int tile_buffers(MxProduct p) { return p == kMxTile128 ? 2 : 3; }
+constexpr int tile_buffers(MxProduct p) { return p == kMxTile128 || p == kMxTile32 ? 2 : 3; }
 
 // The kernel for few rows: 8 waves sharing one tile of 16 outputs, or 4 waves with one of 32 each.
 // (units of a ring: 3 rows of 5120 x 5120 7.1 us with 2, 9.1 with 3, 9.5 with 4; one of 4096 x 14336 8.5, 8.9, 9.4)
