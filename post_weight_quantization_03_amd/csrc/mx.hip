@@ -905,11 +905,13 @@ __global__ __launch_bounds__(256) void mx_big_kernel(MxArgs a) {
 }
 
 // Y from the sums of the parts, in their order, all loads at once (8 parts of 64 x 4096: 4 us, mostly a
-// launch's; 18 with a loop of loads).
+// launch's; 18 with a loop of loads).  A thread takes 4 outputs of a row, and threads are numbered through all
+// rows: there may be millions of rows of a few outputs.
 template <int SPLITS>
 __global__ __launch_bounds__(256) void mx_sum_kernel(MxArgs a) {
-  const int row = blockIdx.y, o = (blockIdx.x * 256 + threadIdx.x) * 4, n = min(4, a.n - o);
-  if (n <= 0) return;
+  const uint32_t quads = static_cast<uint32_t>(a.n + 3) / 4, g = blockIdx.x * 256 + threadIdx.x, row = g / quads;
+  if (row >= a.m) return;
+  const int o = static_cast<int>(g - row * quads) * 4, n = min(4, a.n - o);
   const float* p = a.part + static_cast<int64_t>(row) * a.n + o;
   f32x4 u[SPLITS];
 #pragma unroll
@@ -1085,7 +1087,8 @@ gptq_status launch_mx_tile(MxArgs a, const MxPlan& p, void* workspace, hipStream
   const dim3 g(static_cast<unsigned>(order_grid(a.order)), static_cast<unsigned>(a.splits));
   GPTQ_LAUNCH((mx_tile_kernel<TM, TN, tile_xb(P, KIND), tile_buffers(P), KIND>), g, dim3(256), 0, stream, a);
   if (p.splits == 1) return GPTQ_OK;
-  const dim3 s((a.n + 1023) / 1024, static_cast<unsigned>(a.m));   // parts are of few tiles: m is small
+  // parts are of at most 64e6 bytes, so there are fewer than 2^23 groups of 4 outputs
+  const dim3 s(static_cast<unsigned>((a.m * ((a.n + 3) / 4) + 255) / 256));
   if (p.splits == 2) GPTQ_LAUNCH(mx_sum_kernel<2>, s, dim3(256), 0, stream, a);
   else if (p.splits == 4) GPTQ_LAUNCH(mx_sum_kernel<4>, s, dim3(256), 0, stream, a);
   else if (p.splits == 8) GPTQ_LAUNCH(mx_sum_kernel<8>, s, dim3(256), 0, stream, a);

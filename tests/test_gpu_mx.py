@@ -446,6 +446,23 @@ def test_elements_past_32_bit_offsets(x):
     check_large(Y[m // 3:m // 3 + 1], torch.ones(1, k, dtype=torch.float64, device="cuda"), W, k, x, "bf16")
 
 
+@pytest.mark.parametrize("x", ["mx", "bf16", "f16"])
+@pytest.mark.parametrize("m,n,k", [(66560, 8, 4096), (70001, 5, 8192), (65539, 16, 8192), (112566, 3, 15040)])
+def test_more_rows_than_a_grid_has_and_parts(m, n, k, x):
+    # parts of the inputs for some type of X each, their sums for more rows than a launch's second dimension may have
+    assert lib().workspace_size(lib().WS_MXFP4_MATMUL, 1, n, k, m) >= 2 * 4 * m * n
+    q, s = random_operand(m, m, k, x)
+    w, ws = random_operand(n, n, k, "mx")
+    Y = lib().mxfp4_matmul(q, w, ws, s, out_dtype=torch.float32)
+    W = wide(w, ws)
+    for at in range(0, m, 16384):
+        end = min(at + 16384, m)
+        check_large(Y[at:end], wide(q[at:end], None if s is None else s[at:end]), W, k, x, "f32")
+    big = torch.full((m, n + 3), 2.5, device="cuda")
+    lib().mxfp4_matmul(q, w, ws, s, out_dtype=torch.float32, out=big[:, :n])
+    assert torch.equal(big[:, :n], Y) and bool((big[:, n:] == 2.5).all())
+
+
 def test_runs_streams_and_workspaces():
     rng = np.random.default_rng(9)
     for x in ("mx", "bf16", "f16"):
