@@ -469,9 +469,11 @@ gptq_status gptq_mxfp4_quantize(int batch, int64_t rows, int cols, gptq_dtype x_
 
 /*
  * The values that such codes stand for: Y[r, c] = scale[r, c / 32] * q[r, c], rounded once to bf16,
- * fp16 or fp32 (fp32 holds all of them, bf16 all up to 2^128; a scale of 255 gives NaN).  Q
- * (16-byte aligned), scales and Y (16-byte aligned) are dense, [rows, cols / 2], [rows, cols / 32] and
- * [rows, cols].  The same sizes as gptq_mxfp4_quantize.
+ * fp16 or fp32.  fp32 and bf16 hold every value below 2^128; those from there on (4 and 6 at scale
+ * 2^126, 2 to 6 at 2^127) are infinite in both.  gptq_mxfp4_quantize gives such a value with scaling 1
+ * alone, for numbers of 1.75 * 2^127 and more.  A scale of 255 gives NaN.  Q (16-byte aligned), scales
+ * and Y (16-byte aligned) are dense, [rows, cols / 2], [rows, cols / 32] and [rows, cols].  The same
+ * sizes as gptq_mxfp4_quantize.
  */
 gptq_status gptq_mxfp4_dequantize(int64_t rows, int cols, const uint8_t* Q, const uint8_t* scales,
                                   gptq_dtype y_dtype, void* Y, hipStream_t stream);

@@ -759,7 +759,7 @@ def _mx_pair(q, scales, what: str):
 def mxfp4_dequantize(q: torch.Tensor, scales: torch.Tensor, dtype: torch.dtype = torch.bfloat16,
                      stream=None) -> torch.Tensor:
     """The values that codes q [.., cols / 2] and scales [.., cols / 32] stand for, [.., cols], in
-    ``dtype`` (fp32 and, below 2^128, bf16 hold all of them)."""
+    ``dtype``.  fp32 and bf16 hold all of them below 2^128, and an infinity from there on."""
     if stream is not None:
         return _on(stream, mxfp4_dequantize, q, scales, dtype)
     if dtype not in _DT:

@@ -192,6 +192,25 @@ def test_dequantize_all_codes_and_scales():
     assert y.shape == (4, 64, 32)
 
 
+def test_values_past_the_largest_are_infinite():
+    # fp32 and bf16 end at 2^128 alike: below it every value, infinities from there on
+    codes = np.tile(np.arange(16, dtype=np.uint8), 2)[None].repeat(3, 0)
+    scales = np.array([[252], [253], [254]], dtype=np.uint8)
+    value = M.E2M1[codes] * 2.0 ** (scales.astype(np.float64) - 127)
+    over = np.abs(value) >= 2.0 ** 128
+    assert [int(o[:8].sum()) for o in over] == [0, 2, 4] and M.E2M1[codes[0]][over[1]].tolist() == [4, 6, -4, -6] * 2
+    for out in ("f32", "bf16"):
+        y = lib().mxfp4_dequantize(*typed(codes, scales), DT[out]).double().cpu().numpy()
+        assert np.array_equal(y[over], np.sign(value[over]) * np.inf) and np.array_equal(y[~over], value[~over])
+        # the rounding comes there with "ceil" alone, from 3.5 * 2^126 on
+        x = torch.zeros(2, 32, dtype=DT[out], device="cuda")
+        x[0, 3], x[1, 3] = 1.75 * 2.0 ** 127, -1.734375 * 2.0 ** 127
+        low = lib().mxfp4_dequantize(*lib().mxfp4_quantize(x, "floor"), DT[out])
+        high = lib().mxfp4_dequantize(*lib().mxfp4_quantize(x, "ceil"), DT[out])
+        assert [float(v) for v in low[:, 3]] == [1.5 * 2.0 ** 127, -1.5 * 2.0 ** 127]
+        assert [float(v) for v in high[:, 3]] == [np.inf, -1.5 * 2.0 ** 127]
+
+
 def test_past_32_bit_offsets():
     X = torch.zeros(140000, 16384, dtype=torch.bfloat16, device="cuda")
     at = [0, 65535, 65536, 131071, 131072, 139999]
