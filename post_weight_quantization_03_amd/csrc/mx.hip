@@ -1188,3 +1188,10 @@ gptq_status mx_matmul_enqueue(const MxProblem& p, hipStream_t stream) {
 }
 
 }  // namespace gptq
+
+// Which form a product takes, for tests that cover every form; not part of the interface.  kind as MxKind,
+// experts 0: not grouped.  MxProduct | wide << 3 | splits << 4 | cap << 9.
+extern "C" int gptq_internal_mxfp4_form(int64_t m, int n, int k, int kind, int experts) {
+  const gptq::MxPlan p = gptq::mx_plan(m, n, k, kind, experts > 0, std::max(experts, 1));
+  return p.kind | p.wide << 3 | p.splits << 4 | p.cap << 9;
+}

@@ -371,13 +371,17 @@ gptq_status launch_half(MlpArgs a, hipStream_t stream) {
 // Waves share a tile's inputs where there are fewer tiles than waves (4 workgroups of 4 for each CU), and
 // where one tile's scales for each wave would take too much LDS: 4 where an expert has one token, else 2, whose
 // tiles share the tokens' rows (16 tokens, 2 of 8 experts, 1408 x 2048: 28 us, 24 so; one token, 6 of 64: 17.5, 17).
+int mlp_waves(bool up, int pairs, int experts, int d, int inner) {
+  const int64_t tiles = static_cast<int64_t>(std::min(experts, pairs)) * (up ? inner / 16 : d / 32);
+  const bool long_rows = (up ? d : inner) > 4096;
+  if (long_rows || tiles <= (pairs <= experts ? 1024 : 384)) return 4;
+  return tiles <= 1024 ? 2 : 1;
+}
 template <bool UP, int KIND>
 gptq_status launch_half(const MlpArgs& a, hipStream_t stream) {
-  const int pairs = a.tokens * a.top_k;
-  const int64_t tiles = static_cast<int64_t>(std::min(a.experts, pairs)) * (UP ? a.inner / 16 : a.d / 32);
-  const bool long_rows = (UP ? a.d : a.inner) > 4096;
-  if (long_rows || tiles <= (pairs <= a.experts ? 1024 : 384)) return launch_half<UP, 4, KIND>(a, stream);
-  if (tiles <= 1024) return launch_half<UP, 2, KIND>(a, stream);
+  const int waves = mlp_waves(UP, a.tokens * a.top_k, a.experts, a.d, a.inner);
+  if (waves == 4) return launch_half<UP, 4, KIND>(a, stream);
+  if (waves == 2) return launch_half<UP, 2, KIND>(a, stream);
   return launch_half<UP, 1, KIND>(a, stream);
 }
 
@@ -416,3 +420,9 @@ gptq_status mx_mlp_enqueue(const MxMlp& p, hipStream_t stream) {
 }
 
 }  // namespace gptq
+
+// How many waves share a tile's inputs in the first (up) or second launch, for tests that cover every form; not
+// part of the interface.
+extern "C" int gptq_internal_mxfp4_mlp_waves(int up, int pairs, int experts, int d, int inner) {
+  return gptq::mlp_waves(up != 0, pairs, experts, d, inner);
+}
