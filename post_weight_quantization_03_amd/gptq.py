@@ -808,7 +808,8 @@ def mxfp4_matmul(X: torch.Tensor, qweight: torch.Tensor, w_scales: torch.Tensor,
     """Y [m, d_out] = X What^T with 4-bit microscaled weights [d_out, d_in / 2] and their scales
     [d_out, d_in / 32] (:func:`mxfp4_quantize`; uint8 tensors are taken as their bits).  X [m, d_in] is
     bf16 or fp16 and multiplied as it is, or [m, d_in / 2] codes with ``x_scales`` [m, d_in / 32].
-    Sums are fp32.  X whose rows do not start at multiples of 16 bytes is copied first."""
+    Sums are fp32.  X whose rows do not start at multiples of 16 bytes is copied first.  ``workspace`` is used
+    if it has :func:`workspace_size` bytes for this m, which are not always more for more rows."""
     if stream is not None:
         return _on(stream, mxfp4_matmul, X, qweight, w_scales, x_scales, out_dtype, out, workspace)
     if qweight.dim() != 2 or qweight.shape[0] < 1:

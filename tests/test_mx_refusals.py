@@ -65,6 +65,15 @@ def test_matmul_workspace_and_empty():
         assert gptq.workspace_size(gptq.WS_MXFP4_MATMUL, *bad) == 0
 
 
+def test_a_workspace_for_more_rows_may_be_too_small_for_fewer():
+    # sizes go by the kernel that m takes: the largest of them serves all, the last does not
+    size = lambda m: gptq.workspace_size(gptq.WS_MXFP4_MATMUL, 1, 4096, 14336, m)
+    assert size(1024) == 256 < size(128)
+    a = {**MATMUL, "n": 4096, "k": 14336, "xt": BF16, "ldx": 14336, "ldy": 4096}
+    assert gptq.lib().gptq_mxfp4_matmul(*{**a, "m": 128, "wsp": 16, "wsb": size(1024)}.values()) == WS
+    assert gptq.lib().gptq_mxfp4_matmul(*{**a, "m": 128, "wsp": 16, "wsb": size(128) // 2 - 1}.values()) == WS
+
+
 def test_too_many_tiles_are_refused():
     for xt, ldx in ((E2M1, 16), (BF16, 32), (F16, 32)):
         for m in (1 << 25, 1 << 40):
