@@ -141,7 +141,7 @@ struct MxArgs : MmArgs {
 // of 16 NM outputs, KS waves of it share a tile's inputs.  All comes by copies to LDS: the rows at once,
 // and weights in units of 256 inputs, up to DEPTH of them in a ring of each wave's own, so that nothing but
 // the matrix instruction's own reads goes through registers.  The waves' sums are added in their order.
-// Bound by reading the weights: one row of 4096 x 14336 8.5 us (31 MB: 3.7 TB/s from the launch on; 12.7 with
+// Bound by reading the weights: one row of 4096 x 14336 8.0 to 8.9 us by card (31 MB: 3.7 TB/s from the launch on; 12.7 with
 // loads to registers), 16 tokens with 6 of 64 experts of 1408 x 2048 13.4 us (5.8 TB/s, part of it from the
 // last-level cache; 26 with loads to registers).  8 waves share a tile of 16 outputs; where there are many
 // tiles 4 waves take one of 32 outputs each, so that 8 times the outputs share the rows of X (these 16 tokens:
@@ -949,7 +949,9 @@ constexpr int tile_buffers(MxProduct p) { return p == kMxTile128 || p == kMxTile
 // The kernel for few rows: 8 waves sharing one tile of 16 outputs, or 4 waves with one of 32 each.
 // (units of a ring: 3 rows of 5120 x 5120 7.1 us with 2, 9.1 with 3, 9.5 with 4; one of 4096 x 14336 8.5, 8.9, 9.4)
 constexpr int FEW_DEPTH = 2;
-constexpr int FEW_LDS = 78 * 1024, FEW_MOST_LDS = 150 * 1024;   // two workgroups on a CU, and one
+// Two workgroups on a CU, and one.  Waves that share a tile hold 8 KB of sums besides, so that a tile of theirs that takes
+// all of the first leaves one there too (5 rows of 16 bits and 4096 inputs: 84 KB).
+constexpr int FEW_LDS = 78 * 1024, FEW_MOST_LDS = 150 * 1024;
 int few_slots(int kb, bool wide) { return std::min((kb + 7) / 8 / (wide ? 1 : 8) + 1, FEW_DEPTH); }
 // LDS without rows of X, and of a row.
 int64_t few_fixed(int kb, bool wide) {
@@ -970,7 +972,8 @@ bool mx_launchable(int64_t m, int n, int experts, const MxPlan& p) {
 
 // What a kernel takes, in us, as measured on the card (two sides of each choice below): the start of a launch
 // and its loop, and its stages of 128 inputs of 16-bit rows or 256 of 4-bit ones where a CU has one workgroup
-// and where it has as many as it holds.
+// and where it has as many as it holds.  Those of 32 x 128 tiles were taken with three buffers and two workgroups
+// on a CU, where there are now two buffers and three workgroups.
 struct MxCost {
   double start, one, full;
   int held;   // workgroups of a CU
@@ -995,14 +998,23 @@ constexpr double big_rest(bool quarters, bool four) {
 constexpr int CUS = 256;
 
 // Which kernel, by sizes alone (the workspace's size goes by the same rule): the one with the least estimate.
-// With them (us, in brackets the best of the other kernels; 64 experts of 1408 x 2048):
-//   16-bit rows   4096 x 14336         14336 x 4096          experts, tokens
-//      2          few 9 (15)           few 10 (14)           16: few 14 (33)
-//      16         32 x 128 15 (18)     32 x 128 15 (18)      256: 32 x 128 38 (45)
-//      256        64 x 128 47 (52)     64 x 128 42 (51)      1024: 64 x 128 78 (85)
-//      512        64 x 128 78 (88)     128 x 128 68 (81)     4096: 128 x 128 196 (232)
-//      2048       256 x 256 214 (227)  256 x 256 207 (245)   16384: 256 x 256 575 (650)
-//   4-bit rows 8: few 9 (12), 32: 32 x 128 13 (14), 512: 64 x 64 41 (59), 1024: 128 x 128 62 (75) of 4096 x 14336
+// What it takes (us, in brackets the best of the other kernels on the same card; experts: 6 of 64 for each token,
+// 1408 x 2048):
+//   16-bit rows   4096 x 14336           14336 x 4096          experts, tokens
+//      2          few 9.5 (14.1)         few 10.7 (13.4)       16: few 14.6 (18.2)
+//      16         32 x 128 14.8 (17.6)   32 x 128 14.4 (17.1)  256: 32 x 128 33 (42)
+//      256        64 x 128 46 (52)       64 x 128 43 (49)      1024: 64 x 128 69 (69)
+//      512        64 x 128 77 (86)       256 x 256 64 (64)     8192: 128 x 128 335 (348)
+//      2048       256 x 256 213 (217)    256 x 256 207 (224)   16384: 256 x 256 579 (633)
+//   4-bit rows    8: few 9.2 (12.6)      8: few 11.1 (11.8)    4: few 9.0 (11.1)
+//      32         64 x 64 13.8 (13.8)    64 x 64 12.1 (13.9)   64: 32 x 128 17.9 (20.6)
+//      512        64 x 64 43 (47)        128 x 128 31 (35)     256: 32 x 128 25 (29)
+//      1024       128 x 128 67 (66)      256 x 256 40 (59)     1024: 128 x 128 43 (45)
+//      4096       256 x 256 105 (171)    256 x 256 139 (196)   4096: 256 x 256 97 (106)
+// It is off where kernels are close and the estimate is that of other buffers, or that of experts, which is low
+// throughout: 16-bit rows, experts of 384, 512 and 4096 tokens 64 x 128 48, 49 and 210 (32 x 128 39 and 43, 128 x 128
+// 192), 4 rows of 14336 x 4096 32 x 128 13.6 (few 11.6); 4-bit rows, experts of 16 and 384 tokens 32 x 128 14.6 and
+// 64 x 64 33 (few 12.9, 32 x 128 27.5).
 MxPlan mx_plan(int64_t m, int n, int k, int kind, bool grouped, int experts) {
   const bool four = kind == kMx4;
   const double used = grouped ? static_cast<double>(std::min<int64_t>(experts, m)) : 1.0;

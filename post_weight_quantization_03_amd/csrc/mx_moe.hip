@@ -18,7 +18,9 @@ namespace {
 
 constexpr int APART = 32;   // counters in a 128-byte line each
 constexpr int MLP_NW = 4, MLP_NT = MLP_NW * 64;
-constexpr int MLP_LDS = 78 * 1024, MLP_MOST_LDS = 150 * 1024;   // two workgroups on a CU, and one
+// Two workgroups on a CU, and one.  Waves that share a tile's inputs hold 8 KB of sums besides, so that one of theirs that
+// takes all of the first leaves one there too (16 tokens, 2 of 8 experts, d 2048, inner 1408: 86 and 85 KB).
+constexpr int MLP_LDS = 78 * 1024, MLP_MOST_LDS = 150 * 1024;
 
 struct MlpArgs {
   int tokens, top_k, experts, d, inner;
