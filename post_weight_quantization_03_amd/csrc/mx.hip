@@ -99,6 +99,10 @@ __global__ __launch_bounds__(256) void mx_dequant_kernel(MxDequantArgs a) {
   __builtin_memcpy(static_cast<T*>(a.Y) + row * a.cols + col, &o, sizeof(o));
 }
 
+// No launch here has more rows, nor outputs (2^22 tiles of 256 rows, 2^24 workgroups of 64): refused ahead of the
+// arithmetic on them, which would overflow at the end of int64.
+constexpr int MX_ROWS = 1 << 30, MX_OUTPUTS = 1 << 30;
+
 // Blocks of a row per workgroup, as a shift: the power of two that holds them, at most 64.
 int block_shift(int kb) {
   int s = 0;
@@ -107,6 +111,7 @@ int block_shift(int kb) {
 }
 // Grid of the two kernels above; false where it is too large.
 bool block_grid(int64_t rows, int kb, int batch, int shift, dim3* grid) {
+  if (rows > MX_ROWS) return false;
   const int64_t gx = (rows + (64 >> shift) - 1) / (64 >> shift), gy = (kb + (1 << shift) - 1) >> shift;
   if (gx > (1 << 24) - 1 || gy > 65535 || batch > 65535) return false;
   *grid = dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy), static_cast<unsigned>(batch));
@@ -1167,10 +1172,9 @@ gptq_status mx_dequantize_enqueue(int64_t rows, int cols, const uint8_t* Q, cons
   return GPTQ_OK;
 }
 
-constexpr int MX_OUTPUTS = 1 << 30;
 size_t mx_workspace(int batch, bool grouped, int64_t m, int n, int k) {
   size_t most = 256;
-  if (m < 1 || n > MX_OUTPUTS) return most;   // nothing is launched
+  if (m < 1 || m > MX_ROWS || n > MX_OUTPUTS) return most;   // nothing is launched
   for (const int kind : {kMx4, kMxBf16})
     most = std::max(most, mx_plan_bytes(mx_plan(m, n, k, kind, grouped, batch), m, n, k, kind, batch));
   return most;
@@ -1185,7 +1189,7 @@ gptq_status mx_matmul_enqueue(const MxProblem& p, hipStream_t stream) {
   a.xs = p.xs; a.xsr = p.xsr;
   const int kind = p.x_dtype == GPTQ_E2M1 ? kMx4 : p.x_dtype == GPTQ_BF16 ? kMxBf16 : kMxF16;
   a.ldx = kind == kMx4 ? p.ldx : 2 * p.ldx;
-  if (a.n > MX_OUTPUTS || (a.off != nullptr && (a.m / 16 + 1) * a.experts > INT32_MAX)) return GPTQ_ERR_UNSUPPORTED;
+  if (a.m > MX_ROWS || a.n > MX_OUTPUTS || (a.off != nullptr && (a.m / 16 + 1) * a.experts > INT32_MAX)) return GPTQ_ERR_UNSUPPORTED;
   MxPlan plan = mx_plan(a.m, a.n, a.k, kind, a.off != nullptr, a.experts);
   // the largest tiles address a tile's rows by 32-bit offsets
   const int64_t span = a.rows == nullptr ? BIG * a.ldx : a.x_rows * a.ldx;

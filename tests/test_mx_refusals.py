@@ -81,6 +81,23 @@ def test_too_many_tiles_are_refused():
             assert gptq.lib().gptq_mxfp4_matmul(*a.values()) == UNS
 
 
+@pytest.mark.parametrize("rows", [(1 << 30) + 1, 1 << 62, (1 << 63) - 40, (1 << 63) - 1])
+def test_rows_up_to_the_end_of_int64_are_refused(rows):
+    L = gptq.lib()
+    for xt, ldx in ((E2M1, 64), (BF16, 128), (F16, 128)):
+        for n in (1, 64, 1 << 20):
+            a = {**MATMUL, "m": rows, "n": n, "xt": xt, "ldx": ldx, "ldy": 1 << 20, "wsp": 16, "wsb": 1 << 62}
+            assert L.gptq_mxfp4_matmul(*a.values()) == UNS
+        for batch, idx in ((1, None), (2, 16), (1024, 16)):
+            a = {**GROUPED, "batch": batch, "xr": rows, "rows": rows, "xt": xt, "ldx": ldx, "idx": idx, "wsp": 16, "wsb": 1 << 62}
+            assert L.gptq_mxfp4_matmul_grouped(*a.values()) == UNS
+    for cols in (32, 64, 4096):
+        assert L.gptq_mxfp4_quantize(1, rows, cols, BF16, 16, cols, 0, 0, 16, 16, None) == UNS
+        assert L.gptq_mxfp4_dequantize(rows, cols, 16, 16, BF16, 16, None) == UNS
+    assert gptq.workspace_size(gptq.WS_MXFP4_MATMUL, 1, 64, 128, rows) == 256
+    assert gptq.workspace_size(gptq.WS_MXFP4_GROUPED, 64, 64, 128, rows) == 256
+
+
 GROUPED = dict(batch=2, xr=8, rows=5, n=64, k=128, xt=E2M1, X=16, ldx=64, xs=3, xsr=4, W=16, ws=3, off=16, idx=None,
                yt=BF16, Y=16, ldy=64, wsp=None, wsb=0, stream=None)
 
